@@ -49,7 +49,7 @@ def listed():
         # few users with very long contexts
         case("decode_4_long", "attend", B=4, past=131071, past_min=90000, heads=(64, 8), page=128),
         # a large batch with long contexts
-        case("decode_32_long", "attend", B=32, past=32767, past_min=20000),
+        case("decode_32_long", "attend", B=32, past=32767, past_min=32001),
         # drafted tokens checked in 32 bits under a window
         case("drafts_f32_window", "attend", dtype="f32", B=16, past=3000, past_min=0, new=5, new_min=1,
              heads=(12, 4), D=64, page=16, window=1024, holes=True),
