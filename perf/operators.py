@@ -77,11 +77,10 @@ def draw(rng):
     c["past"] = spread(1, 131072 if form == "tokens" else 8192)
     while True:   # within the largest listed cases
         total = c["past"] + c["new"]
-        if (c["B"] * total * c["kv_heads"] * c["D"] <= _LARGEST_CODES and
+        if (c["B"] * (total * c["kv_heads"] + 4 * c["new"] * c["q_heads"]) * c["D"] <= 0.98 * _LARGEST_CODES and
                 (kind != "attend" or (
                     c["B"] * c["new"] * total * c["q_heads"] <= _LARGEST_PAIRS and
                     c["B"] * c["new"] * (c["past"] + c["new"] / 2) * c["q_heads"] * c["D"] <= _LARGEST_PRODUCT)) and
-                c["B"] * c["new"] * c["q_heads"] * c["D"] <= _LARGEST_CODES // 8 and
                 (kind == "attend" or c["B"] * c["new"] * c["kv_heads"] * c["D"] <= _LARGEST_CODES // 16)):
             break
         if c["B"] > 1 and (rng.random() < 0.5 or total < 64):
