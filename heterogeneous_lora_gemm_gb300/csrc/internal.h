@@ -40,7 +40,7 @@ struct ChunkRec {
 };
 
 // Bits of the device status word.
-enum : uint32_t { STATUS_BAD_ROW = 1u, STATUS_TIMEOUT = 2u };
+enum : uint32_t { STATUS_BAD_ROW = 1u, STATUS_TIMEOUT = 2u, STATUS_BAD_STEP = 4u };
 
 // Width of one K-extension chunk of the low-rank intermediate (one bf16 MMA K step).
 constexpr int CHUNK = 16;

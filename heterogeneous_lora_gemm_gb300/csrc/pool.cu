@@ -370,6 +370,7 @@ const char* mlora_status_string(mlora_status s) {
         case MLORA_ERR_DEVICE_ROW: return "a row named an invalid or empty slot";
         case MLORA_ERR_UNSUPPORTED: return "unsupported shape";
         case MLORA_ERR_DEVICE_TIMEOUT: return "a kernel pipeline wait gave up";
+        case MLORA_ERR_DEVICE_STEP: return "a step named rows, lengths or pages out of range";
     }
     return "unknown status";
 }

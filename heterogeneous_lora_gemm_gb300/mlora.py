@@ -28,6 +28,7 @@ MLORA_ERR_CUDA = 6
 MLORA_ERR_DEVICE_ROW = 7
 MLORA_ERR_UNSUPPORTED = 8
 MLORA_ERR_DEVICE_TIMEOUT = 9
+MLORA_ERR_DEVICE_STEP = 10
 MLORA_F32 = 0
 MLORA_BF16 = 1
 
@@ -50,6 +51,7 @@ class PoolInfo(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 
 # name -> (restype, argtypes), in header order
 _SIGNATURES = {
@@ -82,6 +84,12 @@ _SIGNATURES = {
     "mlora_project_noalloc": (_I, [_P, _P, _I, _I, _I, _P, _P]),
     "mlora_project_noalloc_status": (_I, [_P]),
     "mlora_debug_noalloc_expire_wait": (_I, [ctypes.c_longlong, _P]),
+    "mlora_cache_create": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.POINTER(_P)]),
+    "mlora_cache_destroy": (_I, [_P]),
+    "mlora_cache_append": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "mlora_cache_read": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "mlora_cache_attend": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, ctypes.c_float, _I, _P]),
+    "mlora_cache_status": (_I, [_P, _P]),
     "mlora_arena_new": (_P, [_I]),
     "mlora_arena_delete": (None, [_P]),
     "mlora_arena_alloc": (_I, [_P, _I, _I]),
@@ -250,6 +258,51 @@ def mlora_dequantize_nf4(codes_ptr: int, absmax_ptr: int, codebook, dout: int, d
                                      stream or None), "mlora_dequantize_nf4")
 
 
+def mlora_cache_create(k_codes_ptr: int, k_scale_ptr: int, v_codes_ptr: int, v_scale_ptr: int, n_pages: int,
+                       page_size: int, kv_heads: int, head_dim: int, q_heads: int) -> int:
+    h = _P()
+    check(lib().mlora_cache_create(k_codes_ptr, k_scale_ptr, v_codes_ptr, v_scale_ptr, n_pages, page_size, kv_heads,
+                                   head_dim, q_heads, ctypes.byref(h)), "mlora_cache_create")
+    return h.value
+
+
+def mlora_cache_destroy(cache: int) -> None:
+    check(lib().mlora_cache_destroy(cache), "mlora_cache_destroy")
+
+
+def mlora_cache_append(cache: int, K_ptr: int, k_row_stride: int, k_head_stride: int, V_ptr: int, v_row_stride: int,
+                       v_head_stride: int, dtype: int, T: int, offsets_ptr: Optional[int], lengths_ptr: int,
+                       pages_ptr: int, n_seqs: int, width: int, max_new: int, stream: int) -> None:
+    check(lib().mlora_cache_append(cache, K_ptr, k_row_stride, k_head_stride, V_ptr, v_row_stride, v_head_stride,
+                                   dtype, T, offsets_ptr or None, lengths_ptr, pages_ptr, n_seqs, width, max_new,
+                                   stream or None), "mlora_cache_append")
+
+
+def mlora_cache_read(cache: int, K_ptr: int, k_row_stride: int, k_head_stride: int, V_ptr: int, v_row_stride: int,
+                     v_head_stride: int, dtype: int, T: int, offsets_ptr: Optional[int], lengths_ptr: int,
+                     pages_ptr: int, n_seqs: int, width: int, max_new: int, stream: int) -> None:
+    check(lib().mlora_cache_read(cache, K_ptr, k_row_stride, k_head_stride, V_ptr, v_row_stride, v_head_stride,
+                                 dtype, T, offsets_ptr or None, lengths_ptr, pages_ptr, n_seqs, width, max_new,
+                                 stream or None), "mlora_cache_read")
+
+
+def mlora_cache_attend(cache: int, Q_ptr: int, q_row_stride: int, q_head_stride: int, O_ptr: int, o_row_stride: int,
+                       o_head_stride: int, dtype: int, T: int, offsets_ptr: Optional[int], lengths_ptr: int,
+                       pages_ptr: int, n_seqs: int, width: int, max_new: int, scale: float, window: int,
+                       stream: int) -> None:
+    check(lib().mlora_cache_attend(cache, Q_ptr, q_row_stride, q_head_stride, O_ptr, o_row_stride, o_head_stride,
+                                   dtype, T, offsets_ptr or None, lengths_ptr, pages_ptr, n_seqs, width, max_new,
+                                   scale, window, stream or None), "mlora_cache_attend")
+
+
+def mlora_cache_status(cache: int, stream: int) -> int:
+    """Returns MLORA_OK, MLORA_ERR_DEVICE_STEP or MLORA_ERR_DEVICE_TIMEOUT; raises on CUDA errors."""
+    s = int(lib().mlora_cache_status(cache, stream or None))
+    if s not in (MLORA_OK, MLORA_ERR_DEVICE_STEP, MLORA_ERR_DEVICE_TIMEOUT):
+        check(s, "mlora_cache_status")
+    return s
+
+
 # ---- torch-facing convenience ------------------------------------------- #
 def _stream_handle(stream) -> int:
     import torch
@@ -367,3 +420,100 @@ class Pool:
         ra = None if row_adapter is None else row_adapter.data_ptr()
         mlora_debug_segments(self.handle, ra, int(perm.shape[0]), perm.data_ptr(), offsets.data_ptr(),
                              _stream_handle(stream))
+
+
+class Cache:
+    """A key/value cache in 8 bits over the caller's pages (torch tensors), see include/mlora.h.
+
+    k_codes, v_codes: int8 [n_pages, kv_heads, page_size, head_dim]; k_scale, v_scale:
+    fp32 [n_pages, kv_heads]; contiguous, on one CUDA device.  The tensors are kept alive
+    by the cache.  A step's arrays: lengths int32 [n_seqs], pages int32 [n_seqs, width],
+    offsets int32 [n_seqs + 1] or None (one row per sequence), max_new >= the rows of any
+    sequence.  Rows are [T, heads, head_dim] bf16 or fp32, a head's elements adjacent
+    (slices of a fused projection's output will do); 16-byte aligned.
+    """
+
+    def __init__(self, k_codes, k_scale, v_codes, v_scale, q_heads: int):
+        import torch
+        self.handle = None
+        self._dtypes = {torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32}
+        self._i32 = torch.int32
+        self._current = torch.cuda.current_stream
+        if k_codes.dim() != 4 or k_codes.dtype != torch.int8 or v_codes.dtype != torch.int8:
+            raise ValueError("codes are int8 [n_pages, kv_heads, page_size, head_dim]")
+        n_pages, kv_heads, page_size, head_dim = k_codes.shape
+        for t, shape in ((k_codes, k_codes.shape), (v_codes, k_codes.shape), (k_scale, (n_pages, kv_heads)),
+                         (v_scale, (n_pages, kv_heads))):
+            if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != k_codes.device or not t.is_cuda:
+                raise ValueError("codes and scales of keys and values are contiguous, alike and on one CUDA device")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise ValueError("scales are fp32 [n_pages, kv_heads]")
+        self._keep = (k_codes, k_scale, v_codes, v_scale)
+        self.device = k_codes.device
+        self.kv_heads, self.q_heads, self.page_size, self.head_dim = kv_heads, q_heads, page_size, head_dim
+        self._lib = lib()
+        with torch.cuda.device(self.device):
+            self.handle = mlora_cache_create(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(),
+                                             v_scale.data_ptr(), n_pages, page_size, kv_heads, head_dim, q_heads)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            mlora_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _call(self, fn, where, a, b, heads, lengths, pages, offsets, max_new, stream, *more):
+        code = self._dtypes.get(a.dtype)
+        if code is None or b.dtype != a.dtype:
+            raise ValueError("rows are bf16 or fp32, both operands alike")
+        T = a.shape[0]
+        if a.shape != (T, heads, self.head_dim) or b.shape != a.shape:
+            raise ValueError(f"rows are [T, {heads}, {self.head_dim}], got {tuple(a.shape)} and {tuple(b.shape)}")
+        (ar, ah, ae), (br, bh, be) = a.stride(), b.stride()
+        if ae != 1 or be != 1:
+            raise ValueError("a head's elements must be adjacent")
+        if pages.dim() != 2 or pages.dtype != self._i32 or not pages.is_contiguous():
+            raise ValueError("pages is a contiguous int32 [n_seqs, width]")
+        n_seqs, width = pages.shape
+        if lengths.shape != (n_seqs,) or lengths.dtype != self._i32 or not lengths.is_contiguous():
+            raise ValueError("lengths is a contiguous int32 [n_seqs]")
+        if offsets is not None and (offsets.shape != (n_seqs + 1,) or offsets.dtype != self._i32 or
+                                    not offsets.is_contiguous()):
+            raise ValueError("offsets is a contiguous int32 [n_seqs + 1]")
+        for t in (a, b, lengths, pages, offsets):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"operands live on the cache's device {self.device}")
+        if stream is None:
+            stream = self._current(self.device)
+        status = fn(self.handle, a.data_ptr(), ar, ah, b.data_ptr(), br, bh, code, T,
+                    None if offsets is None else offsets.data_ptr(), lengths.data_ptr(), pages.data_ptr(), n_seqs,
+                    width, max_new, *more, stream.cuda_stream)
+        if status:
+            check(status, where)
+
+    def append(self, K, V, lengths, pages, offsets=None, max_new: int = 1, stream=None) -> None:
+        """Quantises the step's key and value rows [T, kv_heads, head_dim] into the pages."""
+        self._call(self._lib.mlora_cache_append, "mlora_cache_append", K, V, self.kv_heads, lengths, pages, offsets,
+                   max_new, stream)
+
+    def read(self, K, V, lengths, pages, offsets=None, max_new: int = 1, stream=None) -> None:
+        """Restores the last rows of each sequence into K and V [T, kv_heads, head_dim]."""
+        self._call(self._lib.mlora_cache_read, "mlora_cache_read", K, V, self.kv_heads, lengths, pages, offsets,
+                   max_new, stream)
+
+    def attend(self, Q, O, lengths, pages, offsets=None, max_new: int = 1, scale: Optional[float] = None,
+               window: int = 0, stream=None) -> None:
+        """Causal attention of the step's rows Q [T, q_heads, head_dim] over the cache, into O
+        (scale: head_dim ** -0.5 by default; window: tokens a row sees at most, 0 = all)."""
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        self._call(self._lib.mlora_cache_attend, "mlora_cache_attend", Q, O, self.q_heads, lengths, pages, offsets,
+                   max_new, stream, scale, window)
+
+    def status(self, stream=None) -> int:
+        return mlora_cache_status(self.handle, _stream_handle(stream))

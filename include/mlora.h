@@ -56,7 +56,8 @@ typedef enum mlora_status {
     MLORA_ERR_CUDA = 6,          /* a CUDA runtime call failed (no device, launch failure, ...) */
     MLORA_ERR_DEVICE_ROW = 7,    /* (mlora_pool_status) a row named an invalid or empty slot */
     MLORA_ERR_UNSUPPORTED = 8,   /* shape outside what the kernels handle (see mlora_pool_create) */
-    MLORA_ERR_DEVICE_TIMEOUT = 9 /* (mlora_pool_status) a kernel pipeline wait gave up after its limit */
+    MLORA_ERR_DEVICE_TIMEOUT = 9, /* (mlora_pool_status) a kernel pipeline wait gave up after its limit */
+    MLORA_ERR_DEVICE_STEP = 10   /* (mlora_cache_status) a step named rows, lengths or pages out of range */
 } mlora_status;
 
 typedef enum mlora_dtype { MLORA_F32 = 0, MLORA_BF16 = 1 } mlora_dtype;
@@ -412,6 +413,101 @@ mlora_status mlora_project_noalloc_status(mlora_stream_t stream);
  * Nothing faults or hangs.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_stream_t stream);
+
+/*
+ * Key/value cache in 8 bits and its attention: what a served layer does between its
+ * q|k|v projection and its output projection.  The projections' rows of a step (any
+ * mix of sequences) are appended to each sequence's pages, and each sequence's new
+ * rows then attend to everything the sequence holds.
+ *
+ * The caller owns the pages (device memory, on the device current at creation):
+ *   k_codes, v_codes  int8 [n_pages][kv_heads][page_size][head_dim], 16-byte aligned
+ *   k_scale, v_scale  fp32 [n_pages][kv_heads]
+ * a stored value is code * scale, one scale per page and head, for keys and for values.
+ *
+ * A step is described to every call below by the same arrays (device, int32):
+ *   offsets  [n_seqs + 1]: rows offsets[b] .. offsets[b+1] are sequence b's, in order;
+ *            non-decreasing, at most T (rows outside every range are left alone);
+ *            NULL = one row per sequence (T == n_seqs), the form of a decode step
+ *   lengths  [n_seqs]: tokens sequence b holds once the step is appended; its n_b rows
+ *            are its last ones, at positions lengths[b] - n_b .. lengths[b] - 1
+ *   pages    [n_seqs][width]: page of each block of page_size tokens; entries past
+ *            ceil(lengths[b] / page_size) are not read
+ *   max_new  >= every n_b (host; it sizes the launch)
+ * with n_seqs <= 65535 and width * page_size <= 2^30.
+ * Rows at negative positions (lengths[b] < n_b: a padded slot of a batch, a left-padded
+ * prompt) name no token: append skips them, read and attend write zeros.
+ * Offsets, lengths or page ids out of range make no access out of bounds and set the
+ * status bit that mlora_cache_status reports: a bad range of offsets counts as no rows,
+ * a length is clamped to 0 .. width * page_size, rows past max_new are not processed,
+ * a token in a bad page is not stored and reads as a zero key and value.
+ *
+ * Row operands (K, V, Q, O) are [T][heads][head_dim] of `dtype` (MLORA_BF16 or
+ * MLORA_F32) with element strides row_stride and head_stride and adjacent elements of a
+ * head, e.g. the column slices of a fused q|k|v projection's output; 16-byte aligned,
+ * strides multiples of 16 bytes.  The calls take a stream as described at the top of
+ * this file; a cache, like a pool, serves one stream and one host thread at a time.
+ * Attention may share pages between sequences; a page that is appended to belongs to
+ * one sequence.
+ */
+typedef struct mlora_cache* mlora_cache_t;
+
+/*
+ * Makes a handle over the caller's pages, which stay valid until it is destroyed.
+ *   page_size  tokens per page: 16, 32, 48, ... 256
+ *   head_dim   16, 32, 48, ... 256;  q_heads  a multiple of kv_heads, <= 32767
+ * The handle allocates its workspace (a status word and the partial results of split
+ * sequences) here; append, read and attend allocate nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),
+ * OOM, CUDA.  Argument checks run before any CUDA call.
+ */
+mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, float* v_scale, int n_pages,
+                                int page_size, int kv_heads, int head_dim, int q_heads, mlora_cache_t* out);
+/* Waits for the device's outstanding work and frees the workspace. NULL is a no-op. */
+mlora_status mlora_cache_destroy(mlora_cache_t cache);
+
+/*
+ * Quantises the step's key and value rows into the pages.  Per touched page and head,
+ * with x the values that it then holds (what it held restored, and the new rows):
+ *   s = max(s_old, max over new rows |x| / 127)     (s_old = 0 if the page's first token is new)
+ *   code = rint(x * (1 / s)) clamped to [-127, 127] (ties to even; 0 where s < 2^-120)
+ * in fp32; codes written before change only where s grew.  Infinities and NaN do not
+ * enter the maximum: an infinity is stored as +-127 s, a NaN as 0.
+ * Errors: INVALID_ARG, CUDA.
+ */
+mlora_status mlora_cache_append(mlora_cache_t cache, const void* K, int64_t k_row_stride, int64_t k_head_stride,
+                                const void* V, int64_t v_row_stride, int64_t v_head_stride, mlora_dtype dtype, int T,
+                                const int32_t* offsets, const int32_t* lengths, const int32_t* pages, int n_seqs,
+                                int width, int max_new, mlora_stream_t stream);
+/*
+ * Restores the step's tokens (the last n_b of each sequence) into rows:
+ * K[row] = code * scale, in fp32, rounded once to `dtype`; V likewise.
+ * Errors: INVALID_ARG, CUDA.
+ */
+mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride, int64_t k_head_stride, void* V,
+                              int64_t v_row_stride, int64_t v_head_stride, mlora_dtype dtype, int T,
+                              const int32_t* offsets, const int32_t* lengths, const int32_t* pages, int n_seqs,
+                              int width, int max_new, mlora_stream_t stream);
+/*
+ * Causal attention of the step's rows over the cache (after mlora_cache_append):
+ *   O[i, h] = sum_j p_j v_j,  p = softmax_j(scale * Q[i, h] . k_j)
+ * over the tokens j of the row's sequence with j <= pos(i), and j > pos(i) - window
+ * where window > 0; query head h reads key/value head h / (q_heads / kv_heads).  A row
+ * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums and softmax statistics are fp32; O is rounded
+ * once.  O must not overlap Q.
+ * Errors: INVALID_ARG, CUDA.
+ */
+mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_row_stride, int64_t q_head_stride,
+                                void* O, int64_t o_row_stride, int64_t o_head_stride, mlora_dtype dtype, int T,
+                                const int32_t* offsets, const int32_t* lengths, const int32_t* pages, int n_seqs,
+                                int width, int max_new, float scale, int window, mlora_stream_t stream);
+/*
+ * Synchronizes `stream`, then reads and clears the cache's device status word: MLORA_OK,
+ * MLORA_ERR_DEVICE_STEP (a step since the last call was out of range, see above),
+ * MLORA_ERR_DEVICE_TIMEOUT (a pipeline wait in a kernel gave up after its bounded limit;
+ * that call's output is not valid) or MLORA_ERR_CUDA.
+ */
+mlora_status mlora_cache_status(mlora_cache_t cache, mlora_stream_t stream);
 
 /*
  * Host-only view of the arena allocator the pool uses (no CUDA calls), for tests
