@@ -1,0 +1,20 @@
+// Attention over the 8-bit cache: what the handle (cache.cu) keeps for its kernels.
+#pragma once
+#include "cache.h"
+
+namespace mlora {
+
+constexpr int ATTEND_OCC = 2;               // CTAs per SM of the split kernel
+constexpr int ATTEND_SLOT = 32 * (128 + 2); // floats of one partial result at most
+
+struct AttendWs {
+    CUtensorMap k16, v16;   // codes as rows of head_dim bytes, boxes of 16 tokens
+    float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT]
+    int* counters;          // [sms * ATTEND_OCC] arrivals, zero between calls
+    int sms;
+};
+
+cudaError_t attend_split_init();
+cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
+
+}  // namespace mlora

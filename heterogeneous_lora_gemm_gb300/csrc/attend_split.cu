@@ -1,0 +1,661 @@
+// Causal attention over the 8-bit cache for sequences with few rows in the step (decode:
+// one token), any row and head count (include/mlora.h).
+//
+// Mathematics.  With codes kc, vc and page scales ks, vs, row r (query token i, query head
+// g of the key/value head's group) has  x_t = scale ks_t (q_r . kc_t),  and
+//     o_r = sum_t 2^(x'_t - m) vs_t vc_t / sum_t 2^(x'_t - m),   x' = x log2 e,
+// with a running m: only a lower bound of the maximum is needed, so m moves (and the
+// accumulators are rescaled) only when some x' exceeds m + 8.
+//
+// Products run on mma.sync m16n8k16 with fp32 sums, transposed: tokens (S^T = K Q^T) and
+// head elements (O^T = V^T P^T) are the 16-row side, query rows the 8-column side, so that
+// a group of up to 8 heads wastes nothing.  S^T takes fp16: a code is exact in it (byte ^
+// 0x80 under the exponent of 1024, minus 1152: the cheapest conversion), and so is a bf16
+// query that a power of two per row has brought below 1 (its elements under 2^-14 of the
+// row's largest round to 2^-25 of it).  O^T takes bf16: the weights, times vs, need its
+// range (a heavy token may hold a zero where light ones do not); one rounding of each
+// weight to 8 bits.  fp32 rows run the same products with the query as the sum of two fp16
+// terms (22 bits) and the weights as three bf16 terms (24 bits).
+//
+// Bound: HBM (the codes are read once per row tile).  Each warp streams 16-token chunks
+// of its own through a private ring of TMA copies: no CTA-wide barrier in the loop.
+// Work split: all (sequence, row tile, head) items' tokens in one line, cut into equal
+// ranges, one per CTA (two CTAs per SM); every CTA finds its range from the lengths.  An
+// item cut between CTAs is joined, in range order, by the CTA that finishes it last, so
+// results do not depend on timing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attend.h"
+#include "tc_ptx.cuh"
+
+namespace mlora {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int WARPS = 4, THREADS = 32 * WARPS;
+constexpr int CHUNK_T = 16;               // tokens a warp takes at a time
+constexpr int MIN_UNITS = 2;              // a CTA's range is at least so many units of WARPS chunks
+constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights stay below 2^8
+constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
+
+template <bool F32, int DP, int NT>
+struct Shape {
+    static constexpr int TERMS = F32 ? 2 : 1;          // of a query
+    static constexpr int PTERMS = F32 ? 3 : 1;         // of a weight
+    static constexpr int KS = DP / 16;                 // k steps of q . k = 16-row tiles of O^T
+    static constexpr int RT = 8 * NT;                  // query rows per tile
+    static constexpr int CB = DP == 256 ? 2 : 1;       // column boxes
+    static constexpr int ROWB = DP / CB;               // bytes of a box row
+    static constexpr int BOX = CHUNK_T * ROWB;
+    static constexpr int STAGE = 2 * CB * BOX;         // keys and values of a chunk
+    static constexpr int STAGES = DP == 64 ? 8 : DP == 128 ? 6 : 3;
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
+    static constexpr int SMEM = 1024 + RING + QWORDS * 4;
+    static constexpr int SLOT = RT * (DP + 2);             // floats of a partial result: O, then m, l per row
+    static_assert(WARPS * RT * DP * 4 <= RING, "the join buffer lies in the ring");
+};
+
+// shared-memory offset of 16-byte chunk `c` of box row `r`
+template <int ROWB>
+__device__ __forceinline__ int swz(int r, int c) {
+    return ROWB == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+// two bytes (code + 128) under 0x64 -> two codes in fp16
+__device__ __forceinline__ uint32_t minus1152(uint32_t u) {
+    const __half2 h = __hsub2(*reinterpret_cast<__half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// two bytes under 0x43 -> two codes in bf16: 128 + low 7 bits, minus 128 or (sign bit) 256
+__device__ __forceinline__ uint32_t bf16_codes(uint32_t u) {
+    const uint32_t a = u & 0xFF7FFF7Fu, b = u & 0xFF80FF80u;
+    const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void mma_bf(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf2_of(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A sequence's share of the work line.
+struct Line {
+    SeqRec s;
+    int c0, c1;       // 16-token chunks [c0, c1) that its rows see
+    int tiles, units; // row tiles, units per (tile, head)
+    __device__ long long total(int heads) const { return (long long)tiles * heads * units; }
+};
+template <int RT>
+__device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
+    Line n;
+    n.s = load_seq(a.step, a.pages.page, b, a.status);
+    const int last = n.s.start + n.s.rows - 1;   // position of the last processed row
+    const int lo = a.window > 0 ? max(0, n.s.start - a.window + 1) : 0;
+    n.c0 = lo / CHUNK_T;
+    n.c1 = last >= 0 ? last / CHUNK_T + 1 : n.c0;
+    n.tiles = (int)(((long long)n.s.rows * G + RT - 1) / RT);
+    n.units = max(1, (n.c1 - n.c0 + WARPS - 1) / WARPS);
+    return n;
+}
+
+struct Tail {
+    uint64_t full[WARPS][8];
+    int abort_flag;
+    int first_b, last_of;
+    long long first_at, total;
+    long long scan[WARPS];
+    float qf[32];
+    float m[WARPS][32], l[WARPS][32];
+};
+
+template <typename E>
+__device__ __forceinline__ void store4(E* p, float4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float* p, float4 v) {
+    *reinterpret_cast<float4*>(p) = v;
+}
+template <>
+__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
+template <bool F32, int DP, int NT>
+__global__ void __launch_bounds__(THREADS, 2)
+attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
+                    float* __restrict__ partial, int* __restrict__ counters) {
+    using Sh = Shape<F32, DP, NT>;
+    using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    constexpr int KS = Sh::KS, RT = Sh::RT, TERMS = Sh::TERMS, PTERMS = Sh::PTERMS, CB = Sh::CB;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + Sh::RING);
+    float* join = reinterpret_cast<float*>(smem);
+    __shared__ Tail tl;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+    const CachePages& c = a.pages;
+    const int H = c.heads, G = a.q_heads / H, D = c.dim;
+
+    // ---- this CTA's range of the line
+    if (lane == 0) {
+        for (int s = 0; s < Sh::STAGES; ++s) mbar_init(&tl.full[warp][s], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) tl.abort_flag = 0;
+    const int per = (a.step.n_seqs + THREADS - 1) / THREADS;
+    const int b_lo = min(tid * per, a.step.n_seqs), b_hi = min(b_lo + per, a.step.n_seqs);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += line_of<RT>(a, G, b).total(H);
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(~0u, incl, d);
+        if (lane >= d) incl += v;
+    }
+    if (lane == 31) tl.scan[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += tl.scan[w];
+        total += tl.scan[w];
+    }
+    before += incl - mine;
+    const long long want = (total + MIN_UNITS - 1) / MIN_UNITS;
+    const int ctas = (int)(want < (long long)gridDim.x ? want : (long long)gridDim.x);
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    auto range_at = [&](int i) { return total * i / ctas; };
+    // the CTA whose range holds unit u
+    auto cta_of = [&](long long u) {
+        int i = (int)((u * ctas + ctas) / total);
+        i = min(i, ctas - 1);
+        while (i > 0 && range_at(i) > u) --i;
+        while (i + 1 < ctas && range_at(i + 1) <= u) ++i;
+        return i;
+    };
+    long long at = range_at(cta);
+    const long long end = range_at(cta + 1);
+    if (at >= before && at < before + mine) {
+        long long p = before;
+        int b = b_lo;
+        for (; b < b_hi; ++b) {
+            const long long t = line_of<RT>(a, G, b).total(H);
+            if (at < p + t) break;
+            p += t;
+        }
+        tl.first_b = b;
+        tl.first_at = p;
+    }
+    __syncthreads();
+    int b = tl.first_b;
+    long long b_at = tl.first_at;   // where sequence b begins on the line
+    Line n = line_of<RT>(a, G, b);
+
+    uint32_t issued = 0, used = 0;     // chunks copied and consumed by this warp, over all items
+    uint8_t* ring = smem + warp * Sh::STAGES * Sh::STAGE;
+    volatile int* abort_flag = &tl.abort_flag;
+    bool alive = true;
+
+    while (at < end) {
+        while (at >= b_at + n.total(H)) {
+            b_at += n.total(H);
+            n = line_of<RT>(a, G, ++b);
+        }
+        const int item = (int)((at - b_at) / n.units);
+        const long long item_at = b_at + (long long)item * n.units;
+        const int u0 = (int)(at - item_at), u1 = (int)min((long long)n.units, end - item_at);
+        const int h = item % H, tile = item / H;
+        const int r0 = tile * RT, rows = min(RT, n.s.rows * G - r0);
+        // positions that the tile's rows may see: row r at start + (r0 + r) / G
+        const int pos_lo = n.s.start + r0 / G, pos_hi = n.s.start + (r0 + rows - 1) / G;
+        const int ca = max(n.c0 + u0 * WARPS, a.window > 0 ? max(0, pos_lo - a.window + 1) / CHUNK_T : 0);
+        const int cb = min(min(n.c0 + u1 * WARPS, n.c1), pos_hi >= 0 ? pos_hi / CHUNK_T + 1 : 0);
+        const int count = max(0, (cb - ca - warp + WARPS - 1) / WARPS);   // this warp's chunks: ca + warp, + WARPS, ...
+
+        // ---- page ids and scales of up to 32 chunks, one per lane, a batch ahead
+        auto ids_at = [&](int k) {
+            const int t = (ca + warp + k * WARPS) * CHUNK_T;
+            return k < count ? load_page(a.step, c, b, t / c.page, a.status) : -1;
+        };
+        auto row_of = [&](int id, int k) {   // first code row of chunk k; past the tensor for a bad page
+            const int t = (ca + warp + k * WARPS) * CHUNK_T;
+            return id < 0 ? c.n_pages * H * c.page : (id * H + h) * c.page + t % c.page;
+        };
+        int id = ids_at(lane), id1 = ids_at(32 + lane);
+        float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
+        int row = row_of(id, lane), row1 = row_of(id1, 32 + lane);
+        float ks1 = 0.f, vs1 = 0.f;
+
+        auto issue = [&](int k, int batch) {   // copies chunk k of the item (lane 0); `row` holds batch `batch`
+            const int r = __shfl_sync(~0u, (k >> 5) == batch ? row : row1, k & 31);
+            if (lane == 0) {
+                const uint32_t s = issued % Sh::STAGES;
+                uint8_t* st = ring + s * Sh::STAGE;
+                uint64_t* bar = &tl.full[warp][s];
+                mbar_expect_tx(bar, Sh::STAGE);
+#pragma unroll
+                for (int q = 0; q < CB; ++q) {
+                    tma_2d(st + q * Sh::BOX, &tmK, bar, q * 128, r);
+                    tma_2d(st + (CB + q) * Sh::BOX, &tmV, bar, q * 128, r);
+                }
+            }
+            ++issued;
+        };
+        int next = 0;   // next chunk to copy
+        if (alive)
+            for (; next < min(count, Sh::STAGES); ++next) issue(next, 0);
+
+        // ---- queries: fp16 fragments, one row per warp at a time
+        for (int r = warp; r < RT; r += WARPS) {
+            float x[DP / 32];
+            float top = 0.f;
+            bool fine = true;
+            const E* q = (const E*)a.q.ptr + (int64_t)(n.s.row0 + (r0 + r) / G) * a.q.row +
+                         (int64_t)(h * G + (r0 + r) % G) * a.q.head;
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e) {
+                x[e] = r < rows && lane + 32 * e < D ? (float)q[lane + 32 * e] : 0.f;
+                fine &= fabsf(x[e]) <= 3.402823466e38f;
+                top = fmaxf(top, fabsf(x[e]));
+            }
+            fine = __all_sync(~0u, fine);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            // 2^-k with top 2^-k in [1/2, 1); top below 2^-100 counts as 2^-100
+            // (and above 2^127 stays in [1, 2))
+            const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 127) : 0;
+            const float down = __uint_as_float((uint32_t)(127 - min(k, 126)) << 23);
+            const float down2 = k > 126 ? 0.5f : 1.f;   // 2^-127 is not a normal number: two steps
+            if (lane == 0)
+                tl.qf[r] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e) {
+                const int d = lane + 32 * e, ch = d % 128 / 16, w = d % 16 / 4;
+                const int s = DP == 64 ? w : d / 128 * 8 + ch % 2 * 4 + w, t = DP == 64 ? ch : ch / 2;
+                const float v = fine ? x[e] * down * down2 : 0.f;
+                const __half hi = __float2half_rn(v);
+                __half* dst = reinterpret_cast<__half*>(
+                    qfrag + ((((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + d % 4 / 2)) + d % 2;
+                *dst = hi;
+                if (TERMS == 2) dst[128] = __float2half_rn(v - __half2float(hi));
+            }
+        }
+        __syncthreads();
+        uint2 qreg[KS][NT][TERMS];
+        constexpr bool QREG = KS * NT * TERMS <= 16;
+        auto qf_at = [&](int s, int t, int term) {
+            return *reinterpret_cast<const uint2*>(qfrag + (((s * NT + t) * TERMS + term) * 32 + lane) * 2);
+        };
+        if (QREG)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int term = 0; term < TERMS; ++term) qreg[s][t][term] = qf_at(s, t, term);
+        float qf[NT][2], m[NT][2], l[NT][2], o[KS][NT][4];
+        int hi[NT][2];   // tokens [hi - window, hi) are seen
+        int hi_min = 0x7fffffff, hi_max = -0x7fffffff;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = t * 8 + 2 * tig + e;
+                qf[t][e] = tl.qf[r];
+                m[t][e] = NO_MAX;
+                l[t][e] = 0.f;
+                hi[t][e] = n.s.start + (r0 + min(r, rows - 1)) / G + 1;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) o[s][t][e] = o[s][t][2 + e] = 0.f;
+            }
+        hi_min = pos_lo + 1;
+        hi_max = pos_hi + 1;
+        const int lo_max = a.window > 0 ? hi_max - a.window : 0;
+
+        // ---- this warp's chunks
+        for (int k = 0; k < count && alive; ++k) {
+            if (k && (k & 31) == 0) {
+                id = id1, row = row1, ks = ks1, vs = vs1;
+                id1 = ids_at(k + 32 + lane);
+                row1 = row_of(id1, k + 32 + lane);
+            }
+            if ((k & 31) == 8) {   // the next batch's scales, well before they are used
+                ks1 = id1 >= 0 ? c.k_scale[(size_t)id1 * H + h] : 0.f;
+                vs1 = id1 >= 0 ? c.v_scale[(size_t)id1 * H + h] : 0.f;
+            }
+            const float ksk = __shfl_sync(~0u, ks, k & 31), vsk = __shfl_sync(~0u, vs, k & 31);
+            const uint32_t st = used % Sh::STAGES;
+            alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], (used / Sh::STAGES) & 1, abort_flag, a.status));
+            if (!alive) break;
+            const uint8_t* kb = ring + st * Sh::STAGE;
+            const uint8_t* vb = kb + CB * Sh::BOX;
+
+            float sc[NT][4] = {};
+            constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
+#pragma unroll
+            for (int q = 0; q < CB; ++q)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int ch = J * tig + j;
+                    const uint4 ra = *reinterpret_cast<const uint4*>(kb + q * Sh::BOX + swz<Sh::ROWB>(g, ch));
+                    const uint4 rb = *reinterpret_cast<const uint4*>(kb + q * Sh::BOX + swz<Sh::ROWB>(g + 8, ch));
+                    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int s = (q * J + j) * 4 + w;
+                        const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
+                        const uint32_t a0 = minus1152(prmt(xa, 0x64646464u, 0x4140)),
+                                       a1 = minus1152(prmt(xb, 0x64646464u, 0x4140)),
+                                       a2 = minus1152(prmt(xa, 0x64646464u, 0x4342)),
+                                       a3 = minus1152(prmt(xb, 0x64646464u, 0x4342));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int term = 0; term < TERMS; ++term) {
+                                const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
+                                mma(sc[t], a0, a1, a2, a3, f.x, f.y);
+                            }
+                    }
+                }
+            // scores -> x log2 e; tokens g and g + 8 of the chunk, rows 2 tig and 2 tig + 1 of each tile
+            const int t0 = (ca + warp + k * WARPS) * CHUNK_T;
+            const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
+            bool above = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = qf[t][e] * ksk;
+                    sc[t][e] *= f;
+                    sc[t][2 + e] *= f;
+                    if (edge) {
+                        const int from = a.window > 0 ? hi[t][e] - a.window : 0;
+                        if (t0 + g >= hi[t][e] || t0 + g < from) sc[t][e] = -INFINITY;
+                        if (t0 + g + 8 >= hi[t][e] || t0 + g + 8 < from) sc[t][2 + e] = -INFINITY;
+                    }
+                    above |= fmaxf(sc[t][e], sc[t][2 + e]) > m[t][e] + SLACK;
+                }
+            if (__any_sync(~0u, above)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(sc[t][e], sc[t][2 + e]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+                        x = fmaxf(x, m[t][e]);
+                        const float f = ex2(m[t][e] - x);
+                        m[t][e] = x;
+                        l[t][e] *= f;
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) {
+                            o[s][t][e] *= f;
+                            o[s][t][2 + e] *= f;
+                        }
+                    }
+            }
+            uint32_t p[NT][PTERMS][2];   // weights times vs as the B operand: tokens x rows
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = ex2(sc[t][e] - m[t][e & 1]);
+                l[t][0] += w[0] + w[2];
+                l[t][1] += w[1] + w[3];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    float x0 = w[2 * z] * vsk, x1 = w[2 * z + 1] * vsk;
+#pragma unroll
+                    for (int term = 0; term < PTERMS; ++term) {
+                        const uint32_t u = bf2_of(x0, x1);
+                        p[t][term][z] = transpose8(u);
+                        x0 -= __uint_as_float(u << 16);
+                        x1 -= __uint_as_float(u & 0xFFFF0000u);
+                    }
+                }
+            }
+            // O^T += V^T P^T; thread's elements: 16 (DP 64: 8) adjacent ones, of tokens 2 tig, + 1, + 8, + 9
+            constexpr int W = Sh::ROWB / 32;   // words of a box row per thread
+#pragma unroll
+            for (int q = 0; q < CB; ++q) {
+                uint32_t v[4][W];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int r = 2 * tig + (z & 1) + (z >> 1) * 8;
+                    if (W == 4) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(vb + q * Sh::BOX + swz<Sh::ROWB>(r, g));
+                        v[z][0] = u.x, v[z][1] = u.y, v[z][W - 2] = u.z, v[z][W - 1] = u.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(vb + q * Sh::BOX + swz<Sh::ROWB>(r, g >> 1) +
+                                                                       (g & 1) * 8);
+                        v[z][0] = u.x, v[z][1] = u.y;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    uint32_t y[2][4];   // [token pair][element of the word]
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t e0 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x5140),
+                                       e1 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x7362);
+                        y[z][0] = bf16_codes(prmt(e0, 0x43434343u, 0x4140));
+                        y[z][1] = bf16_codes(prmt(e0, 0x43434343u, 0x4342));
+                        y[z][2] = bf16_codes(prmt(e1, 0x43434343u, 0x4140));
+                        y[z][3] = bf16_codes(prmt(e1, 0x43434343u, 0x4342));
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int s = q * (KS / CB) + w * 2 + z;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                            for (int term = 0; term < PTERMS; ++term)
+                                mma_bf(o[s][t], y[0][2 * z], y[0][2 * z + 1], y[1][2 * z], y[1][2 * z + 1],
+                                       p[t][term][0], p[t][term][1]);
+                        }
+                    }
+                }
+            }
+            ++used;
+            __syncwarp();
+            if (next < count) {
+                issue(next, k >> 5);
+                ++next;
+            }
+        }
+        if (!alive)   // copies in flight land before the ring is used for anything else
+            for (; used != issued; ++used) {
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&tl.full[warp][used % Sh::STAGES], (used / Sh::STAGES) & 1) &&
+                       clock64() - t0 < 200000000ll) {
+                }
+            }
+
+        // ---- join the warps: rows' m and l, then O through shared memory
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(~0u, l[t][e], d);
+                if (g == 0) {
+                    tl.m[warp][t * 8 + 2 * tig + e] = m[t][e];
+                    tl.l[warp][t * 8 + 2 * tig + e] = l[t][e];
+                }
+            }
+        __syncthreads();   // every warp is done with its ring
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = t * 8 + 2 * tig + e;
+                float top = tl.m[0][r];
+#pragma unroll
+                for (int w = 1; w < WARPS; ++w) top = fmaxf(top, tl.m[w][r]);
+                const float f = ex2(m[t][e] - top);
+                float* dst = join + (warp * RT + r) * DP;
+#pragma unroll
+                for (int q = 0; q < CB; ++q) {
+                    constexpr int SB = KS / CB;
+                    // elements q * 128 + g * EPT + 2 s + {0, 1}; rows of 16-byte pieces rotated by the row
+                    // pair so that the four tig of a quarter warp meet different banks
+#pragma unroll
+                    for (int s = 0; s < SB; s += 2) {
+                        const int d = q * 128 + g * (2 * SB) + 2 * s;
+                        float4 v = make_float4(o[q * SB + s][t][e] * f, o[q * SB + s][t][2 + e] * f,
+                                               o[q * SB + s + 1][t][e] * f, o[q * SB + s + 1][t][2 + e] * f);
+                        *reinterpret_cast<float4*>(dst + (d ^ (tig << 2))) = v;
+                    }
+                }
+            }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == n.units;
+        const int first = whole ? cta : cta_of(item_at), lastc = whole ? cta : cta_of(item_at + n.units - 1);
+        float* slot = partial + (size_t)(2 * cta + (u0 == 0 ? 1 : 0)) * Sh::SLOT;
+        for (int i = tid; i < RT * DP / 4; i += THREADS) {
+            const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+            float top = tl.m[0][r], sum = 0.f;
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) top = fmaxf(top, tl.m[w][r]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float4 y = *reinterpret_cast<const float4*>(join + (w * RT + r) * DP + (d ^ ((r >> 1 & 3) << 2)));
+                v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                sum += tl.l[w][r] * ex2(tl.m[w][r] - top);
+            }
+            if (whole) {
+                if (r < rows && d < D) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    E* out = (E*)a.o.ptr + (int64_t)(n.s.row0 + (r0 + r) / G) * a.o.row +
+                             (int64_t)(h * G + (r0 + r) % G) * a.o.head + d;
+                    store4<E>(out, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                }
+            } else {
+                *reinterpret_cast<float4*>(slot + r * DP + d) = v;
+                if (d == 0) {
+                    slot[RT * DP + r] = top;
+                    slot[RT * DP + RT + r] = sum;
+                }
+            }
+        }
+        if (!whole) {
+            // the item's CTAs first .. lastc: the last to arrive joins their slots in order
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int seen = atomicAdd(counters + first, 1);
+                tl.last_of = seen == lastc - first;
+                if (tl.last_of) counters[first] = 0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (tl.last_of) {
+                auto slot_of = [&](int i) { return partial + (size_t)(2 * i + (i == first ? 1 : 0)) * Sh::SLOT; };
+                for (int i = tid; i < RT * DP / 4; i += THREADS) {
+                    const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+                    if (r >= rows || d >= D) continue;
+                    float top = NO_MAX;
+                    for (int k = first; k <= lastc; ++k) top = fmaxf(top, __ldcg(slot_of(k) + RT * DP + r));
+                    float sum = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int k = first; k <= lastc; ++k) {
+                        const float* p = slot_of(k);
+                        const float f = ex2(__ldcg(p + RT * DP + r) - top);
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * DP + d));
+                        sum = fmaf(__ldcg(p + RT * DP + RT + r), f, sum);
+                        v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+                    }
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    E* out = (E*)a.o.ptr + (int64_t)(n.s.row0 + (r0 + r) / G) * a.o.row +
+                             (int64_t)(h * G + (r0 + r) % G) * a.o.head + d;
+                    store4<E>(out, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                }
+            }
+        }
+        at = item_at + u1;
+        if (at < end) {
+            fence_proxy_async_smem();   // the join buffer's generic accesses before the next item's copies
+            __syncthreads();
+        }
+    }
+}
+
+template <bool F32, int DP, int NT>
+cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    using Sh = Shape<F32, DP, NT>;
+    static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
+    attend_split_kernel<F32, DP, NT><<<ws.sms * ATTEND_OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters);
+    return cudaGetLastError();
+}
+
+template <bool F32, int DP, int NT>
+cudaError_t init() {
+    return cudaFuncSetAttribute(attend_split_kernel<F32, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Shape<F32, DP, NT>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t attend_split_init() {
+    cudaError_t e = cudaSuccess;
+    auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
+    one(init<false, 64, 1>()), one(init<false, 64, 2>()), one(init<false, 64, 4>());
+    one(init<false, 128, 1>()), one(init<false, 128, 2>()), one(init<false, 128, 4>());
+    one(init<false, 256, 1>()), one(init<false, 256, 2>());
+    one(init<true, 64, 1>()), one(init<true, 64, 2>()), one(init<true, 64, 4>());
+    one(init<true, 128, 1>()), one(init<true, 128, 2>()), one(init<true, 128, 4>());
+    one(init<true, 256, 1>()), one(init<true, 256, 2>());
+    return e;
+}
+
+// Rows per tile: the fewest 8-row columns that hold a sequence's rows, up to the most
+// that the accumulators leave registers for.
+template <bool F32>
+static cudaError_t by_shape(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
+    const int D = a.pages.dim;
+    if (D <= 64)
+        return rows <= 8 ? launch<F32, 64, 1>(a, ws, st)
+                         : rows <= 16 ? launch<F32, 64, 2>(a, ws, st) : launch<F32, 64, 4>(a, ws, st);
+    if (D <= 128)
+        return rows <= 8 ? launch<F32, 128, 1>(a, ws, st)
+                         : rows <= 16 ? launch<F32, 128, 2>(a, ws, st) : launch<F32, 128, 4>(a, ws, st);
+    return rows <= 8 ? launch<F32, 256, 1>(a, ws, st) : launch<F32, 256, 2>(a, ws, st);
+}
+
+cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    return bf16 ? by_shape<false>(a, ws, st) : by_shape<true>(a, ws, st);
+}
+
+}  // namespace mlora

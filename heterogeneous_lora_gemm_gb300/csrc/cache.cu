@@ -7,7 +7,8 @@
 #include <new>
 
 #include "../../include/mlora.h"
-#include "cache.h"
+#include "attend.h"
+#include "tc.h"
 
 using namespace mlora;
 
@@ -15,7 +16,8 @@ struct mlora_cache {
     int device = 0;
     CachePages pages{};
     int q_heads = 0;
-    char* ws = nullptr;   // the status word
+    char* ws = nullptr;       // the status word, the join counters, the partial results
+    AttendWs attend{};
 };
 
 namespace {
@@ -89,6 +91,17 @@ mlora_status check_rows(const char* name, const void* p, int64_t row, int64_t he
     return MLORA_OK;
 }
 
+// The codes as [n_pages x heads x page] rows of `dim` bytes, in boxes of 16 tokens; a box
+// is 64 or 128 columns wide, its columns past `dim` and rows past the end read as zero.
+bool encode_codes(CUtensorMap* map, const void* codes, const CachePages& c) {
+    const bool narrow = c.dim <= 64;
+    cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)c.n_pages * c.heads * c.page};
+    cuuint64_t strides[1] = {(cuuint64_t)c.dim};
+    cuuint32_t box[2] = {narrow ? 64u : 128u, 16};
+    return tc_encode_typed(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, 2, dims, strides, box,
+                           narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace
 
 extern "C" {
@@ -113,8 +126,17 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     c->pages = CachePages{(int8_t*)k_codes, (int8_t*)v_codes, k_scale, v_scale, n_pages, page_size, kv_heads, head_dim};
     c->q_heads = q_heads;
     cudaError_t e = cudaGetDevice(&c->device);
-    if (e == cudaSuccess) e = cudaMalloc((void**)&c->ws, 256);
-    if (e == cudaSuccess) e = cudaMemset(c->ws, 0, 256);
+    int sms = 0;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
+    const size_t ctas = (size_t)sms * ATTEND_OCC, head = 256 + (ctas * sizeof(int) + 255) / 256 * 256;
+    if (e == cudaSuccess) e = cudaMalloc((void**)&c->ws, head + 2 * ctas * ATTEND_SLOT * sizeof(float));
+    if (e == cudaSuccess) e = cudaMemset(c->ws, 0, head);
+    if (e == cudaSuccess) e = attend_split_init();
+    if (e == cudaSuccess && !(encode_codes(&c->attend.k16, k_codes, c->pages) && encode_codes(&c->attend.v16, v_codes, c->pages)))
+        e = cudaErrorInvalidValue;
+    c->attend.counters = (int*)(c->ws + 256);
+    c->attend.partial = (float*)(c->ws + head);
+    c->attend.sms = sms;
     if (e != cudaSuccess) {
         if (c->ws) cudaFree(c->ws);
         delete c;
@@ -185,7 +207,7 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     if (g.err != cudaSuccess) return cuda_fail(g.err, "cudaSetDevice");
     AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, scale, window,
                  (uint32_t*)c->ws};
-    CU_TRY(launch_attend(dtype == MLORA_BF16, a, (cudaStream_t)stream));
+    CU_TRY(launch_attend_split(dtype == MLORA_BF16, a, c->attend, (cudaStream_t)stream));
     return MLORA_OK;
 }
 

@@ -93,6 +93,5 @@ cudaError_t launch_append(bool bf16, const CachePages& c, const CacheStep& s, co
                           uint32_t* status, cudaStream_t st);
 cudaError_t launch_read(bool bf16, const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v,
                         uint32_t* status, cudaStream_t st);
-cudaError_t launch_attend(bool bf16, const AttendArgs& a, cudaStream_t st);
 
 }  // namespace mlora
