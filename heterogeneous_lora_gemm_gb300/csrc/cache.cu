@@ -132,6 +132,7 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     if (e == cudaSuccess) e = cudaMalloc((void**)&c->ws, head + 2 * ctas * ATTEND_SLOT * sizeof(float));
     if (e == cudaSuccess) e = cudaMemset(c->ws, 0, head);
     if (e == cudaSuccess) e = attend_split_init();
+    if (e == cudaSuccess) e = attend_prompt_init();
     if (e == cudaSuccess && !(encode_codes(&c->attend.k16, k_codes, c->pages) && encode_codes(&c->attend.v16, v_codes, c->pages)))
         e = cudaErrorInvalidValue;
     c->attend.counters = (int*)(c->ws + 256);
@@ -201,13 +202,17 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     if (!(scale > 0.f && scale < 3.0e38f)) return fail(MLORA_ERR_INVALID_ARG, "scale %g", scale);
     if (window < 0) return fail(MLORA_ERR_INVALID_ARG, "window %d is negative", window);
     if (!run) return MLORA_OK;
+    if ((long long)s.max_new * (c->q_heads / c->pages.heads) > 1 << 30)
+        return fail(MLORA_ERR_UNSUPPORTED, "%d rows of %d heads per key head", s.max_new, c->q_heads / c->pages.heads);
     if ((st = check_rows("Q", Q, q_row, q_head, dtype)) != MLORA_OK) return st;
     if ((st = check_rows("O", O, o_row, o_head, dtype)) != MLORA_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, "cudaSetDevice");
     AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, scale, window,
                  (uint32_t*)c->ws};
-    CU_TRY(launch_attend_split(dtype == MLORA_BF16, a, c->attend, (cudaStream_t)stream));
+    const bool bf16 = dtype == MLORA_BF16;
+    CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(a, c->attend, (cudaStream_t)stream)
+                                        : launch_attend_split(bf16, a, c->attend, (cudaStream_t)stream));
     return MLORA_OK;
 }
 
