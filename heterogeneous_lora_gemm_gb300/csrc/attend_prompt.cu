@@ -176,6 +176,79 @@ __device__ __forceinline__ void convert_tile(const uint8_t* codes, uint8_t* dst,
     }
 }
 
+// Bits e of [lo, hi) of 32 columns.
+__device__ __forceinline__ uint32_t column_mask(int lo, int hi) {
+    const uint32_t below = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+    return lo <= 0 ? below : lo >= 32 ? 0u : below & ~((1u << lo) - 1u);
+}
+
+// The row's largest x over a tile (columns [lo, hi) of it if EDGE): the maximum of the raw
+// scores of each 16-token piece, times its factor.
+template <bool EDGE>
+__device__ __forceinline__ float row_max(uint32_t sbase, const float* sc, float qf, int lo, int hi) {
+    float mx = -INFINITY;
+    uint32_t x[2][32];   // quarters of the row's 128 scores, the next one on its way
+    tmem_ld32(sbase, x[0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t* y = x[q & 1];
+        tmem_wait_ld(y);
+        if (q < 3) tmem_ld32(sbase + (q + 1) * 32, x[(q + 1) & 1]);
+        const uint32_t seen = EDGE ? column_mask(lo - q * 32, hi - q * 32) : ~0u;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const int i = g * 16 + e;
+                a = fmaxf(a, !EDGE || (seen >> i & 1) ? __uint_as_float(y[i]) : -INFINITY);
+                b = fmaxf(b, !EDGE || (seen >> (i + 1) & 1) ? __uint_as_float(y[i + 1]) : -INFINITY);
+            }
+            a = fmaxf(a, b);
+            const float v = a * (qf * sc[q * 2 + g]);
+            mx = fmaxf(mx, EDGE && a == -INFINITY ? -INFINITY : v);
+        }
+    }
+    return mx;
+}
+
+// Weights of a row over a tile: their sum into l2, times the value scales in bf16 over the
+// scores that are read (32 columns of scores are 16 of weights).
+template <bool EDGE>
+__device__ __forceinline__ void weigh(uint32_t sbase, const float* sc, float qf, float m, int lo, int hi, uint64_t& l2) {
+    const uint64_t nm = pair(-m, -m);
+    uint32_t x[2][32];
+    tmem_ld32(sbase, x[0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t* y = x[q & 1];
+        uint32_t p[16];
+        tmem_wait_ld(y);
+        if (q < 3) tmem_ld32(sbase + (q + 1) * 32, x[(q + 1) & 1]);
+        const uint32_t seen = EDGE ? column_mask(lo - q * 32, hi - q * 32) : ~0u;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const float f = qf * sc[q * 2 + g], v = sc[8 + q * 2 + g];
+            const uint64_t f2 = pair(f, f), v2 = pair(v, v);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const int i = g * 16 + e;
+                const float2 z = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, nm));
+                float p0 = ex2(z.x), p1 = ex2(z.y);
+                if (EDGE) {
+                    p0 = seen >> i & 1 ? p0 : 0.f;
+                    p1 = seen >> (i + 1) & 1 ? p1 : 0.f;
+                }
+                const uint64_t pp = pair(p0, p1);
+                l2 = add2(l2, pp);
+                const float2 w = unpair(mul2(pp, v2));
+                p[i / 2] = bf2_of(w.x, w.y);
+            }
+        }
+        tmem_st16(sbase + q * 16, p);
+    }
+}
+
 template <int DP>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
@@ -299,30 +372,7 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                 const float* sc = tl.scales[j & 3];
                 const int t0 = ta + j * TILE;
                 const bool edge = t0 + TILE > hi_min || t0 < lo_max;
-                float mx = -INFINITY;
-                uint32_t x[2][32];   // quarters of the row's 128 scores, the next one on its way
-                tmem_ld32(sbase, x[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t* y = x[q & 1];
-                    tmem_wait_ld(y);
-                    if (q < 3) tmem_ld32(sbase + (q + 1) * 32, x[(q + 1) & 1]);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float gm = -INFINITY;
-                        if (!edge) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(y[g * 16 + e]));
-                        } else {
-                            const int tg = t0 + q * 32 + g * 16;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                gm = fmaxf(gm, tg + e < hi && tg + e >= lo ? __uint_as_float(y[g * 16 + e]) : -INFINITY);
-                        }
-                        const float f = qf * sc[q * 2 + g];
-                        mx = fmaxf(mx, gm == -INFINITY ? -INFINITY : gm * f);
-                    }
-                }
+                const float mx = edge ? row_max<true>(sbase, sc, qf, lo - t0, hi - t0) : row_max<false>(sbase, sc, qf, 0, 0);
                 const bool above = mx > m + SLACK;
                 if (__any_sync(~0u, above)) {   // the products so far are complete: S came after them
                     const float now = above ? mx : m, f = ex2(m - now);
@@ -339,36 +389,8 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                             tmem_st32(obase + q * 32, y);
                         }
                 }
-                const uint64_t nm = pair(-m, -m);
-                tmem_ld32(sbase, x[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t* y = x[q & 1];
-                    uint32_t p[16];
-                    tmem_wait_ld(y);
-                    if (q < 3) tmem_ld32(sbase + (q + 1) * 32, x[(q + 1) & 1]);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float f = qf * sc[q * 2 + g], v = sc[8 + q * 2 + g];
-                        const uint64_t f2 = pair(f, f), v2 = pair(v, v);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const int i = g * 16 + e;
-                            const float2 z = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, nm));
-                            float p0 = ex2(z.x), p1 = ex2(z.y);
-                            if (edge) {
-                                const int tg = t0 + q * 32 + i;
-                                p0 = tg < hi && tg >= lo ? p0 : 0.f;
-                                p1 = tg + 1 < hi && tg + 1 >= lo ? p1 : 0.f;
-                            }
-                            const uint64_t pp = pair(p0, p1);
-                            l2 = add2(l2, pp);
-                            const float2 w = unpair(mul2(pp, v2));
-                            p[i / 2] = bf2_of(w.x, w.y);
-                        }
-                    }
-                    tmem_st16(sbase + q * 16, p);   // over scores that every quarter so far has read
-                }
+                if (edge) weigh<true>(sbase, sc, qf, m, lo - t0, hi - t0, l2);
+                else weigh<false>(sbase, sc, qf, m, 0, 0, l2);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&tl.pfull[t]);
