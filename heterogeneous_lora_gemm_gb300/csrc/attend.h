@@ -20,6 +20,6 @@ cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& 
 // Sequences with many rows (attend_prompt.cu): bf16 and head_dim <= 128 only.
 cudaError_t attend_prompt_init();
 bool attend_prompt_takes(bool bf16, const AttendArgs& a);
-cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
+cudaError_t launch_attend_prompt(const AttendArgs& a, cudaStream_t st);
 
 }  // namespace mlora

@@ -2,22 +2,24 @@
 // (prompts), bf16, head_dim <= 128 (include/mlora.h).
 //
 // Mathematics as in attend_split.cu: x = scale ks (q . kc) log2 e, o = sum 2^(x - m) vs vc /
-// sum 2^(x - m), m a running bound that moves when some x exceeds m + 8.  Rows are (query
-// token, query head of the group) pairs of one key/value head, 256 per CTA as two tiles of
-// 128: a converted key/value tile serves both, and one tile's softmax runs under the other
-// tile's products.
+// sum 2^(x - m).  The value scale goes into the exponent, 2^(x - m + log2 vs), and out of the
+// sum again per 16 tokens (a block of vs = 0 is converted to zeros under a scale of 1).  m is a
+// row's largest x when it was last set; a step whose weights sum to more than 2^14 sets it
+// again (no maximum is taken otherwise; bf16 and fp32 hold weights above 1 as well as below).
+// Rows are (query token, query head of the group) pairs of one key/value head, 256 per CTA as
+// two tiles of 128: a converted key/value tile serves both.
 //
-// Products run on tcgen05.mma, 128 rows x 128 tokens: S = Q K^T in fp16 (codes exact,
+// Products run on tcgen05.mma, 128 rows x 64 tokens a step: S = Q K^T in fp16 (codes exact,
 // queries below 1 after a power of two per row), O += P V in bf16 with P = 2^(x - m) vs
-// (one rounding) from tensor memory.  Tensor memory: S of the two tiles (P lies over S)
-// and O of the two tiles, all 512 columns.
+// (one rounding) from tensor memory.  Tensor memory, all 512 columns: two S of 64 columns
+// per tile, so that a step's scores are ready before the last step's weights are done (P
+// lies over its S), and O of the two tiles.
 //
-// Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8-11
-// convert code tiles into fp16 keys (row-major rows of head elements) and bf16 values
-// (tokens as rows: the product reads them column-major), 12 issues products, 13 copies
-// code tiles (16-token boxes, so that pages of any multiple of 16 tokens do).
-// Bound: the tensor pipe's 2 x 4 x 128^3 operations per token tile, closely followed by
-// the softmax and the conversion (about 3.5 and 2 instructions per element).
+// Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8-15 read
+// codes and convert them into fp16 keys (rows of head elements) and bf16 values (tokens as
+// rows: the product reads them column-major), a warp per 16 tokens of 128 with the next 128
+// tokens' codes on their way in registers, 16 and 17 issue the products of tile 0 and 1 (one
+// warp's waits would outlast both tiles' products).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,29 +32,58 @@ using namespace ptx;
 
 namespace {
 
-constexpr int TILE = 128;                  // rows per tile and tokens per tile
+constexpr int TILE = 128;                  // rows per tile, and tokens converted at a time
+constexpr int STEP = 64;                   // tokens per product
 constexpr int PROMPT_ROWS = 2 * TILE;      // rows per CTA
-constexpr int PROMPT_THREADS = 14 * 32;
-constexpr float SLACK = 8.f, NO_MAX = -1e38f;
+constexpr int SOFT = 8, CONV = 8;          // softmax and conversion warps
+constexpr int PROMPT_THREADS = 32 * (SOFT + CONV + 2);
+constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
+constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
 
 template <int DP>
 struct PShape {
     static constexpr int BLK = DP / 64;                 // 64-element column blocks (128-byte rows)
     static constexpr int OPER = BLK * TILE * 128;       // bytes of a Q, K or V operand tile
-    static constexpr int CODES = TILE * DP;             // bytes of a code tile
-    static constexpr int SMEM = 1024 + 6 * OPER + 2 * CODES + 512;
+    static constexpr int SMEM = 1024 + 6 * OPER + 768;
 };
 
 struct PTail {
-    uint64_t cfull[2], cempty[2];     // code tiles (keys, values)
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-    uint64_t scfull[4], sfull[2], pfull[2], qfull, ofull;
-    float scales[4][16];              // of a tile's 16-token pieces: 8 of keys, 8 of values
+    uint64_t scfull[4], sfull[2][2], pfull[2][2], odone[2][2], qfull[2], alldone[2];   // [tile][S buffer]
+    float scales[4][24];              // of 128 tokens' 16-token pieces: ks, log2 vs, 1 / vs (8 each)
     uint32_t tmem;
     int abort_flag;
 };
-static_assert(sizeof(PTail) <= 512, "barriers and scales");
+static_assert(sizeof(PTail) <= 768 && 16 * CONV == TILE, "barriers and scales; a warp per piece");
 
+// mbar_wait (tc_ptx.cuh) that sleeps: the waiting warps share issue slots with the busy ones.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    auto sleep_wait = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)   // ns
+            : "memory");
+        return ok != 0;
+    };
+    if (sleep_wait()) return true;
+    const long long t0 = clock64();
+    while (!sleep_wait()) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > WAIT_LIMIT) {
+            *abort_flag = 1;
+            atomicOr(status, STATUS_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -66,10 +97,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-// Waits for the thread's loads; the loaded registers are operands, so that no use of them
-// moves above the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_loaded16(uint32_t* r) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Names loaded registers as operands after the wait, so that no use of them moves above it.
+__device__ __forceinline__ void tmem_loaded(uint32_t* r) {
+    asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
                    "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
@@ -87,22 +141,37 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// One product of 16 elements of K: D += A B, A in shared (SS) or tensor memory (TS).  The
+// descriptors' low words are made in place from the loop's base and a constant: hoisted out of
+// the loop they would spill, and the reloads would outlast the products.
+template <int A_OFF, int B_OFF>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n add.s64 a, %1, %5;\n add.s64 b, %2, %6;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_OFF >> 4), "n"(B_OFF >> 4)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// D += A B with A in tensor memory
+template <int A_COL, int B_OFF>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-            d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 b;\n .reg .b32 a;\n setp.ne.b32 p, %4, 0;\n add.s32 a, %1, %5;\n add.s64 b, %2, "
+        "%6;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_COL), "n"(B_OFF >> 4)
         : "memory");
+}
+// K steps [0, N): SS in 64-element blocks of 128 rows of 128 bytes, TS over rows of tokens.
+template <int N, int K = 0>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    constexpr int OFF = K / 4 * (128 * 128) + K % 4 * 32;
+    mma_ss<OFF, OFF>(d, a, b, idesc, K > 0);
+    if constexpr (K + 1 < N) product_ss<N, K + 1>(d, a, b, idesc);
+}
+template <int N, int K = 0>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    mma_ts<K * 8, K * 2048>(d, a, b, idesc, K > 0 ? 1u : acc);
+    if constexpr (K + 1 < N) product_ts<N, K + 1>(d, a, b, idesc, acc);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -156,24 +225,15 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
     return make_uint2(minus1152(__byte_perm(w, 0x64646464u, 0x4140)), minus1152(__byte_perm(w, 0x64646464u, 0x4342)));
 }
 
-// One code tile (128 tokens x DP, as 16-token boxes) into an operand tile: DP / 64 blocks of
-// 128 rows of 128 bytes under the 128-byte swizzle.  A warp takes 8 tokens x 64 elements at a
-// time; lanes pair token t with t ^ 5, so that neither the reads (16-byte chunks at c ^ t)
-// nor the writes (at (2 c + z) ^ t) of a quarter warp meet in a bank.
-template <int DP, bool BF>
-__device__ __forceinline__ void convert_tile(const uint8_t* codes, uint8_t* dst, int warp, int lane) {
-    constexpr int N = 16 * (DP / 64) / 4;   // (8-token group, block) pairs per warp
-    const int c = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-        const int combo = warp * N + u, blk = combo % (DP / 64), t = combo / (DP / 64) * 8 + t8;
-        const int from = DP == 64 ? t * 64 + ((c ^ ((t >> 1) & 3)) << 4) : t * 128 + (((blk * 4 + c) ^ (t & 7)) << 4);
-        const uint4 x = *reinterpret_cast<const uint4*>(codes + from);
-        const uint2 a = widen<BF>(x.x), b = widen<BF>(x.y), d = widen<BF>(x.z), e = widen<BF>(x.w);
-        uint8_t* row = dst + blk * (TILE * 128) + t * 128;
-        *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
-    }
+// 16 codes of token t, elements 16 c .. of 64-element block blk, into an operand tile: DP / 64
+// blocks of 128 rows of 128 bytes under the 128-byte swizzle.  (Lanes pair token t with t ^ 5,
+// so that the writes of a quarter warp, at (2 c + z) ^ t, do not meet in a bank.)
+template <bool BF>
+__device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk, int c) {
+    const uint2 a = widen<BF>(x.x), b = widen<BF>(x.y), d = widen<BF>(x.z), e = widen<BF>(x.w);
+    uint8_t* row = dst + blk * (TILE * 128) + t * 128;
+    *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
 }
 
 // Bits e of [lo, hi) of 32 columns.
@@ -182,85 +242,68 @@ __device__ __forceinline__ uint32_t column_mask(int lo, int hi) {
     return lo <= 0 ? below : lo >= 32 ? 0u : below & ~((1u << lo) - 1u);
 }
 
-// The row's largest x over a tile (columns [lo, hi) of it if EDGE): the maximum of the raw
+// The largest x of a row's 64 scores, of columns [lo, hi) of them: the maximum of the raw
 // scores of each 16-token piece, times its factor.
-template <bool EDGE>
-__device__ __forceinline__ float row_max(uint32_t sbase, const float* sc, float qf, int lo, int hi) {
+__device__ __forceinline__ float row_max(uint32_t sat, const float* sc, float qf, int lo, int hi) {
     float mx = -INFINITY;
-    uint32_t x[2][32];   // quarters of the row's 128 scores, the next one on its way
-    tmem_ld32(sbase, x[0]);
+#pragma unroll 1
+    for (int g = 0; g < STEP / 16; ++g) {
+        uint32_t y[16];
+        tmem_ld16(sat + g * 16, y);
+        tmem_wait_ld();
+        tmem_loaded16(y);
+        const uint32_t seen = column_mask(lo - g * 16, hi - g * 16);
+        float a = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint32_t* y = x[q & 1];
-        tmem_wait_ld(y);
-        if (q < 3) tmem_ld32(sbase + (q + 1) * 32, x[(q + 1) & 1]);
-        const uint32_t seen = EDGE ? column_mask(lo - q * 32, hi - q * 32) : ~0u;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const int i = g * 16 + e;
-                a = fmaxf(a, !EDGE || (seen >> i & 1) ? __uint_as_float(y[i]) : -INFINITY);
-                b = fmaxf(b, !EDGE || (seen >> (i + 1) & 1) ? __uint_as_float(y[i + 1]) : -INFINITY);
-            }
-            a = fmaxf(a, b);
-            const float v = a * (qf * sc[q * 2 + g]);
-            mx = fmaxf(mx, EDGE && a == -INFINITY ? -INFINITY : v);
-        }
+        for (int e = 0; e < 16; ++e) a = fmaxf(a, seen >> e & 1 ? __uint_as_float(y[e]) : -INFINITY);
+        mx = fmaxf(mx, a == -INFINITY ? -INFINITY : a * (qf * sc[g]));
     }
     return mx;
 }
 
-// Weights of a row over a tile: their sum into l2, times the value scales in bf16 over the
-// scores that are read (32 columns of scores are 16 of weights).
+// Weights of a row's 64 scores: times the value scales into y[0, 32) (bf16 pairs); returns
+// their sum (without the value scales).
 template <bool EDGE>
-__device__ __forceinline__ void weigh(uint32_t sbase, const float* sc, float qf, float m, int lo, int hi, uint64_t& l2) {
-    const uint64_t nm = pair(-m, -m);
-    uint32_t x[2][32];
-    tmem_ld32(sbase, x[0]);
+__device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float qf, float m, int lo, int hi,
+                                          uint32_t (&y)[STEP]) {
+    tmem_ld32(sat, y);
+    tmem_ld32(sat + 32, y + 32);
+    tmem_wait_ld();
+    tmem_loaded(y);
+    tmem_loaded(y + 32);
+    uint64_t sum = pair(0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint32_t* y = x[q & 1];
-        uint32_t p[16];
-        tmem_wait_ld(y);
-        if (q < 3) tmem_ld32(sbase + (q + 1) * 32, x[(q + 1) & 1]);
-        const uint32_t seen = EDGE ? column_mask(lo - q * 32, hi - q * 32) : ~0u;
+    for (int g = 0; g < STEP / 16; ++g) {
+        const uint32_t seen = EDGE ? column_mask(lo - g * 16, hi - g * 16) : 0u;
+        const float f = qf * sc[g], c = sc[8 + g] - m, v = sc[16 + g];
+        const uint64_t f2 = pair(f, f), c2 = pair(c, c);
+        uint64_t l = pair(0.f, 0.f);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const float f = qf * sc[q * 2 + g], v = sc[8 + q * 2 + g];
-            const uint64_t f2 = pair(f, f), v2 = pair(v, v);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const int i = g * 16 + e;
-                const float2 z = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, nm));
-                float p0 = ex2(z.x), p1 = ex2(z.y);
-                if (EDGE) {
-                    p0 = seen >> i & 1 ? p0 : 0.f;
-                    p1 = seen >> (i + 1) & 1 ? p1 : 0.f;
-                }
-                const uint64_t pp = pair(p0, p1);
-                l2 = add2(l2, pp);
-                const float2 w = unpair(mul2(pp, v2));
-                p[i / 2] = bf2_of(w.x, w.y);
+        for (int e = 0; e < 16; e += 2) {
+            const int i = g * 16 + e;
+            const float2 z = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, c2));
+            float p0 = ex2(z.x), p1 = ex2(z.y);
+            if (EDGE) {
+                p0 = seen >> e & 1 ? p0 : 0.f;
+                p1 = seen >> (e + 1) & 1 ? p1 : 0.f;
             }
+            l = add2(l, pair(p0, p1));
+            y[i / 2] = bf2_of(p0, p1);
         }
-        tmem_st16(sbase + q * 16, p);
+        sum = fma2(l, pair(v, v), sum);
     }
+    return sum;
 }
 
 template <int DP>
-__global__ void __launch_bounds__(PROMPT_THREADS, 1)
-attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
-                     int tiles) {
+__global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const AttendArgs a, int tiles) {
     using Sh = PShape<DP>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* qs = smem;                              // [2 tiles]
     uint8_t* kb = smem + 2 * Sh::OPER;               // [2]
     uint8_t* vb = smem + 4 * Sh::OPER;               // [2]
-    uint8_t* codes = smem + 6 * Sh::OPER;            // keys, values
-    PTail& tl = *reinterpret_cast<PTail*>(codes + 2 * Sh::CODES);
+    PTail& tl = *reinterpret_cast<PTail*>(smem + 6 * Sh::OPER);
     volatile int* abort_flag = &tl.abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const CachePages& c = a.pages;
@@ -275,26 +318,28 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     const int pos_lo = s.start + r0 / G, pos_hi = s.start + (r0 + rows - 1) / G;
     const int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / 16 * 16 : 0;
     const int tb = pos_hi + 1;
-    const int nt = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;
+    const int nt = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;      // conversions
+    const int steps = tb > ta ? (tb - ta + STEP - 1) / STEP : 0;   // products
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&tl.cfull[i], 1);
-            mbar_init(&tl.cempty[i], 128);
-            mbar_init(&tl.kfull[i], 128);
-            mbar_init(&tl.kempty[i], 1);
-            mbar_init(&tl.vfull[i], 128);
-            mbar_init(&tl.vempty[i], 1);
-            mbar_init(&tl.sfull[i], 1);
-            mbar_init(&tl.pfull[i], 128);
+            mbar_init(&tl.kfull[i], 32 * CONV);
+            mbar_init(&tl.kempty[i], two ? 2 : 1);
+            mbar_init(&tl.vfull[i], 32 * CONV);
+            mbar_init(&tl.vempty[i], two ? 2 : 1);
+            mbar_init(&tl.qfull[i], TILE);
+            mbar_init(&tl.alldone[i], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&tl.sfull[i][u], 1);
+                mbar_init(&tl.pfull[i][u], TILE);
+                mbar_init(&tl.odone[i][u], 1);
+            }
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&tl.scfull[i], 1);
-        mbar_init(&tl.qfull, 256);
-        mbar_init(&tl.ofull, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&tl.scfull[i], CONV);
         tl.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == SOFT + CONV) {
         __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tl.tmem)), "r"(512)
                      : "memory");
@@ -306,10 +351,10 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     tc_fence_after();
     const uint32_t tmem = tl.tmem;
 
-    if (warp < 8) {
+    if (warp < SOFT) {
         // ---- softmax and output: a thread per row
         const int t = warp >> 2, q4 = warp & 3;
-        const int r = r0 + t * TILE + q4 * 32 + lane, rl = q4 * 32 + lane;
+        const int rl = q4 * 32 + lane, r = r0 + t * TILE + rl;
         const bool live = r < R;
         const int64_t row = s.row0 + (live ? r : r0) / G, head = h * G + (live ? r : r0) % G;
         // the query: fp16 scaled by a power of two, NaN statistics for a row that is not finite
@@ -350,72 +395,90 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                     make_uint4(v[0], v[1], v[2], v[3]);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&tl.qfull);
+            mbar_arrive(&tl.qfull[t]);
         }
         const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t sbase = lane_base + t * TILE, obase = lane_base + 256 + t * TILE;
         const int hi = s.start + r / G + 1, lo = a.window > 0 ? hi - a.window : 0;   // tokens [lo, hi) are seen
-        // limits of the tile's rows, for the tiles that no limit cuts
+        // limits of the tile's rows, for the token tiles that no limit cuts
         const int rt = r0 + t * TILE;
         const int hi_min = s.start + rt / G + 1, hi_max = s.start + min(R - 1, rt + TILE - 1) / G + 1;
         const int lo_max = a.window > 0 ? hi_max - a.window : 0;
         float m = NO_MAX;
         uint64_t l2 = pair(0.f, 0.f);
         bool ok = true;
-        if (t == 0 || two)
-            for (int j = 0; j < nt; ++j) {
-                ok = mbar_wait(&tl.scfull[j & 3], (j >> 2) & 1, abort_flag, a.status) &&
-                     mbar_wait(&tl.sfull[t], j & 1, abort_flag, a.status);
+        if (t == 0 || two) {
+            for (int i = 0; i < steps; ++i) {
+                ok = wait_for(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
+                if (!(i & 1)) ok = ok && wait_for(&tl.scfull[(i >> 1) & 3], (i >> 3) & 1, abort_flag, a.status);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float* sc = tl.scales[j & 3];
-                const int t0 = ta + j * TILE;
-                const bool edge = t0 + TILE > hi_min || t0 < lo_max;
-                const float mx = edge ? row_max<true>(sbase, sc, qf, lo - t0, hi - t0) : row_max<false>(sbase, sc, qf, 0, 0);
-                const bool above = mx > m + SLACK;
-                if (__any_sync(~0u, above)) {   // the products so far are complete: S came after them
-                    const float now = above ? mx : m, f = ex2(m - now);
-                    m = now;
-                    l2 = mul2(l2, pair(f, f));
-                    if (j > 0)
+                const float* sc = tl.scales[(i >> 1) & 3] + (i & 1) * 4;
+                const int t0 = ta + i * STEP;
+                const bool edge = t0 + STEP > hi_min || t0 < lo_max;
+                const uint32_t sat = sbase + (i & 1) * STEP;
+                uint32_t y[STEP];
+                float2 sum;
+                // first with the bound so far, which usually holds; else the bound moves
+                bool above = true;
+                for (bool move = i == 0;; move = true) {
+                    if (move) {
+                        const float mx = row_max(sat, sc, qf, lo - t0, hi - t0);
+                        const float now = above ? fmaxf(mx, m) : m, f = ex2(m - now);
+                        m = now;
+                        l2 = mul2(l2, pair(f, f));
+                        if (i > 0) {
+                            // O, once the last step's product is complete (the one before it is: these
+                            // scores came after it, so the barrier is at this phase or past it)
+                            ok = __all_sync(~0u, wait_for(&tl.odone[t][(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, a.status));
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int q = 0; q < DP / 32; ++q) {
-                            uint32_t y[32];
-                            tmem_ld32(obase + q * 32, y);
-                            tmem_wait_ld(y);
+                            for (int q = 0; q < DP / 16; ++q) {
+                                uint32_t x[16];
+                                tmem_ld16(obase + q * 16, x);
+                                tmem_wait_ld();
+                                tmem_loaded16(x);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                            tmem_st32(obase + q * 32, y);
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                                tmem_st16(obase + q * 16, x);
+                            }
                         }
+                    }
+                    sum = unpair(edge ? weigh<true>(sat, sc, qf, m, lo - t0, hi - t0, y)
+                                      : weigh<false>(sat, sc, qf, m, 0, 0, y));
+                    above = sum.x + sum.y > MOST;
+                    if (move || !__any_sync(~0u, above)) break;
                 }
-                if (edge) weigh<true>(sbase, sc, qf, m, lo - t0, hi - t0, l2);
-                else weigh<false>(sbase, sc, qf, m, 0, 0, l2);
+                if (!ok) break;
+                l2 = add2(l2, pair(sum.x, sum.y));
+                tmem_st32(sat, y);   // over the scores
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&tl.pfull[t]);
+                mbar_arrive(&tl.pfull[t][i & 1]);
             }
-        if (t == 0 || two) {
-            if (ok && nt > 0) ok = mbar_wait(&tl.ofull, 0, abort_flag, a.status);
-            ok = __all_sync(~0u, ok);
+            if (ok && steps > 0) ok = wait_for(&tl.odone[t][(steps - 1) & 1], ((steps - 1) >> 1) & 1, abort_flag, a.status);
+            __syncwarp();
             tc_fence_after();
             const float2 ls = unpair(l2);
-            const float l = ls.x + ls.y, inv = l == 0.f ? 0.f : 1.f / l;
+            const float l = ls.x + ls.y;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             __nv_bfloat16* o = (__nv_bfloat16*)a.o.ptr + row * a.o.row + head * a.o.head;
 #pragma unroll
             for (int q = 0; q < DP / 32; ++q) {
                 uint32_t x[32];
                 if (nt > 0) {
                     tmem_ld32(obase + q * 32, x);
-                    tmem_wait_ld(x);
+                    tmem_wait_ld();
+                    tmem_loaded(x);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0u;
                 }
-                if (!live) continue;
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
-                    if (q * 32 + e >= D) break;
+                    if (!live || q * 32 + e >= D) continue;
                     uint32_t y[4];
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
@@ -424,121 +487,119 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                 }
             }
         }
-    } else if (warp < 12) {
-        // ---- conversion
+    } else if (warp < SOFT + CONV) {
+        // ---- conversion: the warp's 16 tokens of each tile
+        constexpr int N = 2 * Sh::BLK;   // 16-byte loads per thread and operand
+        const int w = warp - SOFT, c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+        // the warp's tokens of the tile that is loaded next: block and place in the sequence's table
+        int tk = ta + w * 16, blk = tk / c.page, off = tk % c.page;
+        const int dblk = TILE / c.page, doff = TILE % c.page;
+        auto next_id = [&]() { return tk < tb ? load_page(a.step, c, b, blk, a.status) : -1; };   // -1: nothing to read
+        auto advance = [&]() {
+            tk += TILE;
+            blk += dblk;
+            off += doff;
+            if (off >= c.page) off -= c.page, ++blk;
+        };
+        const int lane_off = t8 * D + c4 * 16;
+        auto load = [&](const int8_t* codes, int id, int place, uint4* x) {
+            const int8_t* from = codes + ((size_t)(id < 0 ? 0 : id * H + h) * c.page + place) * D + lane_off;
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                x[u] = id >= 0 && (u % Sh::BLK * 4 + c4) * 16 < D
+                           ? __ldg(reinterpret_cast<const uint4*>(from + u / Sh::BLK * 8 * D + u % Sh::BLK * 64))
+                           : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto scale = [&](const float* p, int id) { return id >= 0 ? p[(size_t)id * H + h] : 0.f; };
+        uint4 kx[N], vx[N];
+        int id = next_id(), place = off;
+        load(c.k_codes, id, place, kx);
+        load(c.v_codes, id, place, vx);
+        float ks = scale(c.k_scale, id), vs = scale(c.v_scale, id);
+        advance();
+        id = next_id();
+        place = off;
         for (int j = 0; j < nt; ++j) {
-            const uint32_t par = j & 1, use = (j >> 1) & 1;
-            if (!mbar_wait(&tl.cfull[0], par, abort_flag, a.status) ||
-                !mbar_wait(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status))
-                break;
-            convert_tile<DP, false>(codes, kb + (j & 1) * Sh::OPER, warp - 8, lane);
-            mbar_arrive(&tl.cempty[0]);
+            const uint32_t use = (j >> 1) & 1;
+            if (!wait_for(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status)) break;
+            const bool none = vs == 0.f;
+            if (lane == 0) {
+                float* sc = tl.scales[j & 3];
+                sc[w] = ks;
+                sc[8 + w] = none ? 0.f : log2f(vs);
+                sc[16 + w] = none ? 1.f : 1.f / vs;
+                mbar_arrive(&tl.scfull[j & 3]);
+            }
+            uint8_t* kd = kb + (j & 1) * Sh::OPER;
+#pragma unroll
+            for (int u = 0; u < N; ++u) convert16<false>(kx[u], kd, w * 16 + u / Sh::BLK * 8 + t8, u % Sh::BLK, c4);
             fence_proxy_async_smem();
             mbar_arrive(&tl.kfull[j & 1]);
-            if (!mbar_wait(&tl.cfull[1], par, abort_flag, a.status) ||
-                !mbar_wait(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status))
-                break;
-            convert_tile<DP, true>(codes + Sh::CODES, vb + (j & 1) * Sh::OPER, warp - 8, lane);
-            mbar_arrive(&tl.cempty[1]);
+            load(c.k_codes, id, place, kx);
+            if (!wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
+            uint8_t* vd = vb + (j & 1) * Sh::OPER;
+            if (none)
+#pragma unroll
+                for (int u = 0; u < N; ++u) vx[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < N; ++u) convert16<true>(vx[u], vd, w * 16 + u / Sh::BLK * 8 + t8, u % Sh::BLK, c4);
             fence_proxy_async_smem();
             mbar_arrive(&tl.vfull[j & 1]);
+            load(c.v_codes, id, place, vx);
+            ks = scale(c.k_scale, id);
+            vs = scale(c.v_scale, id);
+            advance();
+            id = next_id();
+            place = off;
         }
-    } else if (warp == 12) {
-        if (lane == 0 && nt > 0) {
-            // ---- products
-            const uint32_t idesc_s = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);   // fp16
-            const uint32_t idesc_o = idesc_bf16(TILE, DP) | (1u << 16);                                           // B column-major
-            auto scores = [&](int t, int j) {
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t off = k / 4 * (TILE * 128) + k % 4 * 32;
-                    mma_bf16(tmem + t * TILE, sdesc(smem_u32(qs + t * Sh::OPER) + off, 1024, SW128),
-                             sdesc(smem_u32(kb + (j & 1) * Sh::OPER) + off, 1024, SW128), idesc_s, k > 0);
-                }
-                mma_commit(&tl.sfull[t]);
-            };
-            auto values = [&](int t, int j) {
-#pragma unroll
-                for (int k = 0; k < TILE / 16; ++k)
-                    mma_ts(tmem + 256 + t * TILE, tmem + t * TILE + k * 8,
-                           sdesc_lbo(smem_u32(vb + (j & 1) * Sh::OPER) + k * 2048, TILE * 128, 1024, SW128), idesc_o,
-                           j > 0 || k > 0);
-            };
-            auto wait = [&](uint64_t* bar, int parity) {
-                const bool ok = mbar_wait(bar, parity, abort_flag, a.status);
+    } else if (steps > 0 && (warp == SOFT + CONV || two)) {
+        // ---- products of a tile: a step's scores go ahead of the last step's weights
+        const int t = warp - SOFT - CONV;
+        const uint32_t idesc_s = (1u << 4) | ((uint32_t)(STEP >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);   // fp16
+        const uint32_t idesc_o = idesc_bf16(TILE, DP) | (1u << 16);                                           // B column-major
+        const uint64_t dq = sdesc(smem_u32(qs + t * Sh::OPER), 1024, SW128), dk = sdesc(smem_u32(kb), 1024, SW128),
+                       dv = sdesc_lbo(smem_u32(vb), TILE * 128, 1024, SW128);
+        const uint32_t tm = tmem + t * TILE;
+        // operand tile of step i, and the step's 64 rows (tokens) of it
+        auto half_of = [](int i) { return (uint64_t)(((i >> 1) & 1) * (Sh::OPER >> 4) + (i & 1) * (STEP * 128 >> 4)); };
+        auto wait = [&](uint64_t* bar, int parity) {
+            return __all_sync(~0u, wait_for(bar, parity, abort_flag, a.status));
+        };
+        bool ok = wait(&tl.qfull[t], 0);
+        for (int i = 0; ok && i <= steps; ++i) {
+            const int u = i - 1;
+            if (i < steps) {
+                if (!(i & 1) && !(ok = wait(&tl.kfull[(i >> 1) & 1], (i >> 2) & 1))) break;
                 tc_fence_after();
-                return ok;
-            };
-            bool ok = wait(&tl.qfull, 0);
-            for (int j = 0; ok && j < nt; ++j) {
-                if (!(ok = wait(&tl.kfull[j & 1], (j >> 1) & 1))) break;
-                scores(0, j);
-                if (two) {
-                    if (j > 0) {
-                        if (!(ok = wait(&tl.pfull[1], (j - 1) & 1))) break;
-                        values(1, j - 1);
-                        mma_commit(&tl.vempty[(j - 1) & 1]);
-                    }
-                    scores(1, j);
+                if (elect_one()) {
+                    product_ss<DP / 16>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
+                    mma_commit(&tl.sfull[t][i & 1]);
+                    if (i & 1 || i + 1 == steps) mma_commit(&tl.kempty[(i >> 1) & 1]);
                 }
-                mma_commit(&tl.kempty[j & 1]);
-                if (!(ok = wait(&tl.vfull[j & 1], (j >> 1) & 1) && wait(&tl.pfull[0], j & 1))) break;
-                values(0, j);
-                if (!two) mma_commit(&tl.vempty[j & 1]);
+                __syncwarp();
             }
-            if (ok && two) {
-                ok = wait(&tl.pfull[1], (nt - 1) & 1);
-                if (ok) values(1, nt - 1);
-            }
-            mma_commit(&tl.ofull);
-            const long long t0 = clock64();   // the products are complete before the CTA goes
-            while (!mbar_try_wait(&tl.ofull, 0) && clock64() - t0 < 200000000ll) {
+            if (i > 0) {
+                if (!(u & 1) && !(ok = wait(&tl.vfull[(u >> 1) & 1], (u >> 2) & 1))) break;
+                if (!(ok = wait(&tl.pfull[t][u & 1], (u >> 1) & 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    product_ts<STEP / 16>(tm + 256, tm + (u & 1) * STEP, dv + half_of(u), idesc_o, u > 0);
+                    mma_commit(&tl.odone[t][u & 1]);
+                    if (u & 1 || u + 1 == steps) mma_commit(&tl.vempty[(u >> 1) & 1]);
+                }
+                __syncwarp();
             }
         }
-    } else {
-        // ---- code tiles and scales: lanes 0-7 the keys' 16-token pieces, 8-15 the values'
-        const int piece = lane & 7;
-        const bool is_v = lane & 8;
-        int done = 0;
-        bool ok = true;
-        for (int j = 0; j < nt; ++j) {
-            const int tk = ta + j * TILE + piece * 16;
-            int crow = c.n_pages * H * c.page;   // past the end: reads as zero
-            float sc = 0.f;
-            if (lane < 16 && tk < tb) {
-                const int id = load_page(a.step, c, b, tk / c.page, a.status);
-                if (id >= 0) {
-                    crow = (id * H + h) * c.page + tk % c.page;
-                    sc = (is_v ? c.v_scale : c.k_scale)[(size_t)id * H + h];
-                }
-            }
-            ok = mbar_wait(&tl.cempty[0], (j & 1) ^ 1, abort_flag, a.status);
-            if (!__all_sync(~0u, ok)) break;
-            if (lane < 16) tl.scales[j & 3][lane] = sc;
-            if (lane == 0) mbar_expect_tx(&tl.cfull[0], Sh::CODES);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tl.scfull[j & 3]);
-            if (lane < 8) tma_2d(codes + piece * 16 * DP, &tmK, &tl.cfull[0], 0, crow);
-            done = 2 * j + 1;
-            ok = mbar_wait(&tl.cempty[1], (j & 1) ^ 1, abort_flag, a.status);
-            if (!__all_sync(~0u, ok)) break;
-            if (lane == 8) mbar_expect_tx(&tl.cfull[1], Sh::CODES);
-            __syncwarp();
-            if (lane >= 8 && lane < 16) tma_2d(codes + Sh::CODES + piece * 16 * DP, &tmV, &tl.cfull[1], 0, crow);
-            done = 2 * j + 2;
-        }
-        // copies in flight land before the CTA goes
-        for (int i = 0; i < 2; ++i) {
-            const int n = (done + 1 - i) / 2;
-            const long long t0 = clock64();
-            while (n > 0 && !mbar_try_wait(&tl.cfull[i], (n - 1) & 1) && clock64() - t0 < 200000000ll) {
-            }
+        if (elect_one()) mma_commit(&tl.alldone[t]);
+        __syncwarp();
+        const long long t0 = clock64();   // the products are complete before the CTA goes
+        while (!mbar_try_wait(&tl.alldone[t], 0) && clock64() - t0 < 200000000ll) {
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == SOFT + CONV) {
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -546,11 +607,10 @@ attend_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 }
 
 template <int DP>
-cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
     const int tiles = (int)((rows + PROMPT_ROWS - 1) / PROMPT_ROWS);
-    attend_prompt_kernel<DP><<<dim3((unsigned)tiles * a.pages.heads, a.step.n_seqs), PROMPT_THREADS, PShape<DP>::SMEM, st>>>(
-        ws.k16, ws.v16, a, tiles);
+    attend_prompt_kernel<DP><<<dim3((unsigned)tiles * a.pages.heads, a.step.n_seqs), PROMPT_THREADS, PShape<DP>::SMEM, st>>>(a, tiles);
     return cudaGetLastError();
 }
 
@@ -567,8 +627,8 @@ bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return bf16 && a.pages.dim <= 128 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 64;
 }
 
-cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    return a.pages.dim <= 64 ? launch<64>(a, ws, st) : launch<128>(a, ws, st);
+cudaError_t launch_attend_prompt(const AttendArgs& a, cudaStream_t st) {
+    return a.pages.dim <= 64 ? launch<64>(a, st) : launch<128>(a, st);
 }
 
 }  // namespace mlora

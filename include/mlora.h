@@ -423,7 +423,7 @@ mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_stream_t st
  * The caller owns the pages (device memory, on the device current at creation):
  *   k_codes, v_codes  int8 [n_pages][kv_heads][page_size][head_dim], 16-byte aligned
  *   k_scale, v_scale  fp32 [n_pages][kv_heads]
- * a stored value is code * scale, one scale per page and head, for keys and for values.
+ * a stored value is code * scale, one scale (>= 0) per page and head, for keys and for values.
  *
  * A step is described to every call below by the same arrays (device, int32):
  *   offsets  [n_seqs + 1]: rows offsets[b] .. offsets[b+1] are sequence b's, in order;
