@@ -12,6 +12,9 @@ struct AttendWs {
     float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT]
     int* counters;          // [sms * ATTEND_OCC] arrivals, zero between calls
     int sms;
+    uint8_t* operands;      // converted tiles of prompts (attend_prompt.cu), operand_bytes of them
+    size_t operand_bytes;
+    int* operand_at;        // [n_seqs <= 65535] where a sequence's tiles are
 };
 
 cudaError_t attend_split_init();
@@ -19,7 +22,9 @@ cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& 
 
 // Sequences with many rows (attend_prompt.cu): bf16 and head_dim <= 128 only.
 cudaError_t attend_prompt_init();
+// Workspace for the converted tiles of `tokens` tokens.
+size_t attend_prompt_bytes(const CachePages& c, long long tokens);
 bool attend_prompt_takes(bool bf16, const AttendArgs& a);
-cudaError_t launch_attend_prompt(const AttendArgs& a, cudaStream_t st);
+cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
 
 }  // namespace mlora

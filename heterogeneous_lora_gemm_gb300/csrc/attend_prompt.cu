@@ -15,13 +15,21 @@
 // per tile, so that a step's scores are ready before the last step's weights are done (P
 // lies over its S), and O of the two tiles.
 //
-// Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8-15 read
-// codes and convert them into fp16 keys (rows of head elements) and bf16 values (tokens as
+// Conversion: a sequence of several row tiles has its codes converted once, by a kernel
+// before, into operand tiles (as they lie in shared memory) in the handle's workspace, which
+// the attention copies in bulk; converted per row tile the work takes half of the issue slots.
+// A sequence of one row tile, or one for which the workspace has no room left, is converted
+// inside the attention.
+//
+// Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
+// operand tiles or 8-15 read codes and convert them into fp16 keys (rows of head elements) and bf16 values (tokens as
 // rows: the product reads them column-major), a warp per 16 tokens of 128 with the next 128
 // tokens' codes on their way in registers, 16 and 17 issue the products of tile 0 and 1 (one
 // warp's waits would outlast both tiles' products).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <climits>
 
 #include "attend.h"
 #include "tc_ptx.cuh"
@@ -295,8 +303,111 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     return sum;
 }
 
+// 16 tokens (a warp's share of a 128-token tile) of one operand, as codes in registers.
 template <int DP>
-__global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const AttendArgs a, int tiles) {
+struct Piece {
+    static constexpr int N = 2 * PShape<DP>::BLK;   // 16-byte loads per thread
+    uint4 x[N];
+    // tokens `place` .. + 15 of page `id`; zeros where id < 0
+    __device__ __forceinline__ void load(const int8_t* codes, const CachePages& c, int id, int h, int place, int lane) {
+        const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+        const int8_t* from = codes + ((size_t)(id < 0 ? 0 : id * c.heads + h) * c.page + place + t8) * c.dim + c4 * 16;
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            x[u] = id >= 0 && (u % PShape<DP>::BLK * 4 + c4) * 16 < c.dim
+                       ? __ldg(reinterpret_cast<const uint4*>(from + u / PShape<DP>::BLK * 8 * c.dim + u % PShape<DP>::BLK * 64))
+                       : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int u = 0; u < N; ++u) x[u] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // into operand tile `dst` (generic address), as tokens 16 w ..
+    template <bool BF>
+    __device__ __forceinline__ void store(uint8_t* dst, int w, int lane) const {
+        const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            convert16<BF>(x[u], dst, w * 16 + u / PShape<DP>::BLK * 8 + t8, u % PShape<DP>::BLK, c4);
+    }
+};
+// Scales of 16 tokens as the softmax takes them (see the top of the file).
+__device__ __forceinline__ void put_scales(float* sc, int w, float ks, float vs) {
+    const bool none = vs == 0.f;
+    sc[w] = ks;
+    sc[8 + w] = none ? 0.f : log2f(vs);
+    sc[16 + w] = none ? 1.f : 1.f / vs;
+}
+
+// 128-token tiles of a sequence that its rows see.
+struct Span {
+    int j0, j1;
+};
+__device__ __forceinline__ Span span_of(const SeqRec& s, int window) {
+    const int tb = s.start + s.rows, ta = window > 0 ? max(0, s.start - window + 1) : 0;
+    return tb > ta ? Span{ta / TILE, (tb + TILE - 1) / TILE} : Span{0, 0};
+}
+
+constexpr int PRE_THREADS = 32 * CONV;
+constexpr int NOT_HERE = INT_MIN;   // at[b] of a sequence that is converted inside the attention
+
+// Operand tiles in the workspace: at[b] + j is the place of tile j of sequence b (each place
+// holds every head's keys and values, then their scales).
+template <int DP>
+__global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a, uint8_t* __restrict__ operands, int room,
+                                                              int* __restrict__ at) {
+    using Sh = PShape<DP>;
+    const CachePages& c = a.pages;
+    const int H = c.heads, G = a.q_heads / H, b = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto need = [&](int i) {
+        const SeqRec s = load_seq(a.step, c.page, i, a.status);
+        const Span p = span_of(s, a.window);
+        return s.rows * G > PROMPT_ROWS ? p.j1 - p.j0 : 0;
+    };
+    const SeqRec s = load_seq(a.step, c.page, b, a.status);
+    const Span p = span_of(s, a.window);
+    const int mine = need(b);
+    long long before = 0;
+    for (int i = tid; i < b; i += PRE_THREADS) before += need(i);
+    __shared__ long long part[CONV];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) before += __shfl_xor_sync(~0u, before, d);
+    if (lane == 0) part[warp] = before;
+    __syncthreads();
+    before = 0;
+    for (int w = 0; w < CONV; ++w) before += part[w];
+    const bool here = mine > 0 && before + mine <= room;
+    if (blockIdx.x == 0 && tid == 0) at[b] = here ? (int)before - p.j0 : NOT_HERE;
+    if (!here) return;
+    for (int i = blockIdx.x; i < mine * H; i += gridDim.x) {
+        const int j = p.j0 + i / H, h = i % H, tk = j * TILE + warp * 16;
+        const int id = tk < s.start + s.rows ? load_page(a.step, c, b, tk / c.page, a.status) : -1;
+        const int place = tk % c.page;
+        const float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
+        const size_t slot = (size_t)(before + j - p.j0) * H + h;
+        uint8_t* to = operands + slot * 2 * Sh::OPER;
+        Piece<DP> k, v;
+        k.load(c.k_codes, c, id, h, place, lane);
+        v.load(c.v_codes, c, id, h, place, lane);
+        if (vs == 0.f) v.zero();
+        k.template store<false>(to, warp, lane);
+        v.template store<true>(to + Sh::OPER, warp, lane);
+        if (lane == 0)
+            put_scales(reinterpret_cast<float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24, warp, ks, vs);
+    }
+}
+
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <int DP>
+__global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const AttendArgs a, int tiles,
+                                                                           const uint8_t* __restrict__ operands,
+                                                                           int room, const int* __restrict__ at) {
     using Sh = PShape<DP>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -316,16 +427,19 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     const int rows = min(PROMPT_ROWS, R - r0);
     const bool two = rows > TILE;
     const int pos_lo = s.start + r0 / G, pos_hi = s.start + (r0 + rows - 1) / G;
-    const int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / 16 * 16 : 0;
+    const int first = at ? at[b] : NOT_HERE;   // place of the sequence's tile 0 in the workspace
+    const bool pre = first != NOT_HERE;
+    // tokens [ta, tb), whole tiles wherever they are converted: the sums' order is the same
+    const int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / TILE * TILE : 0;
     const int tb = pos_hi + 1;
     const int nt = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;      // conversions
     const int steps = tb > ta ? (tb - ta + STEP - 1) / STEP : 0;   // products
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&tl.kfull[i], 32 * CONV);
+            mbar_init(&tl.kfull[i], pre ? 1 : 32 * CONV);
             mbar_init(&tl.kempty[i], two ? 2 : 1);
-            mbar_init(&tl.vfull[i], 32 * CONV);
+            mbar_init(&tl.vfull[i], pre ? 1 : 32 * CONV);
             mbar_init(&tl.vempty[i], two ? 2 : 1);
             mbar_init(&tl.qfull[i], TILE);
             mbar_init(&tl.alldone[i], 1);
@@ -335,7 +449,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 mbar_init(&tl.odone[i][u], 1);
             }
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&tl.scfull[i], CONV);
+        for (int i = 0; i < 4; ++i) mbar_init(&tl.scfull[i], pre ? 1 : CONV);
         tl.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -356,11 +470,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const int t = warp >> 2, q4 = warp & 3;
         const int rl = q4 * 32 + lane, r = r0 + t * TILE + rl;
         const bool live = r < R;
-        const int64_t row = s.row0 + (live ? r : r0) / G, head = h * G + (live ? r : r0) % G;
         // the query: fp16 scaled by a power of two, NaN statistics for a row that is not finite
         float qf;
         {
-            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q.ptr + row * a.q.row + head * a.q.head;
+            const int rq = live ? r : r0;
+            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q.ptr + (int64_t)(s.row0 + rq / G) * a.q.row +
+                                     (int64_t)(h * G + rq % G) * a.q.head;
             auto load = [&](int i) {
                 return live && i * 8 < D ? *reinterpret_cast<const uint4*>(q + i * 8) : make_uint4(0u, 0u, 0u, 0u);
             };
@@ -464,7 +579,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             const float2 ls = unpair(l2);
             const float l = ls.x + ls.y;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            __nv_bfloat16* o = (__nv_bfloat16*)a.o.ptr + row * a.o.row + head * a.o.head;
+            const int rq = live ? r : r0;
+            __nv_bfloat16* o = (__nv_bfloat16*)a.o.ptr + (int64_t)(s.row0 + rq / G) * a.o.row +
+                               (int64_t)(h * G + rq % G) * a.o.head;
 #pragma unroll
             for (int q = 0; q < DP / 32; ++q) {
                 uint32_t x[32];
@@ -487,70 +604,84 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 }
             }
         }
+    } else if (warp < SOFT + CONV && pre) {
+        // ---- copies of converted tiles
+        if (warp == SOFT) {
+            int done = 0;
+            for (int j = 0; j < nt; ++j) {
+                const uint32_t use = (j >> 1) & 1;
+                const size_t slot = (size_t)(first + ta / TILE + j) * H + h;
+                const uint8_t* from = operands + slot * 2 * Sh::OPER;
+                const float* scales = reinterpret_cast<const float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24;
+                const float sc = lane < 24 ? scales[lane] : 0.f;
+                if (!__all_sync(~0u, wait_for(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status))) break;
+                if (lane < 24) tl.scales[j & 3][lane] = sc;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&tl.scfull[j & 3]);
+                    mbar_expect_tx(&tl.kfull[j & 1], Sh::OPER);
+                    bulk_g2s(kb + (j & 1) * Sh::OPER, from, Sh::OPER, &tl.kfull[j & 1]);
+                }
+                done = 2 * j + 1;
+                if (!__all_sync(~0u, wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&tl.vfull[j & 1], Sh::OPER);
+                    bulk_g2s(vb + (j & 1) * Sh::OPER, from + Sh::OPER, Sh::OPER, &tl.vfull[j & 1]);
+                }
+                done = 2 * j + 2;
+            }
+            // copies in flight land before the CTA goes: each barrier's last phase
+            for (int i = 0; i < 4; ++i) {
+                const int copies = (done + 1 - (i >> 1)) / 2;          // of keys or values
+                const int n = (copies + 1 - (i & 1)) / 2;              // through this buffer
+                uint64_t* bar = (i >> 1 ? tl.vfull : tl.kfull) + (i & 1);
+                const long long t0 = clock64();
+                while (n > 0 && !mbar_try_wait(bar, (n - 1) & 1) && clock64() - t0 < 200000000ll) {
+                }
+            }
+        }
     } else if (warp < SOFT + CONV) {
         // ---- conversion: the warp's 16 tokens of each tile
-        constexpr int N = 2 * Sh::BLK;   // 16-byte loads per thread and operand
-        const int w = warp - SOFT, c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+        const int w = warp - SOFT;
         // the warp's tokens of the tile that is loaded next: block and place in the sequence's table
-        int tk = ta + w * 16, blk = tk / c.page, off = tk % c.page;
-        const int dblk = TILE / c.page, doff = TILE % c.page;
+        int tk = ta + w * 16, blk = tk / c.page, place = tk % c.page;
+        const int dblk = TILE / c.page, dplace = TILE % c.page;
         auto next_id = [&]() { return tk < tb ? load_page(a.step, c, b, blk, a.status) : -1; };   // -1: nothing to read
         auto advance = [&]() {
             tk += TILE;
             blk += dblk;
-            off += doff;
-            if (off >= c.page) off -= c.page, ++blk;
-        };
-        const int lane_off = t8 * D + c4 * 16;
-        auto load = [&](const int8_t* codes, int id, int place, uint4* x) {
-            const int8_t* from = codes + ((size_t)(id < 0 ? 0 : id * H + h) * c.page + place) * D + lane_off;
-#pragma unroll
-            for (int u = 0; u < N; ++u)
-                x[u] = id >= 0 && (u % Sh::BLK * 4 + c4) * 16 < D
-                           ? __ldg(reinterpret_cast<const uint4*>(from + u / Sh::BLK * 8 * D + u % Sh::BLK * 64))
-                           : make_uint4(0u, 0u, 0u, 0u);
+            place += dplace;
+            if (place >= c.page) place -= c.page, ++blk;
         };
         auto scale = [&](const float* p, int id) { return id >= 0 ? p[(size_t)id * H + h] : 0.f; };
-        uint4 kx[N], vx[N];
-        int id = next_id(), place = off;
-        load(c.k_codes, id, place, kx);
-        load(c.v_codes, id, place, vx);
+        Piece<DP> k, v;
+        int id = next_id();
+        k.load(c.k_codes, c, id, h, place, lane);
+        v.load(c.v_codes, c, id, h, place, lane);
         float ks = scale(c.k_scale, id), vs = scale(c.v_scale, id);
         advance();
         id = next_id();
-        place = off;
         for (int j = 0; j < nt; ++j) {
             const uint32_t use = (j >> 1) & 1;
             if (!wait_for(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status)) break;
-            const bool none = vs == 0.f;
             if (lane == 0) {
-                float* sc = tl.scales[j & 3];
-                sc[w] = ks;
-                sc[8 + w] = none ? 0.f : log2f(vs);
-                sc[16 + w] = none ? 1.f : 1.f / vs;
+                put_scales(tl.scales[j & 3], w, ks, vs);
                 mbar_arrive(&tl.scfull[j & 3]);
             }
-            uint8_t* kd = kb + (j & 1) * Sh::OPER;
-#pragma unroll
-            for (int u = 0; u < N; ++u) convert16<false>(kx[u], kd, w * 16 + u / Sh::BLK * 8 + t8, u % Sh::BLK, c4);
+            k.template store<false>(kb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.kfull[j & 1]);
-            load(c.k_codes, id, place, kx);
+            k.load(c.k_codes, c, id, h, place, lane);
             if (!wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
-            uint8_t* vd = vb + (j & 1) * Sh::OPER;
-            if (none)
-#pragma unroll
-                for (int u = 0; u < N; ++u) vx[u] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int u = 0; u < N; ++u) convert16<true>(vx[u], vd, w * 16 + u / Sh::BLK * 8 + t8, u % Sh::BLK, c4);
+            if (vs == 0.f) v.zero();
+            v.template store<true>(vb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.vfull[j & 1]);
-            load(c.v_codes, id, place, vx);
+            v.load(c.v_codes, c, id, h, place, lane);
             ks = scale(c.k_scale, id);
             vs = scale(c.v_scale, id);
             advance();
             id = next_id();
-            place = off;
         }
     } else if (steps > 0 && (warp == SOFT + CONV || two)) {
         // ---- products of a tile: a step's scores go ahead of the last step's weights
@@ -607,10 +738,20 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 }
 
 template <int DP>
-cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
+cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
     const int tiles = (int)((rows + PROMPT_ROWS - 1) / PROMPT_ROWS);
-    attend_prompt_kernel<DP><<<dim3((unsigned)tiles * a.pages.heads, a.step.n_seqs), PROMPT_THREADS, PShape<DP>::SMEM, st>>>(a, tiles);
+    const int room = (int)(ws.operand_bytes / ((size_t)a.pages.heads * (2 * PShape<DP>::OPER + 96)));
+    const bool pre = tiles > 1 && room > 0;
+    if (pre) {
+        // a few thousand warps in all, as many blocks for each sequence
+        const int blocks = a.step.n_seqs >= 8 * ws.sms ? 1 : (8 * ws.sms + a.step.n_seqs - 1) / a.step.n_seqs;
+        convert_kernel<DP><<<dim3(blocks, a.step.n_seqs), PRE_THREADS, 0, st>>>(a, ws.operands, room, ws.operand_at);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    attend_prompt_kernel<DP><<<dim3((unsigned)tiles * a.pages.heads, a.step.n_seqs), PROMPT_THREADS, PShape<DP>::SMEM, st>>>(
+        a, tiles, ws.operands, room, pre ? ws.operand_at : nullptr);
     return cudaGetLastError();
 }
 
@@ -623,12 +764,18 @@ cudaError_t attend_prompt_init() {
     return e;
 }
 
+size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
+    if (c.dim > 128) return 0;
+    const size_t oper = c.dim <= 64 ? PShape<64>::OPER : PShape<128>::OPER;
+    return (size_t)((tokens + TILE - 1) / TILE) * c.heads * (2 * oper + 96);
+}
+
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return bf16 && a.pages.dim <= 128 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 64;
 }
 
-cudaError_t launch_attend_prompt(const AttendArgs& a, cudaStream_t st) {
-    return a.pages.dim <= 64 ? launch<64>(a, st) : launch<128>(a, st);
+cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    return a.pages.dim <= 64 ? launch<64>(a, ws, st) : launch<128>(a, ws, st);
 }
 
 }  // namespace mlora

@@ -107,7 +107,8 @@ bool encode_codes(CUtensorMap* map, const void* codes, const CachePages& c) {
 extern "C" {
 
 mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, float* v_scale, int n_pages,
-                                int page_size, int kv_heads, int head_dim, int q_heads, mlora_cache_t* out) {
+                                int page_size, int kv_heads, int head_dim, int q_heads, uint64_t prompt_bytes,
+                                mlora_cache_t* out) {
     if (!out) return fail(MLORA_ERR_INVALID_ARG, "out is NULL");
     *out = nullptr;
     if (!k_codes || !k_scale || !v_codes || !v_scale) return fail(MLORA_ERR_INVALID_ARG, "codes/scale is NULL");
@@ -129,7 +130,11 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     int sms = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
     const size_t ctas = (size_t)sms * ATTEND_OCC, head = 256 + (ctas * sizeof(int) + 255) / 256 * 256;
-    if (e == cudaSuccess) e = cudaMalloc((void**)&c->ws, head + 2 * ctas * ATTEND_SLOT * sizeof(float));
+    const size_t slots = 2 * ctas * ATTEND_SLOT * sizeof(float), table = 65536 * sizeof(int);
+    // converted prompt tiles: no more than all pages' tokens (and a tile's rest per page)
+    const size_t most = attend_prompt_bytes(c->pages, (long long)n_pages * page_size + 128);
+    const size_t operands = (size_t)prompt_bytes < most ? (size_t)prompt_bytes : most;
+    if (e == cudaSuccess) e = cudaMalloc((void**)&c->ws, head + slots + table + operands);
     if (e == cudaSuccess) e = cudaMemset(c->ws, 0, head);
     if (e == cudaSuccess) e = attend_split_init();
     if (e == cudaSuccess) e = attend_prompt_init();
@@ -138,6 +143,9 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     c->attend.counters = (int*)(c->ws + 256);
     c->attend.partial = (float*)(c->ws + head);
     c->attend.sms = sms;
+    c->attend.operand_at = (int*)(c->ws + head + slots);
+    c->attend.operands = (uint8_t*)(c->ws + head + slots + table);
+    c->attend.operand_bytes = operands;
     if (e != cudaSuccess) {
         if (c->ws) cudaFree(c->ws);
         delete c;
@@ -211,7 +219,7 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, scale, window,
                  (uint32_t*)c->ws};
     const bool bf16 = dtype == MLORA_BF16;
-    CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(a, (cudaStream_t)stream)
+    CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(a, c->attend, (cudaStream_t)stream)
                                         : launch_attend_split(bf16, a, c->attend, (cudaStream_t)stream));
     return MLORA_OK;
 }

@@ -84,7 +84,7 @@ _SIGNATURES = {
     "mlora_project_noalloc": (_I, [_P, _P, _I, _I, _I, _P, _P]),
     "mlora_project_noalloc_status": (_I, [_P]),
     "mlora_debug_noalloc_expire_wait": (_I, [ctypes.c_longlong, _P]),
-    "mlora_cache_create": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.POINTER(_P)]),
+    "mlora_cache_create": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_uint64, ctypes.POINTER(_P)]),
     "mlora_cache_destroy": (_I, [_P]),
     "mlora_cache_append": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
     "mlora_cache_read": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
@@ -259,10 +259,10 @@ def mlora_dequantize_nf4(codes_ptr: int, absmax_ptr: int, codebook, dout: int, d
 
 
 def mlora_cache_create(k_codes_ptr: int, k_scale_ptr: int, v_codes_ptr: int, v_scale_ptr: int, n_pages: int,
-                       page_size: int, kv_heads: int, head_dim: int, q_heads: int) -> int:
+                       page_size: int, kv_heads: int, head_dim: int, q_heads: int, prompt_bytes: int) -> int:
     h = _P()
     check(lib().mlora_cache_create(k_codes_ptr, k_scale_ptr, v_codes_ptr, v_scale_ptr, n_pages, page_size, kv_heads,
-                                   head_dim, q_heads, ctypes.byref(h)), "mlora_cache_create")
+                                   head_dim, q_heads, prompt_bytes, ctypes.byref(h)), "mlora_cache_create")
     return h.value
 
 
@@ -430,10 +430,11 @@ class Cache:
     by the cache.  A step's arrays: lengths int32 [n_seqs], pages int32 [n_seqs, width],
     offsets int32 [n_seqs + 1] or None (one row per sequence), max_new >= the rows of any
     sequence.  Rows are [T, heads, head_dim] bf16 or fp32, a head's elements adjacent
-    (slices of a fused projection's output will do); 16-byte aligned.
+    (slices of a fused projection's output will do); 16-byte aligned.  prompt_bytes bounds the
+    workspace for prompts' keys and values in 16 bits.
     """
 
-    def __init__(self, k_codes, k_scale, v_codes, v_scale, q_heads: int):
+    def __init__(self, k_codes, k_scale, v_codes, v_scale, q_heads: int, prompt_bytes: int = 256 << 20):
         import torch
         self.handle = None
         self._dtypes = {torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32}
@@ -454,7 +455,8 @@ class Cache:
         self._lib = lib()
         with torch.cuda.device(self.device):
             self.handle = mlora_cache_create(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(),
-                                             v_scale.data_ptr(), n_pages, page_size, kv_heads, head_dim, q_heads)
+                                             v_scale.data_ptr(), n_pages, page_size, kv_heads, head_dim, q_heads,
+                                             prompt_bytes)
 
     def close(self) -> None:
         if getattr(self, "handle", None):

@@ -456,13 +456,18 @@ typedef struct mlora_cache* mlora_cache_t;
  * Makes a handle over the caller's pages, which stay valid until it is destroyed.
  *   page_size  tokens per page: 16, 32, 48, ... 256
  *   head_dim   16, 32, 48, ... 256;  q_heads  a multiple of kv_heads, <= 32767
- * The handle allocates its workspace (a status word and the partial results of split
- * sequences) here; append, read and attend allocate nothing.
+ *   prompt_bytes  device memory for prompts' keys and values in 16 bits (4 bytes per
+ *              token, head and element, head_dim rounded up to 64 or 128), at most what
+ *              all pages' tokens take; attend converts a long prompt's codes once into it
+ *              where they fit, and again for every 256 rows where they do not (0: always)
+ * The handle allocates its workspace (a status word, the partial results of split
+ * sequences, about 10 MB, and prompt_bytes) here; append, read and attend allocate nothing.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),
  * OOM, CUDA.  Argument checks run before any CUDA call.
  */
 mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, float* v_scale, int n_pages,
-                                int page_size, int kv_heads, int head_dim, int q_heads, mlora_cache_t* out);
+                                int page_size, int kv_heads, int head_dim, int q_heads, uint64_t prompt_bytes,
+                                mlora_cache_t* out);
 /* Waits for the device's outstanding work and frees the workspace. NULL is a no-op. */
 mlora_status mlora_cache_destroy(mlora_cache_t cache);
 

@@ -13,7 +13,8 @@ def lib():
     return mlora
 
 
-OK = dict(k_codes=16, k_scale=16, v_codes=16, v_scale=16, n_pages=4, page_size=16, kv_heads=2, head_dim=64, q_heads=4)
+OK = dict(k_codes=16, k_scale=16, v_codes=16, v_scale=16, n_pages=4, page_size=16, kv_heads=2, head_dim=64, q_heads=4,
+          prompt_bytes=0)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -33,7 +34,7 @@ def test_create_refuses(lib, change, code):
 
 def test_null_cache_is_invalid_arg(lib):
     L = lib.lib()
-    assert L.mlora_cache_create(16, 16, 16, 16, 4, 16, 2, 64, 4, None) == 1
+    assert L.mlora_cache_create(16, 16, 16, 16, 4, 16, 2, 64, 4, 0, None) == 1
     for fn in (L.mlora_cache_append, L.mlora_cache_read):
         assert fn(None, 16, 64, 64, 16, 64, 64, 1, 1, None, 16, 16, 1, 1, 1, None) == 1
     assert L.mlora_cache_attend(None, 16, 64, 64, 16, 64, 64, 1, 1, None, 16, 16, 1, 1, 1, 1.0, 0, None) == 1

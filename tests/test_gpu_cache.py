@@ -506,3 +506,21 @@ def test_pages_past_32_bit_offsets():
         want = torch.einsum("ht,thd->hd", w.softmax(-1), v)
         assert (O[b] - want).abs().max() < 1e-3 * want.abs().max()
     assert cache.status() == mlora.MLORA_OK
+
+
+def test_prompts_converted_once_or_in_place_give_the_same_bits():
+    """Room for all, one, or none of a step's sequences in the workspace for prompts."""
+    rows, lengths = [400, 300, 70, 512], [900, 300, 333, 512]
+    u = Setup(lengths, 2, 128, 64, Hq=4, seed=27)
+    q = strided(np.random.default_rng(28).standard_normal((sum(rows), 4, 128)).astype(F), "bf16")
+    tile = 128 * 2 * 128 * 4                                  # bytes of 128 tokens, two heads
+    outs = []
+    for room in (256 << 20, 9 * tile, 0):
+        cache = Cache(*u.dev, 4, prompt_bytes=room)
+        for window in (0, 200):
+            o = torch.full_like(q, float("nan"))
+            cache.attend(q, o, u.len, u.pages, offsets=offsets_of(rows), max_new=max(rows), window=window)
+            outs.append(o)
+        assert cache.status() == mlora.MLORA_OK
+    for k in (2, 4):
+        assert torch.equal(outs[0], outs[k]) and torch.equal(outs[1], outs[k + 1])
