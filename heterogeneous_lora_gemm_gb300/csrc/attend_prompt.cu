@@ -696,30 +696,35 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         auto wait = [&](uint64_t* bar, int parity) {
             return __all_sync(~0u, wait_for(bar, parity, abort_flag, a.status));
         };
-        bool ok = wait(&tl.qfull[t], 0);
-        for (int i = 0; ok && i <= steps; ++i) {
-            const int u = i - 1;
-            if (i < steps) {
-                if (!(i & 1) && !(ok = wait(&tl.kfull[(i >> 1) & 1], (i >> 2) & 1))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    product_ss<DP / 16>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
-                    mma_commit(&tl.sfull[t][i & 1]);
-                    if (i & 1 || i + 1 == steps) mma_commit(&tl.kempty[(i >> 1) & 1]);
-                }
-                __syncwarp();
+        auto scores = [&](int i) {
+            product_ss<DP / 16>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
+            mma_commit(&tl.sfull[t][i & 1]);
+            if (i & 1 || i + 1 == steps) mma_commit(&tl.kempty[(i >> 1) & 1]);
+        };
+        // steps 0 and 1 have a score buffer each; from then on a step's values free the buffer of
+        // the scores two steps on
+        bool ok = wait(&tl.qfull[t], 0) && wait(&tl.kfull[0], 0);
+        tc_fence_after();
+        if (ok && elect_one()) {
+            scores(0);
+            if (steps > 1) scores(1);
+        }
+        __syncwarp();
+        for (int i = 0; ok && i < steps; ++i) {
+            if (!(i & 1)) {   // operand tiles of this step's values and of the scores two steps on
+                ok = wait(&tl.vfull[(i >> 1) & 1], (i >> 2) & 1);
+                if (ok && i + 2 < steps) ok = wait(&tl.kfull[(i + 2) >> 1 & 1], ((i + 2) >> 2) & 1);
             }
-            if (i > 0) {
-                if (!(u & 1) && !(ok = wait(&tl.vfull[(u >> 1) & 1], (u >> 2) & 1))) break;
-                if (!(ok = wait(&tl.pfull[t][u & 1], (u >> 1) & 1))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    product_ts<STEP / 16>(tm + 256, tm + (u & 1) * STEP, dv + half_of(u), idesc_o, u > 0);
-                    mma_commit(&tl.odone[t][u & 1]);
-                    if (u & 1 || u + 1 == steps) mma_commit(&tl.vempty[(u >> 1) & 1]);
-                }
-                __syncwarp();
+            ok = ok && wait(&tl.pfull[t][i & 1], (i >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                product_ts<STEP / 16>(tm + 256, tm + (i & 1) * STEP, dv + half_of(i), idesc_o, i > 0);
+                mma_commit(&tl.odone[t][i & 1]);
+                if (i & 1 || i + 1 == steps) mma_commit(&tl.vempty[(i >> 1) & 1]);
+                if (i + 2 < steps) scores(i + 2);
             }
+            __syncwarp();
         }
         if (elect_one()) mma_commit(&tl.alldone[t]);
         __syncwarp();
