@@ -285,7 +285,7 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
         const uint32_t seen = EDGE ? column_mask(lo - g * 16, hi - g * 16) : 0u;
         const float f = qf * sc[g], c = sc[8 + g] - m, v = sc[16 + g];
         const uint64_t f2 = pair(f, f), c2 = pair(c, c);
-        uint64_t l = pair(0.f, 0.f);
+        uint64_t l[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
             const int i = g * 16 + e;
@@ -295,10 +295,10 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
                 p0 = seen >> e & 1 ? p0 : 0.f;
                 p1 = seen >> (e + 1) & 1 ? p1 : 0.f;
             }
-            l = add2(l, pair(p0, p1));
+            l[e / 2 & 1] = add2(l[e / 2 & 1], pair(p0, p1));
             y[i / 2] = bf2_of(p0, p1);
         }
-        sum = fma2(l, pair(v, v), sum);
+        sum = fma2(add2(l[0], l[1]), pair(v, v), sum);
     }
     return sum;
 }
