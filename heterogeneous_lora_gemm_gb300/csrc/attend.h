@@ -4,7 +4,7 @@
 
 namespace mlora {
 
-constexpr int ATTEND_OCC = 2;               // CTAs per SM of the split kernel
+constexpr int ATTEND_OCC = 3;               // CTAs per SM of the split kernel at most
 constexpr int ATTEND_SLOT = 32 * (128 + 2); // floats of one partial result at most
 
 struct AttendWs {

@@ -20,9 +20,9 @@
 // Bound: HBM (the codes are read once per row tile).  Each warp streams 16-token chunks
 // of its own through a private ring of TMA copies: no CTA-wide barrier in the loop.
 // Work split: all (sequence, row tile, head) items' tokens in one line, cut into equal
-// ranges, one per CTA (two CTAs per SM); every CTA finds its range from the lengths.  An
-// item cut between CTAs is joined, in range order, by the CTA that finishes it last, so
-// results do not depend on timing.
+// ranges, one per resident CTA; every CTA finds its range from the lengths.  An item is as
+// long as its tokens plus what its start costs (LEAD).  An item cut between CTAs is joined,
+// in range order, by the CTA that finishes it last, so results do not depend on timing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,7 +37,8 @@ namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int CHUNK_T = 16;               // tokens a warp takes at a time
-constexpr int MIN_UNITS = 2;              // a CTA's range is at least so many units of WARPS chunks
+constexpr int LEAD = 2;                   // units (of WARPS chunks) that starting an item costs
+constexpr int MIN_UNITS = LEAD + 2;       // a CTA's range is at least so long
 constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights stay below 2^8
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
@@ -51,7 +52,9 @@ struct Shape {
     static constexpr int ROWB = DP / CB;               // bytes of a box row
     static constexpr int BOX = CHUNK_T * ROWB;
     static constexpr int STAGE = 2 * CB * BOX;         // keys and values of a chunk
-    static constexpr int STAGES = DP == 64 ? 8 : DP == 128 ? 6 : 3;
+    // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
+    static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
+    static constexpr int STAGES = OCC == 3 ? (DP == 64 ? 8 : 4) : DP == 64 ? 8 : DP == 128 ? 6 : 3;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
     static constexpr int SMEM = 1024 + RING + QWORDS * 4;
@@ -106,12 +109,14 @@ __device__ __forceinline__ uint32_t bf2_of(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A sequence's share of the work line.
+// A sequence's share of the work line: tiles x heads items, each LEAD + units long (1 where the
+// rows see nothing: zeros are written).
 struct Line {
     SeqRec s;
     int c0, c1;       // 16-token chunks [c0, c1) that its rows see
-    int tiles, units; // row tiles, units per (tile, head)
-    __device__ long long total(int heads) const { return (long long)tiles * heads * units; }
+    int tiles, units; // row tiles, units of tokens per item
+    __device__ int length() const { return units ? LEAD + units : 1; }
+    __device__ long long total(int heads) const { return (long long)tiles * heads * length(); }
 };
 template <int RT>
 __device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
@@ -121,8 +126,8 @@ __device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
     const int lo = a.window > 0 ? max(0, n.s.start - a.window + 1) : 0;
     n.c0 = lo / CHUNK_T;
     n.c1 = last >= 0 ? last / CHUNK_T + 1 : n.c0;
-    n.tiles = (int)(((long long)n.s.rows * G + RT - 1) / RT);
-    n.units = max(1, (n.c1 - n.c0 + WARPS - 1) / WARPS);
+    n.tiles = (n.s.rows * G + RT - 1) / RT;
+    n.units = (n.c1 - n.c0 + WARPS - 1) / WARPS;
     return n;
 }
 
@@ -130,11 +135,40 @@ struct Tail {
     uint64_t full[WARPS][8];
     int abort_flag;
     int first_b, last_of;
-    long long first_at, total;
+    long long first_at;
+    Line first;
     long long scan[WARPS];
     float qf[32];
     float m[WARPS][32], l[WARPS][32];
 };
+
+// N adjacent elements as floats (N x their size: 4 to 32 bytes, aligned), zeros unless `there`
+template <int N>
+__device__ __forceinline__ void load_elements(const float* p, bool there, float* x) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 v = there ? *reinterpret_cast<const float2*>(p + e) : make_float2(0.f, 0.f);
+        x[e] = v.x, x[e + 1] = v.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_elements(const __nv_bfloat16* p, bool there, float* x) {
+    uint32_t w[N / 2];
+    if (N == 2) w[0] = there ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+    if (N == 4) {
+        const uint2 u = there ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+        w[0] = u.x, w[N / 2 - 1] = u.y;
+    }
+    if (N == 8) {
+        const uint4 u = there ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+        w[0] = u.x, w[1 % (N / 2)] = u.y, w[2 % (N / 2)] = u.z, w[3 % (N / 2)] = u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
 
 template <typename E>
 __device__ __forceinline__ void store4(E* p, float4 v);
@@ -149,7 +183,7 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v
 }
 
 template <bool F32, int DP, int NT>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, (Shape<F32, DP, NT>::OCC))
 attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
                     float* __restrict__ partial, int* __restrict__ counters) {
     using Sh = Shape<F32, DP, NT>;
@@ -170,10 +204,18 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) tl.abort_flag = 0;
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmK) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmV) : "memory");
+    }
     const int per = (a.step.n_seqs + THREADS - 1) / THREADS;
     const int b_lo = min(tid * per, a.step.n_seqs), b_hi = min(b_lo + per, a.step.n_seqs);
+    Line n;
     long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += line_of<RT>(a, G, b).total(H);
+    for (int b = b_lo; b < b_hi; ++b) {
+        n = line_of<RT>(a, G, b);
+        mine += n.total(H);
+    }
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -189,36 +231,36 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         total += tl.scan[w];
     }
     before += incl - mine;
-    const long long want = (total + MIN_UNITS - 1) / MIN_UNITS;
-    const int ctas = (int)(want < (long long)gridDim.x ? want : (long long)gridDim.x);
     const int cta = blockIdx.x;
+    const int ctas = total >= (long long)MIN_UNITS * gridDim.x ? (int)gridDim.x : ((int)total + MIN_UNITS - 1) / MIN_UNITS;
     if (cta >= ctas) return;
-    auto range_at = [&](int i) { return total * i / ctas; };
-    // the CTA whose range holds unit u
-    auto cta_of = [&](long long u) {
-        int i = (int)((u * ctas + ctas) / total);
-        i = min(i, ctas - 1);
-        while (i > 0 && range_at(i) > u) --i;
-        while (i + 1 < ctas && range_at(i + 1) <= u) ++i;
-        return i;
+    // ranges: the first `over` of them one longer than the others
+    const long long each = total >> 31 ? total / ctas : (uint32_t)total / (uint32_t)ctas;
+    const int over = (int)(total - each * ctas);
+    auto range_at = [&](int i) { return each * i + min(i, over); };
+    auto cta_of = [&](long long u) {   // the CTA whose range holds position u
+        const long long cut = (each + 1) * over, v = u < cut ? u : u - cut, w = u < cut ? each + 1 : each;
+        return (u < cut ? 0 : over) + (int)(total >> 31 ? v / w : (uint32_t)v / (uint32_t)w);
     };
     long long at = range_at(cta);
     const long long end = range_at(cta + 1);
     if (at >= before && at < before + mine) {
         long long p = before;
         int b = b_lo;
-        for (; b < b_hi; ++b) {
-            const long long t = line_of<RT>(a, G, b).total(H);
-            if (at < p + t) break;
-            p += t;
-        }
+        if (per > 1)
+            for (; b < b_hi; ++b) {
+                n = line_of<RT>(a, G, b);
+                if (at < p + n.total(H)) break;
+                p += n.total(H);
+            }
         tl.first_b = b;
         tl.first_at = p;
+        tl.first = n;
     }
     __syncthreads();
     int b = tl.first_b;
     long long b_at = tl.first_at;   // where sequence b begins on the line
-    Line n = line_of<RT>(a, G, b);
+    n = tl.first;
 
     uint32_t issued = 0, used = 0;     // chunks copied and consumed by this warp, over all items
     uint8_t* ring = smem + warp * Sh::STAGES * Sh::STAGE;
@@ -230,25 +272,54 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             b_at += n.total(H);
             n = line_of<RT>(a, G, ++b);
         }
-        const int item = (int)((at - b_at) / n.units);
-        const long long item_at = b_at + (long long)item * n.units;
-        const int u0 = (int)(at - item_at), u1 = (int)min((long long)n.units, end - item_at);
-        const int h = item % H, tile = item / H;
+        const long long into = at - b_at;
+        const int item = (int)(into >> 31 ? into / n.length() : (uint32_t)into / (uint32_t)n.length());
+        const long long item_at = b_at + (long long)item * n.length();
+        const int tile = item / H, h = item - tile * H;
         const int r0 = tile * RT, rows = min(RT, n.s.rows * G - r0);
-        // positions that the tile's rows may see: row r at start + (r0 + r) / G
-        const int pos_lo = n.s.start + r0 / G, pos_hi = n.s.start + (r0 + rows - 1) / G;
+        const int i0 = quotient(a.group, r0);   // the tile's first query token, and its head in the group
+        const int g0 = r0 - i0 * G;
+        auto token_of = [&](int r) { return quotient(a.group, g0 + r); };   // row r's query token, from i0 on
+        auto out_of = [&](int r) {
+            const int i = token_of(r);
+            return (E*)a.o.ptr + (int64_t)(n.s.row0 + i0 + i) * a.o.row + (int64_t)(h * G + g0 + r - i * G) * a.o.head;
+        };
+        if (!n.units) {   // the rows see nothing
+            for (int i = tid; i < rows * (D / 4); i += THREADS) {
+                const int r = i / (D / 4);
+                store4<E>(out_of(r) + (i - r * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+            }
+            at = item_at + 1;
+            continue;
+        }
+        const int u0 = (int)max(at - item_at - LEAD, 0ll), u1 = (int)(min((long long)n.length(), end - item_at) - LEAD);
+        at = item_at + n.length();
+        if (u1 <= u0) break;   // only the lead is in this range: the item is the next CTA's
+        // positions that the tile's rows may see: row r at start + i0 + token_of(r)
+        const int pos_lo = n.s.start + i0, pos_hi = pos_lo + token_of(rows - 1);
         const int ca = max(n.c0 + u0 * WARPS, a.window > 0 ? max(0, pos_lo - a.window + 1) / CHUNK_T : 0);
         const int cb = min(min(n.c0 + u1 * WARPS, n.c1), pos_hi >= 0 ? pos_hi / CHUNK_T + 1 : 0);
         const int count = max(0, (cb - ca - warp + WARPS - 1) / WARPS);   // this warp's chunks: ca + warp, + WARPS, ...
 
+        // ---- the tile's queries, a row per warp at a time: their loads first
+        constexpr int EL = DP / 32;
+        float x[RT / WARPS][EL];
+#pragma unroll
+        for (int k = 0; k < RT / WARPS; ++k) {
+            const int r = warp + k * WARPS, i = token_of(r);
+            const E* q = (const E*)a.q.ptr + (int64_t)(n.s.row0 + i0 + i) * a.q.row +
+                         (int64_t)(h * G + g0 + r - i * G) * a.q.head + lane * EL;
+            load_elements<EL>(q, r < rows && lane * EL < D, x[k]);
+        }
+
         // ---- page ids and scales of up to 32 chunks, one per lane, a batch ahead
         auto ids_at = [&](int k) {
             const int t = (ca + warp + k * WARPS) * CHUNK_T;
-            return k < count ? load_page(a.step, c, b, t / c.page, a.status) : -1;
+            return k < count ? load_page(a.step, c, b, quotient(a.page, t), a.status) : -1;
         };
         auto row_of = [&](int id, int k) {   // first code row of chunk k; past the tensor for a bad page
             const int t = (ca + warp + k * WARPS) * CHUNK_T;
-            return id < 0 ? c.n_pages * H * c.page : (id * H + h) * c.page + t % c.page;
+            return id < 0 ? c.n_pages * H * c.page : (id * H + h) * c.page + t - quotient(a.page, t) * c.page;
         };
         int id = ids_at(lane), id1 = ids_at(32 + lane);
         float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
@@ -274,22 +345,19 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (alive)
             for (; next < min(count, Sh::STAGES); ++next) issue(next, 0);
 
-        // ---- queries: fp16 fragments, one row per warp at a time
-        for (int r = warp; r < RT; r += WARPS) {
-            float x[DP / 32];
+        // ---- queries as fp16 fragments
+#pragma unroll
+        for (int kk = 0; kk < RT / WARPS; ++kk) {
+            const int r = warp + kk * WARPS;
             float top = 0.f;
             bool fine = true;
-            const E* q = (const E*)a.q.ptr + (int64_t)(n.s.row0 + (r0 + r) / G) * a.q.row +
-                         (int64_t)(h * G + (r0 + r) % G) * a.q.head;
 #pragma unroll
-            for (int e = 0; e < DP / 32; ++e) {
-                x[e] = r < rows && lane + 32 * e < D ? (float)q[lane + 32 * e] : 0.f;
-                fine &= fabsf(x[e]) <= 3.402823466e38f;
-                top = fmaxf(top, fabsf(x[e]));
+            for (int e = 0; e < EL; ++e) {
+                fine &= fabsf(x[kk][e]) <= 3.402823466e38f;
+                top = fmaxf(top, fabsf(x[kk][e]));
             }
             fine = __all_sync(~0u, fine);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));   // (>= 0: ordered like its bits)
             // 2^-k with top 2^-k in [1/2, 1); top below 2^-100 counts as 2^-100
             // (and above 2^127 stays in [1, 2))
             const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 127) : 0;
@@ -298,15 +366,18 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (lane == 0)
                 tl.qf[r] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
 #pragma unroll
-            for (int e = 0; e < DP / 32; ++e) {
-                const int d = lane + 32 * e, ch = d % 128 / 16, w = d % 16 / 4;
+            for (int e = 0; e < EL; e += 2) {
+                const int d = lane * EL + e, ch = d % 128 / 16, w = d % 16 / 4;
                 const int s = DP == 64 ? w : d / 128 * 8 + ch % 2 * 4 + w, t = DP == 64 ? ch : ch / 2;
-                const float v = fine ? x[e] * down * down2 : 0.f;
-                const __half hi = __float2half_rn(v);
-                __half* dst = reinterpret_cast<__half*>(
-                    qfrag + ((((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + d % 4 / 2)) + d % 2;
-                *dst = hi;
-                if (TERMS == 2) dst[128] = __float2half_rn(v - __half2float(hi));
+                const float v0 = fine ? x[kk][e] * down * down2 : 0.f, v1 = fine ? x[kk][e + 1] * down * down2 : 0.f;
+                const __half2 hi = __floats2half2_rn(v0, v1);
+                uint32_t* dst = qfrag + (((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + d % 4 / 2;
+                *dst = *reinterpret_cast<const uint32_t*>(&hi);
+                if (TERMS == 2) {
+                    const float2 f = __half22float2(hi);
+                    const __half2 lo = __floats2half2_rn(v0 - f.x, v1 - f.y);
+                    dst[64] = *reinterpret_cast<const uint32_t*>(&lo);
+                }
             }
         }
         __syncthreads();
@@ -333,7 +404,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 qf[t][e] = tl.qf[r];
                 m[t][e] = NO_MAX;
                 l[t][e] = 0.f;
-                hi[t][e] = n.s.start + (r0 + min(r, rows - 1)) / G + 1;
+                hi[t][e] = pos_lo + token_of(min(r, rows - 1)) + 1;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) o[s][t][e] = o[s][t][2 + e] = 0.f;
             }
@@ -359,7 +430,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const uint8_t* kb = ring + st * Sh::STAGE;
             const uint8_t* vb = kb + CB * Sh::BOX;
 
-            float sc[NT][4] = {};
+            float sc[NT][4] = {}, sc1[NT][4] = {};   // even and odd k steps
             constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
 #pragma unroll
             for (int q = 0; q < CB; ++q)
@@ -382,7 +453,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                             for (int term = 0; term < TERMS; ++term) {
                                 const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
-                                mma(sc[t], a0, a1, a2, a3, f.x, f.y);
+                                mma(s & 1 ? sc1[t] : sc[t], a0, a1, a2, a3, f.x, f.y);
                             }
                     }
                 }
@@ -395,8 +466,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float f = qf[t][e] * ksk;
-                    sc[t][e] *= f;
-                    sc[t][2 + e] *= f;
+                    sc[t][e] = (sc[t][e] + sc1[t][e]) * f;
+                    sc[t][2 + e] = (sc[t][2 + e] + sc1[t][2 + e]) * f;
                     if (edge) {
                         const int from = a.window > 0 ? hi[t][e] - a.window : 0;
                         if (t0 + g >= hi[t][e] || t0 + g < from) sc[t][e] = -INFINITY;
@@ -539,7 +610,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == n.units;
-        const int first = whole ? cta : cta_of(item_at), lastc = whole ? cta : cta_of(item_at + n.units - 1);
+        const int first = whole ? cta : cta_of(item_at + LEAD), lastc = whole ? cta : cta_of(item_at + n.length() - 1);
         float* slot = partial + (size_t)(2 * cta + (u0 == 0 ? 1 : 0)) * Sh::SLOT;
         for (int i = tid; i < RT * DP / 4; i += THREADS) {
             const int r = i / (DP / 4), d = i % (DP / 4) * 4;
@@ -556,9 +627,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (whole) {
                 if (r < rows && d < D) {
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    E* out = (E*)a.o.ptr + (int64_t)(n.s.row0 + (r0 + r) / G) * a.o.row +
-                             (int64_t)(h * G + (r0 + r) % G) * a.o.head + d;
-                    store4<E>(out, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                    store4<E>(out_of(r) + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             } else {
                 *reinterpret_cast<float4*>(slot + r * DP + d) = v;
@@ -570,13 +639,12 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         if (!whole) {
             // the item's CTAs first .. lastc: the last to arrive joins their slots in order
-            __threadfence();
             __syncthreads();
-            if (tid == 0) {
-                const int seen = atomicAdd(counters + first, 1);
+            if (tid == 0) {   // (release and acquire for the whole CTA, around its barriers)
+                int seen;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(counters + first) : "memory");
                 tl.last_of = seen == lastc - first;
                 if (tl.last_of) counters[first] = 0;
-                __threadfence();
             }
             __syncthreads();
             if (tl.last_of) {
@@ -597,13 +665,10 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
                     }
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    E* out = (E*)a.o.ptr + (int64_t)(n.s.row0 + (r0 + r) / G) * a.o.row +
-                             (int64_t)(h * G + (r0 + r) % G) * a.o.head + d;
-                    store4<E>(out, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                    store4<E>(out_of(r) + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             }
         }
-        at = item_at + u1;
         if (at < end) {
             fence_proxy_async_smem();   // the join buffer's generic accesses before the next item's copies
             __syncthreads();
@@ -615,7 +680,8 @@ template <bool F32, int DP, int NT>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     using Sh = Shape<F32, DP, NT>;
     static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
-    attend_split_kernel<F32, DP, NT><<<ws.sms * ATTEND_OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters);
+    static_assert(Sh::OCC <= ATTEND_OCC, "workspace slots");
+    attend_split_kernel<F32, DP, NT><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters);
     return cudaGetLastError();
 }
 

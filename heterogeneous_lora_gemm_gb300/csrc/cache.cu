@@ -18,6 +18,7 @@ struct mlora_cache {
     int q_heads = 0;
     char* ws = nullptr;       // the status word, the join counters, the partial results
     AttendWs attend{};
+    Divide page_div{}, group_div{};
 };
 
 namespace {
@@ -126,6 +127,8 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     if (!c) return fail(MLORA_ERR_OOM, "host memory");
     c->pages = CachePages{(int8_t*)k_codes, (int8_t*)v_codes, k_scale, v_scale, n_pages, page_size, kv_heads, head_dim};
     c->q_heads = q_heads;
+    c->page_div = divide_by(page_size);
+    c->group_div = divide_by(q_heads / kv_heads);
     cudaError_t e = cudaGetDevice(&c->device);
     int sms = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
@@ -216,8 +219,8 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     if ((st = check_rows("O", O, o_row, o_head, dtype)) != MLORA_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, "cudaSetDevice");
-    AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, scale, window,
-                 (uint32_t*)c->ws};
+    AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, c->page_div,
+                 c->group_div, scale, window, (uint32_t*)c->ws};
     const bool bf16 = dtype == MLORA_BF16;
     CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(a, c->attend, (cudaStream_t)stream)
                                         : launch_attend_split(bf16, a, c->attend, (cudaStream_t)stream));

@@ -36,6 +36,20 @@ struct RowsOf {
 using RowsIn = RowsOf<const void*>;
 using RowsOut = RowsOf<void*>;
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
+// mul = ceil(2^(31+s) / d), n mul exceeds n 2^(31+s) / d by less than 2^(31+s) / d.
+struct Divide {
+    uint32_t mul;   // 0: d = 1
+    int shift;
+    int d;
+};
+inline Divide divide_by(int d) {
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    if (s == 0) return Divide{0u, 0, 1};
+    return Divide{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s - 1, d};
+}
+
 // One sequence of a step, checked: rows row0 .. row0 + rows - 1 are processed and lie at
 // positions start, start + 1, ... (start may be negative), of `len` tokens held.
 struct SeqRec {
@@ -43,6 +57,9 @@ struct SeqRec {
 };
 
 #ifdef __CUDACC__
+__device__ __forceinline__ int quotient(const Divide& v, int n) {
+    return v.mul ? (int)(__umulhi((uint32_t)n, v.mul) >> v.shift) : n;
+}
 __device__ __forceinline__ SeqRec load_seq(const CacheStep& s, int page, int b, uint32_t* status) {
     SeqRec r;
     int n = 1;
@@ -84,6 +101,7 @@ struct AttendArgs {
     RowsIn q;
     RowsOut o;
     int q_heads;
+    Divide page, group;   // by pages.page, by query heads per key/value head
     float scale;
     int window;
     uint32_t* status;
