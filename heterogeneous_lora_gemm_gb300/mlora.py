@@ -439,7 +439,8 @@ class Cache:
         self.handle = None
         self._dtypes = {torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32}
         self._i32 = torch.int32
-        self._current = torch.cuda.current_stream
+        # (the current stream's handle without a Stream object: a decode step's calls are short)
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         if k_codes.dim() != 4 or k_codes.dtype != torch.int8 or v_codes.dtype != torch.int8:
             raise ValueError("codes are int8 [n_pages, kv_heads, page_size, head_dim]")
         n_pages, kv_heads, page_size, head_dim = k_codes.shape
@@ -450,7 +451,7 @@ class Cache:
         if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
             raise ValueError("scales are fp32 [n_pages, kv_heads]")
         self._keep = (k_codes, k_scale, v_codes, v_scale)
-        self.device = k_codes.device
+        self.device, self._index = k_codes.device, k_codes.get_device()
         self.kv_heads, self.q_heads, self.page_size, self.head_dim = kv_heads, q_heads, page_size, head_dim
         self._lib = lib()
         with torch.cuda.device(self.device):
@@ -470,31 +471,33 @@ class Cache:
             pass
 
     def _call(self, fn, where, a, b, heads, lengths, pages, offsets, max_new, stream, *more):
-        code = self._dtypes.get(a.dtype)
+        code, index, i32 = self._dtypes.get(a.dtype), self._index, self._i32
         if code is None or b.dtype != a.dtype:
             raise ValueError("rows are bf16 or fp32, both operands alike")
-        T = a.shape[0]
-        if a.shape != (T, heads, self.head_dim) or b.shape != a.shape:
-            raise ValueError(f"rows are [T, {heads}, {self.head_dim}], got {tuple(a.shape)} and {tuple(b.shape)}")
+        shape = a.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim or b.shape != shape:
+            raise ValueError(f"rows are [T, {heads}, {self.head_dim}], got {tuple(shape)} and {tuple(b.shape)}")
         (ar, ah, ae), (br, bh, be) = a.stride(), b.stride()
         if ae != 1 or be != 1:
             raise ValueError("a head's elements must be adjacent")
-        if pages.dim() != 2 or pages.dtype != self._i32 or not pages.is_contiguous():
+        if pages.dim() != 2 or pages.dtype != i32 or not pages.is_contiguous():
             raise ValueError("pages is a contiguous int32 [n_seqs, width]")
         n_seqs, width = pages.shape
-        if lengths.shape != (n_seqs,) or lengths.dtype != self._i32 or not lengths.is_contiguous():
+        if lengths.shape != (n_seqs,) or lengths.dtype != i32 or not lengths.is_contiguous():
             raise ValueError("lengths is a contiguous int32 [n_seqs]")
-        if offsets is not None and (offsets.shape != (n_seqs + 1,) or offsets.dtype != self._i32 or
-                                    not offsets.is_contiguous()):
-            raise ValueError("offsets is a contiguous int32 [n_seqs + 1]")
-        for t in (a, b, lengths, pages, offsets):
-            if t is not None and t.device != self.device:
+        at = None
+        if offsets is not None:
+            if offsets.shape != (n_seqs + 1,) or offsets.dtype != i32 or not offsets.is_contiguous():
+                raise ValueError("offsets is a contiguous int32 [n_seqs + 1]")
+            if offsets.get_device() != index:
                 raise ValueError(f"operands live on the cache's device {self.device}")
-        if stream is None:
-            stream = self._current(self.device)
-        status = fn(self.handle, a.data_ptr(), ar, ah, b.data_ptr(), br, bh, code, T,
-                    None if offsets is None else offsets.data_ptr(), lengths.data_ptr(), pages.data_ptr(), n_seqs,
-                    width, max_new, *more, stream.cuda_stream)
+            at = offsets.data_ptr()
+        if (a.get_device() != index or b.get_device() != index or lengths.get_device() != index or
+                pages.get_device() != index):
+            raise ValueError(f"operands live on the cache's device {self.device}")
+        handle = self._raw_stream(index) if stream is None else stream.cuda_stream
+        status = fn(self.handle, a.data_ptr(), ar, ah, b.data_ptr(), br, bh, code, shape[0], at, lengths.data_ptr(),
+                    pages.data_ptr(), n_seqs, width, max_new, *more, handle)
         if status:
             check(status, where)
 
