@@ -19,6 +19,11 @@ namespace {
 
 constexpr float TINY_SCALE = 0x1p-120f;   // below it the codes are 0 (1 / s stays finite above)
 constexpr int THREADS = 128;
+// CTAs per SM (register limits): of 1 to 16 each, those that measured best at 100k tokens read and
+// at 28k tokens appended
+constexpr int READ_CTAS = 10;
+template <typename T>
+constexpr int APPEND_CTAS = sizeof(T) == 2 ? 9 : 4;
 constexpr int HELD = 4;                    // vectors per thread kept in registers
 
 // 16 elements of a row as they lie in memory
@@ -114,7 +119,7 @@ __device__ __forceinline__ float group_max(float m) {
 }
 
 template <typename T, int GROUP>
-__global__ void __launch_bounds__(THREADS) append_kernel(CachePages c, CacheStep s, RowsIn K, RowsIn V, Divide per_row,
+__global__ void __launch_bounds__(THREADS, APPEND_CTAS<T>) append_kernel(CachePages c, CacheStep s, RowsIn K, RowsIn V, Divide per_row,
                                                          uint32_t* status) {
     const int part = blockIdx.y * (THREADS / GROUP) + threadIdx.x / GROUP, t = threadIdx.x % GROUP;
     const int b = blockIdx.z, h = part >> 1;
@@ -205,19 +210,15 @@ __device__ __forceinline__ void store16<float>(float* p, const uint32_t (&w)[4],
                                                       __fmul_rn(value_of(w, 4 * i + 2), sc), __fmul_rn(value_of(w, 4 * i + 3), sc));
 }
 
+// Restores the x-th block that sequence b's rows may touch.
 template <typename T, int GROUP>
-__global__ void __launch_bounds__(THREADS) read_kernel(CachePages c, CacheStep s, RowsOut K, RowsOut V, Divide per_row,
-                                                       uint32_t* status) {
-    const int part = blockIdx.y * (THREADS / GROUP) + threadIdx.x / GROUP, t = threadIdx.x % GROUP;
-    const int b = blockIdx.z, h = part >> 1;
-    const bool is_v = part & 1;
-    if (h >= c.heads) return;
-    const SeqRec q = load_seq(s, c.page, b, status);
-    const int j = floor_div(q.start, c.page) + (int)blockIdx.x;   // negative: rows that name no token
+__device__ __forceinline__ void read_block(const CachePages& c, const CacheStep& s, const SeqRec& q, const RowsOut& R,
+                                           bool is_v, int b, int h, int x, const Divide& per_row, uint32_t* status) {
+    const int t = threadIdx.x % GROUP;
+    const int j = floor_div(q.start, c.page) + x;   // negative: rows that name no token
     const int lo = max(q.start - j * c.page, 0), hi = min(q.start + q.rows - j * c.page, c.page);
     if (hi <= lo) return;
     const int id = j >= 0 ? load_page(s, c, b, j, status) : -1;
-    const RowsOut& R = is_v ? V : K;
     T* dst = (T*)R.ptr + (q.row0 + (j * c.page + lo - q.start)) * R.row + h * R.head;
     const size_t at = (size_t)(id < 0 ? 0 : id) * c.heads + h;
     const int8_t* src = (is_v ? c.v_codes : c.k_codes) + (at * c.page + lo) * c.dim;
@@ -241,14 +242,27 @@ __global__ void __launch_bounds__(THREADS) read_kernel(CachePages c, CacheStep s
     }
 }
 
+// TWO: rows that touch two blocks at most, mostly one of them; one CTA looks at both (a CTA
+// that finds nothing costs a third of one that does).
+template <typename T, int GROUP, bool TWO>
+__global__ void __launch_bounds__(THREADS, READ_CTAS) read_kernel(CachePages c, CacheStep s, RowsOut K, RowsOut V,
+                                                                  Divide per_row, uint32_t* status) {
+    const int part = blockIdx.y * (THREADS / GROUP) + threadIdx.x / GROUP, b = blockIdx.z, h = part >> 1;
+    if (h >= c.heads) return;
+    const SeqRec q = load_seq(s, c.page, b, status);
+#pragma unroll 1
+    for (int x = blockIdx.x; x < (TWO ? 2 : (int)blockIdx.x + 1); ++x)
+        read_block<T, GROUP>(c, s, q, part & 1 ? V : K, part & 1, b, h, x, per_row, status);
+}
+
 // Blocks that max_new consecutive positions can touch.
 int most_blocks(int max_new, int page) { return (max_new + page - 2) / page + 1; }
 
-template <typename T, int GROUP, typename Rows, typename Kernel>
-cudaError_t launch(Kernel kernel, const CachePages& c, const CacheStep& s, const Rows& k, const Rows& v, uint32_t* status,
-                   cudaStream_t st) {
+template <int GROUP, typename Rows, typename Kernel>
+cudaError_t launch(Kernel kernel, int blocks, const CachePages& c, const CacheStep& s, const Rows& k, const Rows& v,
+                   uint32_t* status, cudaStream_t st) {
     constexpr int PARTS = THREADS / GROUP;
-    const dim3 grid(most_blocks(s.max_new, c.page), (2 * c.heads + PARTS - 1) / PARTS, s.n_seqs);
+    const dim3 grid(blocks, (2 * c.heads + PARTS - 1) / PARTS, s.n_seqs);
     kernel<<<grid, THREADS, 0, st>>>(c, s, k, v, divide_by(c.dim / 16), status);
     return cudaGetLastError();
 }
@@ -260,20 +274,26 @@ bool few_rows(const CachePages& c, const CacheStep& s) { return (long long)s.max
 
 cudaError_t launch_append(bool bf16, const CachePages& c, const CacheStep& s, const RowsIn& k, const RowsIn& v,
                           uint32_t* status, cudaStream_t st) {
+    const int blocks = most_blocks(s.max_new, c.page);
     if (few_rows(c, s))
-        return bf16 ? launch<__nv_bfloat16, 32>(append_kernel<__nv_bfloat16, 32>, c, s, k, v, status, st)
-                    : launch<float, 32>(append_kernel<float, 32>, c, s, k, v, status, st);
-    return bf16 ? launch<__nv_bfloat16, THREADS>(append_kernel<__nv_bfloat16, THREADS>, c, s, k, v, status, st)
-                : launch<float, THREADS>(append_kernel<float, THREADS>, c, s, k, v, status, st);
+        return bf16 ? launch<32>(append_kernel<__nv_bfloat16, 32>, blocks, c, s, k, v, status, st)
+                    : launch<32>(append_kernel<float, 32>, blocks, c, s, k, v, status, st);
+    return bf16 ? launch<THREADS>(append_kernel<__nv_bfloat16, THREADS>, blocks, c, s, k, v, status, st)
+                : launch<THREADS>(append_kernel<float, THREADS>, blocks, c, s, k, v, status, st);
+}
+
+template <typename T>
+static cudaError_t read_by_shape(const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v,
+                                 uint32_t* status, cudaStream_t st) {
+    const int blocks = most_blocks(s.max_new, c.page);
+    if (few_rows(c, s)) return launch<32>(read_kernel<T, 32, false>, blocks, c, s, k, v, status, st);
+    if (blocks == 2) return launch<THREADS>(read_kernel<T, THREADS, true>, 1, c, s, k, v, status, st);
+    return launch<THREADS>(read_kernel<T, THREADS, false>, blocks, c, s, k, v, status, st);
 }
 
 cudaError_t launch_read(bool bf16, const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v,
                         uint32_t* status, cudaStream_t st) {
-    if (few_rows(c, s))
-        return bf16 ? launch<__nv_bfloat16, 32>(read_kernel<__nv_bfloat16, 32>, c, s, k, v, status, st)
-                    : launch<float, 32>(read_kernel<float, 32>, c, s, k, v, status, st);
-    return bf16 ? launch<__nv_bfloat16, THREADS>(read_kernel<__nv_bfloat16, THREADS>, c, s, k, v, status, st)
-                : launch<float, THREADS>(read_kernel<float, THREADS>, c, s, k, v, status, st);
+    return bf16 ? read_by_shape<__nv_bfloat16>(c, s, k, v, status, st) : read_by_shape<float>(c, s, k, v, status, st);
 }
 
 }  // namespace mlora
