@@ -13,9 +13,10 @@
 // 0x80 under the exponent of 1024, minus 1152: the cheapest conversion), and so is a bf16
 // query that a power of two per row has brought below 1 (its elements under 2^-14 of the
 // row's largest round to 2^-25 of it).  O^T takes bf16: the weights, times vs, need its
-// range (a heavy token may hold a zero where light ones do not); one rounding of each
-// weight to 8 bits.  fp32 rows run the same products with the query as the sum of two fp16
-// terms (22 bits) and the weights as three bf16 terms (24 bits).
+// range (a heavy token may hold a zero where light ones do not), as the sum of two terms (16
+// bits: one term's 8 would be off by as much as the rounded output; the tensor pipe has room
+// under the codes' stream).  fp32 rows run the same products with the query as the sum of two
+// fp16 terms (22 bits) and the weights as three bf16 terms (24 bits).
 //
 // Bound: HBM (the codes are read once per row tile).  Each warp streams 16-token chunks
 // of its own through a private ring of TMA copies: no CTA-wide barrier in the loop.
@@ -45,7 +46,7 @@ constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: 
 template <bool F32, int DP, int NT>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query
-    static constexpr int PTERMS = F32 ? 3 : 1;         // of a weight
+    static constexpr int PTERMS = F32 ? 3 : 2;         // of a weight
     static constexpr int KS = DP / 16;                 // k steps of q . k = 16-row tiles of O^T
     static constexpr int RT = 8 * NT;                  // query rows per tile
     static constexpr int CB = DP == 256 ? 2 : 1;       // column boxes
@@ -544,16 +545,13 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         y[z][3] = bf16_codes(prmt(e1, 0x43434343u, 0x4342));
                     }
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int s = q * (KS / CB) + w * 2 + z;
+                    for (int term = 0; term < PTERMS; ++term)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
+                        for (int z = 0; z < 2; ++z)
 #pragma unroll
-                            for (int term = 0; term < PTERMS; ++term)
-                                mma_bf(o[s][t], y[0][2 * z], y[0][2 * z + 1], y[1][2 * z], y[1][2 * z + 1],
-                                       p[t][term][0], p[t][term][1]);
-                        }
-                    }
+                            for (int t = 0; t < NT; ++t)
+                                mma_bf(o[q * (KS / CB) + w * 2 + z][t], y[0][2 * z], y[0][2 * z + 1], y[1][2 * z],
+                                       y[1][2 * z + 1], p[t][term][0], p[t][term][1]);
                 }
             }
             ++used;
