@@ -18,7 +18,7 @@
 // under the codes' stream).  fp32 rows run the same products with the query as the sum of two
 // fp16 terms (22 bits) and the weights as three bf16 terms (24 bits).
 //
-// Bound: HBM (the codes are read once per row tile).  Each warp streams 16-token chunks
+// Bound: HBM (the codes are read once per row tile).  Each warp streams 32-token chunks
 // of its own through a private ring of TMA copies: no CTA-wide barrier in the loop.
 // Work split: all (sequence, row tile, head) items' tokens in one line, cut into equal
 // ranges, one per resident CTA; every CTA finds its range from the lengths.  An item is as
@@ -37,9 +37,9 @@ using namespace ptx;
 namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
-constexpr int CHUNK_T = 16;               // tokens a warp takes at a time
-constexpr int LEAD = 2;                   // units (of WARPS chunks) that starting an item costs
-constexpr int MIN_UNITS = LEAD + 2;       // a CTA's range is at least so long
+constexpr int PIECE = 16;                 // tokens of a copied box and of a product
+constexpr int LEAD = 1;                   // units (of WARPS chunks) that starting an item costs
+constexpr int MIN_UNITS = LEAD + 1;       // a CTA's range is at least so long
 constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights stay below 2^8
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
@@ -51,11 +51,16 @@ struct Shape {
     static constexpr int RT = 8 * NT;                  // query rows per tile
     static constexpr int CB = DP == 256 ? 2 : 1;       // column boxes
     static constexpr int ROWB = DP / CB;               // bytes of a box row
-    static constexpr int BOX = CHUNK_T * ROWB;
-    static constexpr int STAGE = 2 * CB * BOX;         // keys and values of a chunk
+    static constexpr int BOX = PIECE * ROWB;
+    // a warp takes a chunk of two pieces at a time: waits, votes and issues are per chunk
+    // (one where the accumulators leave no registers for two)
+    static constexpr int SUB = DP == 256 || DP * NT == 512 ? 1 : 2;
+    static constexpr int CHUNK_T = PIECE * SUB;
+    static constexpr int PART = 2 * CB * BOX;          // keys and values of a piece
+    static constexpr int STAGE = SUB * PART;
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
-    static constexpr int STAGES = OCC == 3 ? (DP == 64 ? 8 : 4) : DP == 64 ? 8 : DP == 128 ? 6 : 3;
+    static constexpr int STAGES = (OCC == 3 ? 64 : 96) * 1024 / WARPS / STAGE;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
     static constexpr int SMEM = 1024 + RING + QWORDS * 4;
@@ -114,12 +119,12 @@ __device__ __forceinline__ uint32_t bf2_of(float a, float b) {
 // rows see nothing: zeros are written).
 struct Line {
     SeqRec s;
-    int c0, c1;       // 16-token chunks [c0, c1) that its rows see
+    int c0, c1;       // chunks [c0, c1) that its rows see
     int tiles, units; // row tiles, units of tokens per item
     __device__ int length() const { return units ? LEAD + units : 1; }
     __device__ long long total(int heads) const { return (long long)tiles * heads * length(); }
 };
-template <int RT>
+template <int RT, int CHUNK_T>
 __device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
     Line n;
     n.s = load_seq(a.step, a.pages.page, b, a.status);
@@ -189,7 +194,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     float* __restrict__ partial, int* __restrict__ counters) {
     using Sh = Shape<F32, DP, NT>;
     using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
-    constexpr int KS = Sh::KS, RT = Sh::RT, TERMS = Sh::TERMS, PTERMS = Sh::PTERMS, CB = Sh::CB;
+    constexpr int KS = Sh::KS, RT = Sh::RT, SUB = Sh::SUB, CHUNK_T = Sh::CHUNK_T, TERMS = Sh::TERMS, PTERMS = Sh::PTERMS, CB = Sh::CB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + Sh::RING);
@@ -214,7 +219,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     Line n;
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-        n = line_of<RT>(a, G, b);
+        n = line_of<RT, Sh::CHUNK_T>(a, G, b);
         mine += n.total(H);
     }
     long long incl = mine;
@@ -250,7 +255,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         int b = b_lo;
         if (per > 1)
             for (; b < b_hi; ++b) {
-                n = line_of<RT>(a, G, b);
+                n = line_of<RT, Sh::CHUNK_T>(a, G, b);
                 if (at < p + n.total(H)) break;
                 p += n.total(H);
             }
@@ -271,7 +276,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     while (at < end) {
         while (at >= b_at + n.total(H)) {
             b_at += n.total(H);
-            n = line_of<RT>(a, G, ++b);
+            n = line_of<RT, Sh::CHUNK_T>(a, G, ++b);
         }
         const long long into = at - b_at;
         const int item = (int)(into >> 31 ? into / n.length() : (uint32_t)into / (uint32_t)n.length());
@@ -313,33 +318,37 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             load_elements<EL>(q, r < rows && lane * EL < D, x[k]);
         }
 
-        // ---- page ids and scales of up to 32 chunks, one per lane, a batch ahead
-        auto ids_at = [&](int k) {
-            const int t = (ca + warp + k * WARPS) * CHUNK_T;
-            return k < count ? load_page(a.step, c, b, quotient(a.page, t), a.status) : -1;
+        // ---- page ids and scales of 32 pieces, one per lane, a batch ahead
+        constexpr int BATCH = 32 / SUB;   // chunks
+        auto token_at = [&](int k) { return (ca + warp + k * WARPS) * CHUNK_T; };   // of this warp's chunk k
+        auto id_at = [&](int k, int t) {   // nothing is read past the last token that the tile sees
+            return k < count && t <= pos_hi ? load_page(a.step, c, b, quotient(a.page, t), a.status) : -1;
         };
-        auto row_of = [&](int id, int k) {   // first code row of chunk k; past the tensor for a bad page
-            const int t = (ca + warp + k * WARPS) * CHUNK_T;
+        auto row_of = [&](int id, int t) {   // first code row of the piece; past the tensor for a bad page
             return id < 0 ? c.n_pages * H * c.page : (id * H + h) * c.page + t - quotient(a.page, t) * c.page;
         };
-        int id = ids_at(lane), id1 = ids_at(32 + lane);
-        float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
-        int row = row_of(id, lane), row1 = row_of(id1, 32 + lane);
-        float ks1 = 0.f, vs1 = 0.f;
-
-        auto issue = [&](int k, int batch) {   // copies chunk k of the item (lane 0); `row` holds batch `batch`
-            const int r = __shfl_sync(~0u, (k >> 5) == batch ? row : row1, k & 31);
-            if (lane == 0) {
-                const uint32_t s = issued % Sh::STAGES;
-                uint8_t* st = ring + s * Sh::STAGE;
-                uint64_t* bar = &tl.full[warp][s];
-                mbar_expect_tx(bar, Sh::STAGE);
-#pragma unroll
-                for (int q = 0; q < CB; ++q) {
-                    tma_2d(st + q * Sh::BOX, &tmK, bar, q * 128, r);
-                    tma_2d(st + (CB + q) * Sh::BOX, &tmV, bar, q * 128, r);
-                }
-            }
+        const int my_k = lane / SUB, my_off = lane % SUB * PIECE;
+        int id1;
+        int row, row1;
+        float ks, vs, ks1 = 0.f, vs1 = 0.f;
+        {
+            const int t = token_at(my_k) + my_off, t1 = token_at(BATCH + my_k) + my_off, id = id_at(my_k, t);
+            id1 = id_at(BATCH + my_k, t1);
+            row = row_of(id, t), row1 = row_of(id1, t1);
+            ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;
+            vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
+        }
+        // copies chunk k of the item, a box per lane; `row` holds batch `batch`
+        const int box = lane % (2 * CB * SUB), box_sub = box / (2 * CB), box_v = box / CB & 1, box_q = box % CB;
+        auto issue = [&](int k, int batch) {
+            const int r = __shfl_sync(~0u, k / BATCH == batch ? row : row1, k % BATCH * SUB + box_sub);
+            const uint32_t st = issued % Sh::STAGES;
+            uint64_t* bar = &tl.full[warp][st];
+            if (lane == 0) mbar_expect_tx(bar, Sh::STAGE);
+            __syncwarp();
+            if (lane < 2 * CB * SUB)
+                tma_2d(ring + st * Sh::STAGE + box_sub * Sh::PART + (box_v * CB + box_q) * Sh::BOX, box_v ? &tmV : &tmK, bar,
+                       box_q * 128, r);
             ++issued;
         };
         int next = 0;   // next chunk to copy
@@ -415,73 +424,90 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
         // ---- this warp's chunks
         for (int k = 0; k < count && alive; ++k) {
-            if (k && (k & 31) == 0) {
-                id = id1, row = row1, ks = ks1, vs = vs1;
-                id1 = ids_at(k + 32 + lane);
-                row1 = row_of(id1, k + 32 + lane);
+            if (k && k % BATCH == 0) {
+                row = row1, ks = ks1, vs = vs1;
+                const int t = token_at(k + BATCH + my_k) + my_off;
+                id1 = id_at(k + BATCH + my_k, t);
+                row1 = row_of(id1, t);
             }
-            if ((k & 31) == 8) {   // the next batch's scales, well before they are used
+            if (k % BATCH == BATCH / 4) {   // the next batch's scales, well before they are used
                 ks1 = id1 >= 0 ? c.k_scale[(size_t)id1 * H + h] : 0.f;
                 vs1 = id1 >= 0 ? c.v_scale[(size_t)id1 * H + h] : 0.f;
             }
-            const float ksk = __shfl_sync(~0u, ks, k & 31), vsk = __shfl_sync(~0u, vs, k & 31);
+            float ksk[SUB], vsk[SUB];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                ksk[u] = __shfl_sync(~0u, ks, k % BATCH * SUB + u);
+                vsk[u] = __shfl_sync(~0u, vs, k % BATCH * SUB + u);
+            }
             const uint32_t st = used % Sh::STAGES;
             alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], (used / Sh::STAGES) & 1, abort_flag, a.status));
             if (!alive) break;
-            const uint8_t* kb = ring + st * Sh::STAGE;
-            const uint8_t* vb = kb + CB * Sh::BOX;
+            const uint8_t* stage = ring + st * Sh::STAGE;
 
-            float sc[NT][4] = {}, sc1[NT][4] = {};   // even and odd k steps
+            constexpr int CH = 2 / SUB;                  // independent sums per piece (even and odd k steps)
+            float sc[SUB][CH][NT][4] = {};
             constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
 #pragma unroll
             for (int q = 0; q < CB; ++q)
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int ch = J * tig + j;
-                    const uint4 ra = *reinterpret_cast<const uint4*>(kb + q * Sh::BOX + swz<Sh::ROWB>(g, ch));
-                    const uint4 rb = *reinterpret_cast<const uint4*>(kb + q * Sh::BOX + swz<Sh::ROWB>(g + 8, ch));
-                    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int s = (q * J + j) * 4 + w;
-                        const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
-                        const uint32_t a0 = minus1152(prmt(xa, 0x64646464u, 0x4140)),
-                                       a1 = minus1152(prmt(xb, 0x64646464u, 0x4140)),
-                                       a2 = minus1152(prmt(xa, 0x64646464u, 0x4342)),
-                                       a3 = minus1152(prmt(xb, 0x64646464u, 0x4342));
+                    for (int u = 0; u < SUB; ++u) {
+                        const uint8_t* kb = stage + u * Sh::PART + q * Sh::BOX;
+                        const int ch = J * tig + j;
+                        const uint4 ra = *reinterpret_cast<const uint4*>(kb + swz<Sh::ROWB>(g, ch));
+                        const uint4 rb = *reinterpret_cast<const uint4*>(kb + swz<Sh::ROWB>(g + 8, ch));
+                        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
+                        for (int w = 0; w < 4; ++w) {
+                            const int s = (q * J + j) * 4 + w;
+                            const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
+                            const uint32_t a0 = minus1152(prmt(xa, 0x64646464u, 0x4140)),
+                                           a1 = minus1152(prmt(xb, 0x64646464u, 0x4140)),
+                                           a2 = minus1152(prmt(xa, 0x64646464u, 0x4342)),
+                                           a3 = minus1152(prmt(xb, 0x64646464u, 0x4342));
 #pragma unroll
-                            for (int term = 0; term < TERMS; ++term) {
-                                const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
-                                mma(s & 1 ? sc1[t] : sc[t], a0, a1, a2, a3, f.x, f.y);
-                            }
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int term = 0; term < TERMS; ++term) {
+                                    const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
+                                    mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
+                                }
+                        }
                     }
-                }
-            // scores -> x log2 e; tokens g and g + 8 of the chunk, rows 2 tig and 2 tig + 1 of each tile
-            const int t0 = (ca + warp + k * WARPS) * CHUNK_T;
+            // scores -> x log2 e; tokens g and g + 8 of each piece, rows 2 tig and 2 tig + 1 of each tile
+            const int t0 = token_at(k);
             const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
             bool above = false;
+            float top[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float f = qf[t][e] * ksk;
-                    sc[t][e] = (sc[t][e] + sc1[t][e]) * f;
-                    sc[t][2 + e] = (sc[t][2 + e] + sc1[t][2 + e]) * f;
-                    if (edge) {
-                        const int from = a.window > 0 ? hi[t][e] - a.window : 0;
-                        if (t0 + g >= hi[t][e] || t0 + g < from) sc[t][e] = -INFINITY;
-                        if (t0 + g + 8 >= hi[t][e] || t0 + g + 8 < from) sc[t][2 + e] = -INFINITY;
+                    top[t][e] = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        const float f = qf[t][e] * ksk[u];
+                        float& x0 = sc[u][0][t][e];
+                        float& x1 = sc[u][0][t][2 + e];
+                        x0 = (CH == 2 ? x0 + sc[u][CH - 1][t][e] : x0) * f;
+                        x1 = (CH == 2 ? x1 + sc[u][CH - 1][t][2 + e] : x1) * f;
+                        if (edge) {
+                            const int at = t0 + u * PIECE + g, from = a.window > 0 ? hi[t][e] - a.window : 0;
+                            if (at >= hi[t][e] || at < from) x0 = -INFINITY;
+                            if (at + 8 >= hi[t][e] || at + 8 < from) x1 = -INFINITY;
+                        }
+                        top[t][e] = fmaxf(top[t][e], fmaxf(x0, x1));
                     }
-                    above |= fmaxf(sc[t][e], sc[t][2 + e]) > m[t][e] + SLACK;
+                    above |= top[t][e] > m[t][e] + SLACK;
                 }
             if (__any_sync(~0u, above)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(sc[t][e], sc[t][2 + e]);
+                        float x = top[t][e];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
                         x = fmaxf(x, m[t][e]);
@@ -495,69 +521,72 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         }
                     }
             }
-            uint32_t p[NT][PTERMS][2];   // weights times vs as the B operand: tokens x rows
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float w[4];
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t p[NT][PTERMS][2];   // weights times vs as the B operand: tokens x rows
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ex2(sc[t][e] - m[t][e & 1]);
-                l[t][0] += w[0] + w[2];
-                l[t][1] += w[1] + w[3];
+                for (int t = 0; t < NT; ++t) {
+                    float w[4];
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    float x0 = w[2 * z] * vsk, x1 = w[2 * z + 1] * vsk;
-#pragma unroll
-                    for (int term = 0; term < PTERMS; ++term) {
-                        const uint32_t u = bf2_of(x0, x1);
-                        p[t][term][z] = transpose8(u);
-                        x0 -= __uint_as_float(u << 16);
-                        x1 -= __uint_as_float(u & 0xFFFF0000u);
-                    }
-                }
-            }
-            // O^T += V^T P^T; thread's elements: 16 (DP 64: 8) adjacent ones, of tokens 2 tig, + 1, + 8, + 9
-            constexpr int W = Sh::ROWB / 32;   // words of a box row per thread
-#pragma unroll
-            for (int q = 0; q < CB; ++q) {
-                uint32_t v[4][W];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int r = 2 * tig + (z & 1) + (z >> 1) * 8;
-                    if (W == 4) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(vb + q * Sh::BOX + swz<Sh::ROWB>(r, g));
-                        v[z][0] = u.x, v[z][1] = u.y, v[z][W - 2] = u.z, v[z][W - 1] = u.w;
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(vb + q * Sh::BOX + swz<Sh::ROWB>(r, g >> 1) +
-                                                                       (g & 1) * 8);
-                        v[z][0] = u.x, v[z][1] = u.y;
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    uint32_t y[2][4];   // [token pair][element of the word]
+                    for (int e = 0; e < 4; ++e) w[e] = ex2(sc[u][0][t][e] - m[t][e & 1]);
+                    l[t][0] += w[0] + w[2];
+                    l[t][1] += w[1] + w[3];
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        const uint32_t e0 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x5140),
-                                       e1 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x7362);
-                        y[z][0] = bf16_codes(prmt(e0, 0x43434343u, 0x4140));
-                        y[z][1] = bf16_codes(prmt(e0, 0x43434343u, 0x4342));
-                        y[z][2] = bf16_codes(prmt(e1, 0x43434343u, 0x4140));
-                        y[z][3] = bf16_codes(prmt(e1, 0x43434343u, 0x4342));
+                        float x0 = w[2 * z] * vsk[u], x1 = w[2 * z + 1] * vsk[u];
+#pragma unroll
+                        for (int term = 0; term < PTERMS; ++term) {
+                            const uint32_t y = bf2_of(x0, x1);
+                            p[t][term][z] = transpose8(y);
+                            x0 -= __uint_as_float(y << 16);
+                            x1 -= __uint_as_float(y & 0xFFFF0000u);
+                        }
+                    }
+                }
+                // O^T += V^T P^T; thread's elements: 16 (DP 64: 8) adjacent ones, of tokens 2 tig, + 1, + 8, + 9
+                constexpr int W = Sh::ROWB / 32;   // words of a box row per thread
+#pragma unroll
+                for (int q = 0; q < CB; ++q) {
+                    const uint8_t* vb = stage + u * Sh::PART + (CB + q) * Sh::BOX;
+                    uint32_t v[4][W];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int r = 2 * tig + (z & 1) + (z >> 1) * 8;
+                        if (W == 4) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(vb + swz<Sh::ROWB>(r, g));
+                            v[z][0] = y.x, v[z][1] = y.y, v[z][W - 2] = y.z, v[z][W - 1] = y.w;
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2*>(vb + swz<Sh::ROWB>(r, g >> 1) + (g & 1) * 8);
+                            v[z][0] = y.x, v[z][1] = y.y;
+                        }
                     }
 #pragma unroll
-                    for (int term = 0; term < PTERMS; ++term)
+                    for (int w = 0; w < W; ++w) {
+                        uint32_t y[2][4];   // [token pair][element of the word]
 #pragma unroll
-                        for (int z = 0; z < 2; ++z)
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t e0 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x5140),
+                                           e1 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x7362);
+                            y[z][0] = bf16_codes(prmt(e0, 0x43434343u, 0x4140));
+                            y[z][1] = bf16_codes(prmt(e0, 0x43434343u, 0x4342));
+                            y[z][2] = bf16_codes(prmt(e1, 0x43434343u, 0x4140));
+                            y[z][3] = bf16_codes(prmt(e1, 0x43434343u, 0x4342));
+                        }
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                mma_bf(o[q * (KS / CB) + w * 2 + z][t], y[0][2 * z], y[0][2 * z + 1], y[1][2 * z],
-                                       y[1][2 * z + 1], p[t][term][0], p[t][term][1]);
+                        for (int term = 0; term < PTERMS; ++term)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                                for (int t = 0; t < NT; ++t)
+                                    mma_bf(o[q * (KS / CB) + w * 2 + z][t], y[0][2 * z], y[0][2 * z + 1], y[1][2 * z],
+                                           y[1][2 * z + 1], p[t][term][0], p[t][term][1]);
+                    }
                 }
             }
             ++used;
             __syncwarp();
             if (next < count) {
-                issue(next, k >> 5);
+                issue(next, k / BATCH);
                 ++next;
             }
         }
