@@ -44,7 +44,11 @@ constexpr int TILE = 128;                  // rows per tile, and tokens converte
 constexpr int STEP = 64;                   // tokens per product
 constexpr int PROMPT_ROWS = 2 * TILE;      // rows per CTA
 constexpr int SOFT = 8, CONV = 8;          // softmax and conversion warps
-constexpr int PROMPT_THREADS = 32 * (SOFT + CONV + 2);
+constexpr int PROMPT_THREADS = 32 * (SOFT + CONV + 4);   // (two warps only complete a warpgroup)
+// Registers per thread: 96 at launch, then the softmax warps take what the others leave; the
+// sum may not exceed the launch's.
+constexpr int REGS_SOFT = 128, REGS_REST = 72;
+static_assert(32 * (SOFT * REGS_SOFT + (CONV + 4) * REGS_REST) <= PROMPT_THREADS * 96, "register split");
 constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
 constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
 
@@ -242,6 +246,15 @@ __device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk,
     uint8_t* row = dst + blk * (TILE * 128) + t * 128;
     *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
     *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+}
+
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Bits e of [lo, hi) of 32 columns.
@@ -465,7 +478,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     tc_fence_after();
     const uint32_t tmem = tl.tmem;
 
+    if (warp >= SOFT) registers_down<REGS_REST>();
     if (warp < SOFT) {
+        registers_up<REGS_SOFT>();
         // ---- softmax and output: a thread per row
         const int t = warp >> 2, q4 = warp & 3;
         const int rl = q4 * 32 + lane, r = r0 + t * TILE + rl;
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             advance();
             id = next_id();
         }
-    } else if (steps > 0 && (warp == SOFT + CONV || two)) {
+    } else if (steps > 0 && (warp == SOFT + CONV || (two && warp == SOFT + CONV + 1))) {
         // ---- products of a tile: a step's scores go ahead of the last step's weights
         const int t = warp - SOFT - CONV;
         const uint32_t idesc_s = (1u << 4) | ((uint32_t)(STEP >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);   // fp16
