@@ -6,10 +6,11 @@ namespace mlora {
 
 constexpr int ATTEND_OCC = 3;               // CTAs per SM of the split kernel at most
 constexpr int ATTEND_SLOT = 32 * (128 + 2); // floats of one partial result at most
+constexpr int PROMPT_SLOT = 256 * (128 + 2);// floats of one partial result of the prompt kernel (one per SM at most)
 
 struct AttendWs {
     CUtensorMap k16, v16;   // codes as rows of head_dim bytes, boxes of 16 tokens
-    float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT]
+    float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT], or [sms][PROMPT_SLOT]
     int* counters;          // [sms * ATTEND_OCC] arrivals, zero between calls
     int sms;
     uint8_t* operands;      // converted tiles of prompts (attend_prompt.cu), operand_bytes of them

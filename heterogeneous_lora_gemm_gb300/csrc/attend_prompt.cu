@@ -21,6 +21,9 @@
 // A sequence of one row tile, or one for which the workspace has no room left, is converted
 // inside the attention.
 //
+// Where row tiles are fewer than half the SMs, each one's tokens are cut into equal parts, a CTA
+// each; the CTA that finishes a row tile last joins the parts, in their order.
+//
 // Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
 // operand tiles or 8-15 read codes and convert them into fp16 keys (rows of head elements) and bf16 values (tokens as
 // rows: the product reads them column-major), a warp per 16 tokens of 128 with the next 128
@@ -42,7 +45,9 @@ namespace {
 
 constexpr int TILE = 128;                  // rows per tile, and tokens converted at a time
 constexpr int STEP = 64;                   // tokens per product
+constexpr int PART_TILES = 4;              // a part of a row tile's tokens has at least so many tiles
 constexpr int PROMPT_ROWS = 2 * TILE;      // rows per CTA
+static_assert(PROMPT_SLOT == PROMPT_ROWS * (128 + 2), "workspace slot");
 constexpr int SOFT = 8, CONV = 8;          // softmax and conversion warps
 constexpr int PROMPT_THREADS = 32 * (SOFT + CONV + 4);   // (two warps only complete a warpgroup)
 // Registers per thread: 96 at launch, then the softmax warps take what the others leave; the
@@ -64,7 +69,7 @@ struct PTail {
     uint64_t scfull[4], sfull[2][2], pfull[2][2], odone[2][2], qfull[2], alldone[2];   // [tile][S buffer]
     float scales[4][24];              // of 128 tokens' 16-token pieces: ks, log2 vs, 1 / vs (8 each)
     uint32_t tmem;
-    int abort_flag;
+    int abort_flag, last;
 };
 static_assert(sizeof(PTail) <= 768 && 16 * CONV == TILE, "barriers and scales; a warp per piece");
 
@@ -257,6 +262,12 @@ __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Barrier of the softmax warps.
+__device__ __forceinline__ void soft_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * SOFT) : "memory");
+}
+
 // Bits e of [lo, hi) of 32 columns.
 __device__ __forceinline__ uint32_t column_mask(int lo, int hi) {
     const uint32_t below = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -419,6 +430,8 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 
 template <int DP>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const AttendArgs a, int tiles,
+                                                                           float* __restrict__ partial,
+                                                                           int* __restrict__ counters,
                                                                            const uint8_t* __restrict__ operands,
                                                                            int room, const int* __restrict__ at) {
     using Sh = PShape<DP>;
@@ -433,6 +446,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     const CachePages& c = a.pages;
     const int H = c.heads, G = a.q_heads / H, D = c.dim;
     const int b = blockIdx.y, h = blockIdx.x % H, tile = tiles - 1 - blockIdx.x / H;   // the longest first
+    const int part = blockIdx.z, item = blockIdx.y * gridDim.x + blockIdx.x;
 
     const SeqRec s = load_seq(a.step, c.page, b, a.status);
     const int R = s.rows * G, r0 = tile * PROMPT_ROWS;
@@ -443,8 +457,16 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     const int first = at ? at[b] : NOT_HERE;   // place of the sequence's tile 0 in the workspace
     const bool pre = first != NOT_HERE;
     // tokens [ta, tb), whole tiles wherever they are converted: the sums' order is the same
-    const int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / TILE * TILE : 0;
-    const int tb = pos_hi + 1;
+    int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / TILE * TILE : 0;
+    int tb = pos_hi + 1;
+    const int all = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;
+    const int parts = max(1, min((int)gridDim.z, all / PART_TILES));
+    if (part >= parts) return;
+    if (parts > 1) {   // this CTA's part of them
+        const int from = ta + all * part / parts * TILE;
+        tb = min(tb, ta + all * (part + 1) / parts * TILE);
+        ta = from;
+    }
     const int nt = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;      // conversions
     const int steps = tb > ta ? (tb - ta + STEP - 1) / STEP : 0;   // products
 
@@ -537,6 +559,23 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         float m = NO_MAX;
         uint64_t l2 = pair(0.f, 0.f);
         bool ok = true;
+        // 32 elements of the row, from the q-th on, times f
+        auto put32 = [&](const uint32_t (&x)[32], float f, int q) {
+            __nv_bfloat16* o = (__nv_bfloat16*)a.o.ptr + (int64_t)(s.row0 + r / G) * a.o.row + (int64_t)(h * G + r % G) * a.o.head;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                if (q * 32 + e >= D) continue;
+                uint32_t y[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    y[z] = bf2_of(__uint_as_float(x[e + 2 * z]) * f, __uint_as_float(x[e + 2 * z + 1]) * f);
+                *reinterpret_cast<uint4*>(o + q * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        };
+        // the row in its part's slot: O as [DP / 4][256 rows] of 16 bytes, then m and l
+        float* slot = partial + ((size_t)item * gridDim.z + part) * PROMPT_SLOT;
+        uint4* mine = reinterpret_cast<uint4*>(slot) + t * TILE + rl;
+        float* ml = slot + DP * PROMPT_ROWS + t * TILE + rl;
         if (t == 0 || two) {
             for (int i = 0; i < steps; ++i) {
                 ok = wait_for(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
@@ -592,11 +631,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             __syncwarp();
             tc_fence_after();
             const float2 ls = unpair(l2);
-            const float l = ls.x + ls.y;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int rq = live ? r : r0;
-            __nv_bfloat16* o = (__nv_bfloat16*)a.o.ptr + (int64_t)(s.row0 + rq / G) * a.o.row +
-                               (int64_t)(h * G + rq % G) * a.o.head;
+            const float l = ls.x + ls.y, inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
             for (int q = 0; q < DP / 32; ++q) {
                 uint32_t x[32];
@@ -608,14 +643,63 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0u;
                 }
+                if (!live) continue;
+                if (parts > 1) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    if (!live || q * 32 + e >= D) continue;
-                    uint32_t y[4];
+                    for (int e = 0; e < 32; e += 4)
+                        mine[(q * 8 + e / 4) * PROMPT_ROWS] = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                } else {
+                    put32(x, inv, q);
+                }
+            }
+            if (parts > 1 && live) {
+                ml[0] = m;
+                ml[PROMPT_ROWS] = l;
+            }
+        }
+        if (parts > 1) {
+            // the last CTA to finish joins the row tile's parts (release and acquire for all its
+            // softmax threads, around their barrier)
+            soft_sync();
+            if (tid == 0) {
+                int seen;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(counters + item) : "memory");
+                tl.last = seen == parts - 1;
+                if (tl.last) counters[item] = 0;
+            }
+            soft_sync();
+            if (tl.last && live) {
+                const size_t next = PROMPT_SLOT / 4;   // from a part to the next, in 16 bytes
+                const uint4* first4 = mine - part * next;
+                const float* first_ml = ml - (size_t)part * PROMPT_SLOT;
+                float top = NO_MAX, sum = 0.f;
+                for (int z = 0; z < parts; ++z) top = fmaxf(top, __ldcg(first_ml + (size_t)z * PROMPT_SLOT));
+                for (int z = 0; z < parts; ++z) {
+                    const float* p = first_ml + (size_t)z * PROMPT_SLOT;
+                    sum = fmaf(__ldcg(p + PROMPT_ROWS), ex2(__ldcg(p) - top), sum);
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+                for (int q = 0; q < DP / 32; ++q) {
+                    float o[32] = {};
+#pragma unroll 1
+                    for (int z = 0; z < parts; ++z) {
+                        const float f = ex2(__ldcg(first_ml + (size_t)z * PROMPT_SLOT) - top);
+                        uint4 y[8];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        y[z] = bf2_of(__uint_as_float(x[e + 2 * z]) * inv, __uint_as_float(x[e + 2 * z + 1]) * inv);
-                    *reinterpret_cast<uint4*>(o + q * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(first4 + z * next + (q * 8 + e) * PROMPT_ROWS);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            o[4 * e] = fmaf(__uint_as_float(y[e].x), f, o[4 * e]);
+                            o[4 * e + 1] = fmaf(__uint_as_float(y[e].y), f, o[4 * e + 1]);
+                            o[4 * e + 2] = fmaf(__uint_as_float(y[e].z), f, o[4 * e + 2]);
+                            o[4 * e + 3] = fmaf(__uint_as_float(y[e].w), f, o[4 * e + 3]);
+                        }
+                    }
+                    uint32_t x[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e]);
+                    put32(x, inv, q);
                 }
             }
         }
@@ -770,8 +854,12 @@ cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    attend_prompt_kernel<DP><<<dim3((unsigned)tiles * a.pages.heads, a.step.n_seqs), PROMPT_THREADS, PShape<DP>::SMEM, st>>>(
-        a, tiles, ws.operands, room, pre ? ws.operand_at : nullptr);
+    // fewer row tiles than half the SMs: as many parts of each as give every SM a CTA
+    const long long ctas = (long long)tiles * a.pages.heads * a.step.n_seqs;
+    const int parts = ctas * 2 <= ws.sms ? (int)(ws.sms / ctas) : 1;
+    const dim3 grid((unsigned)tiles * a.pages.heads, a.step.n_seqs, parts);
+    attend_prompt_kernel<DP><<<grid, PROMPT_THREADS, PShape<DP>::SMEM, st>>>(a, tiles, ws.partial, ws.counters, ws.operands,
+                                                                            room, pre ? ws.operand_at : nullptr);
     return cudaGetLastError();
 }
 

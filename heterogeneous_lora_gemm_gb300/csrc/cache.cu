@@ -133,7 +133,8 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     int sms = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, c->device);
     const size_t ctas = (size_t)sms * ATTEND_OCC, head = 256 + (ctas * sizeof(int) + 255) / 256 * 256;
-    const size_t slots = 2 * ctas * ATTEND_SLOT * sizeof(float), table = 65536 * sizeof(int);
+    const size_t split = 2 * ctas * ATTEND_SLOT * sizeof(float), prompt = (size_t)sms * PROMPT_SLOT * sizeof(float);
+    const size_t slots = split > prompt ? split : prompt, table = 65536 * sizeof(int);
     // converted prompt tiles: no more than all pages' tokens (and a tile's rest per page)
     const size_t most = attend_prompt_bytes(c->pages, (long long)n_pages * page_size + 128);
     const size_t operands = (size_t)prompt_bytes < most ? (size_t)prompt_bytes : most;

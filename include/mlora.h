@@ -461,7 +461,7 @@ typedef struct mlora_cache* mlora_cache_t;
  *              all pages' tokens take; attend converts a long prompt's codes once into it
  *              where they fit, and again for every 256 rows where they do not (0: always)
  * The handle allocates its workspace (a status word, the partial results of split
- * sequences, about 10 MB, and prompt_bytes) here; append, read and attend allocate nothing.
+ * sequences, about 20 MB, and prompt_bytes) here; append, read and attend allocate nothing.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),
  * OOM, CUDA.  Argument checks run before any CUDA call.
  */
