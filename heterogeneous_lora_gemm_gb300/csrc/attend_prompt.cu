@@ -294,7 +294,8 @@ __device__ __forceinline__ float row_max(uint32_t sat, const float* sc, float qf
 }
 
 // Weights of a row's 64 scores: times the value scales into y[0, 32) (bf16 pairs); returns
-// their sum (without the value scales).
+// the sum of what was rounded (without the value scales), so that a heavy token's rounding is
+// divided out again.
 template <bool EDGE>
 __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float qf, float m, int lo, int hi,
                                           uint32_t (&y)[STEP]) {
@@ -319,8 +320,9 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
                 p0 = seen >> e & 1 ? p0 : 0.f;
                 p1 = seen >> (e + 1) & 1 ? p1 : 0.f;
             }
-            l[e / 2 & 1] = add2(l[e / 2 & 1], pair(p0, p1));
-            y[i / 2] = bf2_of(p0, p1);
+            const uint32_t w = bf2_of(p0, p1);
+            l[e / 2 & 1] = add2(l[e / 2 & 1], pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)));
+            y[i / 2] = w;
         }
         sum = fma2(add2(l[0], l[1]), pair(v, v), sum);
     }
@@ -879,7 +881,7 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
 }
 
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
-    return bf16 && a.pages.dim <= 128 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 64;
+    return bf16 && a.pages.dim <= 128 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }
 
 cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
