@@ -21,7 +21,7 @@ struct AttendWs {
 cudaError_t attend_split_init();
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
 
-// Sequences with many rows (attend_prompt.cu): bf16 and head_dim <= 128 only.
+// Sequences with many rows (attend_prompt.cu), bf16 only.
 cudaError_t attend_prompt_init();
 // Workspace for the converted tiles of `tokens` tokens.
 size_t attend_prompt_bytes(const CachePages& c, long long tokens);

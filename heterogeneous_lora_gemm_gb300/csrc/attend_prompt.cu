@@ -1,5 +1,5 @@
 // Causal attention over the 8-bit cache for sequences with many rows in the step
-// (prompts), bf16, head_dim <= 128 (include/mlora.h).
+// (prompts), bf16 (include/mlora.h).
 //
 // Mathematics as in attend_split.cu: x = scale ks (q . kc) log2 e, o = sum 2^(x - m) vs vc /
 // sum 2^(x - m).  The value scale goes into the exponent, 2^(x - m + log2 vs), and out of the
@@ -43,11 +43,9 @@ using namespace ptx;
 
 namespace {
 
-constexpr int TILE = 128;                  // rows per tile, and tokens converted at a time
+constexpr int TILE = 128;                  // rows per tile
 constexpr int STEP = 64;                   // tokens per product
-constexpr int PART_TILES = 4;              // a part of a row tile's tokens has at least so many tiles
-constexpr int PROMPT_ROWS = 2 * TILE;      // rows per CTA
-static_assert(PROMPT_SLOT == PROMPT_ROWS * (128 + 2), "workspace slot");
+constexpr int PART = 512;                  // a part of a row tile's tokens is at least so long
 constexpr int SOFT = 8, CONV = 8;          // softmax and conversion warps
 constexpr int PROMPT_THREADS = 32 * (SOFT + CONV + 4);   // (two warps only complete a warpgroup)
 // Registers per thread: 96 at launch, then the softmax warps take what the others leave; the
@@ -59,19 +57,29 @@ constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
 
 template <int DP>
 struct PShape {
+    // elements up to 256 leave tensor memory for one row tile, and shared memory for key and value
+    // tiles of 64 tokens
+    static constexpr int TILES = DP == 256 ? 1 : 2;     // row tiles per CTA
+    static constexpr int ROWS = TILES * TILE;
+    static constexpr int KT = DP == 256 ? 64 : 128;     // tokens converted at a time
+    static constexpr int SPT = KT / STEP;               // steps per token tile
     static constexpr int BLK = DP / 64;                 // 64-element column blocks (128-byte rows)
-    static constexpr int OPER = BLK * TILE * 128;       // bytes of a Q, K or V operand tile
-    static constexpr int SMEM = 1024 + 6 * OPER + 768;
+    static constexpr int QOPER = BLK * TILE * 128;      // bytes of a Q operand tile
+    static constexpr int OPER = BLK * KT * 128;         // of a K or V operand tile
+    static constexpr int SMEM = 1024 + TILES * QOPER + 4 * OPER + 768;
+    static constexpr int PIECES = KT / 16;              // of 16 tokens; a conversion warp (or two, half
+    static constexpr int WARP_BLK = BLK * PIECES / CONV;   // the blocks each) per piece
+    static_assert(PROMPT_SLOT >= ROWS * (DP + 2), "workspace slot");
 };
 
 struct PTail {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
     uint64_t scfull[4], sfull[2][2], pfull[2][2], odone[2][2], qfull[2], alldone[2];   // [tile][S buffer]
-    float scales[4][24];              // of 128 tokens' 16-token pieces: ks, log2 vs, 1 / vs (8 each)
+    float scales[4][24];              // of a token tile's 16-token pieces: ks, log2 vs, 1 / vs (8 each)
     uint32_t tmem;
     int abort_flag, last;
 };
-static_assert(sizeof(PTail) <= 768 && 16 * CONV == TILE, "barriers and scales; a warp per piece");
+static_assert(sizeof(PTail) <= 768, "barriers and scales");
 
 // mbar_wait (tc_ptx.cuh) that sleeps: the waiting warps share issue slots with the busy ones.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
@@ -178,12 +186,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A_COL), "n"(B_OFF >> 4)
         : "memory");
 }
-// K steps [0, N): SS in 64-element blocks of 128 rows of 128 bytes, TS over rows of tokens.
-template <int N, int K = 0>
+// K steps [0, N): SS in 64-element blocks of 128 (A) and B_ROWS rows of 128 bytes, TS over rows
+// of tokens.
+template <int N, int B_ROWS, int K = 0>
 __device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    constexpr int OFF = K / 4 * (128 * 128) + K % 4 * 32;
-    mma_ss<OFF, OFF>(d, a, b, idesc, K > 0);
-    if constexpr (K + 1 < N) product_ss<N, K + 1>(d, a, b, idesc);
+    mma_ss<K / 4 * (128 * 128) + K % 4 * 32, K / 4 * (B_ROWS * 128) + K % 4 * 32>(d, a, b, idesc, K > 0);
+    if constexpr (K + 1 < N) product_ss<N, B_ROWS, K + 1>(d, a, b, idesc);
 }
 template <int N, int K = 0>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -243,12 +251,12 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
 }
 
 // 16 codes of token t, elements 16 c .. of 64-element block blk, into an operand tile: DP / 64
-// blocks of 128 rows of 128 bytes under the 128-byte swizzle.  (Lanes pair token t with t ^ 5,
+// blocks of KT rows of 128 bytes under the 128-byte swizzle.  (Lanes pair token t with t ^ 5,
 // so that the writes of a quarter warp, at (2 c + z) ^ t, do not meet in a bank.)
-template <bool BF>
+template <bool BF, int KT>
 __device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk, int c) {
     const uint2 a = widen<BF>(x.x), b = widen<BF>(x.y), d = widen<BF>(x.z), e = widen<BF>(x.w);
-    uint8_t* row = dst + blk * (TILE * 128) + t * 128;
+    uint8_t* row = dst + blk * (KT * 128) + t * 128;
     *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
     *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
 }
@@ -329,32 +337,37 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     return sum;
 }
 
-// 16 tokens (a warp's share of a 128-token tile) of one operand, as codes in registers.
+// A conversion warp's share of a token tile of one operand, 16 tokens and WARP_BLK column
+// blocks, as codes in registers.
 template <int DP>
 struct Piece {
-    static constexpr int N = 2 * PShape<DP>::BLK;   // 16-byte loads per thread
+    using Sh = PShape<DP>;
+    static constexpr int WB = Sh::WARP_BLK, N = 2 * WB;   // 16-byte loads per thread
+    // warp w's 16-token piece and first column block
+    static __device__ __forceinline__ int piece(int w) { return Sh::PIECES == CONV ? w : w % Sh::PIECES; }
+    static __device__ __forceinline__ int blk0(int w) { return Sh::PIECES == CONV ? 0 : w / Sh::PIECES * WB; }
     uint4 x[N];
     // tokens `place` .. + 15 of page `id`; zeros where id < 0
-    __device__ __forceinline__ void load(const int8_t* codes, const CachePages& c, int id, int h, int place, int lane) {
-        const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
-        const int8_t* from = codes + ((size_t)(id < 0 ? 0 : id * c.heads + h) * c.page + place + t8) * c.dim + c4 * 16;
+    __device__ __forceinline__ void load(const int8_t* codes, const CachePages& c, int id, int h, int place, int w, int lane) {
+        const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), b0 = blk0(w);
+        const int8_t* from = codes + ((size_t)(id < 0 ? 0 : id * c.heads + h) * c.page + place + t8) * c.dim + b0 * 64 + c4 * 16;
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            x[u] = id >= 0 && (u % PShape<DP>::BLK * 4 + c4) * 16 < c.dim
-                       ? __ldg(reinterpret_cast<const uint4*>(from + u / PShape<DP>::BLK * 8 * c.dim + u % PShape<DP>::BLK * 64))
+            x[u] = id >= 0 && ((b0 + u % WB) * 4 + c4) * 16 < c.dim
+                       ? __ldg(reinterpret_cast<const uint4*>(from + u / WB * 8 * c.dim + u % WB * 64))
                        : make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int u = 0; u < N; ++u) x[u] = make_uint4(0u, 0u, 0u, 0u);
     }
-    // into operand tile `dst` (generic address), as tokens 16 w ..
+    // into operand tile `dst` (generic address)
     template <bool BF>
     __device__ __forceinline__ void store(uint8_t* dst, int w, int lane) const {
-        const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+        const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), b0 = blk0(w);
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            convert16<BF>(x[u], dst, w * 16 + u / PShape<DP>::BLK * 8 + t8, u % PShape<DP>::BLK, c4);
+            convert16<BF, Sh::KT>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4);
     }
 };
 // Scales of 16 tokens as the softmax takes them (see the top of the file).
@@ -365,13 +378,14 @@ __device__ __forceinline__ void put_scales(float* sc, int w, float ks, float vs)
     sc[16 + w] = none ? 1.f : 1.f / vs;
 }
 
-// 128-token tiles of a sequence that its rows see.
+// Token tiles of a sequence that its rows see.
 struct Span {
     int j0, j1;
 };
+template <int KT>
 __device__ __forceinline__ Span span_of(const SeqRec& s, int window) {
     const int tb = s.start + s.rows, ta = window > 0 ? max(0, s.start - window + 1) : 0;
-    return tb > ta ? Span{ta / TILE, (tb + TILE - 1) / TILE} : Span{0, 0};
+    return tb > ta ? Span{ta / KT, (tb + KT - 1) / KT} : Span{0, 0};
 }
 
 constexpr int PRE_THREADS = 32 * CONV;
@@ -388,11 +402,11 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto need = [&](int i) {
         const SeqRec s = load_seq(a.step, c.page, i, a.status);
-        const Span p = span_of(s, a.window);
-        return s.rows * G > PROMPT_ROWS ? p.j1 - p.j0 : 0;
+        const Span p = span_of<Sh::KT>(s, a.window);
+        return s.rows * G > Sh::ROWS ? p.j1 - p.j0 : 0;
     };
     const SeqRec s = load_seq(a.step, c.page, b, a.status);
-    const Span p = span_of(s, a.window);
+    const Span p = span_of<Sh::KT>(s, a.window);
     const int mine = need(b);
     long long before = 0;
     for (int i = tid; i < b; i += PRE_THREADS) before += need(i);
@@ -407,19 +421,19 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
     if (blockIdx.x == 0 && tid == 0) at[b] = here ? (int)before - p.j0 : NOT_HERE;
     if (!here) return;
     for (int i = blockIdx.x; i < mine * H; i += gridDim.x) {
-        const int j = p.j0 + i / H, h = i % H, tk = j * TILE + warp * 16;
+        const int j = p.j0 + i / H, h = i % H, tk = j * Sh::KT + Piece<DP>::piece(warp) * 16;
         const int id = tk < s.start + s.rows ? load_page(a.step, c, b, tk / c.page, a.status) : -1;
         const int place = tk % c.page;
         const float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
         const size_t slot = (size_t)(before + j - p.j0) * H + h;
         uint8_t* to = operands + slot * 2 * Sh::OPER;
         Piece<DP> k, v;
-        k.load(c.k_codes, c, id, h, place, lane);
-        v.load(c.v_codes, c, id, h, place, lane);
+        k.load(c.k_codes, c, id, h, place, warp, lane);
+        v.load(c.v_codes, c, id, h, place, warp, lane);
         if (vs == 0.f) v.zero();
         k.template store<false>(to, warp, lane);
         v.template store<true>(to + Sh::OPER, warp, lane);
-        if (lane == 0)
+        if (lane == 0 && warp < Sh::PIECES)
             put_scales(reinterpret_cast<float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24, warp, ks, vs);
     }
 }
@@ -439,10 +453,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     using Sh = PShape<DP>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* qs = smem;                              // [2 tiles]
-    uint8_t* kb = smem + 2 * Sh::OPER;               // [2]
-    uint8_t* vb = smem + 4 * Sh::OPER;               // [2]
-    PTail& tl = *reinterpret_cast<PTail*>(smem + 6 * Sh::OPER);
+    constexpr int KT = Sh::KT, SPT = Sh::SPT;
+    uint8_t* qs = smem;                              // [TILES]
+    uint8_t* kb = smem + Sh::TILES * Sh::QOPER;      // [2]
+    uint8_t* vb = kb + 2 * Sh::OPER;                 // [2]
+    PTail& tl = *reinterpret_cast<PTail*>(vb + 2 * Sh::OPER);
     volatile int* abort_flag = &tl.abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const CachePages& c = a.pages;
@@ -451,25 +466,25 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     const int part = blockIdx.z, item = blockIdx.y * gridDim.x + blockIdx.x;
 
     const SeqRec s = load_seq(a.step, c.page, b, a.status);
-    const int R = s.rows * G, r0 = tile * PROMPT_ROWS;
+    const int R = s.rows * G, r0 = tile * Sh::ROWS;
     if (r0 >= R) return;
-    const int rows = min(PROMPT_ROWS, R - r0);
+    const int rows = min(Sh::ROWS, R - r0);
     const bool two = rows > TILE;
     const int pos_lo = s.start + r0 / G, pos_hi = s.start + (r0 + rows - 1) / G;
     const int first = at ? at[b] : NOT_HERE;   // place of the sequence's tile 0 in the workspace
     const bool pre = first != NOT_HERE;
     // tokens [ta, tb), whole tiles wherever they are converted: the sums' order is the same
-    int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / TILE * TILE : 0;
+    int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / KT * KT : 0;
     int tb = pos_hi + 1;
-    const int all = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;
-    const int parts = max(1, min((int)gridDim.z, all / PART_TILES));
+    const int all = tb > ta ? (tb - ta + KT - 1) / KT : 0;
+    const int parts = max(1, min((int)gridDim.z, all * KT / PART));
     if (part >= parts) return;
     if (parts > 1) {   // this CTA's part of them
-        const int from = ta + all * part / parts * TILE;
-        tb = min(tb, ta + all * (part + 1) / parts * TILE);
+        const int from = ta + all * part / parts * KT;
+        tb = min(tb, ta + all * (part + 1) / parts * KT);
         ta = from;
     }
-    const int nt = tb > ta ? (tb - ta + TILE - 1) / TILE : 0;      // conversions
+    const int nt = tb > ta ? (tb - ta + KT - 1) / KT : 0;      // conversions
     const int steps = tb > ta ? (tb - ta + STEP - 1) / STEP : 0;   // products
 
     if (tid == 0) {
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 mbar_init(&tl.odone[i][u], 1);
             }
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&tl.scfull[i], pre ? 1 : CONV);
+        for (int i = 0; i < 4; ++i) mbar_init(&tl.scfull[i], pre ? 1 : Sh::PIECES);
         tl.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -510,8 +525,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const int rl = q4 * 32 + lane, r = r0 + t * TILE + rl;
         const bool live = r < R;
         // the query: fp16 scaled by a power of two, NaN statistics for a row that is not finite
-        float qf;
-        {
+        float qf = 0.f;
+        if (Sh::TILES == 2 || t == 0) {
             const int rq = live ? r : r0;
             const __nv_bfloat16* q = (const __nv_bfloat16*)a.q.ptr + (int64_t)(s.row0 + rq / G) * a.q.row +
                                      (int64_t)(h * G + rq % G) * a.q.head;
@@ -545,7 +560,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                                                         __uint_as_float(u[e] & 0xFFFF0000u) * down);
                     v[e] = fine ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
                 }
-                *reinterpret_cast<uint4*>(qs + t * Sh::OPER + i / 8 * (TILE * 128) + rl * 128 + (((i & 7) ^ (rl & 7)) << 4)) =
+                *reinterpret_cast<uint4*>(qs + t * Sh::QOPER + i / 8 * (TILE * 128) + rl * 128 + (((i & 7) ^ (rl & 7)) << 4)) =
                     make_uint4(v[0], v[1], v[2], v[3]);
             }
             fence_proxy_async_smem();
@@ -577,15 +592,15 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         // the row in its part's slot: O as [DP / 4][256 rows] of 16 bytes, then m and l
         float* slot = partial + ((size_t)item * gridDim.z + part) * PROMPT_SLOT;
         uint4* mine = reinterpret_cast<uint4*>(slot) + t * TILE + rl;
-        float* ml = slot + DP * PROMPT_ROWS + t * TILE + rl;
+        float* ml = slot + DP * Sh::ROWS + t * TILE + rl;
         if (t == 0 || two) {
             for (int i = 0; i < steps; ++i) {
                 ok = wait_for(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
-                if (!(i & 1)) ok = ok && wait_for(&tl.scfull[(i >> 1) & 3], (i >> 3) & 1, abort_flag, a.status);
+                if (i % SPT == 0) ok = ok && wait_for(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1, abort_flag, a.status);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float* sc = tl.scales[(i >> 1) & 3] + (i & 1) * 4;
+                const float* sc = tl.scales[i / SPT & 3] + i % SPT * 4;
                 const int t0 = ta + i * STEP;
                 const bool edge = t0 + STEP > hi_min || t0 < lo_max;
                 const uint32_t sat = sbase + (i & 1) * STEP;
@@ -649,14 +664,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 if (parts > 1) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        mine[(q * 8 + e / 4) * PROMPT_ROWS] = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        mine[(q * 8 + e / 4) * Sh::ROWS] = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                 } else {
                     put32(x, inv, q);
                 }
             }
             if (parts > 1 && live) {
                 ml[0] = m;
-                ml[PROMPT_ROWS] = l;
+                ml[Sh::ROWS] = l;
             }
         }
         if (parts > 1) {
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 for (int z = 0; z < parts; ++z) top = fmaxf(top, __ldcg(first_ml + (size_t)z * PROMPT_SLOT));
                 for (int z = 0; z < parts; ++z) {
                     const float* p = first_ml + (size_t)z * PROMPT_SLOT;
-                    sum = fmaf(__ldcg(p + PROMPT_ROWS), ex2(__ldcg(p) - top), sum);
+                    sum = fmaf(__ldcg(p + Sh::ROWS), ex2(__ldcg(p) - top), sum);
                 }
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
@@ -689,7 +704,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                         const float f = ex2(__ldcg(first_ml + (size_t)z * PROMPT_SLOT) - top);
                         uint4 y[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(first4 + z * next + (q * 8 + e) * PROMPT_ROWS);
+                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(first4 + z * next + (q * 8 + e) * Sh::ROWS);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             o[4 * e] = fmaf(__uint_as_float(y[e].x), f, o[4 * e]);
@@ -711,7 +726,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             int done = 0;
             for (int j = 0; j < nt; ++j) {
                 const uint32_t use = (j >> 1) & 1;
-                const size_t slot = (size_t)(first + ta / TILE + j) * H + h;
+                const size_t slot = (size_t)(first + ta / KT + j) * H + h;
                 const uint8_t* from = operands + slot * 2 * Sh::OPER;
                 const float* scales = reinterpret_cast<const float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24;
                 const float sc = lane < 24 ? scales[lane] : 0.f;
@@ -745,11 +760,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         // ---- conversion: the warp's 16 tokens of each tile
         const int w = warp - SOFT;
         // the warp's tokens of the tile that is loaded next: block and place in the sequence's table
-        int tk = ta + w * 16, blk = tk / c.page, place = tk % c.page;
-        const int dblk = TILE / c.page, dplace = TILE % c.page;
+        int tk = ta + Piece<DP>::piece(w) * 16, blk = tk / c.page, place = tk % c.page;
+        const int dblk = KT / c.page, dplace = KT % c.page;
         auto next_id = [&]() { return tk < tb ? load_page(a.step, c, b, blk, a.status) : -1; };   // -1: nothing to read
         auto advance = [&]() {
-            tk += TILE;
+            tk += KT;
             blk += dblk;
             place += dplace;
             if (place >= c.page) place -= c.page, ++blk;
@@ -757,28 +772,28 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         auto scale = [&](const float* p, int id) { return id >= 0 ? p[(size_t)id * H + h] : 0.f; };
         Piece<DP> k, v;
         int id = next_id();
-        k.load(c.k_codes, c, id, h, place, lane);
-        v.load(c.v_codes, c, id, h, place, lane);
+        k.load(c.k_codes, c, id, h, place, w, lane);
+        v.load(c.v_codes, c, id, h, place, w, lane);
         float ks = scale(c.k_scale, id), vs = scale(c.v_scale, id);
         advance();
         id = next_id();
         for (int j = 0; j < nt; ++j) {
             const uint32_t use = (j >> 1) & 1;
             if (!wait_for(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status)) break;
-            if (lane == 0) {
+            if (lane == 0 && (Sh::PIECES == CONV || w < Sh::PIECES)) {
                 put_scales(tl.scales[j & 3], w, ks, vs);
                 mbar_arrive(&tl.scfull[j & 3]);
             }
             k.template store<false>(kb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.kfull[j & 1]);
-            k.load(c.k_codes, c, id, h, place, lane);
+            k.load(c.k_codes, c, id, h, place, w, lane);
             if (!wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
             if (vs == 0.f) v.zero();
             v.template store<true>(vb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.vfull[j & 1]);
-            v.load(c.v_codes, c, id, h, place, lane);
+            v.load(c.v_codes, c, id, h, place, w, lane);
             ks = scale(c.k_scale, id);
             vs = scale(c.v_scale, id);
             advance();
@@ -789,22 +804,24 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const int t = warp - SOFT - CONV;
         const uint32_t idesc_s = (1u << 4) | ((uint32_t)(STEP >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);   // fp16
         const uint32_t idesc_o = idesc_bf16(TILE, DP) | (1u << 16);                                           // B column-major
-        const uint64_t dq = sdesc(smem_u32(qs + t * Sh::OPER), 1024, SW128), dk = sdesc(smem_u32(kb), 1024, SW128),
-                       dv = sdesc_lbo(smem_u32(vb), TILE * 128, 1024, SW128);
+        const uint64_t dq = sdesc(smem_u32(qs + t * Sh::QOPER), 1024, SW128), dk = sdesc(smem_u32(kb), 1024, SW128),
+                       dv = sdesc_lbo(smem_u32(vb), KT * 128, 1024, SW128);
         const uint32_t tm = tmem + t * TILE;
         // operand tile of step i, and the step's 64 rows (tokens) of it
-        auto half_of = [](int i) { return (uint64_t)(((i >> 1) & 1) * (Sh::OPER >> 4) + (i & 1) * (STEP * 128 >> 4)); };
+        auto half_of = [](int i) { return (uint64_t)((i / SPT & 1) * (Sh::OPER >> 4) + i % SPT * (STEP * 128 >> 4)); };
+        auto ends = [&](int i) { return i % SPT == SPT - 1 || i + 1 == steps; };   // step i is its token tile's last
         auto wait = [&](uint64_t* bar, int parity) {
             return __all_sync(~0u, wait_for(bar, parity, abort_flag, a.status));
         };
         auto scores = [&](int i) {
-            product_ss<DP / 16>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
+            product_ss<DP / 16, KT>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
             mma_commit(&tl.sfull[t][i & 1]);
-            if (i & 1 || i + 1 == steps) mma_commit(&tl.kempty[(i >> 1) & 1]);
+            if (ends(i)) mma_commit(&tl.kempty[i / SPT & 1]);
         };
         // steps 0 and 1 have a score buffer each; from then on a step's values free the buffer of
         // the scores two steps on
         bool ok = wait(&tl.qfull[t], 0) && wait(&tl.kfull[0], 0);
+        if (SPT == 1 && steps > 1) ok = ok && wait(&tl.kfull[1], 0);
         tc_fence_after();
         if (ok && elect_one()) {
             scores(0);
@@ -812,9 +829,10 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         }
         __syncwarp();
         for (int i = 0; ok && i < steps; ++i) {
-            if (!(i & 1)) {   // operand tiles of this step's values and of the scores two steps on
-                ok = wait(&tl.vfull[(i >> 1) & 1], (i >> 2) & 1);
-                if (ok && i + 2 < steps) ok = wait(&tl.kfull[(i + 2) >> 1 & 1], ((i + 2) >> 2) & 1);
+            if (i % SPT == 0) {   // operand tiles of this step's values and of the scores two steps on
+                const int j = (i + 2) / SPT;
+                ok = wait(&tl.vfull[i / SPT & 1], i / SPT >> 1 & 1);
+                if (ok && i + 2 < steps) ok = wait(&tl.kfull[j & 1], j >> 1 & 1);
             }
             ok = ok && wait(&tl.pfull[t][i & 1], (i >> 1) & 1);
             if (!ok) break;
@@ -822,7 +840,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             if (elect_one()) {
                 product_ts<STEP / 16>(tm + 256, tm + (i & 1) * STEP, dv + half_of(i), idesc_o, i > 0);
                 mma_commit(&tl.odone[t][i & 1]);
-                if (i & 1 || i + 1 == steps) mma_commit(&tl.vempty[(i >> 1) & 1]);
+                if (ends(i)) mma_commit(&tl.vempty[i / SPT & 1]);
                 if (i + 2 < steps) scores(i + 2);
             }
             __syncwarp();
@@ -846,7 +864,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 template <int DP>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    const int tiles = (int)((rows + PROMPT_ROWS - 1) / PROMPT_ROWS);
+    const int tiles = (int)((rows + PShape<DP>::ROWS - 1) / PShape<DP>::ROWS);
     const int room = (int)(ws.operand_bytes / ((size_t)a.pages.heads * (2 * PShape<DP>::OPER + 96)));
     const bool pre = tiles > 1 && room > 0;
     if (pre) {
@@ -871,21 +889,30 @@ cudaError_t attend_prompt_init() {
     cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<64>::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attend_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<128>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_prompt_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<256>::SMEM);
     return e;
 }
 
-size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
-    if (c.dim > 128) return 0;
-    const size_t oper = c.dim <= 64 ? PShape<64>::OPER : PShape<128>::OPER;
-    return (size_t)((tokens + TILE - 1) / TILE) * c.heads * (2 * oper + 96);
+template <int DP>
+static size_t operand_bytes(const CachePages& c, long long tokens) {
+    return (size_t)((tokens + PShape<DP>::KT - 1) / PShape<DP>::KT) * c.heads * (2 * PShape<DP>::OPER + 96);
 }
 
+size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
+    return c.dim <= 64 ? operand_bytes<64>(c, tokens) : c.dim <= 128 ? operand_bytes<128>(c, tokens) : operand_bytes<256>(c, tokens);
+}
+
+// From 17 rows of a sequence and head on: at 6 tokens of 32/8 heads after 4000 tokens, 1, 16 and
+// 64 sequences take 32, 64 and 139 us here and 37, 75 and 135 us in attend_split.cu; at 4 tokens
+// 31, 64 and 138 us against 20, 49 and 83 us.
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
-    return bf16 && a.pages.dim <= 128 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
+    return bf16 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }
 
 cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    return a.pages.dim <= 64 ? launch<64>(a, ws, st) : launch<128>(a, ws, st);
+    const int D = a.pages.dim;
+    return D <= 64 ? launch<64>(a, ws, st) : D <= 128 ? launch<128>(a, ws, st) : launch<256>(a, ws, st);
 }
 
 }  // namespace mlora

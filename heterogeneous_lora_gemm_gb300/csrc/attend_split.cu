@@ -723,8 +723,7 @@ cudaError_t init() {
 cudaError_t attend_split_init() {
     cudaError_t e = cudaSuccess;
     auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
-    one(init<false, 64, 1>()), one(init<false, 64, 2>()), one(init<false, 64, 4>());
-    one(init<false, 128, 1>()), one(init<false, 128, 2>()), one(init<false, 128, 4>());
+    one(init<false, 64, 1>()), one(init<false, 64, 2>()), one(init<false, 128, 1>()), one(init<false, 128, 2>());
     one(init<false, 256, 1>()), one(init<false, 256, 2>());
     one(init<true, 64, 1>()), one(init<true, 64, 2>()), one(init<true, 64, 4>());
     one(init<true, 128, 1>()), one(init<true, 128, 2>()), one(init<true, 128, 4>());
@@ -732,19 +731,21 @@ cudaError_t attend_split_init() {
     return e;
 }
 
-// Rows per tile: the fewest 8-row columns that hold a sequence's rows, up to the most
-// that the accumulators leave registers for.
+// Rows per tile: the fewest 8-row columns that hold a sequence's rows, up to the most that the
+// accumulators leave registers for (bf16 rows past 16 are attend_prompt.cu's).
+template <bool F32, int DP>
+static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
+    if (rows <= 8) return launch<F32, DP, 1>(a, ws, st);
+    if constexpr (F32 && DP < 256)
+        if (rows > 16) return launch<F32, DP, 4>(a, ws, st);
+    return launch<F32, DP, 2>(a, ws, st);
+}
+
 template <bool F32>
 static cudaError_t by_shape(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
     const int D = a.pages.dim;
-    if (D <= 64)
-        return rows <= 8 ? launch<F32, 64, 1>(a, ws, st)
-                         : rows <= 16 ? launch<F32, 64, 2>(a, ws, st) : launch<F32, 64, 4>(a, ws, st);
-    if (D <= 128)
-        return rows <= 8 ? launch<F32, 128, 1>(a, ws, st)
-                         : rows <= 16 ? launch<F32, 128, 2>(a, ws, st) : launch<F32, 128, 4>(a, ws, st);
-    return rows <= 8 ? launch<F32, 256, 1>(a, ws, st) : launch<F32, 256, 2>(a, ws, st);
+    return D <= 64 ? by_rows<F32, 64>(a, ws, st) : D <= 128 ? by_rows<F32, 128>(a, ws, st) : by_rows<F32, 256>(a, ws, st);
 }
 
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {

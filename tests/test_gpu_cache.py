@@ -524,3 +524,32 @@ def test_prompts_converted_once_or_in_place_give_the_same_bits():
         assert cache.status() == mlora.MLORA_OK
     for k in (2, 4):
         assert torch.equal(outs[0], outs[k]) and torch.equal(outs[1], outs[k + 1])
+
+
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,window", [
+    ([20], [3000], 1, 1, 128, 64, 0),                          # few row tiles: their tokens in parts
+    ([40, 3], [2000, 700], 1, 4, 64, 16, 0),
+    ([20, 20, 1], [1100, 20, 0], 2, 2, 256, 32, 0),
+    ([300], [2000], 1, 1, 256, 128, 500),
+    ([5], [5000], 1, 8, 192, 48, 0),
+    ([70], [4500], 1, 2, 80, 64, 3000),
+    ([33], [40], 1, 1, 160, 16, 0),
+])
+@pytest.mark.parametrize("room", [256 << 20, 0])
+def test_prompts_in_parts_and_wide_heads(rows, lengths, H, G, D, ps, window, room):
+    u = Setup(lengths, H, D, ps, Hq=H * G, seed=29)
+    u.cache = Cache(*u.dev, H * G, prompt_bytes=room)
+    first = check_attend(u, rows, "bf16", window)
+    assert torch.equal(first, check_attend(u, rows, "bf16", window))
+
+
+def test_growing_scores_move_the_bound():
+    """Keys that grow along the sequence: the softmax bound moves in the middle of it, for some
+    rows and not for others."""
+    for rows, lengths, G in (([1], [4000], 2), ([150], [1000], 2), ([20], [3000], 1)):
+        u = Setup(lengths, 1, 128, 64, Hq=G, seed=30, k_size=0.02)
+        for j in range(u.table.shape[1]):
+            u.ks[u.table[0, j]] *= F(1.25 ** min(j, 30))
+        u.upload()
+        check_attend(u, rows, "bf16", q_size=2.0)
+        check_attend(u, rows, "f32", q_size=2.0)
