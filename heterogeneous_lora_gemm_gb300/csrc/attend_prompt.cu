@@ -66,7 +66,7 @@ struct PShape {
     static constexpr int BLK = DP / 64;                 // 64-element column blocks (128-byte rows)
     static constexpr int QOPER = BLK * TILE * 128;      // bytes of a Q operand tile
     static constexpr int OPER = BLK * KT * 128;         // of a K or V operand tile
-    static constexpr int SMEM = 1024 + TILES * QOPER + 4 * OPER + 768;
+    static constexpr int SMEM = 1024 + TILES * QOPER + 4 * OPER + 2048;
     static constexpr int PIECES = KT / 16;              // of 16 tokens; a conversion warp (or two, half
     static constexpr int WARP_BLK = BLK * PIECES / CONV;   // the blocks each) per piece
     static_assert(PROMPT_SLOT >= ROWS * (DP + 2), "workspace slot");
@@ -75,11 +75,12 @@ struct PShape {
 struct PTail {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
     uint64_t scfull[4], sfull[2][2], pfull[2][2], odone[2][2], qfull[2], alldone[2];   // [tile][S buffer]
+    float qf[2][TILE];                // per row: scale log2 e over the query's power of two
     float scales[4][24];              // of a token tile's 16-token pieces: ks, log2 vs, 1 / vs (8 each)
     uint32_t tmem;
     int abort_flag, last;
 };
-static_assert(sizeof(PTail) <= 768, "barriers and scales");
+static_assert(sizeof(PTail) <= 2048, "barriers, scales and row factors");
 
 // mbar_wait (tc_ptx.cuh) that sleeps: the waiting warps share issue slots with the busy ones.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
@@ -528,48 +529,76 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const int t = warp >> 2, q4 = warp & 3;
         const int rl = q4 * 32 + lane, r = r0 + t * TILE + rl;
         const bool live = r < R;
-        // the query: fp16 scaled by a power of two, NaN statistics for a row that is not finite
-        float qf = 0.f;
-        if (Sh::TILES == 2 || t == 0) {
-            const int rq = live ? r : r0;
-            const __nv_bfloat16* q = (const __nv_bfloat16*)a.q.ptr + (int64_t)(s.row0 + rq / G) * a.q.row +
-                                     (int64_t)(h * G + rq % G) * a.q.head;
-            auto load = [&](int i) {
-                return live && i * 8 < D ? *reinterpret_cast<const uint4*>(q + i * 8) : make_uint4(0u, 0u, 0u, 0u);
-            };
-            float top = 0.f;
-            bool fine = true;
-#pragma unroll 4
-            for (int i = 0; i < DP / 8; ++i) {
-                const uint4 w = load(i);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = fabsf(__uint_as_float(u[e] << 16)), y = fabsf(__uint_as_float(u[e] & 0xFFFF0000u));
-                    fine &= x <= 3.402823466e38f && y <= 3.402823466e38f;
-                    top = fmaxf(top, fmaxf(x, y));
-                }
+        // A warp's 32 rows lie 16 bytes to a lane: row and 16-byte chunk of its k-th access (of CH)
+        constexpr int CH = DP / 8, PER = CH < 32 ? 32 / CH : 1;   // chunks per row, rows at a time
+        auto row_at = [&](int k) { return q4 * 32 + k * PER + lane / CH; };
+        const int chunk = lane % CH;
+        auto place = [&](int row) {   // of the lane's chunk in tile t of the queries
+            return qs + t * Sh::QOPER + chunk / 8 * (TILE * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        };
+        // the chunk's address in rows with the given strides, and from access k to the next
+        const int rr0 = r0 + t * TILE + row_at(0), tok0 = quotient(a.group, rr0), g0 = rr0 - tok0 * G;
+        const int per_tok = quotient(a.group, PER), per_g = PER - per_tok * G;
+        struct Walk {
+            int64_t at, step, wrap;
+            int g;
+        };
+        auto walk = [&](int64_t row, int64_t head) {
+            return Walk{(int64_t)(s.row0 + tok0) * row + (int64_t)(h * G + g0) * head + chunk * 8, per_tok * row + per_g * head,
+                        row - G * head, g0};
+        };
+        auto advance_row = [&](Walk& v) {
+            v.at += v.step;
+            v.g += per_g;
+            if (v.g >= G) {
+                v.g -= G;
+                v.at += v.wrap;
             }
-            const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 127) : 0;
-            const float down = __uint_as_float((uint32_t)(127 - min(k, 126)) << 23) * (k > 126 ? 0.5f : 1.f);
-            qf = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
-#pragma unroll 4
-            for (int i = 0; i < DP / 8; ++i) {
-                const uint4 w = load(i);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                uint32_t v[4];
+        };
+        auto there = [&](int k) { return rr0 + k * PER < R && chunk * 8 < D; };
+        // the queries: fp16 scaled by a power of two per row, NaN statistics for a row that is not finite
+        if (Sh::TILES == 2 || t == 0) {
+            constexpr int BATCH = 16 < 32 / PER ? 16 : 32 / PER;   // rows' loads in flight
+            Walk at = walk(a.q.row, a.q.head);
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32 / PER; k0 += BATCH) {
+                uint4 w[BATCH];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 p = __floats2half2_rn(__uint_as_float(u[e] << 16) * down,
-                                                        __uint_as_float(u[e] & 0xFFFF0000u) * down);
-                    v[e] = fine ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
+                for (int k = 0; k < BATCH; ++k) {
+                    w[k] = there(k0 + k) ? *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q.ptr + at.at)
+                                         : make_uint4(0u, 0u, 0u, 0u);
+                    advance_row(at);
                 }
-                *reinterpret_cast<uint4*>(qs + t * Sh::QOPER + i / 8 * (TILE * 128) + rl * 128 + (((i & 7) ^ (rl & 7)) << 4)) =
-                    make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    uint32_t top = 0u;   // largest |bits| of the row, as two 16-bit halves (ordered like the values)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, u[e] & 0x7FFF7FFFu);
+#pragma unroll
+                    for (int d = 1; d < CH; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
+                    top = max(top >> 16, top & 0xFFFFu);
+                    const bool fine = top < 0x7F80u;
+                    const int x = fine ? min(max((int)(top >> 7) - 126, -100), 127) : 0;
+                    const float down = __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f);
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 p = __floats2half2_rn(__uint_as_float(u[e] << 16) * down,
+                                                            __uint_as_float(u[e] & 0xFFFF0000u) * down);
+                        v[e] = fine ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
+                    }
+                    const int row = row_at(k0 + k);
+                    *reinterpret_cast<uint4*>(place(row)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (chunk == 0)
+                        tl.qf[t][row] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(&tl.qfull[t]);
         }
+        __syncwarp();
+        const float qf = tl.qf[t][rl];
         const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t sbase = lane_base + t * TILE, obase = lane_base + 256 + t * TILE;
         const int hi = s.start + r / G + 1, lo = a.window > 0 ? hi - a.window : 0;   // tokens [lo, hi) are seen
@@ -580,17 +609,28 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         float m = NO_MAX;
         uint64_t l2 = pair(0.f, 0.f);
         bool ok = true;
-        // 32 elements of the row, from the q-th on, times f
+        // 32 elements of the row, from 32 q on, times f, into the queries' place (the products that read
+        // it are complete), and the warp's rows from there
         auto put32 = [&](const uint32_t (&x)[32], float f, int q) {
-            __nv_bfloat16* o = (__nv_bfloat16*)a.o.ptr + (int64_t)(s.row0 + r / G) * a.o.row + (int64_t)(h * G + r % G) * a.o.head;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
-                if (q * 32 + e >= D) continue;
                 uint32_t y[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
                     y[z] = bf2_of(__uint_as_float(x[e + 2 * z]) * f, __uint_as_float(x[e + 2 * z + 1]) * f);
-                *reinterpret_cast<uint4*>(o + q * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                const int ch = q * 4 + e / 8;
+                *reinterpret_cast<uint4*>(qs + t * Sh::QOPER + ch / 8 * (TILE * 128) + rl * 128 + (((ch & 7) ^ (rl & 7)) << 4)) =
+                    make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        };
+        auto put_rows = [&]() {
+            __syncwarp();
+            Walk at = walk(a.o.row, a.o.head);
+#pragma unroll 4
+            for (int k = 0; k < 32 / PER; ++k) {
+                const uint4 y = *reinterpret_cast<const uint4*>(place(row_at(k)));
+                if (there(k)) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o.ptr + at.at) = y;
+                advance_row(at);
             }
         };
         // the row in its part's slot: O as [DP / 4][256 rows] of 16 bytes, then m and l
@@ -664,16 +704,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0u;
                 }
-                if (!live) continue;
-                if (parts > 1) {
+                if (parts == 1) put32(x, inv, q);
+                else if (live)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         mine[(q * 8 + e / 4) * Sh::ROWS] = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                } else {
-                    put32(x, inv, q);
-                }
             }
-            if (parts > 1 && live) {
+            if (parts == 1) put_rows();
+            else if (live) {
                 ml[0] = m;
                 ml[Sh::ROWS] = l;
             }
@@ -689,7 +727,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 if (tl.last) counters[item] = 0;
             }
             soft_sync();
-            if (tl.last && live) {
+            if (tl.last && (t == 0 || two)) {   // (a dead row's slot holds what it holds: nothing of it is stored)
                 const size_t next = PROMPT_SLOT / 4;   // from a part to the next, in 16 bytes
                 const uint4* first4 = mine - part * next;
                 const float* first_ml = ml - (size_t)part * PROMPT_SLOT;
@@ -722,6 +760,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                     for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e]);
                     put32(x, inv, q);
                 }
+                put_rows();
             }
         }
     } else if (warp < SOFT + CONV && pre) {
