@@ -9,11 +9,10 @@
 // Rows are (query token, query head of the group) pairs of one key/value head, 256 per CTA as
 // two tiles of 128: a converted key/value tile serves both.
 //
-// Products run on tcgen05.mma, 128 rows x 64 tokens a step: S = Q K^T in fp16 (codes exact,
-// queries below 1 after a power of two per row), O += P V in bf16 with P = 2^(x - m) vs
-// (one rounding) from tensor memory.  Tensor memory, all 512 columns: two S of 64 columns
-// per tile, so that a step's scores are ready before the last step's weights are done (P
-// lies over its S), and O of the two tiles.
+// Products run on tcgen05.mma in bf16, 128 rows x 64 tokens a step: S = Q K^T (queries and
+// codes exact), O += P V with P = 2^(x - m) vs (one rounding) from tensor memory.  Tensor
+// memory, all 512 columns: two S of 64 columns per tile, so that a step's scores are ready
+// before the last step's weights are done (P lies over its S), and O of the two tiles.
 //
 // Conversion: a sequence of several row tiles has its codes converted once, by a kernel
 // before, into operand tiles (as they lie in shared memory) in the handle's workspace, which
@@ -30,7 +29,6 @@
 // tokens' codes on their way in registers, 16 and 17 issue the products of tile 0 and 1 (one
 // warp's waits would outlast both tiles' products).
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include <climits>
 
@@ -234,29 +232,27 @@ __device__ __forceinline__ uint32_t bf2_of(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 4 codes of a word as fp16 or bf16 (two words); see attend_split.cu
-__device__ __forceinline__ uint32_t minus1152(uint32_t u) {
-    const __half2 h = __hsub2(*reinterpret_cast<__half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
+// 4 codes of a word as bf16 (two words); see attend_split.cu
 __device__ __forceinline__ uint32_t bf16_codes(uint32_t u) {
     const uint32_t a = u & 0xFF7FFF7Fu, b = u & 0xFF80FF80u;
     const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <bool BF>
 __device__ __forceinline__ uint2 widen(uint32_t w) {
-    if (BF) return make_uint2(bf16_codes(__byte_perm(w, 0x43434343u, 0x4140)), bf16_codes(__byte_perm(w, 0x43434343u, 0x4342)));
-    w ^= 0x80808080u;
-    return make_uint2(minus1152(__byte_perm(w, 0x64646464u, 0x4140)), minus1152(__byte_perm(w, 0x64646464u, 0x4342)));
+    return make_uint2(bf16_codes(__byte_perm(w, 0x43434343u, 0x4140)), bf16_codes(__byte_perm(w, 0x43434343u, 0x4342)));
 }
+// 16 bytes of global memory (zeros where `in` is false) into shared memory
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // 16 codes of token t, elements 16 c .. of 64-element block blk, into an operand tile: DP / 64
 // blocks of KT rows of 128 bytes under the 128-byte swizzle.  (Lanes pair token t with t ^ 5,
 // so that the writes of a quarter warp, at (2 c + z) ^ t, do not meet in a bank.)
-template <bool BF, int KT>
+template <int KT>
 __device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk, int c) {
-    const uint2 a = widen<BF>(x.x), b = widen<BF>(x.y), d = widen<BF>(x.z), e = widen<BF>(x.w);
+    const uint2 a = widen(x.x), b = widen(x.y), d = widen(x.z), e = widen(x.w);
     uint8_t* row = dst + blk * (KT * 128) + t * 128;
     *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
     *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
@@ -367,12 +363,11 @@ struct Piece {
         for (int u = 0; u < N; ++u) x[u] = make_uint4(0u, 0u, 0u, 0u);
     }
     // into operand tile `dst` (generic address)
-    template <bool BF>
     __device__ __forceinline__ void store(uint8_t* dst, int w, int lane) const {
         const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), b0 = blk0(w);
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            convert16<BF, Sh::KT>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4);
+            convert16<Sh::KT>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4);
     }
 };
 // Scales of 16 tokens as the softmax takes them (see the top of the file).
@@ -436,8 +431,8 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
         k.load(c.k_codes, c, id, h, place, warp, lane);
         v.load(c.v_codes, c, id, h, place, warp, lane);
         if (vs == 0.f) v.zero();
-        k.template store<false>(to, warp, lane);
-        v.template store<true>(to + Sh::OPER, warp, lane);
+        k.store(to, warp, lane);
+        v.store(to + Sh::OPER, warp, lane);
         if (lane == 0 && warp < Sh::PIECES)
             put_scales(reinterpret_cast<float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24, warp, ks, vs);
     }
@@ -556,42 +551,48 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             }
         };
         auto there = [&](int k) { return rr0 + k * PER < R && chunk * 8 < D; };
-        // the queries: fp16 scaled by a power of two per row, NaN statistics for a row that is not finite
+        // the queries as they are, but a row outside 2^+-64 brought below 1 by a power of two, and one
+        // that is not finite zeros under NaN statistics
+        tl.qf[t][rl] = a.scale * 1.4426950408889634f;
         if (Sh::TILES == 2 || t == 0) {
-            constexpr int BATCH = 16 < 32 / PER ? 16 : 32 / PER;   // rows' loads in flight
             Walk at = walk(a.q.row, a.q.head);
+#pragma unroll 4
+            for (int k = 0; k < 32 / PER; ++k) {
+                const bool in = there(k);   // (zeros elsewhere)
+                cp_async16_or_zero(smem_u32(place(row_at(k))), (const __nv_bfloat16*)a.q.ptr + (in ? at.at : 0), in);
+                advance_row(at);
+            }
+            cp_async_wait_all();
+            __syncwarp();
+            // largest |bits| of a chunk (ordered like the values)
+            auto top_of = [](const uint4& w) {
+                const uint32_t u = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                            __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+                return max(u >> 16, u & 0xFFFFu);
+            };
+            bool wild = false;
+#pragma unroll 4
+            for (int k = 0; k < 32 / PER; ++k) {
+                const uint32_t top = top_of(*reinterpret_cast<const uint4*>(place(row_at(k))));
+                wild |= top != 0u && (top >> 7) - 63u > 128u;
+            }
+            if (__any_sync(~0u, wild)) {
 #pragma unroll 1
-            for (int k0 = 0; k0 < 32 / PER; k0 += BATCH) {
-                uint4 w[BATCH];
+                for (int k = 0; k < 32 / PER; ++k) {
+                    uint4* to = reinterpret_cast<uint4*>(place(row_at(k)));
+                    const uint4 w = *to;
+                    uint32_t top = top_of(w);
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    w[k] = there(k0 + k) ? *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q.ptr + at.at)
-                                         : make_uint4(0u, 0u, 0u, 0u);
-                    advance_row(at);
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                    uint32_t top = 0u;   // largest |bits| of the row, as two 16-bit halves (ordered like the values)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, u[e] & 0x7FFF7FFFu);
-#pragma unroll
-                    for (int d = 1; d < CH; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
-                    top = max(top >> 16, top & 0xFFFFu);
+                    for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
                     const bool fine = top < 0x7F80u;
                     const int x = fine ? min(max((int)(top >> 7) - 126, -100), 127) : 0;
-                    const float down = __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f);
-                    uint32_t v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 p = __floats2half2_rn(__uint_as_float(u[e] << 16) * down,
-                                                            __uint_as_float(u[e] & 0xFFFF0000u) * down);
-                        v[e] = fine ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
-                    }
-                    const int row = row_at(k0 + k);
-                    *reinterpret_cast<uint4*>(place(row)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    const float down = fine ? __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f) : 0.f;
+                    auto scaled = [&](uint32_t u) {
+                        return fine ? bf2_of(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down) : 0u;
+                    };
+                    *to = make_uint4(scaled(w.x), scaled(w.y), scaled(w.z), scaled(w.w));
                     if (chunk == 0)
-                        tl.qf[t][row] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                        tl.qf[t][row_at(k)] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
                 }
             }
             fence_proxy_async_smem();
@@ -827,13 +828,13 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 put_scales(tl.scales[j & 3], w, ks, vs);
                 mbar_arrive(&tl.scfull[j & 3]);
             }
-            k.template store<false>(kb + (j & 1) * Sh::OPER, w, lane);
+            k.store(kb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.kfull[j & 1]);
             k.load(c.k_codes, c, id, h, place, w, lane);
             if (!wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
             if (vs == 0.f) v.zero();
-            v.template store<true>(vb + (j & 1) * Sh::OPER, w, lane);
+            v.store(vb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.vfull[j & 1]);
             v.load(c.v_codes, c, id, h, place, w, lane);
@@ -845,8 +846,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     } else if (steps > 0 && (warp == SOFT + CONV || (two && warp == SOFT + CONV + 1))) {
         // ---- products of a tile: a step's scores go ahead of the last step's weights
         const int t = warp - SOFT - CONV;
-        const uint32_t idesc_s = (1u << 4) | ((uint32_t)(STEP >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);   // fp16
-        const uint32_t idesc_o = idesc_bf16(TILE, DP) | (1u << 16);                                           // B column-major
+        const uint32_t idesc_s = idesc_bf16(TILE, STEP), idesc_o = idesc_bf16(TILE, DP) | (1u << 16);   // (O: B column-major)
         const uint64_t dq = sdesc(smem_u32(qs + t * Sh::QOPER), 1024, SW128), dk = sdesc(smem_u32(kb), 1024, SW128),
                        dv = sdesc_lbo(smem_u32(vb), KT * 128, 1024, SW128);
         const uint32_t tm = tmem + t * TILE;
