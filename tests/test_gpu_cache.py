@@ -287,6 +287,17 @@ def test_attend_over_sizes_of_queries_and_keys(rows, lengths, q_size, k_size, dt
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size,others", [(1e30, 1.0), (1e-30, 1e-36), (1e-30, 0.0)])
+@pytest.mark.parametrize("rows,lengths,D", [([1, 1, 1], [300, 64, 90], 128), ([131, 30], [200, 30], 128), ([40], [90], 64)])
+def test_attend_over_unequal_query_rows(rows, lengths, D, size, others, dtype):
+    """Every third row far outside the range of the rest, with keys that bring its scores to 1."""
+    u = Setup(lengths, 1, D, 64, Hq=2, seed=25, k_size=1.0 / size)
+    q = np.random.default_rng(26).standard_normal((sum(rows), 2, D)).astype(F) * F(others)
+    q[::3] = (np.random.default_rng(27).standard_normal(q[::3].shape) * size).astype(F)
+    check_attend(u, rows, dtype, q=q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,lengths", [([1, 1], [520, 64]), ([130], [450])])
 def test_attend_over_unequal_value_blocks(rows, lengths, dtype):
     """Scales of value blocks over twelve decades, among them zeros."""
