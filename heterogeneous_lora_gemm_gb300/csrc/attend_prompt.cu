@@ -111,6 +111,15 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// whether the phase is complete, without a wait
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -232,6 +241,12 @@ __device__ __forceinline__ uint32_t bf2_of(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// the halves of a bf16 pair onto two fp32 sums
+__device__ __forceinline__ void add_bf16(float& a, float& b, uint32_t w) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.rn.f32.bf16 %0, l, %0;\n add.rn.f32.bf16 %1, h, %1;\n}"
+        : "+f"(a), "+f"(b)
+        : "r"(w));
+}
 // 4 codes of a word as bf16 (two words); see attend_split.cu
 __device__ __forceinline__ uint32_t bf16_codes(uint32_t u) {
     const uint32_t a = u & 0xFF7FFF7Fu, b = u & 0xFF80FF80u;
@@ -315,7 +330,7 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     for (int g = 0; g < STEP / PG; ++g) {
         const float f = qf * sc[g * (PG / 16)], c = sc[8 + g * (PG / 16)] - m, v = sc[16 + g * (PG / 16)];
         const uint64_t f2 = pair(f, f), c2 = pair(c, c);
-        uint64_t l[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < PG; k += 32) {
             const uint32_t seen = EDGE ? column_mask(lo - g * PG - k, hi - g * PG - k) : 0u;
@@ -329,11 +344,11 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
                     p1 = seen >> (e + 1) & 1 ? p1 : 0.f;
                 }
                 const uint32_t w = bf2_of(p0, p1);
-                l[e / 2 & 1] = add2(l[e / 2 & 1], pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)));
+                add_bf16(l[e & 2], l[(e & 2) + 1], w);
                 y[i / 2] = w;
             }
         }
-        sum = fma2(add2(l[0], l[1]), pair(v, v), sum);
+        sum = fma2(add2(pair(l[0], l[1]), pair(l[2], l[3])), pair(v, v), sum);
     }
     return sum;
 }
@@ -640,8 +655,10 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         float* ml = slot + DP * Sh::ROWS + t * TILE + rl;
         if (t == 0 || two) {
             for (int i = 0; i < steps; ++i) {
+                // (the look at the scales' barrier is under way during the wait for the scores)
+                const bool scales = i % SPT != 0 || mbar_done(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1);
                 ok = wait_for(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
-                if (i % SPT == 0) ok = ok && wait_for(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1, abort_flag, a.status);
+                if (!scales) ok = ok && wait_for(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1, abort_flag, a.status);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -650,10 +667,22 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 const bool edge = t0 + STEP > hi_min || t0 < lo_max;
                 const uint32_t sat = sbase + (i & 1) * STEP;
                 uint32_t y[STEP];
-                float2 sum;
-                // first with the bound so far, which usually holds; else the bound moves
-                bool above = true;
-                for (bool move = i == 0;; move = true) {
+                // P over the scores
+                auto put_weights = [&](float2 sum) {
+                    l2 = add2(l2, pair(sum.x, sum.y));
+                    tmem_st32(sat, y);
+                    tmem_wait_st();
+                };
+                // with the bound so far, which usually holds; else the bound moves.  The usual step has a
+                // path of its own: joined with the other's, it took 70 moves of registers (5% of the time).
+                bool above = true, done = false;
+                if (!edge && i > 0) {
+                    const float2 sum = unpair(weigh<false, PG>(sat, sc, qf, m, 0, 0, y));
+                    above = sum.x + sum.y > MOST;
+                    done = !__any_sync(~0u, above);
+                    if (done) put_weights(sum);
+                }
+                for (bool move = !edge || i == 0; !done; move = true) {
                     if (move) {
                         const float mx = row_max(sat, sc, qf, lo - t0, hi - t0);
                         const float now = above ? fmaxf(mx, m) : m, f = ex2(m - now);
@@ -677,15 +706,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                             }
                         }
                     }
-                    sum = unpair(edge ? weigh<true, PG>(sat, sc, qf, m, lo - t0, hi - t0, y)
-                                      : weigh<false, PG>(sat, sc, qf, m, 0, 0, y));
+                    const float2 sum = unpair(weigh<true, PG>(sat, sc, qf, m, lo - t0, hi - t0, y));
                     above = sum.x + sum.y > MOST;
-                    if (move || !__any_sync(~0u, above)) break;
+                    done = move || !__any_sync(~0u, above);
+                    if (done) put_weights(sum);
                 }
                 if (!ok) break;
-                l2 = add2(l2, pair(sum.x, sum.y));
-                tmem_st32(sat, y);   // over the scores
-                tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&tl.pfull[t][i & 1]);
             }
