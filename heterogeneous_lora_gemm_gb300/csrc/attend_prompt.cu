@@ -80,29 +80,6 @@ struct PTail {
 };
 static_assert(sizeof(PTail) <= 2048, "barriers, scales and row factors");
 
-// mbar_wait (tc_ptx.cuh) that sleeps: the waiting warps share issue slots with the busy ones.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-    auto sleep_wait = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)   // ns
-            : "memory");
-        return ok != 0;
-    };
-    if (sleep_wait()) return true;
-    const long long t0 = clock64();
-    while (!sleep_wait()) {
-        if (*abort_flag) return false;
-        if (clock64() - t0 > WAIT_LIMIT) {
-            *abort_flag = 1;
-            atomicOr(status, STATUS_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -330,7 +307,7 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     for (int g = 0; g < STEP / PG; ++g) {
         const float f = qf * sc[g * (PG / 16)], c = sc[8 + g * (PG / 16)] - m, v = sc[16 + g * (PG / 16)];
         const uint64_t f2 = pair(f, f), c2 = pair(c, c);
-        float l[4] = {0.f, 0.f, 0.f, 0.f};
+        float l[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < PG; k += 32) {
             const uint32_t seen = EDGE ? column_mask(lo - g * PG - k, hi - g * PG - k) : 0u;
@@ -344,11 +321,11 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
                     p1 = seen >> (e + 1) & 1 ? p1 : 0.f;
                 }
                 const uint32_t w = bf2_of(p0, p1);
-                add_bf16(l[e & 2], l[(e & 2) + 1], w);
+                add_bf16(l[0], l[1], w);
                 y[i / 2] = w;
             }
         }
-        sum = fma2(add2(pair(l[0], l[1]), pair(l[2], l[3])), pair(v, v), sum);
+        sum = fma2(pair(l[0], l[1]), pair(v, v), sum);
     }
     return sum;
 }
@@ -657,8 +634,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             for (int i = 0; i < steps; ++i) {
                 // (the look at the scales' barrier is under way during the wait for the scores)
                 const bool scales = i % SPT != 0 || mbar_done(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1);
-                ok = wait_for(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
-                if (!scales) ok = ok && wait_for(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1, abort_flag, a.status);
+                ok = mbar_wait(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
+                if (!scales) ok = ok && mbar_wait(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1, abort_flag, a.status);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -691,7 +668,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                         if (i > 0) {
                             // O, once the last step's product is complete (the one before it is: these
                             // scores came after it, so the barrier is at this phase or past it)
-                            ok = __all_sync(~0u, wait_for(&tl.odone[t][(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, a.status));
+                            ok = __all_sync(~0u, mbar_wait(&tl.odone[t][(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, a.status));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -715,7 +692,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 tc_fence_before();
                 mbar_arrive(&tl.pfull[t][i & 1]);
             }
-            if (ok && steps > 0) ok = wait_for(&tl.odone[t][(steps - 1) & 1], ((steps - 1) >> 1) & 1, abort_flag, a.status);
+            if (ok && steps > 0) ok = mbar_wait(&tl.odone[t][(steps - 1) & 1], ((steps - 1) >> 1) & 1, abort_flag, a.status);
             __syncwarp();
             tc_fence_after();
             const float2 ls = unpair(l2);
@@ -800,7 +777,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 const uint8_t* from = operands + slot * 2 * Sh::OPER;
                 const float* scales = reinterpret_cast<const float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24;
                 const float sc = lane < 24 ? scales[lane] : 0.f;
-                if (!__all_sync(~0u, wait_for(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status))) break;
+                if (!__all_sync(~0u, mbar_wait(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status))) break;
                 if (lane < 24) tl.scales[j & 3][lane] = sc;
                 __syncwarp();
                 if (lane == 0) {
@@ -809,7 +786,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                     bulk_g2s(kb + (j & 1) * Sh::OPER, from, Sh::OPER, &tl.kfull[j & 1]);
                 }
                 done = 2 * j + 1;
-                if (!__all_sync(~0u, wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status))) break;
+                if (!__all_sync(~0u, mbar_wait(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status))) break;
                 if (lane == 0) {
                     mbar_expect_tx(&tl.vfull[j & 1], Sh::OPER);
                     bulk_g2s(vb + (j & 1) * Sh::OPER, from + Sh::OPER, Sh::OPER, &tl.vfull[j & 1]);
@@ -849,7 +826,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         id = next_id();
         for (int j = 0; j < nt; ++j) {
             const uint32_t use = (j >> 1) & 1;
-            if (!wait_for(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status)) break;
+            if (!mbar_wait(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status)) break;
             if (lane == 0 && (Sh::PIECES == CONV || w < Sh::PIECES)) {
                 put_scales(tl.scales[j & 3], w, ks, vs);
                 mbar_arrive(&tl.scfull[j & 3]);
@@ -858,7 +835,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             fence_proxy_async_smem();
             mbar_arrive(&tl.kfull[j & 1]);
             k.load(c.k_codes, c, id, h, place, w, lane);
-            if (!wait_for(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
+            if (!mbar_wait(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
             if (vs == 0.f) v.zero();
             v.store(vb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
@@ -880,7 +857,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         auto half_of = [](int i) { return (uint64_t)((i / SPT & 1) * (Sh::OPER >> 4) + i % SPT * (STEP * 128 >> 4)); };
         auto ends = [&](int i) { return i % SPT == SPT - 1 || i + 1 == steps; };   // step i is its token tile's last
         auto wait = [&](uint64_t* bar, int parity) {
-            return __all_sync(~0u, wait_for(bar, parity, abort_flag, a.status));
+            return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, a.status));
         };
         auto scores = [&](int i) {
             product_ss<DP / 16, KT>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
