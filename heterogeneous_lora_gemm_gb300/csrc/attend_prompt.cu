@@ -7,25 +7,39 @@
 // row's largest x when it was last set; a step whose weights sum to more than 2^14 sets it
 // again (no maximum is taken otherwise; bf16 and fp32 hold weights above 1 as well as below).
 // Rows are (query token, query head of the group) pairs of one key/value head, 256 per CTA as
-// two tiles of 128: a converted key/value tile serves both.
+// two tiles of 128 (one, where heads have more than 128 elements): a converted key/value tile
+// serves both.
 //
 // Products run on tcgen05.mma in bf16, 128 rows x 64 tokens a step: S = Q K^T (queries and
 // codes exact), O += P V with P = 2^(x - m) vs (one rounding) from tensor memory.  Tensor
 // memory, all 512 columns: two S of 64 columns per tile, so that a step's scores are ready
-// before the last step's weights are done (P lies over its S), and O of the two tiles.
+// before the last step's weights are done (P lies over its S), and O of the two tiles (or of
+// one, of up to 256 columns).
+//
+// Bound: the products, 2 x 2 x 128 x 64 x head_dim operations per tile and step.  8192 tokens of
+// 32/8 heads of 128 take 376 us, 1460 TFLOP/s; 4096 take 122 us, 1120 TFLOP/s (the tensor pipe is
+// busy 61% of the time, the issue slots of the softmax warps half of it).  A step takes 1500
+// cycles, of which the products could do with 1280: half of the exponentials or half of the
+// products left out changes it by 2%, the weights' sum left out by 6%: what counts is a softmax
+// warp's own chain of some 300 instructions.  A row tile's start and end take 9000 cycles.
+//
+// What measured slower (8192 tokens): scores of 128 tokens a product, without a second buffer
+// (487 us); two threads per row (423); the sums by mma.sync (570); one arrival per warp (396);
+// the tiles' products in turns (426); waits that sleep (389).
 //
 // Conversion: a sequence of several row tiles has its codes converted once, by a kernel
 // before, into operand tiles (as they lie in shared memory) in the handle's workspace, which
 // the attention copies in bulk; converted per row tile the work takes half of the issue slots.
 // A sequence of one row tile, or one for which the workspace has no room left, is converted
-// inside the attention.
+// inside the attention (8192 tokens: 496 us against 572 at the time).
 //
 // Where row tiles are fewer than half the SMs, each one's tokens are cut into equal parts, a CTA
-// each; the CTA that finishes a row tile last joins the parts, in their order.
+// each; the CTA that finishes a row tile last joins the parts, in their order (300 tokens after
+// 5000 of one sequence: 49 us).
 //
 // Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
-// operand tiles or 8-15 read codes and convert them into fp16 keys (rows of head elements) and bf16 values (tokens as
-// rows: the product reads them column-major), a warp per 16 tokens of 128 with the next 128
+// operand tiles or 8-15 read codes and convert them into keys and values in bf16 (tokens as rows; the
+// second product reads them column-major), a warp per 16 tokens of 128 with the next 128
 // tokens' codes on their way in registers, 16 and 17 issue the products of tile 0 and 1 (one
 // warp's waits would outlast both tiles' products).
 #include <cuda_bf16.h>
@@ -293,7 +307,7 @@ __device__ __forceinline__ float row_max(uint32_t sat, const float* sc, float qf
 // Weights of a row's 64 scores: times the value scales into y[0, 32) (bf16 pairs); returns
 // the sum of what was rounded (without the value scales), so that a heavy token's rounding is
 // divided out again.  PG tokens share their scales: 16, or 64 where pages are multiples of it
-// (8192 tokens, 32/8 heads, pages of 64: 466 us with PG 64, 474 us with PG 16).
+// (8192 tokens, 32/8 heads, pages of 64: 466 us with PG 64, 474 us with PG 16, when measured).
 template <bool EDGE, int PG>
 __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float qf, float m, int lo, int hi,
                                           uint32_t (&y)[STEP]) {
@@ -955,9 +969,9 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
     return c.dim <= 64 ? operand_bytes<64>(c, tokens) : c.dim <= 128 ? operand_bytes<128>(c, tokens) : operand_bytes<256>(c, tokens);
 }
 
-// From 17 rows of a sequence and head on: at 6 tokens of 32/8 heads after 4000 tokens, 1, 16 and
-// 64 sequences take 32, 64 and 139 us here and 37, 75 and 135 us in attend_split.cu; at 4 tokens
-// 31, 64 and 138 us against 20, 49 and 83 us.
+// From 17 rows of a sequence and head on: at 6 tokens of 32/8 heads after 4000 tokens (2000
+// where they are 64 sequences), 1, 16 and 64 sequences take 25, 60 and 127 us here and 22, 79 and
+// 145 us in attend_split.cu; at 4 tokens 25, 61 and 127 us against 22, 48 and 83 us.
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return bf16 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }

@@ -18,7 +18,10 @@
 // under the codes' stream).  fp32 rows run the same products with the query as the sum of two
 // fp16 terms (22 bits) and the weights as three bf16 terms (24 bits).
 //
-// Bound: HBM (the codes are read once per row tile).  Each warp streams 32-token chunks
+// Bound: HBM (the codes are read once per row tile): 32 sequences of 32k tokens, 32/8 heads of
+// 128, bf16, take 331 us, 6.4 TB/s; 4 sequences 150 us, 5.9 TB/s; 32 of 3 to 4k with as many key
+// heads as query heads 83 us, 5.1 TB/s; one short sequence 9.7 us, the chain of a CTA's start, a
+// range's loads and the join.  Each warp streams 32-token chunks
 // of its own through a private ring of TMA copies: no CTA-wide barrier in the loop.
 // Work split: all (sequence, row tile, head) items' tokens in one line, cut into equal
 // ranges, one per resident CTA; every CTA finds its range from the lengths.  An item is as

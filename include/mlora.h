@@ -457,9 +457,10 @@ typedef struct mlora_cache* mlora_cache_t;
  *   page_size  tokens per page: 16, 32, 48, ... 256
  *   head_dim   16, 32, 48, ... 256;  q_heads  a multiple of kv_heads, <= 32767
  *   prompt_bytes  device memory for prompts' keys and values in 16 bits (4 bytes per
- *              token, head and element, head_dim rounded up to 64 or 128), at most what
- *              all pages' tokens take; attend converts a long prompt's codes once into it
- *              where they fit, and again for every 256 rows where they do not (0: always)
+ *              token, head and element, head_dim rounded up to 64, 128 or 256), at most
+ *              what all pages' tokens take; attend converts a long prompt's codes once into
+ *              it where they fit, and where they do not again for every 256 rows (128 where
+ *              head_dim > 128; 0: always)
  * The handle allocates its workspace (a status word, the partial results of split
  * sequences, about 20 MB, and prompt_bytes) here; append, read and attend allocate nothing.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),
@@ -498,9 +499,9 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  *   O[i, h] = sum_j p_j v_j,  p = softmax_j(scale * Q[i, h] . k_j)
  * over the tokens j of the row's sequence with j <= pos(i), and j > pos(i) - window
  * where window > 0; query head h reads key/value head h / (q_heads / kv_heads).  A row
- * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums and softmax statistics are fp32; O is rounded
- * once.  O must not overlap Q.
- * Errors: INVALID_ARG, CUDA.
+ * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums
+ * and softmax statistics are fp32; O is rounded once.  O must not overlap Q.
+ * Errors: INVALID_ARG, UNSUPPORTED (max_new * q_heads / kv_heads > 2^30), CUDA.
  */
 mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_row_stride, int64_t q_head_stride,
                                 void* O, int64_t o_row_stride, int64_t o_head_stride, mlora_dtype dtype, int T,
