@@ -7,11 +7,10 @@
 //
 // Bound: HBM, 3 bytes per bf16 element each way: 106k tokens of 8 heads of 128 are read in 104 us,
 // 6.3 TB/s; 30k tokens written and read back take 63 us, 5.8 TB/s; the rows of 256 sequences, 32
-// heads, written and the pages that they lie in read back take 50 us, 4.2 TB/s.
-// A tile's loads depend on the sequence's
-// length, then on its page: small groups (16 CTAs of 128 threads per SM), each with all its
-// loads in flight at once, cover that chain.  A step of few rows (decode) gives a tile to a
-// warp: it is one row, and its time is the chain's.
+// heads, written and the pages that they lie in read back take 47 us, 4.5 TB/s.  A tile's loads
+// depend on the sequence's length, then on its page: small groups, each with all its loads in
+// flight at once, cover that chain.  A step of few rows (decode) gives a tile to a warp: it is one
+// row, and its time is the chain's.
 #include <cuda_bf16.h>
 
 #include "cache.h"
@@ -25,9 +24,9 @@ constexpr int THREADS = 128;
 // CTAs per SM (register limits): of 1 to 16 each, those that measured best at 100k tokens read and
 // at 28k tokens appended
 constexpr int READ_CTAS = 10;
-template <typename T>
-constexpr int APPEND_CTAS = sizeof(T) == 2 ? 9 : 4;
-constexpr int HELD = 4;                    // vectors per thread kept in registers
+template <typename T, int HELD>
+constexpr int APPEND_CTAS = HELD == 1 ? (sizeof(T) == 2 ? 12 : 8) : sizeof(T) == 2 ? 9 : 4;
+constexpr int HELD = 4;                    // vectors per thread kept in registers at most
 
 // 16 elements of a row as they lie in memory
 template <typename T>
@@ -121,8 +120,8 @@ __device__ __forceinline__ float group_max(float m) {
     return m;
 }
 
-template <typename T, int GROUP>
-__global__ void __launch_bounds__(THREADS, APPEND_CTAS<T>) append_kernel(CachePages c, CacheStep s, RowsIn K, RowsIn V, Divide per_row,
+template <typename T, int GROUP, int HELD>
+__global__ void __launch_bounds__(THREADS, (APPEND_CTAS<T, HELD>)) append_kernel(CachePages c, CacheStep s, RowsIn K, RowsIn V, Divide per_row,
                                                          uint32_t* status) {
     const int part = blockIdx.y * (THREADS / GROUP) + threadIdx.x / GROUP, t = threadIdx.x % GROUP;
     const int b = blockIdx.z, h = part >> 1;
@@ -278,11 +277,16 @@ bool few_rows(const CachePages& c, const CacheStep& s) { return (long long)s.max
 cudaError_t launch_append(bool bf16, const CachePages& c, const CacheStep& s, const RowsIn& k, const RowsIn& v,
                           uint32_t* status, cudaStream_t st) {
     const int blocks = most_blocks(s.max_new, c.page);
+    // decode: a row's vectors are one per lane at most, and more warps fit an SM with them alone (256
+    // rows of 32 heads, and their pages read back: 47 us, 50 us with room for HELD; fp32 81, 87 us)
+    if ((long long)s.max_new * (c.dim / 16) <= 32)
+        return bf16 ? launch<32>(append_kernel<__nv_bfloat16, 32, 1>, blocks, c, s, k, v, status, st)
+                    : launch<32>(append_kernel<float, 32, 1>, blocks, c, s, k, v, status, st);
     if (few_rows(c, s))
-        return bf16 ? launch<32>(append_kernel<__nv_bfloat16, 32>, blocks, c, s, k, v, status, st)
-                    : launch<32>(append_kernel<float, 32>, blocks, c, s, k, v, status, st);
-    return bf16 ? launch<THREADS>(append_kernel<__nv_bfloat16, THREADS>, blocks, c, s, k, v, status, st)
-                : launch<THREADS>(append_kernel<float, THREADS>, blocks, c, s, k, v, status, st);
+        return bf16 ? launch<32>(append_kernel<__nv_bfloat16, 32, HELD>, blocks, c, s, k, v, status, st)
+                    : launch<32>(append_kernel<float, 32, HELD>, blocks, c, s, k, v, status, st);
+    return bf16 ? launch<THREADS>(append_kernel<__nv_bfloat16, THREADS, HELD>, blocks, c, s, k, v, status, st)
+                : launch<THREADS>(append_kernel<float, THREADS, HELD>, blocks, c, s, k, v, status, st);
 }
 
 template <typename T>
