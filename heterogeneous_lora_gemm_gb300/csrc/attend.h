@@ -5,7 +5,7 @@
 namespace mlora {
 
 constexpr int ATTEND_OCC = 3;               // CTAs per SM of the split kernel at most
-constexpr int ATTEND_SLOT = 32 * (128 + 2); // floats of one partial result at most
+constexpr int ATTEND_SLOT = 16 * (256 + 2); // floats of one partial result at most
 constexpr int PROMPT_SLOT = 256 * (128 + 2);// floats of one partial result of the prompt kernel (one per SM at most)
 
 struct AttendWs {
@@ -21,11 +21,11 @@ struct AttendWs {
 cudaError_t attend_split_init();
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
 
-// Sequences with many rows (attend_prompt.cu), bf16 only.
+// Sequences with many rows (attend_prompt.cu): bf16, and fp32 with heads of up to 128 elements.
 cudaError_t attend_prompt_init();
 // Workspace for the converted tiles of `tokens` tokens.
 size_t attend_prompt_bytes(const CachePages& c, long long tokens);
 bool attend_prompt_takes(bool bf16, const AttendArgs& a);
-cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
+cudaError_t launch_attend_prompt(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
 
 }  // namespace mlora

@@ -1,5 +1,5 @@
 // Causal attention over the 8-bit cache for sequences with many rows in the step
-// (prompts), bf16 (include/mlora.h).
+// (prompts) (include/mlora.h).
 //
 // Mathematics as in attend_split.cu: x = scale ks (q . kc) log2 e, o = sum 2^(x - m) vs vc /
 // sum 2^(x - m).  The value scale goes into the exponent, 2^(x - m + log2 vs), and out of the
@@ -7,14 +7,16 @@
 // row's largest x when it was last set; a step whose weights sum to more than 2^14 sets it
 // again (no maximum is taken otherwise; bf16 and fp32 hold weights above 1 as well as below).
 // Rows are (query token, query head of the group) pairs of one key/value head, 256 per CTA as
-// two tiles of 128 (one, where heads have more than 128 elements): a converted key/value tile
-// serves both.
+// two tiles of 128 (one, where heads have more than 128 elements or rows are fp32): a converted
+// key/value tile serves both.
 //
 // Products run on tcgen05.mma in bf16, 128 rows x 64 tokens a step: S = Q K^T (queries and
 // codes exact), O += P V with P = 2^(x - m) vs (one rounding) from tensor memory.  Tensor
 // memory, all 512 columns: two S of 64 columns per tile, so that a step's scores are ready
 // before the last step's weights are done (P lies over its S), and O of the two tiles (or of
-// one, of up to 256 columns).
+// one, of up to 256 columns).  fp32 rows run the same products over three bf16 terms of the
+// queries and of the weights (24 bits), which lie beside the scores: 2 x 1000 rows of 16/8 heads
+// of 128 take 56 us (266 us in attend_split.cu).
 //
 // Bound: the products, 2 x 2 x 128 x 64 x head_dim operations per tile and step.  8192 tokens of
 // 32/8 heads of 128 take 376 us, 1460 TFLOP/s; 4096 take 122 us, 1120 TFLOP/s (the tensor pipe is
@@ -45,6 +47,7 @@
 #include <cuda_bf16.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "attend.h"
 #include "tc_ptx.cuh"
@@ -67,20 +70,26 @@ static_assert(32 * (SOFT * REGS_SOFT + (CONV + 4) * REGS_REST) <= PROMPT_THREADS
 constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
 constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
 
-template <int DP>
+template <int DP, bool F32 = false>
 struct PShape {
     // elements up to 256 leave tensor memory for one row tile, and shared memory for key and value
-    // tiles of 64 tokens
-    static constexpr int TILES = DP == 256 ? 1 : 2;     // row tiles per CTA
+    // tiles of 64 tokens; so do fp32 rows' terms for one row tile
+    static_assert(!F32 || DP <= 128, "queries in three terms");
+    static constexpr int TERMS = F32 ? 3 : 1;           // bf16 terms of a query and of a weight
+    static constexpr int TILES = DP == 256 || F32 ? 1 : 2;   // row tiles per CTA
+    // columns of tensor memory: scores at 0, and the weights' terms of a step apart (0: over the
+    // scores), then O
+    static constexpr int P_AT = F32 ? 2 * STEP : 0, P_COLS = F32 ? TERMS * STEP / 2 : STEP;
+    static constexpr int O_AT = F32 ? P_AT + 2 * P_COLS : 256;
     static constexpr int ROWS = TILES * TILE;
     static constexpr int KT = DP == 256 ? 64 : 128;     // tokens converted at a time
     static constexpr int SPT = KT / STEP;               // steps per token tile
     static constexpr int BLK = DP / 64;                 // 64-element column blocks (128-byte rows)
     static constexpr int QOPER = BLK * TILE * 128;      // bytes of a Q operand tile
     static constexpr int OPER = BLK * KT * 128;         // of a K or V operand tile
-    static constexpr int SMEM = 1024 + TILES * QOPER + 4 * OPER + 2048;
-    static constexpr int PIECES = KT / 16;              // of 16 tokens; a conversion warp (or two, half
-    static constexpr int WARP_BLK = BLK * PIECES / CONV;   // the blocks each) per piece
+    static constexpr int SMEM = 1024 + TILES * TERMS * QOPER + 4 * OPER + 2048;
+    static_assert(SMEM <= 232448 && O_AT + TILES * DP <= 512, "shared and tensor memory");
+    static constexpr int PIECES = KT / 16;              // of 16 tokens
     static_assert(PROMPT_SLOT >= ROWS * (DP + 2), "workspace slot");
 };
 
@@ -188,9 +197,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // K steps [0, N): SS in 64-element blocks of 128 (A) and B_ROWS rows of 128 bytes, TS over rows
 // of tokens.
 template <int N, int B_ROWS, int K = 0>
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    mma_ss<K / 4 * (128 * 128) + K % 4 * 32, K / 4 * (B_ROWS * 128) + K % 4 * 32>(d, a, b, idesc, K > 0);
-    if constexpr (K + 1 < N) product_ss<N, B_ROWS, K + 1>(d, a, b, idesc);
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    mma_ss<K / 4 * (128 * 128) + K % 4 * 32, K / 4 * (B_ROWS * 128) + K % 4 * 32>(d, a, b, idesc, K > 0 ? 1u : acc);
+    if constexpr (K + 1 < N) product_ss<N, B_ROWS, K + 1>(d, a, b, idesc, acc);
 }
 template <int N, int K = 0>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -344,12 +353,58 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     return sum;
 }
 
-// A conversion warp's share of a token tile of one operand, 16 tokens and WARP_BLK column
+// The same for fp32 rows, the weights as three bf16 terms (24 bits) into columns pat, + 32 and
+// + 64; the sum is that of the weights themselves.
+template <bool EDGE, int PG>
+__device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const float* sc, float qf, float m, int lo, int hi) {
+    constexpr int N = PG < 32 ? PG : 32;
+    uint64_t sum = pair(0.f, 0.f);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t y[32], w2[16], w3[16];
+        tmem_ld32(sat + half * 32, y);
+        tmem_wait_ld();
+        tmem_loaded(y);
+        const uint32_t seen = EDGE ? column_mask(lo - half * 32, hi - half * 32) : 0u;
+#pragma unroll
+        for (int g = 0; g < 32; g += N) {
+            const float* at = sc + half * 2 + g / 16;
+            const float f = qf * at[0], c = at[8] - m, v = at[16];
+            const uint64_t f2 = pair(f, f), c2 = pair(c, c);
+            uint64_t l = pair(0.f, 0.f);
+#pragma unroll
+            for (int i = g; i < g + N; i += 2) {
+                const float2 z = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, c2));
+                float p0 = ex2(z.x), p1 = ex2(z.y);
+                if (EDGE) {
+                    p0 = seen >> i & 1 ? p0 : 0.f;
+                    p1 = seen >> (i + 1) & 1 ? p1 : 0.f;
+                }
+                l = add2(l, pair(p0, p1));
+                const uint32_t u = bf2_of(p0, p1);
+                p0 -= __uint_as_float(u << 16);
+                p1 -= __uint_as_float(u & 0xFFFF0000u);
+                const uint32_t t = bf2_of(p0, p1);
+                y[i / 2] = u;
+                w2[i / 2] = t;
+                w3[i / 2] = bf2_of(p0 - __uint_as_float(t << 16), p1 - __uint_as_float(t & 0xFFFF0000u));
+            }
+            sum = fma2(l, pair(v, v), sum);
+        }
+        tmem_st16(pat + half * 16, y);
+        tmem_st16(pat + 32 + half * 16, w2);
+        tmem_st16(pat + 64 + half * 16, w3);
+    }
+    return sum;
+}
+
+// A conversion warp's share of a token tile of one operand, 16 tokens and WB column
 // blocks, as codes in registers.
 template <int DP>
 struct Piece {
     using Sh = PShape<DP>;
-    static constexpr int WB = Sh::WARP_BLK, N = 2 * WB;   // 16-byte loads per thread
+    // a warp per 16 tokens, or two with half of the blocks each; 16-byte loads per thread
+    static constexpr int WB = Sh::BLK * Sh::PIECES / CONV, N = 2 * WB;
     // warp w's 16-token piece and first column block
     static __device__ __forceinline__ int piece(int w) { return Sh::PIECES == CONV ? w : w % Sh::PIECES; }
     static __device__ __forceinline__ int blk0(int w) { return Sh::PIECES == CONV ? 0 : w / Sh::PIECES * WB; }
@@ -399,10 +454,10 @@ constexpr int NOT_HERE = INT_MIN;   // at[b] of a sequence that is converted ins
 
 // Operand tiles in the workspace: at[b] + j is the place of tile j of sequence b (each place
 // holds every head's keys and values, then their scales).
-template <int DP>
+template <int DP, bool F32>
 __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a, uint8_t* __restrict__ operands, int room,
                                                               int* __restrict__ at) {
-    using Sh = PShape<DP>;
+    using Sh = PShape<DP, F32>;
     const CachePages& c = a.pages;
     const int H = c.heads, G = a.q_heads / H, b = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -450,18 +505,19 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                  : "memory");
 }
 
-template <int DP, int PG>
+template <int DP, int PG, bool F32>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const AttendArgs a, int tiles,
                                                                            float* __restrict__ partial,
                                                                            int* __restrict__ counters,
                                                                            const uint8_t* __restrict__ operands,
                                                                            int room, const int* __restrict__ at) {
-    using Sh = PShape<DP>;
+    using Sh = PShape<DP, F32>;
+    using E = std::conditional_t<F32, float, __nv_bfloat16>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     constexpr int KT = Sh::KT, SPT = Sh::SPT;
-    uint8_t* qs = smem;                              // [TILES]
-    uint8_t* kb = smem + Sh::TILES * Sh::QOPER;      // [2]
+    uint8_t* qs = smem;                              // [TILES][TERMS]
+    uint8_t* kb = smem + Sh::TILES * Sh::TERMS * Sh::QOPER;   // [2]
     uint8_t* vb = kb + 2 * Sh::OPER;                 // [2]
     PTail& tl = *reinterpret_cast<PTail*>(vb + 2 * Sh::OPER);
     volatile int* abort_flag = &tl.abort_flag;
@@ -531,7 +587,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const int rl = q4 * 32 + lane, r = r0 + t * TILE + rl;
         const bool live = r < R;
         // A warp's 32 rows lie 16 bytes to a lane: row and 16-byte chunk of its k-th access (of CH)
-        constexpr int CH = DP / 8, PER = CH < 32 ? 32 / CH : 1;   // chunks per row, rows at a time
+        constexpr int EPC = 16 / sizeof(E), CH = DP / EPC, PER = CH < 32 ? 32 / CH : 1;   // chunks per row, rows at a time
         auto row_at = [&](int k) { return q4 * 32 + k * PER + lane / CH; };
         const int chunk = lane % CH;
         auto place = [&](int row) {   // of the lane's chunk in tile t of the queries
@@ -545,7 +601,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             int g;
         };
         auto walk = [&](int64_t row, int64_t head) {
-            return Walk{(int64_t)(s.row0 + tok0) * row + (int64_t)(h * G + g0) * head + chunk * 8, per_tok * row + per_g * head,
+            return Walk{(int64_t)(s.row0 + tok0) * row + (int64_t)(h * G + g0) * head + chunk * EPC, per_tok * row + per_g * head,
                         row - G * head, g0};
         };
         auto advance_row = [&](Walk& v) {
@@ -556,58 +612,106 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 v.at += v.wrap;
             }
         };
-        auto there = [&](int k) { return rr0 + k * PER < R && chunk * 8 < D; };
-        // the queries as they are, but a row outside 2^+-64 brought below 1 by a power of two, and one
-        // that is not finite zeros under NaN statistics
-        tl.qf[t][rl] = a.scale * 1.4426950408889634f;
-        if (Sh::TILES == 2 || t == 0) {
-            Walk at = walk(a.q.row, a.q.head);
-#pragma unroll 4
-            for (int k = 0; k < 32 / PER; ++k) {
-                const bool in = there(k);   // (zeros elsewhere)
-                cp_async16_or_zero(smem_u32(place(row_at(k))), (const __nv_bfloat16*)a.q.ptr + (in ? at.at : 0), in);
-                advance_row(at);
-            }
-            cp_async_wait_all();
-            __syncwarp();
-            // largest |bits| of a chunk (ordered like the values)
-            auto top_of = [](const uint4& w) {
-                const uint32_t u = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                            __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-                return max(u >> 16, u & 0xFFFFu);
-            };
-            bool wild = false;
-#pragma unroll 4
-            for (int k = 0; k < 32 / PER; ++k) {
-                const uint32_t top = top_of(*reinterpret_cast<const uint4*>(place(row_at(k))));
-                wild |= top != 0u && (top >> 7) - 63u > 128u;
-            }
-            if (__any_sync(~0u, wild)) {
+        auto there = [&](int k) { return rr0 + k * PER < R && chunk * EPC < D; };
+        if constexpr (F32) {
+            // the queries below 1 by a power of two per row, as three bf16 terms; a row that is not
+            // finite zeros under NaN statistics
+            if (t == 0) {
+                constexpr int BATCH = 8;   // rows' loads in flight
+                Walk at = walk(a.q.row, a.q.head);
 #pragma unroll 1
-                for (int k = 0; k < 32 / PER; ++k) {
-                    uint4* to = reinterpret_cast<uint4*>(place(row_at(k)));
-                    const uint4 w = *to;
-                    uint32_t top = top_of(w);
+                for (int k0 = 0; k0 < 32 / PER; k0 += BATCH) {
+                    uint4 w[BATCH];
 #pragma unroll
-                    for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-                    const bool fine = top < 0x7F80u;
-                    const int x = fine ? min(max((int)(top >> 7) - 126, -100), 127) : 0;
-                    const float down = fine ? __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f) : 0.f;
-                    auto scaled = [&](uint32_t u) {
-                        return fine ? bf2_of(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down) : 0u;
-                    };
-                    *to = make_uint4(scaled(w.x), scaled(w.y), scaled(w.z), scaled(w.w));
-                    if (chunk == 0)
-                        tl.qf[t][row_at(k)] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                    for (int k = 0; k < BATCH; ++k) {
+                        w[k] = there(k0 + k) ? *reinterpret_cast<const uint4*>((const E*)a.q.ptr + at.at) : make_uint4(0u, 0u, 0u, 0u);
+                        advance_row(at);
+                    }
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                        uint32_t top = 0u;   // largest |bits| of the row (ordered like the values)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = max(top, u[e] & 0x7FFFFFFFu);
+#pragma unroll
+                        for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+                        const bool fine = top < 0x7F800000u;
+                        const int x = fine ? min(max((int)(top >> 23) - 126, -100), 127) : 0;
+                        const float down = fine ? __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f) : 0.f;
+                        float v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = fine ? __uint_as_float(u[e]) * down : 0.f;
+                        const int row = row_at(k0 + k);
+                        uint8_t* to = qs + chunk / 16 * (TILE * 128) + row * 128 + (((chunk % 16 / 2) ^ (row & 7)) << 4) + chunk % 2 * 8;
+#pragma unroll
+                        for (int z = 0; z < Sh::TERMS; ++z) {
+                            const uint2 y = make_uint2(bf2_of(v[0], v[1]), bf2_of(v[2], v[3]));
+                            *reinterpret_cast<uint2*>(to + z * Sh::QOPER) = y;
+                            v[0] -= __uint_as_float(y.x << 16);
+                            v[1] -= __uint_as_float(y.x & 0xFFFF0000u);
+                            v[2] -= __uint_as_float(y.y << 16);
+                            v[3] -= __uint_as_float(y.y & 0xFFFF0000u);
+                        }
+                        if (chunk == 0)
+                            tl.qf[t][row] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                    }
                 }
+                fence_proxy_async_smem();
+                mbar_arrive(&tl.qfull[t]);
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&tl.qfull[t]);
+        } else {
+            // the queries as they are, but a row outside 2^+-64 brought below 1 by a power of two, and one
+            // that is not finite zeros under NaN statistics
+            tl.qf[t][rl] = a.scale * 1.4426950408889634f;
+            if (Sh::TILES == 2 || t == 0) {
+                Walk at = walk(a.q.row, a.q.head);
+#pragma unroll 4
+                for (int k = 0; k < 32 / PER; ++k) {
+                    const bool in = there(k);   // (zeros elsewhere)
+                    cp_async16_or_zero(smem_u32(place(row_at(k))), (const __nv_bfloat16*)a.q.ptr + (in ? at.at : 0), in);
+                    advance_row(at);
+                }
+                cp_async_wait_all();
+                __syncwarp();
+                // largest |bits| of a chunk (ordered like the values)
+                auto top_of = [](const uint4& w) {
+                    const uint32_t u = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                                __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+                    return max(u >> 16, u & 0xFFFFu);
+                };
+                bool wild = false;
+#pragma unroll 4
+                for (int k = 0; k < 32 / PER; ++k) {
+                    const uint32_t top = top_of(*reinterpret_cast<const uint4*>(place(row_at(k))));
+                    wild |= top != 0u && (top >> 7) - 63u > 128u;
+                }
+                if (__any_sync(~0u, wild)) {
+#pragma unroll 1
+                    for (int k = 0; k < 32 / PER; ++k) {
+                        uint4* to = reinterpret_cast<uint4*>(place(row_at(k)));
+                        const uint4 w = *to;
+                        uint32_t top = top_of(w);
+#pragma unroll
+                        for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+                        const bool fine = top < 0x7F80u;
+                        const int x = fine ? min(max((int)(top >> 7) - 126, -100), 127) : 0;
+                        const float down = fine ? __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f) : 0.f;
+                        auto scaled = [&](uint32_t u) {
+                            return fine ? bf2_of(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down) : 0u;
+                        };
+                        *to = make_uint4(scaled(w.x), scaled(w.y), scaled(w.z), scaled(w.w));
+                        if (chunk == 0)
+                            tl.qf[t][row_at(k)] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&tl.qfull[t]);
+            }
         }
         __syncwarp();
         const float qf = tl.qf[t][rl];
         const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
-        const uint32_t sbase = lane_base + t * TILE, obase = lane_base + 256 + t * TILE;
+        const uint32_t sbase = lane_base + t * TILE, obase = lane_base + Sh::O_AT + t * TILE;
         const int hi = s.start + r / G + 1, lo = a.window > 0 ? hi - a.window : 0;   // tokens [lo, hi) are seen
         // limits of the tile's rows, for the token tiles that no limit cuts
         const int rt = r0 + t * TILE;
@@ -620,12 +724,13 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         // it are complete), and the warp's rows from there
         auto put32 = [&](const uint32_t (&x)[32], float f, int q) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
+            for (int e = 0; e < 32; e += EPC) {
                 uint32_t y[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
-                    y[z] = bf2_of(__uint_as_float(x[e + 2 * z]) * f, __uint_as_float(x[e + 2 * z + 1]) * f);
-                const int ch = q * 4 + e / 8;
+                    y[z] = F32 ? __float_as_uint(__uint_as_float(x[e + z]) * f)
+                               : bf2_of(__uint_as_float(x[e + 2 * z % EPC]) * f, __uint_as_float(x[e + (2 * z + 1) % EPC]) * f);
+                const int ch = (q * 32 + e) / EPC;
                 *reinterpret_cast<uint4*>(qs + t * Sh::QOPER + ch / 8 * (TILE * 128) + rl * 128 + (((ch & 7) ^ (rl & 7)) << 4)) =
                     make_uint4(y[0], y[1], y[2], y[3]);
             }
@@ -636,7 +741,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 #pragma unroll 4
             for (int k = 0; k < 32 / PER; ++k) {
                 const uint4 y = *reinterpret_cast<const uint4*>(place(row_at(k)));
-                if (there(k)) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o.ptr + at.at) = y;
+                if (there(k)) *reinterpret_cast<uint4*>((E*)a.o.ptr + at.at) = y;
                 advance_row(at);
             }
         };
@@ -658,17 +763,20 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 const bool edge = t0 + STEP > hi_min || t0 < lo_max;
                 const uint32_t sat = sbase + (i & 1) * STEP;
                 uint32_t y[STEP];
-                // P over the scores
+                // P over the scores (of fp32 rows: there already)
                 auto put_weights = [&](float2 sum) {
                     l2 = add2(l2, pair(sum.x, sum.y));
-                    tmem_st32(sat, y);
+                    if (!F32) tmem_st32(sat, y);
                     tmem_wait_st();
                 };
+                const uint32_t pat = lane_base + Sh::P_AT + (i & 1) * Sh::P_COLS;
                 // with the bound so far, which usually holds; else the bound moves.  The usual step has a
                 // path of its own: joined with the other's, it took 70 moves of registers (5% of the time).
                 bool above = true, done = false;
                 if (!edge && i > 0) {
-                    const float2 sum = unpair(weigh<false, PG>(sat, sc, qf, m, 0, 0, y));
+                    float2 sum;
+                    if constexpr (F32) sum = unpair(weigh3<false, PG>(sat, pat, sc, qf, m, 0, 0));
+                    else sum = unpair(weigh<false, PG>(sat, sc, qf, m, 0, 0, y));
                     above = sum.x + sum.y > MOST;
                     done = !__any_sync(~0u, above);
                     if (done) put_weights(sum);
@@ -697,7 +805,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                             }
                         }
                     }
-                    const float2 sum = unpair(weigh<true, PG>(sat, sc, qf, m, lo - t0, hi - t0, y));
+                    float2 sum;
+                    if constexpr (F32) sum = unpair(weigh3<true, PG>(sat, pat, sc, qf, m, lo - t0, hi - t0));
+                    else sum = unpair(weigh<true, PG>(sat, sc, qf, m, lo - t0, hi - t0, y));
                     above = sum.x + sum.y > MOST;
                     done = move || !__any_sync(~0u, above);
                     if (done) put_weights(sum);
@@ -874,7 +984,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, a.status));
         };
         auto scores = [&](int i) {
-            product_ss<DP / 16, KT>(tm + (i & 1) * STEP, dq, dk + half_of(i), idesc_s);
+#pragma unroll
+            for (int z = 0; z < Sh::TERMS; ++z)
+                product_ss<DP / 16, KT>(tm + (i & 1) * STEP, dq + z * (Sh::QOPER >> 4), dk + half_of(i), idesc_s, z > 0);
             mma_commit(&tl.sfull[t][i & 1]);
             if (ends(i)) mma_commit(&tl.kempty[i / SPT & 1]);
         };
@@ -898,7 +1010,10 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product_ts<STEP / 16>(tm + 256, tm + (i & 1) * STEP, dv + half_of(i), idesc_o, i > 0);
+#pragma unroll
+                for (int z = 0; z < Sh::TERMS; ++z)
+                    product_ts<STEP / 16>(tm + Sh::O_AT, tm + Sh::P_AT + (i & 1) * Sh::P_COLS + z * (STEP / 2), dv + half_of(i),
+                                          idesc_o, i > 0 || z > 0);
                 mma_commit(&tl.odone[t][i & 1]);
                 if (ends(i)) mma_commit(&tl.vempty[i / SPT & 1]);
                 if (i + 2 < steps) scores(i + 2);
@@ -921,16 +1036,17 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     }
 }
 
-template <int DP, int PG>
+template <int DP, int PG, bool F32>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    using Sh = PShape<DP, F32>;
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    const int tiles = (int)((rows + PShape<DP>::ROWS - 1) / PShape<DP>::ROWS);
-    const int room = (int)(ws.operand_bytes / ((size_t)a.pages.heads * (2 * PShape<DP>::OPER + 96)));
+    const int tiles = (int)((rows + Sh::ROWS - 1) / Sh::ROWS);
+    const int room = (int)(ws.operand_bytes / ((size_t)a.pages.heads * (2 * Sh::OPER + 96)));
     const bool pre = tiles > 1 && room > 0;
     if (pre) {
         // a few thousand warps in all, as many blocks for each sequence
         const int blocks = a.step.n_seqs >= 8 * ws.sms ? 1 : (8 * ws.sms + a.step.n_seqs - 1) / a.step.n_seqs;
-        convert_kernel<DP><<<dim3(blocks, a.step.n_seqs), PRE_THREADS, 0, st>>>(a, ws.operands, room, ws.operand_at);
+        convert_kernel<DP, F32><<<dim3(blocks, a.step.n_seqs), PRE_THREADS, 0, st>>>(a, ws.operands, room, ws.operand_at);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -938,25 +1054,28 @@ cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long ctas = (long long)tiles * a.pages.heads * a.step.n_seqs;
     const int parts = ctas * 2 <= ws.sms ? (int)(ws.sms / ctas) : 1;
     const dim3 grid((unsigned)tiles * a.pages.heads, a.step.n_seqs, parts);
-    attend_prompt_kernel<DP, PG><<<grid, PROMPT_THREADS, PShape<DP>::SMEM, st>>>(a, tiles, ws.partial, ws.counters, ws.operands,
+    attend_prompt_kernel<DP, PG, F32><<<grid, PROMPT_THREADS, Sh::SMEM, st>>>(a, tiles, ws.partial, ws.counters, ws.operands,
                                                                             room, pre ? ws.operand_at : nullptr);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-template <int DP>
+template <int DP, bool F32>
 static cudaError_t init() {
-    cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<DP, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<DP>::SMEM);
+    constexpr int bytes = PShape<DP, F32>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<DP, 16, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attend_prompt_kernel<DP, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<DP>::SMEM);
+        e = cudaFuncSetAttribute(attend_prompt_kernel<DP, STEP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     return e;
 }
 
 cudaError_t attend_prompt_init() {
-    cudaError_t e = init<64>();
-    if (e == cudaSuccess) e = init<128>();
-    if (e == cudaSuccess) e = init<256>();
+    cudaError_t e = init<64, false>();
+    if (e == cudaSuccess) e = init<128, false>();
+    if (e == cudaSuccess) e = init<256, false>();
+    if (e == cudaSuccess) e = init<64, true>();
+    if (e == cudaSuccess) e = init<128, true>();
     return e;
 }
 
@@ -969,18 +1088,25 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
     return c.dim <= 64 ? operand_bytes<64>(c, tokens) : c.dim <= 128 ? operand_bytes<128>(c, tokens) : operand_bytes<256>(c, tokens);
 }
 
-// From 17 rows of a sequence and head on: at 6 tokens of 32/8 heads after 4000 tokens (2000
+// From 17 rows of a sequence and head on (fp32 rows of more than 128 elements excepted: their
+// terms outgrow shared memory): at 6 tokens of 32/8 heads after 4000 tokens (2000
 // where they are 64 sequences), 1, 16 and 64 sequences take 25, 60 and 127 us here and 22, 79 and
-// 145 us in attend_split.cu; at 4 tokens 25, 61 and 127 us against 22, 48 and 83 us.
+// 145 us in attend_split.cu; at 4 tokens 25, 61 and 127 us against 22, 48 and 83 us.  fp32 rows:
+// 35, 99 and 217 against 49, 140 and 255 us; at 4 tokens 35, 99 and 216 against 23, 52 and 95 us.
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
-    return bf16 && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
+    return (bf16 || a.pages.dim <= 128) && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }
 
-cudaError_t launch_attend_prompt(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+template <int PG>
+static cudaError_t launch_by_dim(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const int D = a.pages.dim;
-    if (a.pages.page % STEP)
-        return D <= 64 ? launch<64, 16>(a, ws, st) : D <= 128 ? launch<128, 16>(a, ws, st) : launch<256, 16>(a, ws, st);
-    return D <= 64 ? launch<64, STEP>(a, ws, st) : D <= 128 ? launch<128, STEP>(a, ws, st) : launch<256, STEP>(a, ws, st);
+    if (!bf16) return D <= 64 ? launch<64, PG, true>(a, ws, st) : launch<128, PG, true>(a, ws, st);
+    return D <= 64 ? launch<64, PG, false>(a, ws, st)
+                   : D <= 128 ? launch<128, PG, false>(a, ws, st) : launch<256, PG, false>(a, ws, st);
+}
+
+cudaError_t launch_attend_prompt(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    return a.pages.page % STEP ? launch_by_dim<16>(bf16, a, ws, st) : launch_by_dim<STEP>(bf16, a, ws, st);
 }
 
 }  // namespace mlora

@@ -57,7 +57,7 @@ struct Shape {
     static constexpr int BOX = PIECE * ROWB;
     // a warp takes a chunk of two pieces at a time: waits, votes and issues are per chunk
     // (one where the accumulators leave no registers for two)
-    static constexpr int SUB = DP == 256 || DP * NT == 512 ? 1 : 2;
+    static constexpr int SUB = DP == 256 ? 1 : 2;
     static constexpr int CHUNK_T = PIECE * SUB;
     static constexpr int PART = 2 * CB * BOX;          // keys and values of a piece
     static constexpr int STAGE = SUB * PART;
@@ -728,21 +728,17 @@ cudaError_t attend_split_init() {
     auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
     one(init<false, 64, 1>()), one(init<false, 64, 2>()), one(init<false, 128, 1>()), one(init<false, 128, 2>());
     one(init<false, 256, 1>()), one(init<false, 256, 2>());
-    one(init<true, 64, 1>()), one(init<true, 64, 2>()), one(init<true, 64, 4>());
-    one(init<true, 128, 1>()), one(init<true, 128, 2>()), one(init<true, 128, 4>());
+    one(init<true, 64, 1>()), one(init<true, 64, 2>()), one(init<true, 128, 1>()), one(init<true, 128, 2>());
     one(init<true, 256, 1>()), one(init<true, 256, 2>());
     return e;
 }
 
-// Rows per tile: the fewest 8-row columns that hold a sequence's rows, up to the most that the
-// accumulators leave registers for (bf16 rows past 16 are attend_prompt.cu's).
+// Rows per tile: 8, or 16 where a sequence and head has more (past 16 only fp32 rows of more than
+// 128 elements come here, in tiles of 16; the rest are attend_prompt.cu's).
 template <bool F32, int DP>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    if (rows <= 8) return launch<F32, DP, 1>(a, ws, st);
-    if constexpr (F32 && DP < 256)
-        if (rows > 16) return launch<F32, DP, 4>(a, ws, st);
-    return launch<F32, DP, 2>(a, ws, st);
+    return rows <= 8 ? launch<F32, DP, 1>(a, ws, st) : launch<F32, DP, 2>(a, ws, st);
 }
 
 template <bool F32>

@@ -223,7 +223,7 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, c->page_div,
                  c->group_div, scale, window, (uint32_t*)c->ws};
     const bool bf16 = dtype == MLORA_BF16;
-    CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(a, c->attend, (cudaStream_t)stream)
+    CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(bf16, a, c->attend, (cudaStream_t)stream)
                                         : launch_attend_split(bf16, a, c->attend, (cudaStream_t)stream));
     return MLORA_OK;
 }
