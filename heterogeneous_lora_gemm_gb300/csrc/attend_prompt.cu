@@ -30,11 +30,11 @@
 // (487 us); two threads per row (423); the sums by mma.sync (570); one arrival per warp (396);
 // the tiles' products in turns (426); waits that sleep (389).
 //
-// Conversion: a sequence of several row tiles has its codes converted once, by a kernel
+// Conversion: a sequence of many row tiles (PRE_TILES) has its codes converted once, by a kernel
 // before, into operand tiles (as they lie in shared memory) in the handle's workspace, which
-// the attention copies in bulk; converted per row tile the work takes half of the issue slots.
-// A sequence of one row tile, or one for which the workspace has no room left, is converted
-// inside the attention (8192 tokens: 496 us against 572 at the time).
+// the attention copies in bulk; converted per row tile the work takes half of the issue slots
+// (8192 tokens: 496 us against 572 at the time).  One of fewer, or one for which the workspace
+// has no room left, is converted inside the attention.
 //
 // Where row tiles are fewer than half the SMs, each one's tokens are cut into equal parts, a CTA
 // each; the CTA that finishes a row tile last joins the parts, in their order (300 tokens after
@@ -451,6 +451,12 @@ __device__ __forceinline__ Span span_of(const SeqRec& s, int window) {
 }
 
 constexpr int PRE_THREADS = 32 * CONV;
+// Row tiles over which a sequence is converted before: 64 KB written and read again per 128 tokens
+// and head (of 128) cost more than to convert 16 KB for each of a few row tiles.  32/8 heads of 128, before
+// and in place: 16 x 128 tokens after 4000, 2 row tiles, 220 and 146 us; 32 x 600, 10 tiles, 228 and
+// 220 us; 8 x 1200, 19 tiles, 145 and 144 us; 1024 after 6000, 16 tiles, 104 and 116 us; 4 prompts
+// of 14 to 32 tiles 139 and 150 us; heads of 256, 2 x 1000 rows, 16 tiles, 49 and 53 us.
+constexpr int PRE_TILES = 12;
 constexpr int NOT_HERE = INT_MIN;   // at[b] of a sequence that is converted inside the attention
 
 // Operand tiles in the workspace: at[b] + j is the place of tile j of sequence b (each place
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
     auto need = [&](int i) {
         const SeqRec s = load_seq(a.step, c.page, i, a.status);
         const Span p = span_of<Sh::KT>(s, a.window);
-        return s.rows * G > Sh::ROWS ? p.j1 - p.j0 : 0;
+        return s.rows * G > PRE_TILES * Sh::ROWS ? p.j1 - p.j0 : 0;
     };
     const SeqRec s = load_seq(a.step, c.page, b, a.status);
     const Span p = span_of<Sh::KT>(s, a.window);
@@ -1043,7 +1049,7 @@ cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
     const int tiles = (int)((rows + Sh::ROWS - 1) / Sh::ROWS);
     const int room = (int)(ws.operand_bytes / ((size_t)a.pages.heads * (2 * Sh::OPER + 96)));
-    const bool pre = tiles > 1 && room > 0;
+    const bool pre = tiles > PRE_TILES && room > 0;
     if (pre) {
         // a few thousand warps in all, as many blocks for each sequence
         const int blocks = a.step.n_seqs >= 8 * ws.sms ? 1 : (8 * ws.sms + a.step.n_seqs - 1) / a.step.n_seqs;

@@ -459,8 +459,9 @@ typedef struct mlora_cache* mlora_cache_t;
  *   prompt_bytes  device memory for prompts' keys and values in 16 bits (4 bytes per
  *              token, head and element, head_dim rounded up to 64, 128 or 256), at most
  *              what all pages' tokens take; attend converts a long prompt's codes once into
- *              it where they fit, and where they do not again for every 256 rows (128 where
- *              head_dim > 128; 0: always)
+ *              it where they fit: one of more than 12 tiles of 256 rows, tokens x query heads
+ *              per key head (of 128 where head_dim > 128 or the rows are fp32).  Shorter ones,
+ *              and all others, are converted again for every tile (0: always)
  * The handle allocates its workspace (a status word, the partial results of split
  * sequences, about 20 MB, and prompt_bytes) here; append, read and attend allocate nothing.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),

@@ -537,6 +537,20 @@ def test_prompts_converted_once_or_in_place_give_the_same_bits():
         assert torch.equal(outs[0], outs[k]) and torch.equal(outs[1], outs[k + 1])
 
 
+@pytest.mark.parametrize("D,ps,dtype", [(128, 64, "bf16"), (64, 16, "bf16"), (80, 48, "bf16"), (256, 32, "bf16"),
+                                        (128, 128, "f32"), (48, 16, "f32")])
+@pytest.mark.parametrize("window", [0, 150])
+def test_long_prompts_converted_once_or_in_place(D, ps, dtype, window):
+    """More rows than are converted in place: room for all, for the first, or for none of the sequences."""
+    rows, lengths = [250, 60, 410], [250, 500, 700]
+    u = Setup(lengths, 1, D, ps, Hq=16, seed=31)
+    outs = []
+    for room in (256 << 20, 140000 * (64 if D <= 64 else 128 if D <= 128 else 256) // 128, 0):
+        u.cache = Cache(*u.dev, 16, prompt_bytes=room)
+        outs.append(check_attend(u, rows, dtype, window).clone())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 @pytest.mark.parametrize("rows,lengths,H,G,D,ps,window", [
     ([20], [3000], 1, 1, 128, 64, 0),                          # few row tiles: their tokens in parts
     ([40, 3], [2000, 700], 1, 4, 64, 16, 0),
