@@ -15,9 +15,8 @@
 // memory, all 512 columns: two S of 64 columns per tile, so that a step's scores are ready
 // before the last step's weights are done (P lies over its S), and O of the two tiles (or of
 // one, of up to 256 columns).  fp32 rows run the same products over three bf16 terms of the
-// queries and of the weights (24 bits), which lie beside the scores: 2 x 1000 rows of 16/8 heads
-// of 128 take 56 us (266 us in attend_split.cu), 8192 tokens of 32/8 heads 1297 us, 424 TFLOP/s
-// or 1270 of the terms' products.
+// queries and of the weights (24 bits): 2 x 1000 rows of 16/8 heads of 128 take 60 us (266 us in
+// attend_split.cu), 8192 tokens of 32/8 heads 1332 us, 413 TFLOP/s or 1240 of the terms' products.
 //
 // Bound: the products, 2 x 2 x 128 x 64 x head_dim operations per tile and step.  8192 tokens of
 // 32/8 heads of 128 take 376 us, 1460 TFLOP/s; 4096 take 122 us, 1120 TFLOP/s (the tensor pipe is
@@ -78,10 +77,12 @@ struct PShape {
     static_assert(!F32 || DP <= 128, "queries in three terms");
     static constexpr int TERMS = F32 ? 3 : 1;           // bf16 terms of a query and of a weight
     static constexpr int TILES = DP == 256 || F32 ? 1 : 2;   // row tiles per CTA
-    // columns of tensor memory: scores at 0, and the weights' terms of a step apart (0: over the
-    // scores), then O
-    static constexpr int P_AT = F32 ? 2 * STEP : 0, P_COLS = F32 ? TERMS * STEP / 2 : STEP;
-    static constexpr int O_AT = F32 ? P_AT + 2 * P_COLS : 256;
+    // columns of tensor memory: scores at 0, and a step's weights over them; of fp32 rows their
+    // lower two terms at P_AT; O, and after it (fp32) that of the lower terms: the tensor cores'
+    // sums drop bits, those of the full size one in 16 tokens rather than three
+    static constexpr int P_AT = 2 * STEP, P_COLS = (TERMS - 1) * STEP / 2;
+    static constexpr int O_AT = 256, O_COLS = (F32 ? 2 : 1) * DP;
+    static_assert(!F32 || P_AT + 2 * P_COLS <= O_AT, "lower terms");
     static constexpr int ROWS = TILES * TILE;
     static constexpr int KT = DP == 256 ? 64 : 128;     // tokens converted at a time
     static constexpr int SPT = KT / STEP;               // steps per token tile
@@ -89,7 +90,7 @@ struct PShape {
     static constexpr int QOPER = BLK * TILE * 128;      // bytes of a Q operand tile
     static constexpr int OPER = BLK * KT * 128;         // of a K or V operand tile
     static constexpr int SMEM = 1024 + TILES * TERMS * QOPER + 4 * OPER + 2048;
-    static_assert(SMEM <= 232448 && O_AT + TILES * DP <= 512, "shared and tensor memory");
+    static_assert(SMEM <= 232448 && O_AT + TILES * O_COLS <= 512, "shared and tensor memory");
     static constexpr int PIECES = KT / 16;              // of 16 tokens
     static_assert(PROMPT_SLOT >= ROWS * (DP + 2), "workspace slot");
 };
@@ -354,18 +355,19 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     return sum;
 }
 
-// The same for fp32 rows, the weights as three bf16 terms (24 bits) into columns pat, + 32 and
-// + 64; the sum is that of the weights themselves.
+// The same for fp32 rows, the weights as three bf16 terms (24 bits): the first into y, the others
+// into columns pat and pat + 32; the sum is that of the weights themselves.
 template <bool EDGE, int PG>
-__device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const float* sc, float qf, float m, int lo, int hi) {
+__device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const float* sc, float qf, float m, int lo, int hi,
+                                           uint32_t (&y)[STEP]) {
     constexpr int N = PG < 32 ? PG : 32;
     uint64_t sum = pair(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint32_t y[32], w2[16], w3[16];
-        tmem_ld32(sat + half * 32, y);
+        uint32_t x[32], w2[16], w3[16];
+        tmem_ld32(sat + half * 32, x);
         tmem_wait_ld();
-        tmem_loaded(y);
+        tmem_loaded(x);
         const uint32_t seen = EDGE ? column_mask(lo - half * 32, hi - half * 32) : 0u;
 #pragma unroll
         for (int g = 0; g < 32; g += N) {
@@ -375,7 +377,7 @@ __device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const flo
             uint64_t l = pair(0.f, 0.f);
 #pragma unroll
             for (int i = g; i < g + N; i += 2) {
-                const float2 z = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, c2));
+                const float2 z = unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, c2));
                 float p0 = ex2(z.x), p1 = ex2(z.y);
                 if (EDGE) {
                     p0 = seen >> i & 1 ? p0 : 0.f;
@@ -386,15 +388,14 @@ __device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const flo
                 p0 -= __uint_as_float(u << 16);
                 p1 -= __uint_as_float(u & 0xFFFF0000u);
                 const uint32_t t = bf2_of(p0, p1);
-                y[i / 2] = u;
+                y[half * 16 + i / 2] = u;
                 w2[i / 2] = t;
                 w3[i / 2] = bf2_of(p0 - __uint_as_float(t << 16), p1 - __uint_as_float(t & 0xFFFF0000u));
             }
             sum = fma2(l, pair(v, v), sum);
         }
-        tmem_st16(pat + half * 16, y);
-        tmem_st16(pat + 32 + half * 16, w2);
-        tmem_st16(pat + 64 + half * 16, w3);
+        tmem_st16(pat + half * 16, w2);
+        tmem_st16(pat + 32 + half * 16, w3);
     }
     return sum;
 }
@@ -770,10 +771,10 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 const bool edge = t0 + STEP > hi_min || t0 < lo_max;
                 const uint32_t sat = sbase + (i & 1) * STEP;
                 uint32_t y[STEP];
-                // P over the scores (of fp32 rows: there already)
+                // P (of fp32 rows its first term) over the scores
                 auto put_weights = [&](float2 sum) {
                     l2 = add2(l2, pair(sum.x, sum.y));
-                    if (!F32) tmem_st32(sat, y);
+                    tmem_st32(sat, y);
                     tmem_wait_st();
                 };
                 const uint32_t pat = lane_base + Sh::P_AT + (i & 1) * Sh::P_COLS;
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 bool above = true, done = false;
                 if (!edge && i > 0) {
                     float2 sum;
-                    if constexpr (F32) sum = unpair(weigh3<false, PG>(sat, pat, sc, qf, m, 0, 0));
+                    if constexpr (F32) sum = unpair(weigh3<false, PG>(sat, pat, sc, qf, m, 0, 0, y));
                     else sum = unpair(weigh<false, PG>(sat, sc, qf, m, 0, 0, y));
                     above = sum.x + sum.y > MOST;
                     done = !__any_sync(~0u, above);
@@ -801,7 +802,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int q = 0; q < DP / 16; ++q) {
+                            for (int q = 0; q < Sh::O_COLS / 16; ++q) {
                                 uint32_t x[16];
                                 tmem_ld16(obase + q * 16, x);
                                 tmem_wait_ld();
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                         }
                     }
                     float2 sum;
-                    if constexpr (F32) sum = unpair(weigh3<true, PG>(sat, pat, sc, qf, m, lo - t0, hi - t0));
+                    if constexpr (F32) sum = unpair(weigh3<true, PG>(sat, pat, sc, qf, m, lo - t0, hi - t0, y));
                     else sum = unpair(weigh<true, PG>(sat, sc, qf, m, lo - t0, hi - t0, y));
                     above = sum.x + sum.y > MOST;
                     done = move || !__any_sync(~0u, above);
@@ -835,6 +836,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                     tmem_ld32(obase + q * 32, x);
                     tmem_wait_ld();
                     tmem_loaded(x);
+                    if constexpr (F32) {
+                        uint32_t low[32];
+                        tmem_ld32(obase + DP + q * 32, low);
+                        tmem_wait_ld();
+                        tmem_loaded(low);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(low[e]));
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0u;
@@ -992,8 +1001,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         };
         auto scores = [&](int i) {
 #pragma unroll
-            for (int z = 0; z < Sh::TERMS; ++z)
-                product_ss<DP / 16, KT>(tm + (i & 1) * STEP, dq + z * (Sh::QOPER >> 4), dk + half_of(i), idesc_s, z > 0);
+            for (int z = Sh::TERMS - 1; z >= 0; --z)   // (the smallest first: fewer sums of the full size)
+                product_ss<DP / 16, KT>(tm + (i & 1) * STEP, dq + z * (Sh::QOPER >> 4), dk + half_of(i), idesc_s,
+                                        z < Sh::TERMS - 1);
             mma_commit(&tl.sfull[t][i & 1]);
             if (ends(i)) mma_commit(&tl.kempty[i / SPT & 1]);
         };
@@ -1017,10 +1027,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
+                product_ts<STEP / 16>(tm + Sh::O_AT, tm + (i & 1) * STEP, dv + half_of(i), idesc_o, i > 0);
 #pragma unroll
-                for (int z = 0; z < Sh::TERMS; ++z)
-                    product_ts<STEP / 16>(tm + Sh::O_AT, tm + Sh::P_AT + (i & 1) * Sh::P_COLS + z * (STEP / 2), dv + half_of(i),
-                                          idesc_o, i > 0 || z > 0);
+                for (int z = 0; z < Sh::TERMS - 1; ++z)
+                    product_ts<STEP / 16>(tm + Sh::O_AT + DP, tm + Sh::P_AT + (i & 1) * Sh::P_COLS + z * (STEP / 2),
+                                          dv + half_of(i), idesc_o, i > 0 || z > 0);
                 mma_commit(&tl.odone[t][i & 1]);
                 if (ends(i)) mma_commit(&tl.vempty[i / SPT & 1]);
                 if (i + 2 < steps) scores(i + 2);
@@ -1099,7 +1110,7 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
 // terms outgrow shared memory): at 6 tokens of 32/8 heads after 4000 tokens (2000
 // where they are 64 sequences), 1, 16 and 64 sequences take 25, 60 and 127 us here and 22, 79 and
 // 145 us in attend_split.cu; at 4 tokens 25, 61 and 127 us against 22, 48 and 83 us.  fp32 rows:
-// 35, 99 and 217 against 49, 140 and 255 us; at 4 tokens 35, 99 and 216 against 23, 52 and 95 us.
+// 38, 114 and 242 against 49, 140 and 255 us; at 4 tokens some 35, 100 and 220 against 23, 52, 95.
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return (bf16 || a.pages.dim <= 128) && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }
