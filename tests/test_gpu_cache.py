@@ -568,6 +568,29 @@ def test_prompts_in_parts_and_wide_heads(rows, lengths, H, G, D, ps, window, roo
     assert torch.equal(first, check_attend(u, rows, "bf16", window))
 
 
+def test_long_sums_of_fp32_rows_keep_their_bits():
+    """Values of one sign over many tokens, as many items as CTAs, so that each sums a long range.  A
+    sum of n / 16 parts rounded to nearest is off by some sqrt(n / 16) 2^-24 of it, here 1.9e-6;
+    sums that drop bits instead are off by n / 16 of half of them."""
+    B, H, D, ps, n = 152, 2, 64, 64, 16000
+    rng = np.random.default_rng(32)
+    kc = torch.from_numpy(rng.integers(-127, 128, (n // ps, H, ps, D)).astype(np.int8)).cuda()
+    vc = torch.from_numpy(rng.integers(60, 128, (n // ps, H, ps, D)).astype(np.int8)).cuda()
+    ks, vs = (torch.full((n // ps, H), 0.01, device="cuda") for _ in range(2))
+    cache = Cache(kc, ks, vc, vs, H)
+    q = torch.from_numpy((rng.standard_normal((B, H, D)) * 0.3).astype(F)).cuda()
+    o = torch.empty_like(q)
+    lengths = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    pages = torch.arange(n // ps, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()   # shared by all
+    cache.attend(q, o, lengths, pages)
+    k = (kc.double() * ks.double()[:, :, None, None]).permute(1, 0, 2, 3).reshape(H, n, D)
+    v = (vc.double() * vs.double()[:, :, None, None]).permute(1, 0, 2, 3).reshape(H, n, D)
+    p = torch.softmax(D ** -0.5 * torch.einsum("bhd,hnd->bhn", q.double(), k), dim=2)
+    want = torch.einsum("bhn,hnd->bhd", p, v)
+    assert (o.double() - want).norm() < 2.0 ** -18 * want.norm()
+    assert cache.status() == mlora.MLORA_OK
+
+
 def test_growing_scores_move_the_bound():
     """Keys that grow along the sequence: the softmax bound moves in the middle of it, for some
     rows and not for others."""
