@@ -17,6 +17,9 @@
 // one, of up to 256 columns).  fp32 rows run the same products over three bf16 terms of the
 // queries and of the weights (24 bits): 2 x 1000 rows of 16/8 heads of 128 take 60 us (266 us in
 // attend_split.cu), 8192 tokens of 32/8 heads 1332 us, 413 TFLOP/s or 1240 of the terms' products.
+// The tensor cores cut their fp32 sums off at every 16 tokens: over 16000 tokens 2.1e-7 of the
+// output for values of both signs, 5.6e-5 for values of one sign, which is taken here (the codes
+// hold 8 bits); attend_split.cu, where such a range costs more time, rounds instead.
 //
 // Bound: the products, 2 x 2 x 128 x 64 x head_dim operations per tile and step.  8192 tokens of
 // 32/8 heads of 128 take 376 us, 1460 TFLOP/s; 4096 take 122 us, 1120 TFLOP/s (the tensor pipe is
