@@ -15,11 +15,11 @@
 // memory, all 512 columns: two S of 64 columns per tile, so that a step's scores are ready
 // before the last step's weights are done (P lies over its S), and O of the two tiles (or of
 // one, of up to 256 columns).  fp32 rows run the same products over three bf16 terms of the
-// queries and of the weights (24 bits): 2 x 1000 rows of 16/8 heads of 128 take 60 us (266 us in
-// attend_split.cu), 8192 tokens of 32/8 heads 1332 us, 413 TFLOP/s or 1240 of the terms' products.
-// The tensor cores cut their fp32 sums off at every 16 tokens: over 16000 tokens 2.1e-7 of the
-// output for values of both signs, 5.6e-5 for values of one sign, which is taken here (the codes
-// hold 8 bits); attend_split.cu, where such a range costs more time, rounds instead.
+// queries and of the weights (24 bits): 2 x 1000 rows of 16/8 heads of 128 take 62 us (266 us in
+// attend_split.cu), 8192 tokens of 32/8 heads 1670 us, 329 TFLOP/s or 990 of the terms' products.
+// The tensor cores cut their fp32 sums off at every 16 tokens, so that fp32 rows' O is taken out
+// every FOLD steps (118 x 6000 tokens: error against 64 bits 1.1e-6, 2.0e-6 with twice the steps, 5.6e-6
+// without, 1.4e-6 in plain fp32; 8192 tokens: 1670, 1485 and 1335 us).
 //
 // Bound: the products, 2 x 2 x 128 x 64 x head_dim operations per tile and step.  8192 tokens of
 // 32/8 heads of 128 take 376 us, 1460 TFLOP/s; 4096 take 122 us, 1120 TFLOP/s (the tensor pipe is
@@ -70,6 +70,7 @@ constexpr int PROMPT_THREADS = 32 * (SOFT + CONV + 4);   // (two warps only comp
 // sum may not exceed the launch's.
 constexpr int REGS_SOFT = 128, REGS_REST = 72;
 static_assert(32 * (SOFT * REGS_SOFT + (CONV + 4) * REGS_REST) <= PROMPT_THREADS * 96, "register split");
+constexpr int FOLD = 16;                   // steps of fp32 rows between roundings of O into fp32 outside
 constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
 constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
 
@@ -760,8 +761,56 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         float* slot = partial + ((size_t)item * gridDim.z + part) * PROMPT_SLOT;
         uint4* mine = reinterpret_cast<uint4*>(slot) + t * TILE + rl;
         float* ml = slot + DP * Sh::ROWS + t * TILE + rl;
+        // fp32 rows: the tensor cores' sums cut off, so that O is taken out every FOLD steps and added,
+        // rounded to nearest, to the row's sum of before, which waits in the output row (or the part's
+        // slot) under the bound `under`
+        float under = m;
+        float* held = nullptr;
+        const int group4 = parts == 1 ? 4 : 4 * Sh::ROWS;   // floats from 4 elements to the next
+        if constexpr (F32) {
+            const int tok = quotient(a.group, r), g = r - tok * G;
+            held = parts == 1 ? (float*)a.o.ptr + (int64_t)(s.row0 + tok) * a.o.row + (int64_t)(h * G + g) * a.o.head : (float*)mine;
+        }
+        // 4 elements of that sum, times f
+        auto held_at = [&](int k) { return live && (parts > 1 || k * 4 < D) ? reinterpret_cast<float4*>(held + k * group4) : nullptr; };
+        // 32 elements of O, from 32 q on
+        auto sum_of = [&](int q, uint32_t (&x)[32], bool more, float f) {
+            uint32_t low[32];
+            __syncwarp();
+            tmem_ld32(obase + q * 32, x);
+            tmem_ld32(obase + DP + q * 32, low);
+            tmem_wait_ld();
+            tmem_loaded(x);
+            tmem_loaded(low);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4* p = held_at(q * 8 + e / 4);
+                const float4 y = more && p ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[e + k] = __float_as_uint(fmaf(z[k], f, __uint_as_float(x[e + k]) + __uint_as_float(low[e + k])));
+            }
+        };
         if (t == 0 || two) {
             for (int i = 0; i < steps; ++i) {
+                if constexpr (F32)
+                    if (i > 0 && i % FOLD == 0) {   // (the wait: as where the bound moves, below)
+                        ok = __all_sync(~0u, mbar_wait(&tl.odone[t][(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, a.status));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < DP / 32; ++q) {
+                            uint32_t x[32];
+                            sum_of(q, x, i > FOLD, ex2(under - m));
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                if (float4* p = held_at(q * 8 + e / 4))
+                                    *p = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
+                                                     __uint_as_float(x[e + 3]));
+                        }
+                        under = m;
+                    }
                 // (the look at the scales' barrier is under way during the wait for the scores)
                 const bool scales = i % SPT != 0 || mbar_done(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1);
                 ok = mbar_wait(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
@@ -836,16 +885,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             for (int q = 0; q < DP / 32; ++q) {
                 uint32_t x[32];
                 if (nt > 0) {
-                    tmem_ld32(obase + q * 32, x);
-                    tmem_wait_ld();
-                    tmem_loaded(x);
-                    if constexpr (F32) {
-                        uint32_t low[32];
-                        tmem_ld32(obase + DP + q * 32, low);
+                    if constexpr (F32) sum_of(q, x, steps > FOLD, ex2(under - m));
+                    else {
+                        __syncwarp();
+                        tmem_ld32(obase + q * 32, x);
                         tmem_wait_ld();
-                        tmem_loaded(low);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(low[e]));
+                        tmem_loaded(x);
                     }
                 } else {
 #pragma unroll
@@ -1030,11 +1075,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                product_ts<STEP / 16>(tm + Sh::O_AT, tm + (i & 1) * STEP, dv + half_of(i), idesc_o, i > 0);
+                product_ts<STEP / 16>(tm + Sh::O_AT, tm + (i & 1) * STEP, dv + half_of(i), idesc_o,
+                                      F32 ? i % FOLD > 0 : i > 0);
 #pragma unroll
                 for (int z = 0; z < Sh::TERMS - 1; ++z)
                     product_ts<STEP / 16>(tm + Sh::O_AT + DP, tm + Sh::P_AT + (i & 1) * Sh::P_COLS + z * (STEP / 2),
-                                          dv + half_of(i), idesc_o, i > 0 || z > 0);
+                                          dv + half_of(i), idesc_o, i % FOLD > 0 || z > 0);
                 mma_commit(&tl.odone[t][i & 1]);
                 if (ends(i)) mma_commit(&tl.vempty[i / SPT & 1]);
                 if (i + 2 < steps) scores(i + 2);

@@ -591,6 +591,30 @@ def test_long_sums_of_fp32_rows_keep_their_bits():
     assert cache.status() == mlora.MLORA_OK
 
 
+def test_long_sums_of_fp32_prompts_keep_their_bits():
+    """The same for prompts: sums that cut off in the tensor cores, of 1024 tokens at most, lose at most
+    2^-23 of the sum so far at each of 64 steps, 2^-18 of the whole."""
+    B, R, D, ps, n = 152, 20, 64, 64, 16000
+    rng = np.random.default_rng(33)
+    kc = torch.from_numpy(rng.integers(-127, 128, (n // ps, 1, ps, D)).astype(np.int8)).cuda()
+    vc = torch.from_numpy(rng.integers(60, 128, (n // ps, 1, ps, D)).astype(np.int8)).cuda()
+    ks, vs = (torch.full((n // ps, 1), 0.01, device="cuda") for _ in range(2))
+    cache = Cache(kc, ks, vc, vs, 1)
+    q = torch.from_numpy((rng.standard_normal((B * R, 1, D)) * 0.3).astype(F)).cuda()
+    o = torch.full_like(q, float("nan"))
+    lengths = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    pages = torch.arange(n // ps, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    cache.attend(q, o, lengths, pages, offsets=offsets_of([R] * B), max_new=R)
+    k = (kc.double() * ks.double()[:, :, None, None]).reshape(n, D)
+    v = (vc.double() * vs.double()[:, :, None, None]).reshape(n, D)
+    pos = n - R + torch.arange(B * R, device="cuda") % R
+    x = D ** -0.5 * q[:, 0].double() @ k.T
+    x = x.masked_fill(torch.arange(n, device="cuda")[None] > pos[:, None], -float("inf"))
+    want = torch.softmax(x, dim=1) @ v
+    assert (o[:, 0].double() - want).norm() < 2.0 ** -18 * want.norm()
+    assert cache.status() == mlora.MLORA_OK
+
+
 def test_growing_scores_move_the_bound():
     """Keys that grow along the sequence: the softmax bound moves in the middle of it, for some
     rows and not for others."""
