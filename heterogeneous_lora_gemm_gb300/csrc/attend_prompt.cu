@@ -1159,7 +1159,8 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
 // terms outgrow shared memory): at 6 tokens of 32/8 heads after 4000 tokens (2000
 // where they are 64 sequences), 1, 16 and 64 sequences take 25, 60 and 127 us here and 22, 79 and
 // 145 us in attend_split.cu; at 4 tokens 25, 61 and 127 us against 22, 48 and 83 us.  fp32 rows:
-// 38, 114 and 242 against 49, 140 and 255 us; at 4 tokens some 35, 100 and 220 against 23, 52, 95.
+// 38, 129 and 265 against 49, 140 and 255 us, and at 12 tokens 134 against 243 us (16 sequences);
+// at 4 tokens some 35, 100 and 220 against 23, 52 and 95.
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return (bf16 || a.pages.dim <= 128) && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }
