@@ -451,7 +451,7 @@ struct Span {
 };
 template <int KT>
 __device__ __forceinline__ Span span_of(const SeqRec& s, int window) {
-    const int tb = s.start + s.rows, ta = window > 0 ? max(0, s.start - window + 1) : 0;
+    const int tb = s.start + s.rows, ta = first_seen(s.start, window);
     return tb > ta ? Span{ta / KT, (tb + KT - 1) / KT} : Span{0, 0};
 }
 
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     const int first = at ? at[b] : NOT_HERE;   // place of the sequence's tile 0 in the workspace
     const bool pre = first != NOT_HERE;
     // tokens [ta, tb), whole tiles wherever they are converted: the sums' order is the same
-    int ta = a.window > 0 ? max(0, pos_lo - a.window + 1) / KT * KT : 0;
+    int ta = first_seen(pos_lo, a.window) / KT * KT;
     int tb = pos_hi + 1;
     const int all = tb > ta ? (tb - ta + KT - 1) / KT : 0;
     const int parts = max(1, min((int)gridDim.z, all * KT / PART));
@@ -724,11 +724,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const float qf = tl.qf[t][rl];
         const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t sbase = lane_base + t * TILE, obase = lane_base + Sh::O_AT + t * TILE;
-        const int hi = s.start + r / G + 1, lo = a.window > 0 ? hi - a.window : 0;   // tokens [lo, hi) are seen
+        const int hi = s.start + r / G + 1, lo = first_seen(hi - 1, a.window);   // tokens [lo, hi) are seen
         // limits of the tile's rows, for the token tiles that no limit cuts
         const int rt = r0 + t * TILE;
         const int hi_min = s.start + rt / G + 1, hi_max = s.start + min(R - 1, rt + TILE - 1) / G + 1;
-        const int lo_max = a.window > 0 ? hi_max - a.window : 0;
+        const int lo_max = first_seen(hi_max - 1, a.window);
         float m = NO_MAX;
         uint64_t l2 = pair(0.f, 0.f);
         bool ok = true;

@@ -132,8 +132,7 @@ __device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
     Line n;
     n.s = load_seq(a.step, a.pages.page, b, a.status);
     const int last = n.s.start + n.s.rows - 1;   // position of the last processed row
-    const int lo = a.window > 0 ? max(0, n.s.start - a.window + 1) : 0;
-    n.c0 = lo / CHUNK_T;
+    n.c0 = first_seen(n.s.start, a.window) / CHUNK_T;
     n.c1 = last >= 0 ? last / CHUNK_T + 1 : n.c0;
     n.tiles = (n.s.rows * G + RT - 1) / RT;
     n.units = (n.c1 - n.c0 + WARPS - 1) / WARPS;
@@ -306,7 +305,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (u1 <= u0) break;   // only the lead is in this range: the item is the next CTA's
         // positions that the tile's rows may see: row r at start + i0 + token_of(r)
         const int pos_lo = n.s.start + i0, pos_hi = pos_lo + token_of(rows - 1);
-        const int ca = max(n.c0 + u0 * WARPS, a.window > 0 ? max(0, pos_lo - a.window + 1) / CHUNK_T : 0);
+        const int ca = max(n.c0 + u0 * WARPS, first_seen(pos_lo, a.window) / CHUNK_T);
         const int cb = min(min(n.c0 + u1 * WARPS, n.c1), pos_hi >= 0 ? pos_hi / CHUNK_T + 1 : 0);
         const int count = max(0, (cb - ca - warp + WARPS - 1) / WARPS);   // this warp's chunks: ca + warp, + WARPS, ...
 
@@ -407,7 +406,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) qreg[s][t][term] = qf_at(s, t, term);
         float qf[NT][2], m[NT][2], l[NT][2], o[KS][NT][4];
-        int hi[NT][2];   // tokens [hi - window, hi) are seen
+        int hi[NT][2];   // tokens first_seen(hi - 1) .. hi - 1 are seen
         int hi_min = 0x7fffffff, hi_max = -0x7fffffff;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -423,7 +422,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
         hi_min = pos_lo + 1;
         hi_max = pos_hi + 1;
-        const int lo_max = a.window > 0 ? hi_max - a.window : 0;
+        const int lo_max = first_seen(pos_hi, a.window);
 
         // ---- this warp's chunks
         for (int k = 0; k < count && alive; ++k) {
@@ -497,7 +496,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         x0 = (CH == 2 ? x0 + sc[u][CH - 1][t][e] : x0) * f;
                         x1 = (CH == 2 ? x1 + sc[u][CH - 1][t][2 + e] : x1) * f;
                         if (edge) {
-                            const int at = t0 + u * PIECE + g, from = a.window > 0 ? hi[t][e] - a.window : 0;
+                            const int at = t0 + u * PIECE + g, from = first_seen(hi[t][e] - 1, a.window);
                             if (at >= hi[t][e] || at < from) x0 = -INFINITY;
                             if (at + 8 >= hi[t][e] || at + 8 < from) x1 = -INFINITY;
                         }

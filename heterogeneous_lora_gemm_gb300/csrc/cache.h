@@ -93,6 +93,12 @@ __device__ __forceinline__ int load_page(const CacheStep& s, const CachePages& c
     atomicOr(status, STATUS_BAD_STEP);
     return -1;
 }
+
+// First token that a row at position pos sees; window 0: all of them.  (A difference is taken only
+// where it is not negative: pos reaches -2^31, and the window 2^31 - 1.)
+__device__ __forceinline__ int first_seen(int pos, int window) {
+    return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
 #endif
 
 struct AttendArgs {
