@@ -52,6 +52,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
+_INT_MAX = 2 ** 31 - 1
 
 # name -> (restype, argtypes), in header order
 _SIGNATURES = {
@@ -258,8 +259,18 @@ def mlora_dequantize_nf4(codes_ptr: int, absmax_ptr: int, codebook, dout: int, d
                                      stream or None), "mlora_dequantize_nf4")
 
 
+def _ints(**values) -> None:
+    """Refuses what a C int does not hold (ctypes would pass its low 32 bits)."""
+    for name, v in values.items():
+        if not -_INT_MAX <= v <= _INT_MAX:
+            raise ValueError(f"{name} {v} does not fit 32 bits")
+
+
 def mlora_cache_create(k_codes_ptr: int, k_scale_ptr: int, v_codes_ptr: int, v_scale_ptr: int, n_pages: int,
                        page_size: int, kv_heads: int, head_dim: int, q_heads: int, prompt_bytes: int) -> int:
+    _ints(n_pages=n_pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim, q_heads=q_heads)
+    if not 0 <= prompt_bytes < 1 << 64:
+        raise ValueError(f"prompt_bytes {prompt_bytes} does not fit 64 bits")
     h = _P()
     check(lib().mlora_cache_create(k_codes_ptr, k_scale_ptr, v_codes_ptr, v_scale_ptr, n_pages, page_size, kv_heads,
                                    head_dim, q_heads, prompt_bytes, ctypes.byref(h)), "mlora_cache_create")
@@ -273,6 +284,7 @@ def mlora_cache_destroy(cache: int) -> None:
 def mlora_cache_append(cache: int, K_ptr: int, k_row_stride: int, k_head_stride: int, V_ptr: int, v_row_stride: int,
                        v_head_stride: int, dtype: int, T: int, offsets_ptr: Optional[int], lengths_ptr: int,
                        pages_ptr: int, n_seqs: int, width: int, max_new: int, stream: int) -> None:
+    _ints(T=T, n_seqs=n_seqs, width=width, max_new=max_new)
     check(lib().mlora_cache_append(cache, K_ptr, k_row_stride, k_head_stride, V_ptr, v_row_stride, v_head_stride,
                                    dtype, T, offsets_ptr or None, lengths_ptr, pages_ptr, n_seqs, width, max_new,
                                    stream or None), "mlora_cache_append")
@@ -281,6 +293,7 @@ def mlora_cache_append(cache: int, K_ptr: int, k_row_stride: int, k_head_stride:
 def mlora_cache_read(cache: int, K_ptr: int, k_row_stride: int, k_head_stride: int, V_ptr: int, v_row_stride: int,
                      v_head_stride: int, dtype: int, T: int, offsets_ptr: Optional[int], lengths_ptr: int,
                      pages_ptr: int, n_seqs: int, width: int, max_new: int, stream: int) -> None:
+    _ints(T=T, n_seqs=n_seqs, width=width, max_new=max_new)
     check(lib().mlora_cache_read(cache, K_ptr, k_row_stride, k_head_stride, V_ptr, v_row_stride, v_head_stride,
                                  dtype, T, offsets_ptr or None, lengths_ptr, pages_ptr, n_seqs, width, max_new,
                                  stream or None), "mlora_cache_read")
@@ -290,6 +303,7 @@ def mlora_cache_attend(cache: int, Q_ptr: int, q_row_stride: int, q_head_stride:
                        o_head_stride: int, dtype: int, T: int, offsets_ptr: Optional[int], lengths_ptr: int,
                        pages_ptr: int, n_seqs: int, width: int, max_new: int, scale: float, window: int,
                        stream: int) -> None:
+    _ints(T=T, n_seqs=n_seqs, width=width, max_new=max_new, window=window)
     check(lib().mlora_cache_attend(cache, Q_ptr, q_row_stride, q_head_stride, O_ptr, o_row_stride, o_head_stride,
                                    dtype, T, offsets_ptr or None, lengths_ptr, pages_ptr, n_seqs, width, max_new,
                                    scale, window, stream or None), "mlora_cache_attend")
@@ -485,6 +499,8 @@ class Cache:
         n_seqs, width = pages.shape
         if lengths.shape != (n_seqs,) or lengths.dtype != i32 or not lengths.is_contiguous():
             raise ValueError("lengths is a contiguous int32 [n_seqs]")
+        if not (-_INT_MAX <= max_new <= _INT_MAX and shape[0] <= _INT_MAX and n_seqs <= _INT_MAX and width <= _INT_MAX):
+            _ints(T=shape[0], n_seqs=n_seqs, width=width, max_new=max_new)
         at = None
         if offsets is not None:
             if offsets.shape != (n_seqs + 1,) or offsets.dtype != i32 or not offsets.is_contiguous():
@@ -517,6 +533,8 @@ class Cache:
         (scale: head_dim ** -0.5 by default; window: tokens a row sees at most, 0 = all)."""
         if scale is None:
             scale = self.head_dim ** -0.5
+        if not -_INT_MAX <= window <= _INT_MAX:
+            _ints(window=window)
         self._call(self._lib.mlora_cache_attend, "mlora_cache_attend", Q, O, self.q_heads, lengths, pages, offsets,
                    max_new, stream, scale, window)
 
