@@ -3,7 +3,9 @@
 //
 // Mathematics as in attend_split.cu: x = scale ks (q . kc) log2 e, o = sum 2^(x - m) vs vc /
 // sum 2^(x - m).  The value scale goes into the exponent, 2^(x - m + log2 vs), and out of the
-// sum again per 16 tokens (a block of vs = 0 is converted to zeros under a scale of 1).  m is a
+// sum again per 16 tokens.  Weights under 2^-126 are lost, so that vs has to stay well above: a block of
+// vs < 2^-64 has its codes brought down by 2^-64 (exact in bf16) under a scale of 2^64 vs, and one of
+// vs < 2^-120, whose codes append stores as 0, is converted to zeros under a scale of 1.  m is a
 // row's largest x when it was last set; a step whose weights sum to more than 2^14 sets it
 // again (no maximum is taken otherwise; bf16 and fp32 hold weights above 1 as well as below).
 // Rows are (query token, query head of the group) pairs of one key/value head, 256 per CTA as
@@ -73,6 +75,7 @@ static_assert(32 * (SOFT * REGS_SOFT + (CONV + 4) * REGS_REST) <= PROMPT_THREADS
 constexpr int FOLD = 16;                   // steps of fp32 rows between roundings of O into fp32 outside
 constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
 constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
+constexpr float SMALL_SCALE = 0x1p-64f;    // value scales below it are brought up by 1 / SMALL_SCALE
 
 template <int DP, bool F32 = false>
 struct PShape {
@@ -262,6 +265,11 @@ __device__ __forceinline__ uint32_t bf16_codes(uint32_t u) {
 __device__ __forceinline__ uint2 widen(uint32_t w) {
     return make_uint2(bf16_codes(__byte_perm(w, 0x43434343u, 0x4140)), bf16_codes(__byte_perm(w, 0x43434343u, 0x4342)));
 }
+// two bf16 times SMALL_SCALE
+__device__ __forceinline__ uint32_t bf16_small(uint32_t u) {
+    const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(SMALL_SCALE));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 // 16 bytes of global memory (zeros where `in` is false) into shared memory
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -271,9 +279,15 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // 16 codes of token t, elements 16 c .. of 64-element block blk, into an operand tile: DP / 64
 // blocks of KT rows of 128 bytes under the 128-byte swizzle.  (Lanes pair token t with t ^ 5,
 // so that the writes of a quarter warp, at (2 c + z) ^ t, do not meet in a bank.)
-template <int KT>
+// DOWN: times SMALL_SCALE.
+template <int KT, bool DOWN>
 __device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk, int c) {
-    const uint2 a = widen(x.x), b = widen(x.y), d = widen(x.z), e = widen(x.w);
+    auto values = [](uint32_t w) {
+        uint2 u = widen(w);
+        if (DOWN) u.x = bf16_small(u.x), u.y = bf16_small(u.y);
+        return u;
+    };
+    const uint2 a = values(x.x), b = values(x.y), d = values(x.z), e = values(x.w);
     uint8_t* row = dst + blk * (KT * 128) + t * 128;
     *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
     *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
@@ -404,6 +418,9 @@ __device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const flo
     return sum;
 }
 
+// Whether a block of value scale vs counts as zeros.
+__device__ __forceinline__ bool no_values(float vs) { return fabsf(vs) < TINY_SCALE; }
+
 // A conversion warp's share of a token tile of one operand, 16 tokens and WB column
 // blocks, as codes in registers.
 template <int DP>
@@ -430,19 +447,27 @@ struct Piece {
         for (int u = 0; u < N; ++u) x[u] = make_uint4(0u, 0u, 0u, 0u);
     }
     // into operand tile `dst` (generic address)
+    template <bool DOWN = false>
     __device__ __forceinline__ void store(uint8_t* dst, int w, int lane) const {
         const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), b0 = blk0(w);
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            convert16<Sh::KT>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4);
+            convert16<Sh::KT, DOWN>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4);
+    }
+    // values under scale vs (see put_scales)
+    __device__ __forceinline__ void store_values(uint8_t* dst, int w, int lane, float vs) {
+        if (no_values(vs)) zero();
+        if (vs < SMALL_SCALE) store<true>(dst, w, lane);
+        else store(dst, w, lane);
     }
 };
 // Scales of 16 tokens as the softmax takes them (see the top of the file).
 __device__ __forceinline__ void put_scales(float* sc, int w, float ks, float vs) {
-    const bool none = vs == 0.f;
+    const bool none = no_values(vs);
+    const float up = vs < SMALL_SCALE ? vs * (1.f / SMALL_SCALE) : vs;
     sc[w] = ks;
-    sc[8 + w] = none ? 0.f : log2f(vs);
-    sc[16 + w] = none ? 1.f : 1.f / vs;
+    sc[8 + w] = none ? 0.f : log2f(up);
+    sc[16 + w] = none ? 1.f : 1.f / up;
 }
 
 // Token tiles of a sequence that its rows see.
@@ -503,9 +528,8 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
         Piece<DP> k, v;
         k.load(c.k_codes, c, id, h, place, warp, lane);
         v.load(c.v_codes, c, id, h, place, warp, lane);
-        if (vs == 0.f) v.zero();
         k.store(to, warp, lane);
-        v.store(to + Sh::OPER, warp, lane);
+        v.store_values(to + Sh::OPER, warp, lane, vs);
         if (lane == 0 && warp < Sh::PIECES)
             put_scales(reinterpret_cast<float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24, warp, ks, vs);
     }
@@ -1024,8 +1048,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             mbar_arrive(&tl.kfull[j & 1]);
             k.load(c.k_codes, c, id, h, place, w, lane);
             if (!mbar_wait(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
-            if (vs == 0.f) v.zero();
-            v.store(vb + (j & 1) * Sh::OPER, w, lane);
+            v.store_values(vb + (j & 1) * Sh::OPER, w, lane, vs);
             fence_proxy_async_smem();
             mbar_arrive(&tl.vfull[j & 1]);
             v.load(c.v_codes, c, id, h, place, w, lane);

@@ -10,6 +10,8 @@
 
 namespace mlora {
 
+constexpr float TINY_SCALE = 0x1p-120f;   // codes under a smaller scale are 0 (1 / s stays finite above)
+
 // The caller's pages: codes [n_pages][heads][page][dim], scales [n_pages][heads].
 struct CachePages {
     int8_t* k_codes;

@@ -19,7 +19,6 @@ namespace mlora {
 
 namespace {
 
-constexpr float TINY_SCALE = 0x1p-120f;   // below it the codes are 0 (1 / s stays finite above)
 constexpr int THREADS = 128;
 // CTAs per SM (register limits): of 1 to 16 each, those that measured best at 100k tokens read and
 // at 28k tokens appended

@@ -501,8 +501,9 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * over the tokens j of the row's sequence with j <= pos(i), and j > pos(i) - window
  * where window > 0; query head h reads key/value head h / (q_heads / kv_heads).  A row
  * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums
- * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums); O is
- * rounded once.  O must not overlap Q: fp32 rows of it may hold sums during the call.
+ * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, value
+ * scales under 2^-96 lose low bits, under 2^-120 they may count as 0); O is rounded
+ * once.  O must not overlap Q: fp32 rows of it may hold sums during the call.
  * Errors: INVALID_ARG, UNSUPPORTED (max_new * q_heads / kv_heads > 2^30), CUDA.
  */
 mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_row_stride, int64_t q_head_stride,

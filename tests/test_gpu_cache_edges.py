@@ -10,7 +10,7 @@ if not torch.cuda.is_available():   # pragma: no cover - CPU machine
     pytest.skip("needs a GPU", allow_module_level=True)
 
 from heterogeneous_lora_gemm_gb300 import Cache, mlora  # noqa: E402
-from test_gpu_cache import F, Setup, as_np, check_attend, offsets_of, plain_attend, strided  # noqa: E402
+from test_gpu_cache import F, Setup, as_np, check_attend, offsets_of, plain_attend, strided, tolerance  # noqa: E402
 
 
 # ---- windows --------------------------------------------------------------- #
@@ -26,3 +26,51 @@ def test_a_window_larger_than_any_position_is_no_window(rows, lengths, H, G, D, 
     u = Setup(lengths, H, D, ps, Hq=H * G, seed=40)
     limited = check_attend(u, rows, dtype, window)
     assert torch.equal(limited, check_attend(u, rows, dtype, 0))
+
+
+# ---- value scales far below 1 ------------------------------------------------ #
+# rows, lengths, H, G, D, page, bytes for prompts (few rows; prompts in place; prompts converted ahead)
+TINY = [([1, 1], [520, 64], 1, 2, 64, 16, 0), ([130], [450], 1, 2, 64, 16, 0), ([70, 20], [300, 90], 1, 3, 128, 64, 0),
+        ([40], [400], 1, 2, 256, 32, 0), ([250, 60], [250, 500], 1, 16, 128, 64, 256 << 20)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tiny", [2.0 ** -63, 2.0 ** -65, 2.0 ** -119, 1e-36, 1e-38, 1e-41])
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,room", TINY)
+def test_tokens_of_tiny_value_blocks_keep_their_weight(rows, lengths, H, G, D, ps, room, tiny, dtype):
+    """Every other block's values are next to nothing; its tokens' weights stay in the softmax's sum."""
+    u = Setup(lengths, H, D, ps, Hq=H * G, seed=41)
+    for t in u.table:
+        u.vs[t[1::2][t[1::2] >= 0]] = tiny
+    u.upload()
+    u.cache = Cache(*u.dev, H * G, prompt_bytes=room)
+    check_attend(u, rows, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,room", TINY)
+def test_values_that_are_all_tiny(rows, lengths, H, G, D, ps, room, dtype):
+    """Value scales around 2^-96: attention of values times 2^90 would give the outputs times 2^90."""
+    u = Setup(lengths, H, D, ps, Hq=H * G, seed=42, v_size=0.7 * 2.0 ** -90)
+    u.cache = Cache(*u.dev, H * G, prompt_bytes=room)
+    Q = strided(np.random.default_rng(43).standard_normal((sum(rows), H * G, D)).astype(F), dtype)
+    O = torch.empty_like(Q)
+    u.cache.attend(Q, O, u.len, u.pages, offsets=offsets_of(rows), max_new=max(rows))
+    o, A, S = (x * 2.0 ** 90 if k < 2 else x for k, x in enumerate(plain_attend(u, as_np(Q), rows, D ** -0.5, 0)))
+    got = O.double().cpu().numpy() * 2.0 ** 90
+    assert (np.abs(got - o) <= tolerance(o, A, S, dtype)).all()
+    assert u.cache.status() == mlora.MLORA_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_block_of_denormal_rows_beside_normal_ones(rows, dtype):
+    """As the append stores it: a scale of some 1e-40 and codes of 0."""
+    u = Setup([96], 1, 64, 32, Hq=2, seed=44)
+    x = np.random.default_rng(45).standard_normal((96, 1, 64)).astype(F)
+    x[32:64] *= F(1e-38)
+    K = strided(x, dtype)
+    u.cache.append(K, K, u.len, u.pages, offsets=offsets_of([96]), max_new=96)
+    u.kc, u.ks, u.vc, u.vs = (t.cpu().numpy() for t in u.dev)
+    assert 0 < u.vs[u.table[0, 1], 0] < 1e-39 and not u.vc[u.table[0, 1]].any()
+    check_attend(u, [rows], dtype)
