@@ -144,6 +144,8 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     if (e == cudaSuccess) e = attend_prompt_init();
     if (e == cudaSuccess && !(encode_codes(&c->attend.k16, k_codes, c->pages) && encode_codes(&c->attend.v16, v_codes, c->pages)))
         e = cudaErrorInvalidValue;
+    // the memset is queued on the legacy stream, which other streams need not wait for
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     c->attend.counters = (int*)(c->ws + 256);
     c->attend.partial = (float*)(c->ws + head);
     c->attend.sms = sms;

@@ -74,3 +74,24 @@ def test_a_block_of_denormal_rows_beside_normal_ones(rows, dtype):
     u.kc, u.ks, u.vc, u.vs = (t.cpu().numpy() for t in u.dev)
     assert 0 < u.vs[u.table[0, 1], 0] < 1e-39 and not u.vc[u.table[0, 1]].any()
     check_attend(u, [rows], dtype)
+
+
+# ---- creation --------------------------------------------------------------------- #
+@pytest.mark.parametrize("rows,lengths,G", [([1, 1], [3000, 2500], 4), ([30], [2500], 4)])
+def test_a_new_cache_may_be_used_on_any_stream_at_once(rows, lengths, G):
+    """Its workspace is cleared when the call returns, however much is queued on the default stream:
+    attention split over many CTAs (their arrivals are counted in it) on a stream that waits for none."""
+    u = Setup(lengths, 1, 128, 64, Hq=G, seed=47)
+    Q = strided(np.random.default_rng(48).standard_normal((sum(rows), G, 128)).astype(F), "bf16")
+    want, off = torch.empty_like(Q), offsets_of(rows)
+    u.cache.attend(Q, want, u.len, u.pages, offsets=off, max_new=max(rows))
+    side = torch.cuda.Stream()
+    got = [torch.zeros_like(Q) for _ in range(4)]
+    torch.cuda.synchronize()
+    for o in got:
+        torch.cuda._sleep(20_000_000)       # some 10 ms on the default stream
+        cache = Cache(*u.dev, G)
+        assert torch.cuda.default_stream().query()
+        cache.attend(Q, o, u.len, u.pages, offsets=off, max_new=max(rows), stream=side)
+        assert cache.status(side) == mlora.MLORA_OK
+    assert all(torch.equal(o, want) for o in got)
