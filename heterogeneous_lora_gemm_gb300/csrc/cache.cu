@@ -34,6 +34,7 @@ mlora_status fail(mlora_status s, const char* fmt, ...) {
 }
 
 mlora_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();   // reported here: not the next launch's error
     return fail(MLORA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
@@ -153,6 +154,7 @@ mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, fl
     c->attend.operands = (uint8_t*)(c->ws + head + slots + table);
     c->attend.operand_bytes = operands;
     if (e != cudaSuccess) {
+        cudaGetLastError();   // (as in cuda_fail)
         if (c->ws) cudaFree(c->ws);
         delete c;
         return e == cudaErrorMemoryAllocation ? fail(MLORA_ERR_OOM, "workspace: %s", cudaGetErrorString(e))

@@ -38,6 +38,7 @@ mlora_status fail(mlora_status s, const char* fmt, ...) {
 }
 
 mlora_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();   // reported here: not the next launch's error
     return fail(MLORA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
@@ -404,6 +405,7 @@ mlora_status mlora_pool_create(int max_slots, int rank_budget, int max_rank, int
     p->slots.assign(max_slots, SlotHost{});
 
     auto bail = [&](mlora_status s) {
+        cudaGetLastError();   // (as in cuda_fail)
         mlora_pool_destroy(p);
         return s;
     };
@@ -713,6 +715,7 @@ mlora_status mlora_host_adapter_add(mlora_pool_t p, int id, const void* down, co
     ha.scale = scale;
     const size_t db = (size_t)ha.rpad * p->din * p->esize, ub = (size_t)ha.rpad * p->dout * p->esize;
     auto drop = [&](mlora_status s) {
+        cudaGetLastError();   // (as in cuda_fail)
         if (ha.down) cudaFreeHost(ha.down);
         if (ha.up) cudaFreeHost(ha.up);
         if (ha.busy) cudaEventDestroy(ha.busy);

@@ -95,3 +95,16 @@ def test_a_new_cache_may_be_used_on_any_stream_at_once(rows, lengths, G):
         cache.attend(Q, o, u.len, u.pages, offsets=off, max_new=max(rows), stream=side)
         assert cache.status(side) == mlora.MLORA_OK
     assert all(torch.equal(o, want) for o in got)
+
+
+@pytest.mark.parametrize("what", ["cache", "pool"])
+def test_a_creation_that_fails_leaves_the_next_calls_alone(what):
+    """Out of memory is the answer to that call, and not to the next launch."""
+    u = Setup([20], 1, 64, 16, seed=46)
+    with pytest.raises(mlora.MloraError) as e:
+        if what == "cache":    # a workspace for 2^30 tokens of 256 elements: over a terabyte
+            mlora.mlora_cache_create(*[t.data_ptr() for t in u.dev], 1 << 26, 16, 1, 256, 1, 1 << 62)
+        else:                  # 2^20 rank units of 2^20 elements: two
+            mlora.mlora_pool_create(1, 1 << 20, 16, 1 << 20, 64, mlora.MLORA_BF16, 16)
+    assert e.value.status == mlora.MLORA_ERR_OOM
+    check_attend(u, [1], "bf16")
