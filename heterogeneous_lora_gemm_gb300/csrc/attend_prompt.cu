@@ -470,14 +470,14 @@ __device__ __forceinline__ void put_scales(float* sc, int w, float ks, float vs)
     sc[16 + w] = none ? 1.f : 1.f / up;
 }
 
-// Token tiles of a sequence that its rows see.
+// Token tiles of a sequence that its rows see, from token `lo` on.
 struct Span {
-    int j0, j1;
+    int j0, j1, lo;
 };
 template <int KT>
 __device__ __forceinline__ Span span_of(const SeqRec& s, int window) {
     const int tb = s.start + s.rows, ta = first_seen(s.start, window);
-    return tb > ta ? Span{ta / KT, (tb + KT - 1) / KT} : Span{0, 0};
+    return tb > ta ? Span{ta / KT, (tb + KT - 1) / KT, ta} : Span{0, 0, 0};
 }
 
 constexpr int PRE_THREADS = 32 * CONV;
@@ -520,8 +520,9 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
     if (!here) return;
     for (int i = blockIdx.x; i < mine * H; i += gridDim.x) {
         const int j = p.j0 + i / H, h = i % H, tk = j * Sh::KT + Piece<DP>::piece(warp) * 16;
-        const int id = tk < s.start + s.rows ? load_page(a.step, c, b, tk / c.page, a.status) : -1;
-        const int place = tk % c.page;
+        // (no page is looked up that holds no token that is seen)
+        const int blk = tk / c.page, place = tk % c.page;
+        const int id = tk < s.start + s.rows && blk >= p.lo / c.page ? load_page(a.step, c, b, blk, a.status) : -1;
         const float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
         const size_t slot = (size_t)(before + j - p.j0) * H + h;
         uint8_t* to = operands + slot * 2 * Sh::OPER;
@@ -1030,7 +1031,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         };
         auto scale = [&](const float* p, int id) { return id >= 0 ? p[(size_t)id * H + h] : 0.f; };
         Piece<DP> k, v;
-        int id = next_id();
+        int id = blk >= first_seen(pos_lo, a.window) / c.page ? next_id() : -1;   // (pages that no row sees: of the first tile)
         k.load(c.k_codes, c, id, h, place, w, lane);
         v.load(c.v_codes, c, id, h, place, w, lane);
         float ks = scale(c.k_scale, id), vs = scale(c.v_scale, id);

@@ -334,7 +334,9 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         int row, row1;
         float ks, vs, ks1 = 0.f, vs1 = 0.f;
         {
-            const int t = token_at(my_k) + my_off, t1 = token_at(BATCH + my_k) + my_off, id = id_at(my_k, t);
+            const int t = token_at(my_k) + my_off, t1 = token_at(BATCH + my_k) + my_off;
+            // (nor before the first that it sees: where a window begins, in the first chunk)
+            const int id = t + PIECE > first_seen(pos_lo, a.window) ? id_at(my_k, t) : -1;
             id1 = id_at(BATCH + my_k, t1);
             row = row_of(id, t), row1 = row_of(id1, t1);
             ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;

@@ -432,7 +432,9 @@ mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_stream_t st
  *   lengths  [n_seqs]: tokens sequence b holds once the step is appended; its n_b rows
  *            are its last ones, at positions lengths[b] - n_b .. lengths[b] - 1
  *   pages    [n_seqs][width]: page of each block of page_size tokens; entries past
- *            ceil(lengths[b] / page_size) are not read
+ *            ceil(lengths[b] / page_size) are not read, and under a window (attend) none before
+ *            the block of the first token that one of the step's rows sees, so that a page
+ *            whose tokens have all left the window may be given to another sequence
  *   max_new  >= every n_b (host; it sizes the launch)
  * with n_seqs <= 65535 and width * page_size <= 2^30.
  * Rows at negative positions (lengths[b] < n_b: a padded slot of a batch, a left-padded

@@ -108,3 +108,29 @@ def test_a_creation_that_fails_leaves_the_next_calls_alone(what):
             mlora.mlora_pool_create(1, 1 << 20, 16, 1 << 20, 64, mlora.MLORA_BF16, 16)
     assert e.value.status == mlora.MLORA_ERR_OOM
     check_attend(u, [1], "bf16")
+
+
+# ---- pages that no row sees any more ------------------------------------------ #
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("left", ["none", "not a number"])
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,window,room", [
+    ([1, 1, 1], [300, 64, 65], 2, 2, 96, 16, 40, 0),           # 16 tokens of a copied 32 lie behind the window
+    ([1, 3], [1000, 700], 1, 4, 128, 32, 100, 0),
+    ([1], [5000], 1, 3, 256, 16, 1000, 0),
+    ([150, 20], [400, 300], 2, 3, 80, 32, 100, 0),             # prompts: 32 or more of 128
+    ([40], [700], 1, 2, 128, 64, 130, 0),
+    ([300], [2000], 1, 1, 256, 16, 500, 0),
+    ([20], [1500], 1, 4, 64, 48, 77, 0),
+    ([250, 60], [2250, 500], 1, 16, 128, 64, 150, 256 << 20),  # and converted ahead
+])
+def test_pages_behind_the_window_are_not_read(rows, lengths, H, G, D, ps, window, room, left, dtype):
+    """Their entries in the page table hold no page, or one with scales that are not numbers."""
+    u = Setup(lengths, H, D, ps, Hq=H * G, seed=51)
+    free = next(p for p in range(u.n_pages) if p not in u.table)
+    assert np.isnan(u.vs[free]).all()
+    for t, n, length in zip(u.table, rows, lengths):
+        t[:max(0, length - n - window + 1) // ps] = -1 if left == "none" else free
+    assert (u.table == (-1 if left == "none" else free)).sum() > 2
+    u.upload()
+    u.cache = Cache(*u.dev, H * G, prompt_bytes=room)
+    check_attend(u, rows, dtype, window)
