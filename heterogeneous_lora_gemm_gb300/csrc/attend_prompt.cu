@@ -579,8 +579,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     const int parts = max(1, min((int)gridDim.z, all * KT / PART));
     if (part >= parts) return;
     if (parts > 1) {   // this CTA's part of them
-        const int from = ta + all * part / parts * KT;
-        tb = min(tb, ta + all * (part + 1) / parts * KT);
+        auto edge = [&](int z) { return ta + (all / parts * z + all % parts * z / parts) * KT; };   // all z / parts: past 2^31
+        const int from = edge(part);
+        tb = min(tb, edge(part + 1));
         ta = from;
     }
     const int nt = tb > ta ? (tb - ta + KT - 1) / KT : 0;      // conversions

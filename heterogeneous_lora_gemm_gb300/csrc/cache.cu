@@ -220,6 +220,8 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     if (!run) return MLORA_OK;
     if ((long long)s.max_new * (c->q_heads / c->pages.heads) > 1 << 30)
         return fail(MLORA_ERR_UNSUPPORTED, "%d rows of %d heads per key head", s.max_new, c->q_heads / c->pages.heads);
+    if ((long long)s.max_new * c->q_heads > 1ll << 34)   // (row tiles x heads are counted in 32 bits)
+        return fail(MLORA_ERR_UNSUPPORTED, "%d rows of %d heads", s.max_new, c->q_heads);
     if ((st = check_rows("Q", Q, q_row, q_head, dtype)) != MLORA_OK) return st;
     if ((st = check_rows("O", O, o_row, o_head, dtype)) != MLORA_OK) return st;
     DeviceGuard g(c->device);

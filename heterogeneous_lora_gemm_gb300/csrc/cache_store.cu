@@ -101,7 +101,7 @@ __device__ __forceinline__ float value_of(const uint32_t (&w)[4], int e) {
     return __uint_as_float(__byte_perm(w[e / 4] ^ 0x80808080u, 0x4B000000u, 0x7650 | (e & 3))) - 8388736.f;
 }
 
-__device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
+__device__ __forceinline__ int floor_div(int a, int b) { return a / b - (a % b < 0 ? 1 : 0); }
 
 // The largest value over a group of threads (a warp or the CTA); NaN if one is NaN.
 template <int GROUP>
@@ -128,9 +128,10 @@ __global__ void __launch_bounds__(THREADS, (APPEND_CTAS<T, HELD>)) append_kernel
     if (h >= c.heads) return;
     const SeqRec q = load_seq(s, c.page, b, status);
     const int start = q.start < 0 ? 0 : q.start, skip = start - q.start;   // rows at negative positions
-    const int j = start / c.page + (int)blockIdx.x;
+    const int j = start / c.page + (int)blockIdx.x, end = q.start + q.rows;
+    if ((long long)j * c.page >= end) return;   // (the launch covers max_new rows, of up to 2^31)
     const int lo = max(start - j * c.page, 0);                              // tokens of the block held before
-    const int hi = min(q.start + q.rows - j * c.page, c.page);              // and after
+    const int hi = min(end - j * c.page, c.page);                           // and after
     if (hi <= lo || q.rows <= skip) return;
     const int id = load_page(s, c, b, j, status);
     if (id < 0) return;
@@ -217,10 +218,11 @@ __device__ __forceinline__ void read_block(const CachePages& c, const CacheStep&
                                            bool is_v, int b, int h, int x, const Divide& per_row, uint32_t* status) {
     const int t = threadIdx.x % GROUP;
     const int j = floor_div(q.start, c.page) + x;   // negative: rows that name no token
-    const int lo = max(q.start - j * c.page, 0), hi = min(q.start + q.rows - j * c.page, c.page);
+    const long long first = (long long)j * c.page;  // its first position, perhaps outside 32 bits
+    const int lo = (int)max(q.start - first, 0ll), hi = (int)min(q.start + q.rows - first, (long long)c.page);
     if (hi <= lo) return;
     const int id = j >= 0 ? load_page(s, c, b, j, status) : -1;
-    T* dst = (T*)R.ptr + (q.row0 + (j * c.page + lo - q.start)) * R.row + h * R.head;
+    T* dst = (T*)R.ptr + (q.row0 + (first + lo - q.start)) * R.row + h * R.head;
     const size_t at = (size_t)(id < 0 ? 0 : id) * c.heads + h;
     const int8_t* src = (is_v ? c.v_codes : c.k_codes) + (at * c.page + lo) * c.dim;
     const int n = (hi - lo) * per_row.d;
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, READ_CTAS) read_kernel(CachePages c, 
 }
 
 // Blocks that max_new consecutive positions can touch.
-int most_blocks(int max_new, int page) { return (max_new + page - 2) / page + 1; }
+int most_blocks(int max_new, int page) { return (int)(((long long)max_new + page - 2) / page) + 1; }
 
 template <int GROUP, typename Rows, typename Kernel>
 cudaError_t launch(Kernel kernel, int blocks, const CachePages& c, const CacheStep& s, const Rows& k, const Rows& v,

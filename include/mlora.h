@@ -506,7 +506,8 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, value
  * scales under 2^-96 lose low bits, under 2^-120 they may count as 0); O is rounded
  * once.  O must not overlap Q: fp32 rows of it may hold sums during the call.
- * Errors: INVALID_ARG, UNSUPPORTED (max_new * q_heads / kv_heads > 2^30), CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (with max_new taken as T where it is larger: max_new *
+ * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34), CUDA.
  */
 mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_row_stride, int64_t q_head_stride,
                                 void* O, int64_t o_row_stride, int64_t o_head_stride, mlora_dtype dtype, int T,

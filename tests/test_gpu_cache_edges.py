@@ -134,3 +134,62 @@ def test_pages_behind_the_window_are_not_read(rows, lengths, H, G, D, ps, window
     u.upload()
     u.cache = Cache(*u.dev, H * G, prompt_bytes=room)
     check_attend(u, rows, dtype, window)
+
+
+# ---- sizes near 2^31 -------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("length", [700, 2 ** 30])
+def test_append_and_read_launched_for_2_31_rows(length, dtype):
+    """Five rows of a step that may hold 2^31 - 1 (one row of memory), at the end of a sequence."""
+    ps, D, T = 256, 16, 2 ** 31 - 1
+    table = torch.full((1, 2 ** 30 // ps), -1, dtype=torch.int32, device="cuda")   # (one block is touched)
+    table[0, (length - 1) // ps] = 1
+    shape = (3, 1, ps, D)
+    pages = [torch.zeros(shape, dtype=torch.int8, device="cuda"), torch.zeros(shape[:2], device="cuda")]
+    pages += [t.clone() for t in pages]
+    cache = Cache(*pages, 1)
+    row = strided(np.random.default_rng(49).standard_normal((1, 1, D)).astype(F), dtype)
+    step = dict(lengths=torch.tensor([length], dtype=torch.int32, device="cuda"), pages=table, offsets=offsets_of([5]))
+    K = row.expand(T, 1, D)
+    cache.append(K, K, **step, max_new=T)
+    place = slice((length - 5) % ps, (length - 5) % ps + 5)
+    q = torch.clamp(torch.round(row[0, 0].float() / (row.float().abs().max() / 127)), -127, 127)
+    for codes, scale in ((pages[0], pages[1]), (pages[2], pages[3])):
+        assert torch.equal(codes[1, 0, place].float(), q.expand(5, D))
+        assert torch.count_nonzero(codes) == 5 * torch.count_nonzero(q) and torch.count_nonzero(scale) == 1
+    back = torch.full_like(row, 7.0)
+    cache.read(back.expand(T, 1, D), back.expand(T, 1, D), **step, max_new=T)   # (five equal rows into one)
+    assert torch.equal(back[0, 0], (q * pages[1][1]).to(back.dtype))
+    assert cache.status() == mlora.MLORA_OK
+
+
+def test_attention_of_more_row_tiles_than_32_bits_count_is_refused():
+    shape = (2, 1025, 16, 16)
+    pages = [torch.zeros(shape, dtype=torch.int8, device="cuda"), torch.zeros(shape[:2], device="cuda")]
+    cache = Cache(*pages, *pages, 1025)
+    Q = torch.zeros((1, 1, 16), device="cuda").expand(2 ** 30, 1025, 16)
+    with pytest.raises(mlora.MloraError) as e:
+        cache.attend(Q, Q, torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                     offsets=offsets_of([1]), max_new=2 ** 30)
+    assert e.value.status == mlora.MLORA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows,dtype,off", [(1, "bf16", 2.0 ** -7), (1, "f32", 2.0 ** -7), (20, "bf16", 0.06), (20, "f32", 2.0 ** -7)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_over_2_30_tokens(rows, dtype, off, D):
+    """Blocks that are all one page, under equal weights: the mean of its values.  At the most 2^30 / 152
+    tokens are summed in one place.  The tensor cores cut sums off at every 16 tokens: 2^-23 of the sum so
+    far at 441000 of them for prompts of bf16 rows, 5.3%; single tokens' sums are a twelfth as long
+    (2^30 / (304 x 4) tokens: 55000 times, 0.7%), and fp32 rows' are taken out of the tensor cores."""
+    ps, L = 256, 2 ** 30
+    rng = np.random.default_rng(50)
+    codes = torch.from_numpy(rng.integers(60, 128, (2, 1, ps, D)).astype(np.int8)).cuda()
+    scale = torch.full((2, 1), 2.0 ** -7, device="cuda")
+    cache = Cache(codes, scale, codes, scale, 1)
+    table = torch.ones((1, L // ps), dtype=torch.int32, device="cuda")
+    Q = torch.zeros((rows, 1, D), dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+    O = torch.full_like(Q, float("nan"))
+    cache.attend(Q, O, torch.tensor([L], dtype=torch.int32, device="cuda"), table, offsets=offsets_of([rows]), max_new=rows)
+    want = codes[1, 0].double().mean(0) * 2.0 ** -7
+    assert ((O[:, 0].double() - want).abs() <= off * want).all()
+    assert cache.status() == mlora.MLORA_OK
