@@ -869,6 +869,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 }
                 for (bool move = !edge || i == 0; !done; move = true) {
                     if (move) {
+                        // (fp32 rows: the lower terms of weights that are dropped land before the next ones')
+                        if constexpr (F32) tmem_wait_st();
                         const float mx = row_max(sat, sc, qf, lo - t0, hi - t0);
                         const float now = above ? fmaxf(mx, m) : m, f = ex2(m - now);
                         m = now;

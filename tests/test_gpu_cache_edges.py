@@ -193,3 +193,21 @@ def test_attention_over_2_30_tokens(rows, dtype, off, D):
     want = codes[1, 0].double().mean(0) * 2.0 ** -7
     assert ((O[:, 0].double() - want).abs() <= off * want).all()
     assert cache.status() == mlora.MLORA_OK
+
+
+# ---- bounds that move at every step --------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,lengths,G,D,ps", [([150], [2500], 2, 128, 64), ([40, 90], [1500, 800], 1, 64, 64),
+                                                 ([140], [1000], 2, 96, 16), ([1, 1], [2500, 900], 4, 128, 64)])
+def test_scores_that_outgrow_the_bound_at_every_step(rows, lengths, G, D, ps, dtype):
+    """Block after block whose scores lie some 13 above the last one's: the weights that a step first
+    takes are of up to 2^19 and more, and dropped."""
+    u = Setup(lengths, 1, D, ps, Hq=G, seed=52)
+    sign = np.where(np.random.default_rng(53).integers(0, 2, D) > 0, 1, -1)
+    u.kc = (sign * np.random.default_rng(54).integers(115, 128, u.kc.shape)).astype(np.int8)
+    for t in u.table:
+        for j, page in enumerate(t[t >= 0]):
+            u.ks[page] = 13.0 * (j + 1) / (121 * D ** 0.5)
+    u.upload()
+    q = np.random.default_rng(55).uniform(0.9, 1.1, (sum(rows), G, D)).astype(F) * sign.astype(F)
+    check_attend(u, rows, dtype, q=q)
