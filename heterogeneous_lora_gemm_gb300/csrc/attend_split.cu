@@ -63,7 +63,8 @@ struct Shape {
     static constexpr int STAGE = SUB * PART;
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
-    static constexpr int STAGES = (OCC == 3 ? 64 : 96) * 1024 / WARPS / STAGE;
+    // (64 KB of ring also where the queries' fragments leave no more: 16 fp32 rows of up to 256 elements)
+    static constexpr int STAGES = (OCC == 3 || (F32 && DP == 256 && NT == 2) ? 64 : 96) * 1024 / WARPS / STAGE;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
     static constexpr int SMEM = 1024 + RING + QWORDS * 4;
@@ -722,6 +723,8 @@ cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     using Sh = Shape<F32, DP, NT>;
     static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace slots");
+    // ranges are cut for OCC CTAs on each SM (of 228 KB, 1 KB of it the system's per CTA)
+    static_assert(Sh::OCC * (Sh::SMEM + (int)sizeof(Tail) + 1024) <= 228 * 1024, "resident CTAs");
     attend_split_kernel<F32, DP, NT><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters);
     return cudaGetLastError();
 }
