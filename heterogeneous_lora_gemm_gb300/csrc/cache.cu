@@ -248,4 +248,13 @@ mlora_status mlora_cache_status(mlora_cache_t c, mlora_stream_t stream) {
     return MLORA_OK;
 }
 
+mlora_status mlora_debug_cache_expire_wait(mlora_cache_t c, long long cycles, mlora_stream_t stream) {
+    if (!c) return fail(MLORA_ERR_INVALID_ARG, "cache is NULL");
+    if (cycles < 1 || cycles > (1ll << 31)) return fail(MLORA_ERR_INVALID_ARG, "cycles not in [1, 2^31]");
+    DeviceGuard g(c->device);
+    if (g.err != cudaSuccess) return cuda_fail(g.err, "cudaSetDevice");
+    CU_TRY(launch_expired_wait((uint32_t*)c->ws, cycles, (cudaStream_t)stream));
+    return MLORA_OK;
+}
+
 }  // extern "C"

@@ -108,5 +108,7 @@ cudaError_t launch_merge_nf4(bool bf16, uint8_t* q, float* absmax, const float* 
 cudaError_t launch_merge_simt(bool bf16, void* W, const SlotRec* slots, int slot,
                               const void* arena_down, const void* arena_up, const PoolDims& d, float sign,
                               cudaStream_t st);
+// Test hook (noalloc.cu): a kernel whose one pipeline wait gives up after `limit` cycles.
+cudaError_t launch_expired_wait(uint32_t* status, long long limit, cudaStream_t st);
 
 }  // namespace mlora

@@ -124,7 +124,7 @@ namespace {
 // One pipeline wait that nothing completes: an mbarrier expecting one arrival that
 // never comes, waited on with the kernels' bounded wait and the given limit.  Its
 // expiry raises STATUS_TIMEOUT in `status`, as a real pipeline wait that gave up would.
-__global__ void noalloc_expire_wait_kernel(uint32_t* status, long long limit) {
+__global__ void expire_wait_kernel(uint32_t* status, long long limit) {
     __shared__ __align__(8) uint64_t bar;
     __shared__ int abort_flag;
     if (threadIdx.x != 0) return;
@@ -135,6 +135,12 @@ __global__ void noalloc_expire_wait_kernel(uint32_t* status, long long limit) {
 }
 
 }  // namespace
+
+cudaError_t launch_expired_wait(uint32_t* status, long long limit, cudaStream_t st) {
+    expire_wait_kernel<<<1, 32, 0, st>>>(status, limit);
+    return cudaGetLastError();
+}
+
 }  // namespace mlora
 
 extern "C" mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_stream_t stream) {
@@ -147,8 +153,7 @@ extern "C" mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_
     mlora_status st = noalloc_setup(dev, &base);
     if (st != MLORA_OK) return st;
     uint32_t* status = (uint32_t*)((char*)base + NOALLOC_PARTIAL_BYTES + NOALLOC_MAX_TILES * sizeof(int32_t));
-    noalloc_expire_wait_kernel<<<1, 32, 0, (cudaStream_t)stream>>>(status, cycles);
-    e = cudaGetLastError();
+    e = launch_expired_wait(status, cycles, (cudaStream_t)stream);
     if (e != cudaSuccess) return noalloc_fail(MLORA_ERR_CUDA, std::string("launch: ") + cudaGetErrorString(e));
     return MLORA_OK;
 }

@@ -91,6 +91,7 @@ _SIGNATURES = {
     "mlora_cache_read": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
     "mlora_cache_attend": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, ctypes.c_float, _I, _P]),
     "mlora_cache_status": (_I, [_P, _P]),
+    "mlora_debug_cache_expire_wait": (_I, [_P, ctypes.c_longlong, _P]),
     "mlora_arena_new": (_P, [_I]),
     "mlora_arena_delete": (None, [_P]),
     "mlora_arena_alloc": (_I, [_P, _I, _I]),
@@ -315,6 +316,10 @@ def mlora_cache_status(cache: int, stream: int) -> int:
     if s not in (MLORA_OK, MLORA_ERR_DEVICE_STEP, MLORA_ERR_DEVICE_TIMEOUT):
         check(s, "mlora_cache_status")
     return s
+
+
+def mlora_debug_cache_expire_wait(cache: int, cycles: int, stream: int) -> None:
+    check(lib().mlora_debug_cache_expire_wait(cache, int(cycles), stream or None), "mlora_debug_cache_expire_wait")
 
 
 # ---- torch-facing convenience ------------------------------------------- #

@@ -520,6 +520,8 @@ mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_ro
  * that call's output is not valid) or MLORA_ERR_CUDA.
  */
 mlora_status mlora_cache_status(mlora_cache_t cache, mlora_stream_t stream);
+/* Test hook for that status, as mlora_debug_noalloc_expire_wait. Errors: INVALID_ARG, CUDA. */
+mlora_status mlora_debug_cache_expire_wait(mlora_cache_t cache, long long cycles, mlora_stream_t stream);
 
 /*
  * Host-only view of the arena allocator the pool uses (no CUDA calls), for tests

@@ -211,3 +211,23 @@ def test_scores_that_outgrow_the_bound_at_every_step(rows, lengths, G, D, ps, dt
     u.upload()
     q = np.random.default_rng(55).uniform(0.9, 1.1, (sum(rows), G, D)).astype(F) * sign.astype(F)
     check_attend(u, rows, dtype, q=q)
+
+
+# ---- waits that run out ------------------------------------------------------------------ #
+def test_an_expired_wait_is_reported_until_read():
+    """A pipeline wait that gives up (one that nothing completes, bounded to about a millisecond) sets
+    the cache's status; later calls leave it set and are right, the status call reports and clears it."""
+    u = Setup([300, 17], 1, 64, 16, Hq=2, seed=56)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert u.cache.status() == mlora.MLORA_OK
+    mlora.mlora_debug_cache_expire_wait(u.cache.handle, 2_000_000, stream)
+    Q = strided(np.random.default_rng(57).standard_normal((2, 2, 64)).astype(F), "bf16")
+    O = torch.empty_like(Q)
+    u.cache.attend(Q, O, u.len, u.pages)
+    assert u.cache.status() == mlora.MLORA_ERR_DEVICE_TIMEOUT
+    assert u.cache.status() == mlora.MLORA_OK
+    assert torch.equal(O, check_attend(u, [1, 1], "bf16", q=as_np(Q)))
+    for cycles in (0, 2 ** 31 + 1):
+        with pytest.raises(mlora.MloraError) as e:
+            mlora.mlora_debug_cache_expire_wait(u.cache.handle, cycles, stream)
+        assert e.value.status == mlora.MLORA_ERR_INVALID_ARG
