@@ -75,6 +75,7 @@ static_assert(32 * (SOFT * REGS_SOFT + (CONV + 4) * REGS_REST) <= PROMPT_THREADS
 constexpr int FOLD = 16;                   // steps of fp32 rows between roundings of O into fp32 outside
 constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
 constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
+constexpr int MOST_DOWN = 114;             // queries are divided by 2^MOST_DOWN at most (scale 2^128 would leave fp32)
 constexpr float SMALL_SCALE = 0x1p-64f;    // value scales below it are brought up by 1 / SMALL_SCALE
 
 template <int DP, bool F32 = false>
@@ -674,8 +675,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 #pragma unroll
                         for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
                         const bool fine = top < 0x7F800000u;
-                        const int x = fine ? min(max((int)(top >> 23) - 126, -100), 127) : 0;
-                        const float down = fine ? __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f) : 0.f;
+                        const int x = fine ? min(max((int)(top >> 23) - 126, -100), MOST_DOWN) : 0;
+                        const float down = fine ? __uint_as_float((uint32_t)(127 - x) << 23) : 0.f;
                         float v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] = fine ? __uint_as_float(u[e]) * down : 0.f;
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                             v[3] -= __uint_as_float(y.y & 0xFFFF0000u);
                         }
                         if (chunk == 0)
-                            tl.qf[t][row] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                            tl.qf[t][row] = fine ? a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23)) : NAN;
                     }
                 }
                 fence_proxy_async_smem();
@@ -732,14 +733,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
 #pragma unroll
                         for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
                         const bool fine = top < 0x7F80u;
-                        const int x = fine ? min(max((int)(top >> 7) - 126, -100), 127) : 0;
-                        const float down = fine ? __uint_as_float((uint32_t)(127 - min(x, 126)) << 23) * (x > 126 ? 0.5f : 1.f) : 0.f;
+                        const int x = fine ? min(max((int)(top >> 7) - 126, -100), MOST_DOWN) : 0;
+                        const float down = fine ? __uint_as_float((uint32_t)(127 - x) << 23) : 0.f;
                         auto scaled = [&](uint32_t u) {
                             return fine ? bf2_of(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down) : 0u;
                         };
                         *to = make_uint4(scaled(w.x), scaled(w.y), scaled(w.z), scaled(w.w));
                         if (chunk == 0)
-                            tl.qf[t][row_at(k)] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23) : NAN;
+                            tl.qf[t][row_at(k)] = fine ? a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + x) << 23)) : NAN;
                     }
                 }
                 fence_proxy_async_smem();

@@ -373,18 +373,17 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
             fine = __all_sync(~0u, fine);
             top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));   // (>= 0: ordered like its bits)
-            // 2^-k with top 2^-k in [1/2, 1); top below 2^-100 counts as 2^-100
-            // (and above 2^127 stays in [1, 2))
-            const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 127) : 0;
-            const float down = __uint_as_float((uint32_t)(127 - min(k, 126)) << 23);
-            const float down2 = k > 126 ? 0.5f : 1.f;   // 2^-127 is not a normal number: two steps
+            // 2^-k with top 2^-k in [1/2, 1); top below 2^-100 counts as 2^-100, and one above 2^114
+            // stays below 2^14 (within fp16, where a factor of 2^128 would leave fp32)
+            const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 114) : 0;
+            const float down = __uint_as_float((uint32_t)(127 - k) << 23);
             if (lane == 0)
-                tl.qf[r] = fine ? a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
+                tl.qf[r] = fine ? a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23)) : NAN;
 #pragma unroll
             for (int e = 0; e < EL; e += 2) {
                 const int d = lane * EL + e, ch = d % 128 / 16, w = d % 16 / 4;
                 const int s = DP == 64 ? w : d / 128 * 8 + ch % 2 * 4 + w, t = DP == 64 ? ch : ch / 2;
-                const float v0 = fine ? x[kk][e] * down * down2 : 0.f, v1 = fine ? x[kk][e + 1] * down * down2 : 0.f;
+                const float v0 = fine ? x[kk][e] * down : 0.f, v1 = fine ? x[kk][e + 1] * down : 0.f;
                 const __half2 hi = __floats2half2_rn(v0, v1);
                 uint32_t* dst = qfrag + (((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + d % 4 / 2;
                 *dst = *reinterpret_cast<const uint32_t*>(&hi);

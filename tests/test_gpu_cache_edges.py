@@ -231,3 +231,17 @@ def test_an_expired_wait_is_reported_until_read():
         with pytest.raises(mlora.MloraError) as e:
             mlora.mlora_debug_cache_expire_wait(u.cache.handle, cycles, stream)
         assert e.value.status == mlora.MLORA_ERR_INVALID_ARG
+
+
+# ---- queries near the end of fp32 ---------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,lengths,D", [([1, 1], [300, 64], 128), ([131, 30], [200, 30], 128), ([40], [90], 64), ([20], [90], 256)])
+@pytest.mark.parametrize("scale", [0.1, 3.0, 1000.0])
+def test_the_largest_queries(rows, lengths, D, scale, dtype):
+    """Rows up to 2^128 beside rows of 2^100, and keys that bring the scores of the first to about 1."""
+    u = Setup(lengths, 1, D, 64, Hq=2, seed=58)
+    u.ks = np.where(np.isnan(u.ks), u.ks, F(2.0 ** -126 / scale / D ** 0.5 / 8) * (1 + u.ks)).astype(F)
+    u.upload()
+    q = np.random.default_rng(59).uniform(-2.0 ** 100, 2.0 ** 100, (sum(rows), 2, D))
+    q[::2] *= 2.0 ** 27.5
+    check_attend(u, rows, dtype, q=q.astype(F), scale=scale)
