@@ -263,13 +263,11 @@ __device__ __forceinline__ uint32_t bf16_codes(uint32_t u) {
     const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint2 widen(uint32_t w) {
-    return make_uint2(bf16_codes(__byte_perm(w, 0x43434343u, 0x4140)), bf16_codes(__byte_perm(w, 0x43434343u, 0x4342)));
-}
-// two bf16 times SMALL_SCALE
-__device__ __forceinline__ uint32_t bf16_small(uint32_t u) {
-    const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(SMALL_SCALE));
-    return *reinterpret_cast<const uint32_t*>(&h);
+// The upper byte, 0x43 for the codes themselves, holds seven bits of the exponent: 0x23 gives them
+// times SMALL_SCALE.
+constexpr uint32_t OVER = 0x43434343u, OVER_SMALL = 0x23232323u;
+__device__ __forceinline__ uint2 widen(uint32_t w, uint32_t over) {
+    return make_uint2(bf16_codes(__byte_perm(w, over, 0x4140)), bf16_codes(__byte_perm(w, over, 0x4342)));
 }
 // 16 bytes of global memory (zeros where `in` is false) into shared memory
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
@@ -280,15 +278,9 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // 16 codes of token t, elements 16 c .. of 64-element block blk, into an operand tile: DP / 64
 // blocks of KT rows of 128 bytes under the 128-byte swizzle.  (Lanes pair token t with t ^ 5,
 // so that the writes of a quarter warp, at (2 c + z) ^ t, do not meet in a bank.)
-// DOWN: times SMALL_SCALE.
-template <int KT, bool DOWN>
-__device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk, int c) {
-    auto values = [](uint32_t w) {
-        uint2 u = widen(w);
-        if (DOWN) u.x = bf16_small(u.x), u.y = bf16_small(u.y);
-        return u;
-    };
-    const uint2 a = values(x.x), b = values(x.y), d = values(x.z), e = values(x.w);
+template <int KT>
+__device__ __forceinline__ void convert16(uint4 x, uint8_t* dst, int t, int blk, int c, uint32_t over) {
+    const uint2 a = widen(x.x, over), b = widen(x.y, over), d = widen(x.z, over), e = widen(x.w, over);
     uint8_t* row = dst + blk * (KT * 128) + t * 128;
     *reinterpret_cast<uint4*>(row + (((2 * c) ^ (t & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
     *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (t & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
@@ -448,18 +440,16 @@ struct Piece {
         for (int u = 0; u < N; ++u) x[u] = make_uint4(0u, 0u, 0u, 0u);
     }
     // into operand tile `dst` (generic address)
-    template <bool DOWN = false>
-    __device__ __forceinline__ void store(uint8_t* dst, int w, int lane) const {
+    __device__ __forceinline__ void store(uint8_t* dst, int w, int lane, uint32_t over = OVER) const {
         const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), b0 = blk0(w);
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            convert16<Sh::KT, DOWN>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4);
+            convert16<Sh::KT>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4, over);
     }
     // values under scale vs (see put_scales)
     __device__ __forceinline__ void store_values(uint8_t* dst, int w, int lane, float vs) {
         if (no_values(vs)) zero();
-        if (vs < SMALL_SCALE) store<true>(dst, w, lane);
-        else store(dst, w, lane);
+        store(dst, w, lane, vs < SMALL_SCALE ? OVER_SMALL : OVER);
     }
 };
 // Scales of 16 tokens as the softmax takes them (see the top of the file).
