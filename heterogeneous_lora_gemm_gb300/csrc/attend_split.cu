@@ -306,7 +306,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (u1 <= u0) break;   // only the lead is in this range: the item is the next CTA's
         // positions that the tile's rows may see: row r at start + i0 + token_of(r)
         const int pos_lo = n.s.start + i0, pos_hi = pos_lo + token_of(rows - 1);
-        const int ca = max(n.c0 + u0 * WARPS, first_seen(pos_lo, a.window) / CHUNK_T);
+        const int seen_from = first_seen(pos_lo, a.window);
+        const int ca = max(n.c0 + u0 * WARPS, seen_from / CHUNK_T);
         const int cb = min(min(n.c0 + u1 * WARPS, n.c1), pos_hi >= 0 ? pos_hi / CHUNK_T + 1 : 0);
         const int count = max(0, (cb - ca - warp + WARPS - 1) / WARPS);   // this warp's chunks: ca + warp, + WARPS, ...
 
@@ -337,7 +338,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         {
             const int t = token_at(my_k) + my_off, t1 = token_at(BATCH + my_k) + my_off;
             // (nor before the first that it sees: where a window begins, in the first chunk)
-            const int id = t + PIECE > first_seen(pos_lo, a.window) ? id_at(my_k, t) : -1;
+            const int id = t + PIECE > seen_from ? id_at(my_k, t) : -1;
             id1 = id_at(BATCH + my_k, t1);
             row = row_of(id, t), row1 = row_of(id1, t1);
             ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;
