@@ -13,19 +13,24 @@
 // key/value tile serves both.
 //
 // Products run on tcgen05.mma in bf16, 128 rows x 64 tokens a step: S = Q K^T (queries and
-// codes exact), O += P V with P = 2^(x - m) vs (one rounding) from tensor memory.  Tensor
+// codes exact), O += P V with P = 2^(x - m) vs from tensor memory, rounded once to bf16: 8 bits,
+// where attend_split.cu has the room under its codes' stream for 16.  The row's sum takes the
+// rounded weights, so that an error of theirs is none of scale: 0.0019 against 64 bits, of which
+// rounding the output is 0.0017; a second term would add half of the products again, and a subtraction
+// and a conversion per weight to the softmax warps, whose chain is the bound.  The tensor cores also cut the sums of O off at every 16 tokens, which bf16
+// rows leave at that: of a sum of one sign 0.25% over 2^20 tokens, 0.9% over 2^21.  Tensor
 // memory, all 512 columns: two S of 64 columns per tile, so that a step's scores are ready
 // before the last step's weights are done (P lies over its S), and O of the two tiles (or of
 // one, of up to 256 columns).  fp32 rows run the same products over three bf16 terms of the
-// queries and of the weights (24 bits): 2 x 1000 rows of 16/8 heads of 128 take 62 us (266 us in
-// attend_split.cu), 8192 tokens of 32/8 heads 1670 us, 329 TFLOP/s or 990 of the terms' products.
-// The tensor cores cut their fp32 sums off at every 16 tokens, so that fp32 rows' O is taken out
-// every FOLD steps (118 x 6000 tokens: error against 64 bits 1.1e-6, 2.0e-6 with twice the steps, 5.6e-6
-// without, 1.4e-6 in plain fp32; 8192 tokens: 1670, 1485 and 1335 us).
+// queries and of the weights (24 bits): 2 x 1000 rows of 16/8 heads of 128 after 100 take 57 us (266 us
+// in attend_split.cu), 8192 tokens of 32/8 heads 1640 us, 335 TFLOP/s or 1000 of the terms' products.
+// Their O is taken out of the tensor cores every FOLD steps (118 x 6000 tokens: error against 64 bits
+// 1.1e-6, 2.0e-6 with twice the steps, 5.6e-6 without, 1.4e-6 in plain fp32; 8192 tokens 1670, 1485 and
+// 1335 us, when measured).
 //
 // Bound: the products, 2 x 2 x 128 x 64 x head_dim operations per tile and step.  8192 tokens of
-// 32/8 heads of 128 take 376 us, 1460 TFLOP/s; 4096 take 122 us, 1120 TFLOP/s (the tensor pipe is
-// busy 61% of the time, the issue slots of the softmax warps half of it).  A step takes 1500
+// 32/8 heads of 128 take 380 us, 1450 TFLOP/s; 4096 take 121 us, 1130 TFLOP/s (the tensor pipe is
+// busy 55% of the time, tensor memory 61%, the issue slots 47%).  A step takes 1500
 // cycles, of which the products could do with 1280: half of the exponentials or half of the
 // products left out changes it by 2%, the weights' sum left out by 6%: what counts is a softmax
 // warp's own chain of some 300 instructions.  A row tile's start and end take 9000 cycles.
@@ -42,7 +47,7 @@
 //
 // Where row tiles are fewer than half the SMs, each one's tokens are cut into equal parts, a CTA
 // each; the CTA that finishes a row tile last joins the parts, in their order (300 tokens after
-// 5000 of one sequence: 49 us).
+// 5000 of one sequence: 46 us).
 //
 // Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
 // operand tiles or 8-15 read codes and convert them into keys and values in bf16 (tokens as rows; the
@@ -1172,11 +1177,12 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
 }
 
 // From 17 rows of a sequence and head on (fp32 rows of more than 128 elements excepted: their
-// terms outgrow shared memory): at 6 tokens of 32/8 heads after 4000 tokens (2000
-// where they are 64 sequences), 1, 16 and 64 sequences take 25, 60 and 127 us here and 22, 79 and
-// 145 us in attend_split.cu; at 4 tokens 25, 61 and 127 us against 22, 48 and 83 us.  fp32 rows:
-// 38, 129 and 265 against 49, 140 and 255 us, and at 12 tokens 134 against 243 us (16 sequences);
-// at 4 tokens some 35, 100 and 220 against 23, 52 and 95.
+// terms outgrow shared memory).  32/8 heads after 4000 tokens (2000 where they are 64 sequences), this
+// kernel against attend_split.cu, for 1, 16 and 64 sequences: bf16 rows at 6 tokens 25, 60, 127 us
+// against 22, 79, 145, at 4 tokens 25, 61, 127 against 22, 46, 81; fp32 rows at 6 tokens 38, 133, 267
+// against 49, 140, 255, at 12 tokens 134 against 243 (16 sequences), at 4 tokens 35, 100, 220 against
+// 24, 59, 104.  The rule knows neither the number of sequences nor the type: it costs one sequence of
+// bf16 rows 3 us and 64 of fp32 rows 12 us at 6 tokens.
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return (bf16 || a.pages.dim <= 128) && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }

@@ -19,7 +19,7 @@
 // fp16 terms (22 bits) and the weights as three bf16 terms (24 bits).
 //
 // Bound: HBM (the codes are read once per row tile): 32 sequences of 32k tokens, 32/8 heads of
-// 128, bf16, take 331 us, 6.4 TB/s; 4 sequences 150 us, 5.9 TB/s; 32 of 3 to 4k with as many key
+// 128, bf16, take 328 us, 6.5 TB/s; 4 sequences 150 us, 5.9 TB/s; 32 of 3 to 4k with as many key
 // heads as query heads 83 us, 5.1 TB/s; one short sequence 9.7 us, the chain of a CTA's start, a
 // range's loads and the join.  Each warp streams 32-token chunks
 // of its own through a private ring of TMA copies: no CTA-wide barrier in the loop.
@@ -63,7 +63,8 @@ struct Shape {
     static constexpr int STAGE = SUB * PART;
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
-    // (64 KB of ring also where the queries' fragments leave no more: 16 fp32 rows of up to 256 elements)
+    // (64 KB of ring also where the queries' fragments leave no more, 16 fp32 rows of up to 256 elements: 2 x
+    // 300 rows after 1000, 16/8 heads, 124 us, 188 us with the 96 KB that one CTA per SM has room for)
     static constexpr int STAGES = (OCC == 3 || (F32 && DP == 256 && NT == 2) ? 64 : 96) * 1024 / WARPS / STAGE;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
@@ -586,7 +587,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                                 // fp32 rows: the tensor cores' sums drop bits, so that 16 tokens are summed
                                 // there, the small terms first, and rounded into the long sum here (152
                                 // sequences of 16000 tokens: error against 64 bits 7.0e-6 without, 0.9e-6
-                                // with, 2.2e-6 in plain fp32; 16 x 8000 tokens, 32/8 heads: 61 and 67 us)
+                                // with, 2.2e-6 in plain fp32; 16 x 8000 tokens, 32/8 heads: 61 and 67 us when
+                                // measured, 65 us now)
 #pragma unroll
                                 for (int term = PTERMS - 1; term >= 0; --term)
                                     mma_bf(F32 ? part : to, y[0][2 * z], y[0][2 * z + 1], y[1][2 * z], y[1][2 * z + 1],

@@ -5,9 +5,10 @@
 // of threads takes one tile: one (sequence, block, head, keys or values), whose codes are
 // contiguous and whose rows are strided, in vectors of 16 elements.
 //
-// Bound: HBM, 3 bytes per bf16 element each way: 106k tokens of 8 heads of 128 are read in 104 us,
-// 6.3 TB/s; 30k tokens written and read back take 63 us, 5.8 TB/s; the rows of 256 sequences, 32
-// heads, written and the pages that they lie in read back take 47 us, 4.5 TB/s.  A tile's loads
+// Bound: HBM, 3 bytes per bf16 element each way: 106k tokens of 8 heads of 128 are read in 103 us,
+// 6.3 TB/s (fp32 231 us, 4.7 TB/s); 30k tokens written and read back take 63 us, 5.8 TB/s (fp32 123 us,
+// 4.9 TB/s); the rows of 256 sequences, 32 heads, written and the pages that they lie in read back
+// take 46 us, 4.5 TB/s (fp32 80 us).  A tile's loads
 // depend on the sequence's length, then on its page: small groups, each with all its loads in
 // flight at once, cover that chain.  A step of few rows (decode) gives a tile to a warp: it is one
 // row, and its time is the chain's.

@@ -1,6 +1,7 @@
 // PTX wrappers of the sm_103a tensor-core path: mbarrier, TMA (cp.async.bulk.tensor),
 // tcgen05 MMA / commit / TMEM loads, and the shared-memory matrix descriptors.
-// Used by the kernels in tc.cu and tc_prefill.cu.
+// Used by the kernels in tc.cu, tc_prefill.cu, merge_tc.cu, shrink_gemv.cu, attend_split.cu and
+// attend_prompt.cu, and by the test hook in noalloc.cu.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

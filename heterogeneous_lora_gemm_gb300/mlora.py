@@ -450,7 +450,8 @@ class Cache:
     offsets int32 [n_seqs + 1] or None (one row per sequence), max_new >= the rows of any
     sequence.  Rows are [T, heads, head_dim] bf16 or fp32, a head's elements adjacent
     (slices of a fused projection's output will do); 16-byte aligned.  prompt_bytes bounds the
-    workspace for prompts' keys and values in 16 bits.
+    workspace for prompts' keys and values in 16 bits; one cache serves all layers whose pages lie in one
+    array.
     """
 
     def __init__(self, k_codes, k_scale, v_codes, v_scale, q_heads: int, prompt_bytes: int = 256 << 20):

@@ -450,7 +450,8 @@ mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_stream_t st
  * strides multiples of 16 bytes.  The calls take a stream as described at the top of
  * this file; a cache, like a pool, serves one stream and one host thread at a time.
  * Attention may share pages between sequences; a page that is appended to belongs to
- * one sequence.
+ * one sequence.  Keys and values are rows of the adapted projection: a prefix may be shared
+ * only between sequences of one adapter, of one version of it, and not past its update.
  */
 typedef struct mlora_cache* mlora_cache_t;
 
@@ -466,6 +467,8 @@ typedef struct mlora_cache* mlora_cache_t;
  *              and all others, are converted again for every tile (0: always)
  * The handle allocates its workspace (a status word, the partial results of split
  * sequences, about 20 MB, and prompt_bytes) here; append, read and attend allocate nothing.
+ * One handle serves all layers of a model where their pages lie in one array (a page table
+ * per layer names them): the workspace is then there once, as one layer's step uses it at a time.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),
  * OOM, CUDA.  Argument checks run before any CUDA call.
  */
@@ -505,7 +508,10 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums
  * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, value
  * scales under 2^-96 lose low bits, under 2^-120 they may count as 0); O is rounded
- * once.  O must not overlap Q: fp32 rows of it may hold sums during the call.
+ * once.  Weights are held in 24 bits for fp32 rows and in 16 for bf16 rows, in 8 where
+ * max_new * q_heads / kv_heads > 16; in that form sums of one sign come out 0.25% low over
+ * 2^20 tokens, and lower over more.  O must not overlap Q: fp32 rows of it may hold sums
+ * during the call.
  * Errors: INVALID_ARG, UNSUPPORTED (with max_new taken as T where it is larger: max_new *
  * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34), CUDA.
  */
