@@ -1,4 +1,4 @@
-// Attention over the 8-bit cache: what the handle (cache.cu) keeps for its kernels.
+// Attention over the caches: what the handle (cache.cu) keeps for its kernels.
 #pragma once
 #include "cache.h"
 
@@ -9,7 +9,8 @@ constexpr int ATTEND_SLOT = 16 * (256 + 2); // floats of one partial result at m
 constexpr int PROMPT_SLOT = 256 * (128 + 2);// floats of one partial result of the prompt kernel (one per SM at most)
 
 struct AttendWs {
-    CUtensorMap k16, v16;   // codes as rows of head_dim bytes, boxes of 16 tokens
+    CUtensorMap k16, v16;   // 8-bit codes as rows of head_dim bytes, boxes of 16 tokens
+    const uint8_t* zeros;   // a 4-bit block of zeros
     float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT], or [sms][PROMPT_SLOT]
     int* counters;          // [sms * ATTEND_OCC] arrivals, zero between calls
     int sms;
@@ -18,11 +19,11 @@ struct AttendWs {
     int* operand_at;        // [n_seqs <= 65535] where a sequence's tiles are
 };
 
-cudaError_t attend_split_init();
+cudaError_t attend_split_init(int bits);
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
 
 // Sequences with many rows (attend_prompt.cu): bf16, and fp32 with heads of up to 128 elements.
-cudaError_t attend_prompt_init();
+cudaError_t attend_prompt_init(int bits);
 // Workspace for the converted tiles of `tokens` tokens.
 size_t attend_prompt_bytes(const CachePages& c, long long tokens);
 bool attend_prompt_takes(bool bf16, const AttendArgs& a);

@@ -1,4 +1,4 @@
-// Causal attention over the 8-bit cache for sequences with many rows in the step
+// Causal attention over the 8-bit and the 4-bit cache for sequences with many rows in the step
 // (prompts) (include/mlora.h).
 //
 // Mathematics as in attend_split.cu: x = scale ks (q . kc) log2 e, o = sum 2^(x - m) vs vc /
@@ -49,6 +49,10 @@
 // each; the CTA that finishes a row tile last joins the parts, in their order (300 tokens after
 // 5000 of one sequence: 46 us).
 //
+// The 4-bit cache (BITS 4, block4.cuh): a code times its scale is exact in bf16, so that the operand
+// tiles hold the values themselves, over a unit that goes into the scores' factor (on the host) and
+// into the output; tokens have no scales left.
+//
 // Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
 // operand tiles or 8-15 read codes and convert them into keys and values in bf16 (tokens as rows; the
 // second product reads them column-major), a warp per 16 tokens of 128 with the next 128
@@ -60,6 +64,7 @@
 #include <type_traits>
 
 #include "attend.h"
+#include "block4.cuh"
 #include "tc_ptx.cuh"
 
 namespace mlora {
@@ -314,6 +319,7 @@ __device__ __forceinline__ uint32_t column_mask(int lo, int hi) {
 
 // The largest x of a row's 64 scores, of columns [lo, hi) of them: the maximum of the raw
 // scores of each 16-token piece, times its factor.
+template <bool BARE>
 __device__ __forceinline__ float row_max(uint32_t sat, const float* sc, float qf, int lo, int hi) {
     float mx = -INFINITY;
 #pragma unroll 1
@@ -326,7 +332,7 @@ __device__ __forceinline__ float row_max(uint32_t sat, const float* sc, float qf
         float a = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; ++e) a = fmaxf(a, seen >> e & 1 ? __uint_as_float(y[e]) : -INFINITY);
-        mx = fmaxf(mx, a == -INFINITY ? -INFINITY : a * (qf * sc[g]));
+        mx = fmaxf(mx, a == -INFINITY ? -INFINITY : a * (BARE ? qf : qf * sc[g]));
     }
     return mx;
 }
@@ -335,7 +341,8 @@ __device__ __forceinline__ float row_max(uint32_t sat, const float* sc, float qf
 // the sum of what was rounded (without the value scales), so that a heavy token's rounding is
 // divided out again.  PG tokens share their scales: 16, or 64 where pages are multiples of it
 // (8192 tokens, 32/8 heads, pages of 64: 466 us with PG 64, 474 us with PG 16, when measured).
-template <bool EDGE, int PG>
+// BARE: tokens have no scales (4 bits).
+template <bool EDGE, int PG, bool BARE>
 __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float qf, float m, int lo, int hi,
                                           uint32_t (&y)[STEP]) {
     tmem_ld32(sat, y);
@@ -346,7 +353,8 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
     uint64_t sum = pair(0.f, 0.f);
 #pragma unroll
     for (int g = 0; g < STEP / PG; ++g) {
-        const float f = qf * sc[g * (PG / 16)], c = sc[8 + g * (PG / 16)] - m, v = sc[16 + g * (PG / 16)];
+        const float f = BARE ? qf : qf * sc[g * (PG / 16)], c = BARE ? -m : sc[8 + g * (PG / 16)] - m;
+        const float v = BARE ? 1.f : sc[16 + g * (PG / 16)];
         const uint64_t f2 = pair(f, f), c2 = pair(c, c);
         float l[2] = {0.f, 0.f};
 #pragma unroll
@@ -366,14 +374,14 @@ __device__ __forceinline__ uint64_t weigh(uint32_t sat, const float* sc, float q
                 y[i / 2] = w;
             }
         }
-        sum = fma2(pair(l[0], l[1]), pair(v, v), sum);
+        sum = BARE ? add2(pair(l[0], l[1]), sum) : fma2(pair(l[0], l[1]), pair(v, v), sum);
     }
     return sum;
 }
 
 // The same for fp32 rows, the weights as three bf16 terms (24 bits): the first into y, the others
 // into columns pat and pat + 32; the sum is that of the weights themselves.
-template <bool EDGE, int PG>
+template <bool EDGE, int PG, bool BARE>
 __device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const float* sc, float qf, float m, int lo, int hi,
                                            uint32_t (&y)[STEP]) {
     constexpr int N = PG < 32 ? PG : 32;
@@ -388,7 +396,7 @@ __device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const flo
 #pragma unroll
         for (int g = 0; g < 32; g += N) {
             const float* at = sc + half * 2 + g / 16;
-            const float f = qf * at[0], c = at[8] - m, v = at[16];
+            const float f = BARE ? qf : qf * at[0], c = BARE ? -m : at[8] - m, v = BARE ? 1.f : at[16];
             const uint64_t f2 = pair(f, f), c2 = pair(c, c);
             uint64_t l = pair(0.f, 0.f);
 #pragma unroll
@@ -408,7 +416,7 @@ __device__ __forceinline__ uint64_t weigh3(uint32_t sat, uint32_t pat, const flo
                 w2[i / 2] = t;
                 w3[i / 2] = bf2_of(p0 - __uint_as_float(t << 16), p1 - __uint_as_float(t & 0xFFFF0000u));
             }
-            sum = fma2(l, pair(v, v), sum);
+            sum = BARE ? add2(l, sum) : fma2(l, pair(v, v), sum);
         }
         tmem_st16(pat + half * 16, w2);
         tmem_st16(pat + 32 + half * 16, w3);
@@ -421,8 +429,8 @@ __device__ __forceinline__ bool no_values(float vs) { return fabsf(vs) < TINY_SC
 __device__ __forceinline__ uint32_t values_over(float vs) { return vs < SMALL_SCALE ? OVER_SMALL : OVER; }
 
 // A conversion warp's share of a token tile of one operand, 16 tokens and WB column
-// blocks, as codes in registers.
-template <int DP>
+// blocks, as codes in registers.  (VALUES is the 4-bit cache's: its keys and values lie apart.)
+template <int BITS, int DP, bool VALUES>
 struct Piece {
     using Sh = PShape<DP>;
     // a warp per 16 tokens, or two with half of the blocks each; 16-byte loads per thread
@@ -432,7 +440,8 @@ struct Piece {
     static __device__ __forceinline__ int blk0(int w) { return Sh::PIECES == CONV ? 0 : w / Sh::PIECES * WB; }
     uint4 x[N];
     // tokens `place` .. + 15 of page `id`; zeros where id < 0
-    __device__ __forceinline__ void load(const int8_t* codes, const CachePages& c, int id, int h, int place, int w, int lane) {
+    __device__ __forceinline__ void load(const CachePages& c, int id, int h, int place, int w, int lane) {
+        const int8_t* codes = VALUES ? c.v_codes : c.k_codes;
         const int c4 = lane & 3, t8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), b0 = blk0(w);
         const int8_t* from = codes + ((size_t)(id < 0 ? 0 : id * c.heads + h) * c.page + place + t8) * c.dim + b0 * 64 + c4 * 16;
 #pragma unroll
@@ -451,6 +460,69 @@ struct Piece {
 #pragma unroll
         for (int u = 0; u < N; ++u)
             convert16<Sh::KT>(x[u], dst, piece(w) * 16 + u / WB * 8 + t8, b0 + u % WB, c4, over);
+    }
+};
+// In 4 bits a lane takes two atoms (16 elements of a token) that lie together in the block: of keys,
+// tokens g and g + 8 of each 64 elements; of values, tokens 2 tig and 2 tig + 1 of each 8 tokens and 128
+// elements.
+template <int DP, bool VALUES>
+struct Piece<4, DP, VALUES> {
+    using Sh = PShape<DP>;
+    static constexpr int WB = Sh::BLK * Sh::PIECES / CONV, N = VALUES ? (DP == 64 ? 1 : 2) : WB;
+    static __device__ __forceinline__ int piece(int w) { return Sh::PIECES == CONV ? w : w % Sh::PIECES; }
+    static __device__ __forceinline__ int blk0(int w) { return Sh::PIECES == CONV ? 0 : w / Sh::PIECES * WB; }
+    static_assert(!VALUES || DP == 64 || WB == 2, "values are taken 128 elements at a time");
+    uint4 x[N];
+    uint32_t s[N];   // the two scales
+    // the lane's u-th pair: its group (of 16 elements) and first token, and the second's distance
+    static __device__ __forceinline__ int group_of(int u, int w, int lane) {
+        return VALUES ? blk0(w) * 4 + (DP == 64 ? lane >> 2 & 3 : lane >> 2) : (blk0(w) + u) * 4 + (lane & 3);
+    }
+    static __device__ __forceinline__ int token_of(int u, int lane) {
+        return VALUES ? (DP == 64 ? lane >> 4 : u) * 8 + (lane & 3) * 2 : lane >> 2;
+    }
+    __device__ __forceinline__ void load(const CachePages& c, int id, int h, int place, int w, int lane) {
+        const int groups = c.dim >> 4;
+        const uint8_t* block =
+            c.blocks + ((size_t)(id < 0 ? 0 : id * c.heads + h) * (c.page >> 4) + (place >> 4)) * block4_bytes(c.dim);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int gr = group_of(u, w, lane), t = token_of(u, lane);
+            const int at = VALUES ? value_atom(t, gr, groups) : key_atom(t, gr, groups);
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            s[u] = 0u;
+            if (id >= 0 && gr < groups) {
+                x[u] = __ldg(reinterpret_cast<const uint4*>(block + (VALUES ? 8 * c.dim : 0) + at * 8));
+                s[u] = __ldg(reinterpret_cast<const uint16_t*>(block + (VALUES ? 17 * c.dim : 16 * c.dim) + at));
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {}   // (no scale is too small)
+    // 16 values of a token, as 32 bytes of the tile
+    static __device__ __forceinline__ void put(uint8_t* dst, int t, int gr, uint2 codes, uint32_t scale) {
+        const Scale2 sc = scale_bf16(scale);
+        uint8_t* row = dst + (gr >> 2) * (Sh::KT * 128) + t * 128;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const uint32_t w = z ? codes.y : codes.x;
+            const uint32_t a = codes_bf16<0>(w, sc), b = codes_bf16<1>(w, sc), d = codes_bf16<2>(w, sc), e = codes_bf16<3>(w, sc);
+            *reinterpret_cast<uint4*>(row + (((2 * (gr & 3) + z) ^ (t & 7)) << 4)) =
+                make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(d, e, 0x7632));
+        }
+    }
+    // (values: lanes of odd groups store their second token first, so that the stores of a quarter
+    // warp, at (2 group + z) ^ token, do not meet in a bank)
+    __device__ __forceinline__ void store(uint8_t* dst, int w, int lane, uint32_t = 0u) const {
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int gr = group_of(u, w, lane), t = piece(w) * 16 + token_of(u, lane);
+            const bool swap = VALUES && (gr & 1);
+            const uint2 a = make_uint2(x[u].x, x[u].y), b = make_uint2(x[u].z, x[u].w);
+            const uint32_t sa = __byte_perm(s[u], 0u, 0x4040), sb = __byte_perm(s[u], 0u, 0x4141);
+            const int next = VALUES ? 1 : 8;
+            put(dst, t + (swap ? next : 0), gr, swap ? b : a, swap ? sb : sa);
+            put(dst, t + (swap ? 0 : next), gr, swap ? a : b, swap ? sa : sb);
+        }
     }
 };
 // Scales of 16 tokens as the softmax takes them (see the top of the file).
@@ -483,7 +555,7 @@ constexpr int NOT_HERE = INT_MIN;   // at[b] of a sequence that is converted ins
 
 // Operand tiles in the workspace: at[b] + j is the place of tile j of sequence b (each place
 // holds every head's keys and values, then their scales).
-template <int DP, bool F32>
+template <int BITS, int DP, bool F32>
 __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a, uint8_t* __restrict__ operands, int room,
                                                               int* __restrict__ at) {
     using Sh = PShape<DP, F32>;
@@ -511,20 +583,22 @@ __global__ void __launch_bounds__(PRE_THREADS) convert_kernel(const AttendArgs a
     if (blockIdx.x == 0 && tid == 0) at[b] = here ? (int)before - p.j0 : NOT_HERE;
     if (!here) return;
     for (int i = blockIdx.x; i < mine * H; i += gridDim.x) {
-        const int j = p.j0 + i / H, h = i % H, tk = j * Sh::KT + Piece<DP>::piece(warp) * 16;
+        const int j = p.j0 + i / H, h = i % H, tk = j * Sh::KT + Piece<BITS, DP, false>::piece(warp) * 16;
         // (no page is looked up that holds no token that is seen)
         const int blk = tk / c.page, place = tk % c.page;
         const int id = tk < s.start + s.rows && blk >= p.lo / c.page ? load_page(a.step, c, b, blk, a.status) : -1;
-        const float ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
+        float ks = 0.f, vs = 1.f;
+        if constexpr (BITS == 8) ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f, vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
         const size_t slot = (size_t)(before + j - p.j0) * H + h;
         uint8_t* to = operands + slot * 2 * Sh::OPER;
-        Piece<DP> k, v;
-        k.load(c.k_codes, c, id, h, place, warp, lane);
-        v.load(c.v_codes, c, id, h, place, warp, lane);
+        Piece<BITS, DP, false> k;
+        Piece<BITS, DP, true> v;
+        k.load(c, id, h, place, warp, lane);
+        v.load(c, id, h, place, warp, lane);
         if (no_values(vs)) v.zero();   // (ahead of the keys' store: 48 registers, 56 after it; 2 x 1000 rows of 256 44.0, 45.4 us)
         k.store(to, warp, lane);
         v.store(to + Sh::OPER, warp, lane, values_over(vs));
-        if (lane == 0 && warp < Sh::PIECES)
+        if (BITS == 8 && lane == 0 && warp < Sh::PIECES)
             put_scales(reinterpret_cast<float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24, warp, ks, vs);
     }
 }
@@ -535,7 +609,7 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                  : "memory");
 }
 
-template <int DP, int PG, bool F32>
+template <int BITS, int DP, int PG, bool F32>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const AttendArgs a, int tiles,
                                                                            float* __restrict__ partial,
                                                                            int* __restrict__ counters,
@@ -831,7 +905,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                         under = m;
                     }
                 // (the look at the scales' barrier is under way during the wait for the scores)
-                const bool scales = i % SPT != 0 || mbar_done(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1);
+                const bool scales = BITS == 4 || i % SPT != 0 || mbar_done(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1);
                 ok = mbar_wait(&tl.sfull[t][i & 1], (i >> 1) & 1, abort_flag, a.status);
                 if (!scales) ok = ok && mbar_wait(&tl.scfull[i / SPT & 3], i / SPT >> 2 & 1, abort_flag, a.status);
                 ok = __all_sync(~0u, ok);
@@ -854,8 +928,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 bool above = true, done = false;
                 if (!edge && i > 0) {
                     float2 sum;
-                    if constexpr (F32) sum = unpair(weigh3<false, PG>(sat, pat, sc, qf, m, 0, 0, y));
-                    else sum = unpair(weigh<false, PG>(sat, sc, qf, m, 0, 0, y));
+                    if constexpr (F32) sum = unpair(weigh3<false, PG, BITS == 4>(sat, pat, sc, qf, m, 0, 0, y));
+                    else sum = unpair(weigh<false, PG, BITS == 4>(sat, sc, qf, m, 0, 0, y));
                     above = sum.x + sum.y > MOST;
                     done = !__any_sync(~0u, above);
                     if (done) put_weights(sum);
@@ -864,7 +938,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                     if (move) {
                         // (fp32 rows: the lower terms of weights that are dropped land before the next ones')
                         if constexpr (F32) tmem_wait_st();
-                        const float mx = row_max(sat, sc, qf, lo - t0, hi - t0);
+                        const float mx = row_max<BITS == 4>(sat, sc, qf, lo - t0, hi - t0);
                         const float now = above ? fmaxf(mx, m) : m, f = ex2(m - now);
                         m = now;
                         l2 = mul2(l2, pair(f, f));
@@ -887,8 +961,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                         }
                     }
                     float2 sum;
-                    if constexpr (F32) sum = unpair(weigh3<true, PG>(sat, pat, sc, qf, m, lo - t0, hi - t0, y));
-                    else sum = unpair(weigh<true, PG>(sat, sc, qf, m, lo - t0, hi - t0, y));
+                    if constexpr (F32) sum = unpair(weigh3<true, PG, BITS == 4>(sat, pat, sc, qf, m, lo - t0, hi - t0, y));
+                    else sum = unpair(weigh<true, PG, BITS == 4>(sat, sc, qf, m, lo - t0, hi - t0, y));
                     above = sum.x + sum.y > MOST;
                     done = move || !__any_sync(~0u, above);
                     if (done) put_weights(sum);
@@ -901,7 +975,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             __syncwarp();
             tc_fence_after();
             const float2 ls = unpair(l2);
-            const float l = ls.x + ls.y, inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const float l = ls.x + ls.y, inv = parts > 1 ? 1.f : l == 0.f ? 0.f : (BITS == 4 ? c.v_unit : 1.f) / l;
 #pragma unroll
             for (int q = 0; q < DP / 32; ++q) {
                 uint32_t x[32];
@@ -950,7 +1024,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                     const float* p = first_ml + (size_t)z * PROMPT_SLOT;
                     sum = fmaf(__ldcg(p + Sh::ROWS), ex2(__ldcg(p) - top), sum);
                 }
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float inv = sum == 0.f ? 0.f : (BITS == 4 ? c.v_unit : 1.f) / sum;
 #pragma unroll 1
                 for (int q = 0; q < DP / 32; ++q) {
                     float o[32] = {};
@@ -985,12 +1059,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                 const size_t slot = (size_t)(first + ta / KT + j) * H + h;
                 const uint8_t* from = operands + slot * 2 * Sh::OPER;
                 const float* scales = reinterpret_cast<const float*>(operands + (size_t)room * H * 2 * Sh::OPER) + slot * 24;
-                const float sc = lane < 24 ? scales[lane] : 0.f;
+                const float sc = BITS == 8 && lane < 24 ? scales[lane] : 0.f;
                 if (!__all_sync(~0u, mbar_wait(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status))) break;
-                if (lane < 24) tl.scales[j & 3][lane] = sc;
+                if (BITS == 8 && lane < 24) tl.scales[j & 3][lane] = sc;
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&tl.scfull[j & 3]);
+                    if (BITS == 8) mbar_arrive(&tl.scfull[j & 3]);
                     mbar_expect_tx(&tl.kfull[j & 1], Sh::OPER);
                     bulk_g2s(kb + (j & 1) * Sh::OPER, from, Sh::OPER, &tl.kfull[j & 1]);
                 }
@@ -1016,7 +1090,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         // ---- conversion: the warp's 16 tokens of each tile
         const int w = warp - SOFT;
         // the warp's tokens of the tile that is loaded next: block and place in the sequence's table
-        int tk = ta + Piece<DP>::piece(w) * 16, blk = tk / c.page, place = tk % c.page;
+        int tk = ta + Piece<BITS, DP, false>::piece(w) * 16, blk = tk / c.page, place = tk % c.page;
         const int dblk = KT / c.page, dplace = KT % c.page;
         auto next_id = [&]() { return tk < tb ? load_page(a.step, c, b, blk, a.status) : -1; };   // -1: nothing to read
         auto advance = [&]() {
@@ -1025,31 +1099,32 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             place += dplace;
             if (place >= c.page) place -= c.page, ++blk;
         };
-        auto scale = [&](const float* p, int id) { return id >= 0 ? p[(size_t)id * H + h] : 0.f; };
-        Piece<DP> k, v;
+        auto scale = [&](const float* p, int id) { return BITS == 4 ? 1.f : id >= 0 ? p[(size_t)id * H + h] : 0.f; };
+        Piece<BITS, DP, false> k;
+        Piece<BITS, DP, true> v;
         int id = blk >= first_seen(pos_lo, a.window) / c.page ? next_id() : -1;   // (pages that no row sees: of the first tile)
-        k.load(c.k_codes, c, id, h, place, w, lane);
-        v.load(c.v_codes, c, id, h, place, w, lane);
+        k.load(c, id, h, place, w, lane);
+        v.load(c, id, h, place, w, lane);
         float ks = scale(c.k_scale, id), vs = scale(c.v_scale, id);
         advance();
         id = next_id();
         for (int j = 0; j < nt; ++j) {
             const uint32_t use = (j >> 1) & 1;
             if (!mbar_wait(&tl.kempty[j & 1], use ^ 1, abort_flag, a.status)) break;
-            if (lane == 0 && (Sh::PIECES == CONV || w < Sh::PIECES)) {
+            if (BITS == 8 && lane == 0 && (Sh::PIECES == CONV || w < Sh::PIECES)) {
                 put_scales(tl.scales[j & 3], w, ks, vs);
                 mbar_arrive(&tl.scfull[j & 3]);
             }
             k.store(kb + (j & 1) * Sh::OPER, w, lane);
             fence_proxy_async_smem();
             mbar_arrive(&tl.kfull[j & 1]);
-            k.load(c.k_codes, c, id, h, place, w, lane);
+            k.load(c, id, h, place, w, lane);
             if (!mbar_wait(&tl.vempty[j & 1], use ^ 1, abort_flag, a.status)) break;
             if (no_values(vs)) v.zero();
             v.store(vb + (j & 1) * Sh::OPER, w, lane, values_over(vs));
             fence_proxy_async_smem();
             mbar_arrive(&tl.vfull[j & 1]);
-            v.load(c.v_codes, c, id, h, place, w, lane);
+            v.load(c, id, h, place, w, lane);
             ks = scale(c.k_scale, id);
             vs = scale(c.v_scale, id);
             advance();
@@ -1124,7 +1199,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
     }
 }
 
-template <int DP, int PG, bool F32>
+template <int BITS, int DP, int PG, bool F32>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     using Sh = PShape<DP, F32>;
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
@@ -1134,7 +1209,7 @@ cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     if (pre) {
         // a few thousand warps in all, as many blocks for each sequence
         const int blocks = a.step.n_seqs >= 8 * ws.sms ? 1 : (8 * ws.sms + a.step.n_seqs - 1) / a.step.n_seqs;
-        convert_kernel<DP, F32><<<dim3(blocks, a.step.n_seqs), PRE_THREADS, 0, st>>>(a, ws.operands, room, ws.operand_at);
+        convert_kernel<BITS, DP, F32><<<dim3(blocks, a.step.n_seqs), PRE_THREADS, 0, st>>>(a, ws.operands, room, ws.operand_at);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -1142,30 +1217,32 @@ cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long ctas = (long long)tiles * a.pages.heads * a.step.n_seqs;
     const int parts = ctas * 2 <= ws.sms ? (int)(ws.sms / ctas) : 1;
     const dim3 grid((unsigned)tiles * a.pages.heads, a.step.n_seqs, parts);
-    attend_prompt_kernel<DP, PG, F32><<<grid, PROMPT_THREADS, Sh::SMEM, st>>>(a, tiles, ws.partial, ws.counters, ws.operands,
-                                                                            room, pre ? ws.operand_at : nullptr);
+    attend_prompt_kernel<BITS, DP, PG, F32><<<grid, PROMPT_THREADS, Sh::SMEM, st>>>(
+        a, tiles, ws.partial, ws.counters, ws.operands, room, pre ? ws.operand_at : nullptr);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-template <int DP, bool F32>
+template <int BITS, int DP, bool F32>
 static cudaError_t init() {
     constexpr int bytes = PShape<DP, F32>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<DP, 16, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attend_prompt_kernel<DP, STEP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel<BITS, DP, STEP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (BITS == 8 && e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_prompt_kernel<8, DP, 16, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e;
+}
+template <int BITS>
+static cudaError_t init_shapes() {
+    cudaError_t e = init<BITS, 64, false>();
+    if (e == cudaSuccess) e = init<BITS, 128, false>();
+    if (e == cudaSuccess) e = init<BITS, 256, false>();
+    if (e == cudaSuccess) e = init<BITS, 64, true>();
+    if (e == cudaSuccess) e = init<BITS, 128, true>();
     return e;
 }
 
-cudaError_t attend_prompt_init() {
-    cudaError_t e = init<64, false>();
-    if (e == cudaSuccess) e = init<128, false>();
-    if (e == cudaSuccess) e = init<256, false>();
-    if (e == cudaSuccess) e = init<64, true>();
-    if (e == cudaSuccess) e = init<128, true>();
-    return e;
-}
+cudaError_t attend_prompt_init(int bits) { return bits == 4 ? init_shapes<4>() : init_shapes<8>(); }
 
 template <int DP>
 static size_t operand_bytes(const CachePages& c, long long tokens) {
@@ -1187,16 +1264,17 @@ bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return (bf16 || a.pages.dim <= 128) && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }
 
-template <int PG>
+template <int BITS, int PG>
 static cudaError_t launch_by_dim(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const int D = a.pages.dim;
-    if (!bf16) return D <= 64 ? launch<64, PG, true>(a, ws, st) : launch<128, PG, true>(a, ws, st);
-    return D <= 64 ? launch<64, PG, false>(a, ws, st)
-                   : D <= 128 ? launch<128, PG, false>(a, ws, st) : launch<256, PG, false>(a, ws, st);
+    if (!bf16) return D <= 64 ? launch<BITS, 64, PG, true>(a, ws, st) : launch<BITS, 128, PG, true>(a, ws, st);
+    return D <= 64 ? launch<BITS, 64, PG, false>(a, ws, st)
+                   : D <= 128 ? launch<BITS, 128, PG, false>(a, ws, st) : launch<BITS, 256, PG, false>(a, ws, st);
 }
 
 cudaError_t launch_attend_prompt(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    return a.pages.page % STEP ? launch_by_dim<16>(bf16, a, ws, st) : launch_by_dim<STEP>(bf16, a, ws, st);
+    if (a.pages.blocks) return launch_by_dim<4, STEP>(bf16, a, ws, st);
+    return a.pages.page % STEP ? launch_by_dim<8, 16>(bf16, a, ws, st) : launch_by_dim<8, STEP>(bf16, a, ws, st);
 }
 
 }  // namespace mlora

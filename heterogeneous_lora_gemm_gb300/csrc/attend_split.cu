@@ -1,5 +1,5 @@
-// Causal attention over the 8-bit cache for sequences with few rows in the step (decode:
-// one token), any row and head count (include/mlora.h).
+// Causal attention over the 8-bit and the 4-bit cache for sequences with few rows in the step
+// (decode: one token), any row and head count (include/mlora.h).
 //
 // Mathematics.  With codes kc, vc and page scales ks, vs, row r (query token i, query head
 // g of the key/value head's group) has  x_t = scale ks_t (q_r . kc_t),  and
@@ -27,10 +27,16 @@
 // ranges, one per resident CTA; every CTA finds its range from the lengths.  An item is as
 // long as its tokens plus what its start costs (LEAD).  An item cut between CTAs is joined,
 // in range order, by the CTA that finishes it last, so results do not depend on timing.
+//
+// The 4-bit cache (BITS 4, block4.cuh): a code times its scale is exact in fp16 and in bf16, so that the
+// operands are the values themselves, over a unit that goes into the scores' factor (on the host)
+// and into the output.  A piece's keys, values and scales are one copy; an atom (8 bytes) is what a
+// lane turns into its rows' part of four k steps, so that it needs two scales per four steps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "attend.h"
+#include "block4.cuh"
 #include "tc_ptx.cuh"
 
 namespace mlora {
@@ -46,7 +52,7 @@ constexpr int MIN_UNITS = LEAD + 1;       // a CTA's range is at least so long
 constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights stay below 2^8
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
-template <bool F32, int DP, int NT>
+template <int BITS, bool F32, int DP, int NT>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query
     static constexpr int PTERMS = F32 ? 3 : 2;         // of a weight
@@ -59,18 +65,19 @@ struct Shape {
     // (one where the accumulators leave no registers for two)
     static constexpr int SUB = DP == 256 ? 1 : 2;
     static constexpr int CHUNK_T = PIECE * SUB;
-    static constexpr int PART = 2 * CB * BOX;          // keys and values of a piece
+    static constexpr int PART = BITS == 4 ? 18 * DP : 2 * CB * BOX;   // keys and values of a piece
     static constexpr int STAGE = SUB * PART;
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
     // (64 KB of ring also where the queries' fragments leave no more, 16 fp32 rows of up to 256 elements: 2 x
     // 300 rows after 1000, 16/8 heads, 124 us, 188 us with the 96 KB that one CTA per SM has room for)
-    static constexpr int STAGES = (OCC == 3 || (F32 && DP == 256 && NT == 2) ? 64 : 96) * 1024 / WARPS / STAGE;
-    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int FIT = (OCC == 3 || (F32 && DP == 256 && NT == 2) ? 64 : 96) * 1024 / WARPS / STAGE;
+    static constexpr int STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int JOIN = WARPS * RT * DP * 4;       // the join buffer lies in the ring
+    static constexpr int RING = WARPS * STAGES * STAGE > JOIN ? WARPS * STAGES * STAGE : JOIN;
     static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
     static constexpr int SMEM = 1024 + RING + QWORDS * 4;
     static constexpr int SLOT = RT * (DP + 2);             // floats of a partial result: O, then m, l per row
-    static_assert(WARPS * RT * DP * 4 <= RING, "the join buffer lies in the ring");
 };
 
 // shared-memory offset of 16-byte chunk `c` of box row `r`
@@ -192,11 +199,18 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v
     *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
-template <bool F32, int DP, int NT>
-__global__ void __launch_bounds__(THREADS, (Shape<F32, DP, NT>::OCC))
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// `zeros`: a 4-bit block of zeros, in the place of one that cannot be read
+template <int BITS, bool F32, int DP, int NT>
+__global__ void __launch_bounds__(THREADS, (Shape<BITS, F32, DP, NT>::OCC))
 attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
-                    float* __restrict__ partial, int* __restrict__ counters) {
-    using Sh = Shape<F32, DP, NT>;
+                    float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
+    using Sh = Shape<BITS, F32, DP, NT>;
     using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int KS = Sh::KS, RT = Sh::RT, SUB = Sh::SUB, CHUNK_T = Sh::CHUNK_T, TERMS = Sh::TERMS, PTERMS = Sh::PTERMS, CB = Sh::CB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -214,7 +228,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) tl.abort_flag = 0;
-    if (tid == 0) {
+    if (BITS == 8 && tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmK) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmV) : "memory");
     }
@@ -330,6 +344,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             return k < count && t <= pos_hi ? load_page(a.step, c, b, quotient(a.page, t), a.status) : -1;
         };
         auto row_of = [&](int id, int t) {   // first code row of the piece; past the tensor for a bad page
+            if (BITS == 4)                   // the piece's block; -1 for a bad page
+                return id < 0 ? -1 : (id * H + h) * (c.page >> 4) + ((t - quotient(a.page, t) * c.page) >> 4);
             return id < 0 ? c.n_pages * H * c.page : (id * H + h) * c.page + t - quotient(a.page, t) * c.page;
         };
         const int my_k = lane / SUB, my_off = lane % SUB * PIECE;
@@ -342,18 +358,25 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const int id = t + PIECE > seen_from ? id_at(my_k, t) : -1;
             id1 = id_at(BATCH + my_k, t1);
             row = row_of(id, t), row1 = row_of(id1, t1);
-            ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;
-            vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
+            if (BITS == 8) {
+                ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;
+                vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
+            }
         }
         // copies chunk k of the item, a box per lane; `row` holds batch `batch`
-        const int box = lane % (2 * CB * SUB), box_sub = box / (2 * CB), box_v = box / CB & 1, box_q = box % CB;
+        const int box = lane % (2 * CB * SUB), box_v = box / CB & 1, box_q = box % CB;
+        const int box_sub = BITS == 4 ? lane % SUB : box / (2 * CB);
         auto issue = [&](int k, int batch) {
             const int r = __shfl_sync(~0u, k / BATCH == batch ? row : row1, k % BATCH * SUB + box_sub);
             const uint32_t st = issued % Sh::STAGES;
             uint64_t* bar = &tl.full[warp][st];
-            if (lane == 0) mbar_expect_tx(bar, Sh::STAGE);
+            if (lane == 0) mbar_expect_tx(bar, BITS == 4 ? SUB * block4_bytes(D) : Sh::STAGE);
             __syncwarp();
-            if (lane < 2 * CB * SUB)
+            if (BITS == 4) {
+                if (lane < SUB)
+                    bulk_g2s(ring + st * Sh::STAGE + lane * Sh::PART, r < 0 ? zeros : c.blocks + (size_t)r * block4_bytes(D),
+                             block4_bytes(D), bar);
+            } else if (lane < 2 * CB * SUB)
                 tma_2d(ring + st * Sh::STAGE + box_sub * Sh::PART + (box_v * CB + box_q) * Sh::BOX, box_v ? &tmV : &tmK, bar,
                        box_q * 128, r);
             ++issued;
@@ -383,6 +406,20 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 tl.qf[r] = fine ? a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23)) : NAN;
 #pragma unroll
             for (int e = 0; e < EL; e += 2) {
+                if (BITS == 4) {
+                    // k step s takes, of each 64 elements, the pairs (x, x + 4) of the lane's group: codes that
+                    // lie in one nibble of a word's halves
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int d = lane * EL + e + z, x4 = d % 4, s = d / 64 * 4 + d % 16 / 8 * 2 + x4 / 2, t = d % 64 / 16;
+                        const float v = fine ? x[kk][e + z] * down : 0.f;
+                        __half* dst = reinterpret_cast<__half*>(qfrag + (((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + x4 % 2) + d % 8 / 4;
+                        const __half hi = __float2half_rn(v);
+                        *dst = hi;
+                        if (TERMS == 2) dst[128] = __float2half_rn(v - __half2float(hi));
+                    }
+                    continue;
+                }
                 const int d = lane * EL + e, ch = d % 128 / 16, w = d % 16 / 4;
                 const int s = DP == 64 ? w : d / 128 * 8 + ch % 2 * 4 + w, t = DP == 64 ? ch : ch / 2;
                 const float v0 = fine ? x[kk][e] * down : 0.f, v1 = fine ? x[kk][e + 1] * down : 0.f;
@@ -436,15 +473,15 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 id1 = id_at(k + BATCH + my_k, t);
                 row1 = row_of(id1, t);
             }
-            if (k % BATCH == BATCH / 4) {   // the next batch's scales, well before they are used
+            if (BITS == 8 && k % BATCH == BATCH / 4) {   // the next batch's scales, well before they are used
                 ks1 = id1 >= 0 ? c.k_scale[(size_t)id1 * H + h] : 0.f;
                 vs1 = id1 >= 0 ? c.v_scale[(size_t)id1 * H + h] : 0.f;
             }
             float ksk[SUB], vsk[SUB];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                ksk[u] = __shfl_sync(~0u, ks, k % BATCH * SUB + u);
-                vsk[u] = __shfl_sync(~0u, vs, k % BATCH * SUB + u);
+                ksk[u] = BITS == 4 ? 1.f : __shfl_sync(~0u, ks, k % BATCH * SUB + u);
+                vsk[u] = BITS == 4 ? 1.f : __shfl_sync(~0u, vs, k % BATCH * SUB + u);
             }
             const uint32_t st = used % Sh::STAGES;
             alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], (used / Sh::STAGES) & 1, abort_flag, a.status));
@@ -453,7 +490,38 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
             constexpr int CH = 2 / SUB;                  // independent sums per piece (even and odd k steps)
             float sc[SUB][CH][NT][4] = {};
+            auto scores4 = [&](int u, int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int term = 0; term < TERMS; ++term) {
+                        const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
+                        mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
+                    }
+            };
+            if (BITS == 4) {
+                // 64 elements at a time: the lane's atoms of tokens g and g + 8, group tig of the four
+#pragma unroll
+                for (int q = 0; q < DP / 64; ++q)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        const uint8_t* kb = stage + u * Sh::PART;
+                        const int n = min(4, D / 16 - 4 * q), at = q * 64 + (g * n + tig) * 2;
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        uint32_t s16 = 0u;
+                        if (DP == D || tig < n) {
+                            w = *reinterpret_cast<const uint4*>(kb + at * 8);
+                            s16 = *reinterpret_cast<const uint16_t*>(kb + 16 * D + at);
+                        }
+                        const Scale2 sa = scale_f16(prmt(s16, 0u, 0x4040)), sb = scale_f16(prmt(s16, 0u, 0x4141));
+                        scores4(u, 4 * q, codes_f16<0>(w.x, sa), codes_f16<0>(w.z, sb), codes_f16<1>(w.x, sa), codes_f16<1>(w.z, sb));
+                        scores4(u, 4 * q + 1, codes_f16<2>(w.x, sa), codes_f16<2>(w.z, sb), codes_f16<3>(w.x, sa), codes_f16<3>(w.z, sb));
+                        scores4(u, 4 * q + 2, codes_f16<0>(w.y, sa), codes_f16<0>(w.w, sb), codes_f16<1>(w.y, sa), codes_f16<1>(w.w, sb));
+                        scores4(u, 4 * q + 3, codes_f16<2>(w.y, sa), codes_f16<2>(w.w, sb), codes_f16<3>(w.y, sa), codes_f16<3>(w.w, sb));
+                    }
+            }
             constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
+            if (BITS == 8)
 #pragma unroll
             for (int q = 0; q < CB; ++q)
 #pragma unroll
@@ -494,7 +562,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     top[t][e] = -INFINITY;
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
-                        const float f = qf[t][e] * ksk[u];
+                        const float f = BITS == 4 ? qf[t][e] : qf[t][e] * ksk[u];
                         float& x0 = sc[u][0][t][e];
                         float& x1 = sc[u][0][t][2 + e];
                         x0 = (CH == 2 ? x0 + sc[u][CH - 1][t][e] : x0) * f;
@@ -539,7 +607,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     l[t][1] += w[1] + w[3];
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        float x0 = w[2 * z] * vsk[u], x1 = w[2 * z + 1] * vsk[u];
+                        float x0 = w[2 * z], x1 = w[2 * z + 1];
+                        if (BITS == 8) x0 *= vsk[u], x1 *= vsk[u];
 #pragma unroll
                         for (int term = 0; term < PTERMS; ++term) {
                             const uint32_t y = bf2_of(x0, x1);
@@ -553,8 +622,29 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 constexpr int W = Sh::ROWB / 32;   // words of a box row per thread
 #pragma unroll
                 for (int q = 0; q < CB; ++q) {
-                    const uint8_t* vb = stage + u * Sh::PART + (CB + q) * Sh::BOX;
+                    const uint8_t* vb = stage + u * Sh::PART + (BITS == 4 ? 8 * D : (CB + q) * Sh::BOX);
                     uint32_t v[4][W];
+                    Scale2 vsc[2];
+                    if (BITS == 4) {
+                        // atoms of tokens 2 tig and + 1, + 8 and + 9, of the lane's group (DP 64: half a group)
+                        const int n = min(8, D / 16 - 8 * q), gr = DP == 64 ? g >> 1 : g;
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const int at = q * 128 + (z * n + gr) * 8 + tig * 2;
+                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                            uint32_t s16 = 0u;
+                            if (DP == D || gr < n) {
+                                w = *reinterpret_cast<const uint4*>(vb + at * 8);
+                                s16 = *reinterpret_cast<const uint16_t*>(vb + 9 * D + at);
+                            }
+                            vsc[z] = scale_bf16(prmt(s16, 0u, 0x4140));
+                            // words of four elements, token 2 tig in the low half
+                            const uint32_t lo = DP == 64 && (g & 1) ? w.y : w.x, hi = DP == 64 && (g & 1) ? w.w : w.z;
+                            v[z][0] = prmt(lo, hi, 0x5410), v[z][1] = prmt(lo, hi, 0x7632);
+                            if (W == 4) v[z][W - 2] = prmt(w.y, w.w, 0x5410), v[z][W - 1] = prmt(w.y, w.w, 0x7632);
+                        }
+                    }
+                    if (BITS == 8)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         const int r = 2 * tig + (z & 1) + (z >> 1) * 8;
@@ -571,6 +661,13 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         uint32_t y[2][4];   // [token pair][element of the word]
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
+                            if (BITS == 4) {
+                                y[z][0] = codes_bf16<0>(v[z][w], vsc[z]);
+                                y[z][1] = codes_bf16<1>(v[z][w], vsc[z]);
+                                y[z][2] = codes_bf16<2>(v[z][w], vsc[z]);
+                                y[z][3] = codes_bf16<3>(v[z][w], vsc[z]);
+                                continue;
+                            }
                             const uint32_t e0 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x5140),
                                            e1 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x7362);
                             y[z][0] = bf16_codes(prmt(e0, 0x43434343u, 0x4140));
@@ -670,7 +767,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
             if (whole) {
                 if (r < rows && d < D) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const float inv = sum == 0.f ? 0.f : (BITS == 4 ? c.v_unit : 1.f) / sum;
                     store4<E>(out_of(r) + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             } else {
@@ -708,7 +805,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         sum = fmaf(__ldcg(p + RT * DP + RT + r), f, sum);
                         v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
                     }
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const float inv = sum == 0.f ? 0.f : (BITS == 4 ? c.v_unit : 1.f) / sum;
                     store4<E>(out_of(r) + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             }
@@ -720,51 +817,58 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
 }
 
-template <bool F32, int DP, int NT>
+template <int BITS, bool F32, int DP, int NT>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    using Sh = Shape<F32, DP, NT>;
+    using Sh = Shape<BITS, F32, DP, NT>;
     static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace slots");
     // ranges are cut for OCC CTAs on each SM (of 228 KB, 1 KB of it the system's per CTA)
     static_assert(Sh::OCC * (Sh::SMEM + (int)sizeof(Tail) + 1024) <= 228 * 1024, "resident CTAs");
-    attend_split_kernel<F32, DP, NT><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters);
+    attend_split_kernel<BITS, F32, DP, NT>
+        <<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters, ws.zeros);
     return cudaGetLastError();
 }
 
-template <bool F32, int DP, int NT>
+template <int BITS, bool F32, int DP, int NT>
 cudaError_t init() {
-    return cudaFuncSetAttribute(attend_split_kernel<F32, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Shape<F32, DP, NT>::SMEM);
+    return cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Shape<BITS, F32, DP, NT>::SMEM);
+}
+template <int BITS, bool F32>
+cudaError_t init_shapes() {
+    cudaError_t e = cudaSuccess;
+    auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
+    one(init<BITS, F32, 64, 1>()), one(init<BITS, F32, 64, 2>()), one(init<BITS, F32, 128, 1>()), one(init<BITS, F32, 128, 2>());
+    one(init<BITS, F32, 256, 1>()), one(init<BITS, F32, 256, 2>());
+    return e;
 }
 
 }  // namespace
 
-cudaError_t attend_split_init() {
-    cudaError_t e = cudaSuccess;
-    auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
-    one(init<false, 64, 1>()), one(init<false, 64, 2>()), one(init<false, 128, 1>()), one(init<false, 128, 2>());
-    one(init<false, 256, 1>()), one(init<false, 256, 2>());
-    one(init<true, 64, 1>()), one(init<true, 64, 2>()), one(init<true, 128, 1>()), one(init<true, 128, 2>());
-    one(init<true, 256, 1>()), one(init<true, 256, 2>());
+cudaError_t attend_split_init(int bits) {
+    cudaError_t e = bits == 4 ? init_shapes<4, false>() : init_shapes<8, false>();
+    if (e == cudaSuccess) e = bits == 4 ? init_shapes<4, true>() : init_shapes<8, true>();
     return e;
 }
 
 // Rows per tile: 8, or 16 where a sequence and head has more (past 16 only fp32 rows of more than
 // 128 elements come here, in tiles of 16; the rest are attend_prompt.cu's).
-template <bool F32, int DP>
+template <int BITS, bool F32, int DP>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    return rows <= 8 ? launch<F32, DP, 1>(a, ws, st) : launch<F32, DP, 2>(a, ws, st);
+    return rows <= 8 ? launch<BITS, F32, DP, 1>(a, ws, st) : launch<BITS, F32, DP, 2>(a, ws, st);
 }
 
-template <bool F32>
+template <int BITS, bool F32>
 static cudaError_t by_shape(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const int D = a.pages.dim;
-    return D <= 64 ? by_rows<F32, 64>(a, ws, st) : D <= 128 ? by_rows<F32, 128>(a, ws, st) : by_rows<F32, 256>(a, ws, st);
+    return D <= 64 ? by_rows<BITS, F32, 64>(a, ws, st)
+                   : D <= 128 ? by_rows<BITS, F32, 128>(a, ws, st) : by_rows<BITS, F32, 256>(a, ws, st);
 }
 
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    return bf16 ? by_shape<false>(a, ws, st) : by_shape<true>(a, ws, st);
+    if (a.pages.blocks) return bf16 ? by_shape<4, false>(a, ws, st) : by_shape<4, true>(a, ws, st);
+    return bf16 ? by_shape<8, false>(a, ws, st) : by_shape<8, true>(a, ws, st);
 }
 
 }  // namespace mlora

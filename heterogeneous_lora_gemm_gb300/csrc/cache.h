@@ -1,5 +1,6 @@
-// Key/value cache in 8 bits (int8 pages, one fp32 scale per page and head) and the
-// attention over it: declarations shared by cache.cu, cache_store.cu and attend*.cu.
+// Key/value caches, in 8 bits (int8 pages, one fp32 scale per page and head) and in 4 (blocks of 16
+// tokens, block4.cuh), and the attention over them: declarations shared by cache.cu,
+// cache_store.cu, cache4_store.cu and attend*.cu.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -12,13 +13,16 @@ namespace mlora {
 
 constexpr float TINY_SCALE = 0x1p-120f;   // codes under a smaller scale are 0 (1 / s stays finite above)
 
-// The caller's pages: codes [n_pages][heads][page][dim], scales [n_pages][heads].
+// The caller's pages: codes [n_pages][heads][page][dim], scales [n_pages][heads]; or, in 4 bits,
+// blocks [n_pages][heads][page / 16][18 dim] and what a code times its scale counts.
 struct CachePages {
     int8_t* k_codes;
     int8_t* v_codes;
     float* k_scale;
     float* v_scale;
     int n_pages, page, heads, dim;
+    uint8_t* blocks;
+    float k_unit, v_unit;
 };
 
 // One step's rows, lengths and page table (see include/mlora.h).
@@ -119,5 +123,9 @@ cudaError_t launch_append(bool bf16, const CachePages& c, const CacheStep& s, co
                           uint32_t* status, cudaStream_t st);
 cudaError_t launch_read(bool bf16, const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v,
                         uint32_t* status, cudaStream_t st);
+cudaError_t launch_append4(bool bf16, const CachePages& c, const CacheStep& s, const RowsIn& k, const RowsIn& v,
+                           uint32_t* status, cudaStream_t st);
+cudaError_t launch_read4(bool bf16, const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v,
+                         uint32_t* status, cudaStream_t st);
 
 }  // namespace mlora

@@ -1,0 +1,381 @@
+// Norms and rotation of query and key heads ahead of attention (include/mlora.h): C ABI and kernel.
+//
+// Mathematics.  A head x of D elements at position p:  y = w x / sqrt(mean(x^2) + eps)  (left out
+// without weights), then pairs (a, b) of the first R elements turn by p f_i:
+//     a' = a cos - b sin,  b' = a sin + b cos.
+// Angles are held in turns: f / 2 pi as a 64-bit fraction, so that p times it, in wrapping
+// integers, is the angle modulo a turn with no loss at any position; its nearest quarter turn is
+// taken off before it becomes a float.
+//
+// A warp takes a row and some heads of its queries or of its keys.  A lane takes 16 elements of a head,
+// eight pairs, whose sines and cosines the warp computes once for all its heads; 16 lanes at most
+// share a head and its sum of squares.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+#include <type_traits>
+
+#include "../../include/mlora.h"
+#include "cache.h"
+
+using namespace mlora;
+
+struct mlora_rotary {
+    int device = 0, sms = 0;
+    int dim = 0, turned = 0;      // head size, elements that turn
+    bool interleaved = false;
+    uint32_t* ws = nullptr;       // the status word, then the table
+    uint64_t* turns = nullptr;    // [turned / 2] turns per position, in 2^-64
+};
+
+namespace {
+
+constexpr int WARPS = 4, THREADS = 32 * WARPS;
+
+struct RotaryArgs {
+    RowsIn q, k;
+    RowsOut qo, ko;
+    int q_heads, kv_heads, dim, turned;
+    const uint64_t* turns;
+    const float* q_weight;
+    const float* k_weight;
+    float eps;
+    CacheStep step;
+    int q_chunks, per;   // chunks of the queries' heads (the keys' follow), groups of heads in a chunk
+    uint32_t* status;
+};
+
+// 8 adjacent elements
+__device__ __forceinline__ void load8(const float* p, float* x) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sine and cosine of an angle in turns, 2^-64 each.
+__device__ __forceinline__ float2 cos_sin(uint64_t turns) {
+    const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));   // within an eighth of a turn
+    float s, c;
+    sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
+    if (quarter & 1) {
+        const float t = c;
+        c = -s;
+        s = t;
+    }
+    return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
+}
+
+// The sequence that holds a row: the last whose range begins at or before it (32 looks at a time).
+__device__ __forceinline__ int sequence_of(const CacheStep& s, int row, int lane) {
+    int lo = 0, hi = s.n_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const int n = __popc(__ballot_sync(~0u, at < hi && s.offsets[min(at, hi - 1)] <= row));
+        lo += max(n - 1, 0) * step;
+        hi = min(lo + step, hi);
+    }
+    return min(lo, s.n_seqs - 1);
+}
+
+// LANES: of a head (its 16-element slots, rounded up to a power of two)
+template <typename T, int LANES, bool INTERLEAVED>
+__global__ void __launch_bounds__(THREADS) rotary_kernel(const RotaryArgs a) {
+    constexpr int HEADS = 32 / LANES;   // at a time
+    __shared__ float2 turn[WARPS][128];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // lengths and limits of the sequences are as load_seq checks them, up to 2^30 tokens
+    constexpr int PAGE = 1 << 15;
+    if (a.step.offsets && blockIdx.x == 0 && blockIdx.y == 0)   // ranges that hold no row are looked at here
+        for (int b = threadIdx.x; b < a.step.n_seqs; b += THREADS) load_seq(a.step, PAGE, b, a.status);
+    const int row = blockIdx.x * WARPS + warp;
+    if (row >= a.step.T) return;
+    const int b = a.step.offsets ? sequence_of(a.step, row, lane) : row;
+    const SeqRec s = load_seq(a.step, PAGE, b, a.status);
+    const int i = row - s.row0;
+    if (i < 0 || i >= s.rows) return;   // of no sequence
+    const int pos = s.start + i;
+    const bool is_k = (int)blockIdx.y >= a.q_chunks;
+    const RowsIn& from = is_k ? a.k : a.q;
+    const RowsOut& to = is_k ? a.ko : a.qo;
+    const float* weight = is_k ? a.k_weight : a.q_weight;
+    const int heads = is_k ? a.kv_heads : a.q_heads;
+    const int head0 = (blockIdx.y - (is_k ? a.q_chunks : 0)) * a.per * HEADS + lane / LANES;
+    const int slot = lane % LANES;
+    const bool mine = slot * 16 < a.dim, turns = slot * 16 < a.turned;
+    // the slot's two runs of 8 elements: halves of eight pairs, or eight pairs side by side
+    const int at0 = turns && !INTERLEAVED ? slot * 8 : slot * 16;
+    const int at1 = turns && !INTERLEAVED ? a.turned / 2 + slot * 8 : slot * 16 + 8;
+
+    float c[8], sn[8];
+    for (int p = lane; p < a.turned / 2; p += 32) turn[warp][p] = cos_sin((uint64_t)(int64_t)pos * a.turns[p]);
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float2 v = turns ? turn[warp][slot * 8 + e] : make_float2(1.f, 0.f);
+        c[e] = v.x;
+        sn[e] = v.y;
+    }
+    float w[16];
+    if (weight) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = mine ? weight[at0 + e] : 0.f;
+            w[8 + e] = mine ? weight[at1 + e] : 0.f;
+        }
+    }
+    const float inv_dim = 1.f / (float)a.dim;
+    for (int g = 0; g < a.per; ++g) {
+        const int h = head0 + g * HEADS;
+        if (h - lane / LANES >= heads) break;   // (the whole warp)
+        const bool in = mine && h < heads;
+        const T* src = (const T*)from.ptr + row * from.row + h * from.head;
+        T* dst = (T*)to.ptr + row * to.row + h * to.head;
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        if (in && pos >= 0) {
+            load8(src + at0, x);
+            load8(src + at1, x + 8);
+        }
+        if (weight && pos >= 0) {
+            auto squares = [&](float f) {
+                float t = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) t = fmaf(x[e] * f, x[e] * f, t);
+#pragma unroll
+                for (int d = 1; d < LANES; d <<= 1) t += __shfl_xor_sync(~0u, t, d);
+                return t;
+            };
+            float sum = squares(1.f), f = 1.f;
+            // squares that leave fp32, or are lost beside no eps: the head by a power of two
+            const bool far = !(sum <= 0x1p120f) || (sum < 0x1p-90f && a.eps < 0x1p-70f);
+            if (__any_sync(~0u, far)) {
+                const float up = !(sum <= 0x1p120f) ? 0x1p-70f : 0x1p60f;
+                const float again = squares(far ? up : 1.f);
+                if (far) sum = again, f = up;
+            }
+            const float mean = sum * inv_dim + a.eps * f * f;
+            const float inv = mean == 0.f ? 0.f : __frcp_rn(__fsqrt_rn(mean)) * f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * w[e];
+        }
+        float y[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int p = INTERLEAVED ? 2 * e : e, q = INTERLEAVED ? 2 * e + 1 : e + 8;
+            y[p] = x[p] * c[e] - x[q] * sn[e];
+            y[q] = x[p] * sn[e] + x[q] * c[e];
+        }
+        if (in) {
+            store8(dst + at0, turns ? y : x);
+            store8(dst + at1, turns ? y + 8 : x + 8);
+        }
+    }
+}
+
+template <typename T, int LANES>
+cudaError_t launch(RotaryArgs a, bool interleaved, int sms, cudaStream_t st) {
+    constexpr int HEADS = 32 / LANES;
+    const int q_groups = (a.q_heads + HEADS - 1) / HEADS, k_groups = (a.kv_heads + HEADS - 1) / HEADS;
+    // groups of heads per warp: as many as leave some 32 warps to an SM, 8 at most
+    const long long groups = (long long)a.step.T * (q_groups + k_groups) / (32ll * sms);
+    a.per = groups < 1 ? 1 : groups > 8 ? 8 : (int)groups;
+    a.q_chunks = (q_groups + a.per - 1) / a.per;
+    const dim3 grid((unsigned)(((long long)a.step.T + WARPS - 1) / WARPS), a.q_chunks + (k_groups + a.per - 1) / a.per);
+    if (interleaved) rotary_kernel<T, LANES, true><<<grid, THREADS, 0, st>>>(a);
+    else rotary_kernel<T, LANES, false><<<grid, THREADS, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_by_dim(const RotaryArgs& a, bool interleaved, int sms, cudaStream_t st) {
+    const int slots = a.dim / 16;
+    return slots == 1 ? launch<T, 1>(a, interleaved, sms, st)
+         : slots == 2 ? launch<T, 2>(a, interleaved, sms, st)
+         : slots <= 4 ? launch<T, 4>(a, interleaved, sms, st)
+         : slots <= 8 ? launch<T, 8>(a, interleaved, sms, st)
+                      : launch<T, 16>(a, interleaved, sms, st);
+}
+
+mlora_status fail(mlora_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return s;
+}
+
+mlora_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();   // reported here: not the next launch's error
+    return fail(MLORA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+// Makes a device current for the scope of one call and restores the caller's.
+struct DeviceGuard {
+    int prev = -1;
+    bool moved = false;
+    cudaError_t err = cudaSuccess;
+    explicit DeviceGuard(int dev) {
+        err = cudaGetDevice(&prev);
+        if (err == cudaSuccess && prev != dev) {
+            err = cudaSetDevice(dev);
+            moved = err == cudaSuccess;
+        }
+    }
+    ~DeviceGuard() {
+        if (moved) cudaSetDevice(prev);
+    }
+};
+
+mlora_status check_rows(const char* name, const void* p, int64_t row, int64_t head, mlora_dtype dtype) {
+    const int64_t unit = dtype == MLORA_BF16 ? 8 : 4;   // elements per 16 bytes
+    if (!p) return fail(MLORA_ERR_INVALID_ARG, "%s is NULL", name);
+    if (((uintptr_t)p & 15u) || row % unit || head % unit || row < 0 || head < 0)
+        return fail(MLORA_ERR_INVALID_ARG, "%s: 16-byte alignment (strides %lld, %lld elements)", name, (long long)row,
+                    (long long)head);
+    return MLORA_OK;
+}
+
+// A frequency in radians per position as turns per position, modulo 1, in 2^-64: 1 / 2 pi in two
+// doubles, the product's rounding kept.
+uint64_t turns_of(double f) {
+    constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+    if (f < 0) return 0u - turns_of(-f);
+    const double t = f * hi, rest = std::fma(f, hi, -t) + f * lo;
+    return (uint64_t)((t - std::floor(t)) * 0x1p64) + (uint64_t)(int64_t)std::llrint(rest * 0x1p64);   // (the difference is exact)
+}
+
+}  // namespace
+
+extern "C" {
+
+mlora_status mlora_rotary_create(int head_dim, int rotary_dim, const double* freq, int interleaved, mlora_rotary_t* out) {
+    if (!out) return fail(MLORA_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    if (head_dim < 16 || head_dim > 256 || head_dim % 16)
+        return fail(MLORA_ERR_UNSUPPORTED, "head_dim %d must be a multiple of 16 in [16, 256]", head_dim);
+    if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16)
+        return fail(MLORA_ERR_UNSUPPORTED, "rotary_dim %d must be a multiple of 16 in [0, head_dim]", rotary_dim);
+    if (rotary_dim && !freq) return fail(MLORA_ERR_INVALID_ARG, "freq is NULL");
+    uint64_t table[128];
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        if (!(std::fabs(freq[i]) <= 1024.0))
+            return fail(MLORA_ERR_INVALID_ARG, "freq[%d] = %g is not a number of radians per position in [-1024, 1024]", i, freq[i]);
+        table[i] = turns_of(freq[i]);
+    }
+    mlora_rotary* r = new (std::nothrow) mlora_rotary;
+    if (!r) return fail(MLORA_ERR_OOM, "host memory");
+    r->dim = head_dim;
+    r->turned = rotary_dim;
+    r->interleaved = interleaved != 0;
+    cudaError_t e = cudaGetDevice(&r->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r->sms, cudaDevAttrMultiProcessorCount, r->device);
+    if (e == cudaSuccess) e = cudaMalloc((void**)&r->ws, 256 + sizeof table);
+    if (e == cudaSuccess) {
+        r->turns = (uint64_t*)((char*)r->ws + 256);
+        e = cudaMemset(r->ws, 0, 256);
+    }
+    if (e == cudaSuccess && rotary_dim)
+        e = cudaMemcpy(r->turns, table, rotary_dim / 2 * sizeof(uint64_t), cudaMemcpyHostToDevice);
+    // both are queued on the legacy stream, which other streams need not wait for
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+        cudaGetLastError();   // (as in cuda_fail)
+        if (r->ws) cudaFree(r->ws);
+        delete r;
+        return e == cudaErrorMemoryAllocation ? fail(MLORA_ERR_OOM, "workspace: %s", cudaGetErrorString(e))
+                                              : cuda_fail(e, "mlora_rotary_create");
+    }
+    *out = r;
+    return MLORA_OK;
+}
+
+mlora_status mlora_rotary_destroy(mlora_rotary_t r) {
+    if (!r) return MLORA_OK;
+    DeviceGuard g(r->device);
+    cudaError_t e = g.err;
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (r->ws) cudaFree(r->ws);
+    delete r;
+    return e == cudaSuccess ? MLORA_OK : cuda_fail(e, "mlora_rotary_destroy");
+}
+
+mlora_status mlora_rotary_apply(mlora_rotary_t r, const void* Q, int64_t q_row, int64_t q_head, void* Qo, int64_t qo_row,
+                                int64_t qo_head, int q_heads, const void* K, int64_t k_row, int64_t k_head, void* Ko,
+                                int64_t ko_row, int64_t ko_head, int kv_heads, mlora_dtype dtype, int T,
+                                const float* q_weight, const float* k_weight, float eps, const int32_t* offsets,
+                                const int32_t* lengths, int n_seqs, int max_new, mlora_stream_t stream) {
+    if (!r) return fail(MLORA_ERR_INVALID_ARG, "rotary is NULL");
+    if (dtype != MLORA_F32 && dtype != MLORA_BF16) return fail(MLORA_ERR_INVALID_ARG, "dtype %d", (int)dtype);
+    if (T < 0 || n_seqs < 0 || max_new < 0)
+        return fail(MLORA_ERR_INVALID_ARG, "T %d, n_seqs %d or max_new %d is negative", T, n_seqs, max_new);
+    if (n_seqs > 65535) return fail(MLORA_ERR_INVALID_ARG, "n_seqs %d exceeds 65535", n_seqs);
+    if (!offsets && T != n_seqs)
+        return fail(MLORA_ERR_INVALID_ARG, "without offsets T %d must equal n_seqs %d", T, n_seqs);
+    if (q_heads < 1 || q_heads > 32767 || kv_heads < 1 || kv_heads > 32767)
+        return fail(MLORA_ERR_INVALID_ARG, "q_heads %d and kv_heads %d must lie in [1, 32767]", q_heads, kv_heads);
+    if (!(eps >= 0.f && eps < 3.0e38f)) return fail(MLORA_ERR_INVALID_ARG, "eps %g", eps);
+    if (((uintptr_t)q_weight | (uintptr_t)k_weight) & 3u)
+        return fail(MLORA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+    if (!(T > 0 && n_seqs > 0 && max_new > 0)) return MLORA_OK;
+    if (!lengths) return fail(MLORA_ERR_INVALID_ARG, "lengths is NULL");
+    mlora_status st = check_rows("Q", Q, q_row, q_head, dtype);
+    if (st == MLORA_OK) st = check_rows("Q_out", Qo, qo_row, qo_head, dtype);
+    if (st == MLORA_OK) st = check_rows("K", K, k_row, k_head, dtype);
+    if (st == MLORA_OK) st = check_rows("K_out", Ko, ko_row, ko_head, dtype);
+    if (st != MLORA_OK) return st;
+    DeviceGuard g(r->device);
+    if (g.err != cudaSuccess) return cuda_fail(g.err, "cudaSetDevice");
+    const CacheStep step{offsets, lengths, nullptr, n_seqs, 1 << 15, T, max_new < T ? max_new : T};
+    const RotaryArgs a{RowsIn{Q, q_row, q_head}, RowsIn{K, k_row, k_head}, RowsOut{Qo, qo_row, qo_head},
+                       RowsOut{Ko, ko_row, ko_head}, q_heads, kv_heads, r->dim, r->turned, r->turns, q_weight, k_weight,
+                       eps, step, 0, 0, r->ws};
+    const cudaError_t e = dtype == MLORA_BF16
+                              ? launch_by_dim<__nv_bfloat16>(a, r->interleaved, r->sms, (cudaStream_t)stream)
+                              : launch_by_dim<float>(a, r->interleaved, r->sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MLORA_OK : cuda_fail(e, "mlora_rotary_apply");
+}
+
+mlora_status mlora_rotary_status(mlora_rotary_t r, mlora_stream_t stream) {
+    if (!r) return fail(MLORA_ERR_INVALID_ARG, "rotary is NULL");
+    DeviceGuard g(r->device);
+    cudaError_t e = g.err;
+    cudaStream_t st = (cudaStream_t)stream;
+    uint32_t word = 0;
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&word, r->ws, sizeof word, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(r->ws, 0, sizeof word, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return cuda_fail(e, "mlora_rotary_status");
+    if (word & STATUS_BAD_STEP) return fail(MLORA_ERR_DEVICE_STEP, "a step named rows or lengths out of range");
+    return MLORA_OK;
+}
+
+}  // extern "C"

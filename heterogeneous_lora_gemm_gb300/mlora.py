@@ -86,12 +86,19 @@ _SIGNATURES = {
     "mlora_project_noalloc_status": (_I, [_P]),
     "mlora_debug_noalloc_expire_wait": (_I, [ctypes.c_longlong, _P]),
     "mlora_cache_create": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_uint64, ctypes.POINTER(_P)]),
+    "mlora_cache_create4": (_I, [_P, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, ctypes.c_uint64,
+                                 ctypes.POINTER(_P)]),
     "mlora_cache_destroy": (_I, [_P]),
     "mlora_cache_append": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
     "mlora_cache_read": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, _P]),
     "mlora_cache_attend": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _P, _I, _I, _I, ctypes.c_float, _I, _P]),
     "mlora_cache_status": (_I, [_P, _P]),
     "mlora_debug_cache_expire_wait": (_I, [_P, ctypes.c_longlong, _P]),
+    "mlora_rotary_create": (_I, [_I, _I, ctypes.POINTER(ctypes.c_double), _I, ctypes.POINTER(_P)]),
+    "mlora_rotary_destroy": (_I, [_P]),
+    "mlora_rotary_apply": (_I, [_P, _P, _L, _L, _P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _I, _I, _I, _P, _P,
+                                ctypes.c_float, _P, _P, _I, _I, _P]),
+    "mlora_rotary_status": (_I, [_P, _P]),
     "mlora_arena_new": (_P, [_I]),
     "mlora_arena_delete": (None, [_P]),
     "mlora_arena_alloc": (_I, [_P, _I, _I]),
@@ -278,6 +285,17 @@ def mlora_cache_create(k_codes_ptr: int, k_scale_ptr: int, v_codes_ptr: int, v_s
     return h.value
 
 
+def mlora_cache_create4(blocks_ptr: int, n_pages: int, page_size: int, kv_heads: int, head_dim: int, q_heads: int,
+                        k_unit: float, v_unit: float, prompt_bytes: int) -> int:
+    _ints(n_pages=n_pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim, q_heads=q_heads)
+    if not 0 <= prompt_bytes < 1 << 64:
+        raise ValueError(f"prompt_bytes {prompt_bytes} does not fit 64 bits")
+    h = _P()
+    check(lib().mlora_cache_create4(blocks_ptr, n_pages, page_size, kv_heads, head_dim, q_heads, k_unit, v_unit,
+                                    prompt_bytes, ctypes.byref(h)), "mlora_cache_create4")
+    return h.value
+
+
 def mlora_cache_destroy(cache: int) -> None:
     check(lib().mlora_cache_destroy(cache), "mlora_cache_destroy")
 
@@ -320,6 +338,42 @@ def mlora_cache_status(cache: int, stream: int) -> int:
 
 def mlora_debug_cache_expire_wait(cache: int, cycles: int, stream: int) -> None:
     check(lib().mlora_debug_cache_expire_wait(cache, int(cycles), stream or None), "mlora_debug_cache_expire_wait")
+
+
+def mlora_rotary_create(head_dim: int, rotary_dim: int, freq, interleaved: bool) -> int:
+    _ints(head_dim=head_dim, rotary_dim=rotary_dim)
+    freq = [float(f) for f in freq]
+    if len(freq) != max(rotary_dim, 0) // 2:
+        raise ValueError(f"freq has {len(freq)} entries, one per pair of the {rotary_dim} elements that turn is needed")
+    h = _P()
+    check(lib().mlora_rotary_create(head_dim, rotary_dim, (ctypes.c_double * len(freq))(*freq), int(bool(interleaved)),
+                                    ctypes.byref(h)), "mlora_rotary_create")
+    return h.value
+
+
+def mlora_rotary_destroy(rotary: int) -> None:
+    check(lib().mlora_rotary_destroy(rotary), "mlora_rotary_destroy")
+
+
+def mlora_rotary_apply(rotary: int, Q_ptr: int, q_row_stride: int, q_head_stride: int, Q_out_ptr: int,
+                       qo_row_stride: int, qo_head_stride: int, q_heads: int, K_ptr: int, k_row_stride: int,
+                       k_head_stride: int, K_out_ptr: int, ko_row_stride: int, ko_head_stride: int, kv_heads: int,
+                       dtype: int, T: int, q_weight_ptr: Optional[int], k_weight_ptr: Optional[int], eps: float,
+                       offsets_ptr: Optional[int], lengths_ptr: int, n_seqs: int, max_new: int, stream: int) -> None:
+    _ints(T=T, n_seqs=n_seqs, max_new=max_new, q_heads=q_heads, kv_heads=kv_heads)
+    check(lib().mlora_rotary_apply(rotary, Q_ptr, q_row_stride, q_head_stride, Q_out_ptr, qo_row_stride,
+                                   qo_head_stride, q_heads, K_ptr, k_row_stride, k_head_stride, K_out_ptr,
+                                   ko_row_stride, ko_head_stride, kv_heads, dtype, T, q_weight_ptr or None,
+                                   k_weight_ptr or None, eps, offsets_ptr or None, lengths_ptr, n_seqs, max_new,
+                                   stream or None), "mlora_rotary_apply")
+
+
+def mlora_rotary_status(rotary: int, stream: int) -> int:
+    """Returns MLORA_OK or MLORA_ERR_DEVICE_STEP; raises on CUDA errors."""
+    s = int(lib().mlora_rotary_status(rotary, stream or None))
+    if s not in (MLORA_OK, MLORA_ERR_DEVICE_STEP):
+        check(s, "mlora_rotary_status")
+    return s
 
 
 # ---- torch-facing convenience ------------------------------------------- #
@@ -456,11 +510,7 @@ class Cache:
 
     def __init__(self, k_codes, k_scale, v_codes, v_scale, q_heads: int, prompt_bytes: int = 256 << 20):
         import torch
-        self.handle = None
-        self._dtypes = {torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32}
-        self._i32 = torch.int32
-        # (the current stream's handle without a Stream object: a decode step's calls are short)
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._types()
         if k_codes.dim() != 4 or k_codes.dtype != torch.int8 or v_codes.dtype != torch.int8:
             raise ValueError("codes are int8 [n_pages, kv_heads, page_size, head_dim]")
         n_pages, kv_heads, page_size, head_dim = k_codes.shape
@@ -478,6 +528,14 @@ class Cache:
             self.handle = mlora_cache_create(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(),
                                              v_scale.data_ptr(), n_pages, page_size, kv_heads, head_dim, q_heads,
                                              prompt_bytes)
+
+    def _types(self) -> None:
+        import torch
+        self.handle = None
+        self._dtypes = {torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32}
+        self._i32 = torch.int32
+        # (the current stream's handle without a Stream object: a decode step's calls are short)
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
 
     def close(self) -> None:
         if getattr(self, "handle", None):
@@ -546,3 +604,114 @@ class Cache:
 
     def status(self, stream=None) -> int:
         return mlora_cache_status(self.handle, _stream_handle(stream))
+
+
+class Cache4(Cache):
+    """A key/value cache in 4 bits over the caller's blocks (a torch tensor), see include/mlora.h.
+
+    blocks: uint8 [n_pages, kv_heads, page_size // 16, 18 * head_dim]; contiguous, on a CUDA
+    device, kept alive by the cache; what it holds at first does not matter.  k_unit, v_unit: what a
+    code times its scale counts; elements up to 3136 units are held.  Its calls are Cache's.
+    """
+
+    def __init__(self, blocks, q_heads: int, k_unit: float = 0.0625, v_unit: float = 0.0625,
+                 prompt_bytes: int = 256 << 20):
+        import torch
+        self._types()
+        if blocks.dim() != 4 or blocks.dtype != torch.uint8 or blocks.shape[3] % 18:
+            raise ValueError("blocks is uint8 [n_pages, kv_heads, page_size // 16, 18 * head_dim]")
+        if not blocks.is_contiguous() or not blocks.is_cuda:
+            raise ValueError("blocks is contiguous and on a CUDA device")
+        n_pages, kv_heads, page_size, head_dim = blocks.shape[0], blocks.shape[1], blocks.shape[2] * 16, blocks.shape[3] // 18
+        self._keep = (blocks,)
+        self.device, self._index = blocks.device, blocks.get_device()
+        self.kv_heads, self.q_heads, self.page_size, self.head_dim = kv_heads, q_heads, page_size, head_dim
+        self.k_unit, self.v_unit = k_unit, v_unit
+        self._lib = lib()
+        with torch.cuda.device(self.device):
+            self.handle = mlora_cache_create4(blocks.data_ptr(), n_pages, page_size, kv_heads, head_dim, q_heads, k_unit,
+                                              v_unit, prompt_bytes)
+
+
+class Rotary:
+    """Norms and rotation of query and key heads ahead of a cache (torch tensors), see include/mlora.h.
+
+    The first rotary_dim elements of a head (all unless given) turn by position * freq[i] for
+    pair i of rotary_dim // 2: the halves' elements i, or (interleaved) elements 2 i and 2 i + 1.  freq
+    is base ** (-2 i / rotary_dim) unless given.
+    """
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, base: float = 10000.0, freq=None,
+                 interleaved: bool = False, device="cuda"):
+        import torch
+        self.handle = None
+        if rotary_dim is None:
+            rotary_dim = head_dim if freq is None else 2 * len(freq)
+        if freq is None:
+            freq = [float(base) ** (-2.0 * i / rotary_dim) for i in range(max(rotary_dim, 0) // 2)]
+        self._dtypes = {torch.bfloat16: MLORA_BF16, torch.float32: MLORA_F32}
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self.head_dim, self.rotary_dim = head_dim, rotary_dim
+        self._lib = lib()
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("a CUDA device is needed")
+        with torch.cuda.device(device):
+            self._index = torch.cuda.current_device()
+            self.device = torch.device("cuda", self._index)
+            self.handle = mlora_rotary_create(head_dim, rotary_dim, freq, interleaved)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            mlora_rotary_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _rows(self, x, out, code):
+        shape, strides, to = x.shape, x.stride(), out.stride()
+        if len(shape) != 3 or shape[2] != self.head_dim or out.shape != shape:
+            raise ValueError(f"rows are [T, heads, {self.head_dim}], got {tuple(shape)} into {tuple(out.shape)}")
+        if code is None or self._dtypes.get(x.dtype) != code or out.dtype != x.dtype:
+            raise ValueError("rows are bf16 or fp32, all operands alike")
+        if strides[2] != 1 or to[2] != 1:
+            raise ValueError("a head's elements must be adjacent")
+        if x.get_device() != self._index or out.get_device() != self._index:
+            raise ValueError(f"operands live on the rotary's device {self.device}")
+        return x.data_ptr(), strides[0], strides[1], out.data_ptr(), to[0], to[1], shape[1]
+
+    def apply(self, Q, K, lengths, offsets=None, max_new: int = 1, q_weight=None, k_weight=None, eps: float = 1e-6,
+              q_out=None, k_out=None, stream=None) -> None:
+        """Norms (where there is a weight, fp32 [head_dim]) and turns the step's rows Q [T, q_heads, head_dim] and
+        K [T, kv_heads, head_dim], in place or into q_out and k_out.  The step's arrays are the cache's."""
+        code, index = self._dtypes.get(Q.dtype), self._index
+        q = self._rows(Q, Q if q_out is None else q_out, code)
+        k = self._rows(K, K if k_out is None else k_out, code)
+        T, n_seqs = Q.shape[0], lengths.numel()
+        if K.shape[0] != T:
+            raise ValueError(f"Q has {T} rows, K {K.shape[0]}")
+        for t, n in ((lengths, n_seqs), (offsets, n_seqs + 1)):
+            if t is not None and (t.shape != (n,) or t.dtype != self._i32 or not t.is_contiguous() or
+                                  t.get_device() != index):
+                raise ValueError(f"lengths and offsets are contiguous int32 [n_seqs] and [n_seqs + 1] on {self.device}")
+        for t in (q_weight, k_weight):
+            if t is not None and (t.shape != (self.head_dim,) or t.dtype != self._f32 or not t.is_contiguous() or
+                                  t.get_device() != index):
+                raise ValueError(f"weights are contiguous fp32 [{self.head_dim}] on {self.device}")
+        if not (-_INT_MAX <= max_new <= _INT_MAX and T <= _INT_MAX and n_seqs <= _INT_MAX):
+            _ints(T=T, n_seqs=n_seqs, max_new=max_new)
+        handle = self._raw_stream(index) if stream is None else stream.cuda_stream
+        status = self._lib.mlora_rotary_apply(
+            self.handle, *q, *k, code, T, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), eps, None if offsets is None else offsets.data_ptr(),
+            lengths.data_ptr(), n_seqs, max_new, handle)
+        if status:
+            check(status, "mlora_rotary_apply")
+
+    def status(self, stream=None) -> int:
+        return mlora_rotary_status(self.handle, _stream_handle(stream))

@@ -415,15 +415,27 @@ mlora_status mlora_project_noalloc_status(mlora_stream_t stream);
 mlora_status mlora_debug_noalloc_expire_wait(long long cycles, mlora_stream_t stream);
 
 /*
- * Key/value cache in 8 bits and its attention: what a served layer does between its
- * q|k|v projection and its output projection.  The projections' rows of a step (any
+ * Key/value cache in 8 or in 4 bits and its attention: what a served layer does between
+ * its q|k|v projection and its output projection.  The projections' rows of a step (any
  * mix of sequences) are appended to each sequence's pages, and each sequence's new
  * rows then attend to everything the sequence holds.
  *
- * The caller owns the pages (device memory, on the device current at creation):
+ * The caller owns the pages (device memory, on the device current at creation).
+ * In 8 bits (mlora_cache_create):
  *   k_codes, v_codes  int8 [n_pages][kv_heads][page_size][head_dim], 16-byte aligned
  *   k_scale, v_scale  fp32 [n_pages][kv_heads]
  * a stored value is code * scale, one scale (>= 0) per page and head, for keys and for values.
+ * In 4 bits (mlora_cache_create4):
+ *   blocks  bytes [n_pages][kv_heads][page_size / 16][18 * head_dim], 16-byte aligned
+ * a stored value is code * scale * unit, codes -7 .. 7, one e4m3 scale (>= 0) per token, head and
+ * 16 elements, one unit for all keys and one for all values: 4.5 bits an element.  A block holds 16
+ * tokens of a head: head_dim atoms of keys, head_dim atoms of values, then a byte of scale for
+ * each, in the same order.  An atom is 8 bytes, 16 elements of a token, element e in nibble e
+ * (the low nibble of a byte first) as code + 8.  With n = head_dim / 16 groups, the atom of token t
+ * (of 16) and group g is number
+ *   keys    g/4 * 64  + (t%8 * min(4, n - g/4*4) + g%4) * 2 + t/8
+ *   values  g/8 * 128 + (t/8 * min(8, n - g/8*8) + g%8) * 8 + t%8
+ * A token's bytes depend on that token alone; those that nothing was written to may hold anything.
  *
  * A step is described to every call below by the same arrays (device, int32):
  *   offsets  [n_seqs + 1]: rows offsets[b] .. offsets[b+1] are sequence b's, in order;
@@ -475,16 +487,30 @@ typedef struct mlora_cache* mlora_cache_t;
 mlora_status mlora_cache_create(void* k_codes, float* k_scale, void* v_codes, float* v_scale, int n_pages,
                                 int page_size, int kv_heads, int head_dim, int q_heads, uint64_t prompt_bytes,
                                 mlora_cache_t* out);
+/*
+ * Makes a handle over the caller's 4-bit blocks; every call below takes it.
+ *   k_unit, v_unit  in [2^-60, 2^60]: elements up to 3136 units are held (larger ones as 3136), and
+ *              16 whose largest is under 7/1024 of a unit as zeros (under 7/64 with fewer bits of scale); 1/16
+ *              holds 0.007 to 196 well, and down to 0.0005
+ * and the rest as mlora_cache_create's, with the same workspace and errors.
+ */
+mlora_status mlora_cache_create4(void* blocks, int n_pages, int page_size, int kv_heads, int head_dim, int q_heads,
+                                 float k_unit, float v_unit, uint64_t prompt_bytes, mlora_cache_t* out);
 /* Waits for the device's outstanding work and frees the workspace. NULL is a no-op. */
 mlora_status mlora_cache_destroy(mlora_cache_t cache);
 
 /*
- * Quantises the step's key and value rows into the pages.  Per touched page and head,
+ * Quantises the step's key and value rows into the pages.  In 8 bits, per touched page and head,
  * with x the values that it then holds (what it held restored, and the new rows):
  *   s = max(s_old, max over new rows |x| / 127)     (s_old = 0 if the page's first token is new)
  *   code = rint(x * (1 / s)) clamped to [-127, 127] (ties to even; 0 where s < 2^-120)
  * in fp32; codes written before change only where s grew.  Infinities and NaN do not
  * enter the maximum: an infinity is stored as +-127 s, a NaN as 0.
+ * In 4 bits, per token, head and 16 elements x:
+ *   s = e4m3(max |x| * (1 / (7 * unit))), to nearest (ties to even), at most 448
+ *   code = rint(x * (1 / (s * unit))) clamped to [-7, 7] (ties to even; 0 where s = 0)
+ * in fp32, infinities and NaN as above (+-7 s, 0).  A page may then be appended to by several
+ * sequences, as long as no two write one token.
  * Errors: INVALID_ARG, CUDA.
  */
 mlora_status mlora_cache_append(mlora_cache_t cache, const void* K, int64_t k_row_stride, int64_t k_head_stride,
@@ -493,7 +519,7 @@ mlora_status mlora_cache_append(mlora_cache_t cache, const void* K, int64_t k_ro
                                 int width, int max_new, mlora_stream_t stream);
 /*
  * Restores the step's tokens (the last n_b of each sequence) into rows:
- * K[row] = code * scale, in fp32, rounded once to `dtype`; V likewise.
+ * K[row] = code * scale (in 4 bits times the unit), in fp32, rounded once to `dtype`; V likewise.
  * Errors: INVALID_ARG, CUDA.
  */
 mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride, int64_t k_head_stride, void* V,
@@ -506,14 +532,14 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * over the tokens j of the row's sequence with j <= pos(i), and j > pos(i) - window
  * where window > 0; query head h reads key/value head h / (q_heads / kv_heads).  A row
  * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums
- * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, value
- * scales under 2^-96 lose low bits, under 2^-120 they may count as 0); O is rounded
- * once.  Weights are held in 24 bits for fp32 rows and in 16 for bf16 rows, in 8 where
+ * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, 8-bit value
+ * scales under 2^-96 lose low bits, under 2^-120 they may count as 0; 4-bit sums hold values over
+ * their unit, which the output takes at the end); O is rounded once.  Weights are held in 24 bits for fp32 rows and in 16 for bf16 rows, in 8 where
  * max_new * q_heads / kv_heads > 16; in that form sums of one sign come out 0.25% low over
  * 2^20 tokens, and lower over more.  O must not overlap Q: fp32 rows of it may hold sums
  * during the call.
  * Errors: INVALID_ARG, UNSUPPORTED (with max_new taken as T where it is larger: max_new *
- * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34), CUDA.
+ * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34; in 4 bits, scale * k_unit outside [2^-120, 3e38)), CUDA.
  */
 mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_row_stride, int64_t q_head_stride,
                                 void* O, int64_t o_row_stride, int64_t o_head_stride, mlora_dtype dtype, int T,
@@ -528,6 +554,48 @@ mlora_status mlora_cache_attend(mlora_cache_t cache, const void* Q, int64_t q_ro
 mlora_status mlora_cache_status(mlora_cache_t cache, mlora_stream_t stream);
 /* Test hook for that status, as mlora_debug_noalloc_expire_wait. Errors: INVALID_ARG, CUDA. */
 mlora_status mlora_debug_cache_expire_wait(mlora_cache_t cache, long long cycles, mlora_stream_t stream);
+
+/*
+ * Norms and rotation of query and key heads, between the q|k|v projection and
+ * mlora_cache_append, in one pass.  Per row at position p, each head x of head_dim elements:
+ *   y = weight * x / sqrt(mean(x^2) + eps)        (y = x where the weight is NULL)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos),  angle p * freq[i],  for each pair
+ *   i < rotary_dim / 2: (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if interleaved
+ * elements from rotary_dim on do not turn.  fp32 inside, rounded once; angles are exact modulo a
+ * turn to 2^-32 of one.  A head of zeros under eps = 0 gives zeros.
+ */
+typedef struct mlora_rotary* mlora_rotary_t;
+
+/*
+ * Makes a handle (a table of angles and a status word) on the current device.
+ *   head_dim    16, 32, 48, ... 256;  rotary_dim  0, 16, 32, ... head_dim (0: norms alone)
+ *   freq        host [rotary_dim / 2], radians per position, each in [-1024, 1024] (e.g. base ^ (-2 i / rotary_dim),
+ *               or as a scheme for longer contexts changes them); copied
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes), OOM, CUDA.  Argument checks run before any CUDA call.
+ */
+mlora_status mlora_rotary_create(int head_dim, int rotary_dim, const double* freq, int interleaved, mlora_rotary_t* out);
+/* Waits for the device's outstanding work and frees the table. NULL is a no-op. */
+mlora_status mlora_rotary_destroy(mlora_rotary_t rotary);
+/*
+ * Turns the step's query rows Q into Q_out and its key rows K into K_out, each [T][heads][head_dim]
+ * with strides and alignment as mlora_cache_append's rows; an output may be its input itself (same
+ * strides), and overlaps no other operand.  offsets, lengths and max_new describe the step as for the cache's
+ * calls: rows at negative positions name no token and come out as zeros, rows outside every
+ * range are left alone, lengths are clamped to 0 .. 2^30; what is out of range sets the status bit that
+ * mlora_rotary_status reports.
+ *   q_weight, k_weight  device fp32 [head_dim], or NULL: no norm
+ *   eps                 >= 0 (not read without weights)
+ * Allocates nothing.  Calls on one handle may overlap, on any streams.
+ * Errors: INVALID_ARG, CUDA.
+ */
+mlora_status mlora_rotary_apply(mlora_rotary_t rotary, const void* Q, int64_t q_row_stride, int64_t q_head_stride,
+                                void* Q_out, int64_t qo_row_stride, int64_t qo_head_stride, int q_heads, const void* K,
+                                int64_t k_row_stride, int64_t k_head_stride, void* K_out, int64_t ko_row_stride,
+                                int64_t ko_head_stride, int kv_heads, mlora_dtype dtype, int T, const float* q_weight,
+                                const float* k_weight, float eps, const int32_t* offsets, const int32_t* lengths,
+                                int n_seqs, int max_new, mlora_stream_t stream);
+/* Synchronizes `stream`, then reads and clears the status word: MLORA_OK, MLORA_ERR_DEVICE_STEP or MLORA_ERR_CUDA. */
+mlora_status mlora_rotary_status(mlora_rotary_t rotary, mlora_stream_t stream);
 
 /*
  * Host-only view of the arena allocator the pool uses (no CUDA calls), for tests
