@@ -50,12 +50,16 @@ constexpr int PIECE = 16;                 // tokens of a copied box and of a pro
 constexpr int LEAD = 1;                   // units (of WARPS chunks) that starting an item costs
 constexpr int MIN_UNITS = LEAD + 1;       // a CTA's range is at least so long
 constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights stay below 2^8
+// fp16 weights: m is the largest x less OFF16 when it is set, and moves when x > m + OFF16 + SLACK16, so that
+// they stay below 2^15 and their 11 bits reach down to 2^-26 of the largest
+constexpr float OFF16 = 12.f, SLACK16 = 3.f;
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
 template <int BITS, bool F32, int DP, int NT>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query
-    static constexpr int PTERMS = F32 ? 3 : 2;         // of a weight
+    static constexpr bool P16 = BITS == 4 && !F32;     // weights and values in fp16
+    static constexpr int PTERMS = F32 ? 3 : P16 ? 1 : 2;   // of a weight
     static constexpr int KS = DP / 16;                 // k steps of q . k = 16-row tiles of O^T
     static constexpr int RT = 8 * NT;                  // query rows per tile
     static constexpr int CB = DP == 256 ? 2 : 1;       // column boxes
@@ -205,8 +209,9 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                  : "memory");
 }
 
-// `zeros`: a 4-bit block of zeros, in the place of one that cannot be read
-template <int BITS, bool F32, int DP, int NT>
+// `zeros`: a 4-bit block of zeros, in the place of one that cannot be read.  FULL: heads of DP elements,
+// so that a 4-bit block's offsets are constants.
+template <int BITS, bool F32, int DP, int NT, bool FULL>
 __global__ void __launch_bounds__(THREADS, (Shape<BITS, F32, DP, NT>::OCC))
 attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
                     float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
@@ -220,11 +225,11 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     __shared__ Tail tl;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
     const CachePages& c = a.pages;
-    const int H = c.heads, G = a.q_heads / H, D = c.dim;
+    const int H = c.heads, G = a.q_heads / H, D = FULL ? DP : c.dim;
 
     // ---- this CTA's range of the line
     if (lane == 0) {
-        for (int s = 0; s < Sh::STAGES; ++s) mbar_init(&tl.full[warp][s], 1);
+        for (int s = 0; s < Sh::STAGES; ++s) mbar_init(&tl.full[warp][s], BITS == 4 ? Sh::SUB : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) tl.abort_flag = 0;
@@ -287,6 +292,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     n = tl.first;
 
     uint32_t issued = 0, used = 0;     // chunks copied and consumed by this warp, over all items
+    uint32_t fill = 0, drain = 0, turn = 0;   // 4 bits: their stages, and the phase of the one consumed
     uint8_t* ring = smem + warp * Sh::STAGES * Sh::STAGE;
     volatile int* abort_flag = &tl.abort_flag;
     bool alive = true;
@@ -364,19 +370,26 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
         }
         // copies chunk k of the item, a box per lane; `row` holds batch `batch`
-        const int box = lane % (2 * CB * SUB), box_v = box / CB & 1, box_q = box % CB;
-        const int box_sub = BITS == 4 ? lane % SUB : box / (2 * CB);
+        const int box = lane % (2 * CB * SUB), box_sub = box / (2 * CB), box_v = box / CB & 1, box_q = box % CB;
         auto issue = [&](int k, int batch) {
+            if (BITS == 4) {   // (a block by the lane that looked its page up)
+                if (lane / SUB == k % BATCH) {
+                    const int r = k / BATCH == batch ? row : row1;
+                    uint64_t* bar = &tl.full[warp][fill];
+                    mbar_expect_tx(bar, block4_bytes(D));
+                    bulk_g2s(ring + fill * Sh::STAGE + lane % SUB * Sh::PART,
+                             r < 0 ? zeros : c.blocks + (size_t)(uint32_t)r * (uint32_t)block4_bytes(D), block4_bytes(D), bar);
+                }
+                fill = fill + 1 == Sh::STAGES ? 0 : fill + 1;
+                ++issued;
+                return;
+            }
             const int r = __shfl_sync(~0u, k / BATCH == batch ? row : row1, k % BATCH * SUB + box_sub);
             const uint32_t st = issued % Sh::STAGES;
             uint64_t* bar = &tl.full[warp][st];
-            if (lane == 0) mbar_expect_tx(bar, BITS == 4 ? SUB * block4_bytes(D) : Sh::STAGE);
+            if (lane == 0) mbar_expect_tx(bar, Sh::STAGE);
             __syncwarp();
-            if (BITS == 4) {
-                if (lane < SUB)
-                    bulk_g2s(ring + st * Sh::STAGE + lane * Sh::PART, r < 0 ? zeros : c.blocks + (size_t)r * block4_bytes(D),
-                             block4_bytes(D), bar);
-            } else if (lane < 2 * CB * SUB)
+            if (lane < 2 * CB * SUB)
                 tma_2d(ring + st * Sh::STAGE + box_sub * Sh::PART + (box_v * CB + box_q) * Sh::BOX, box_v ? &tmV : &tmK, bar,
                        box_q * 128, r);
             ++issued;
@@ -402,8 +415,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             // stays below 2^14 (within fp16, where a factor of 2^128 would leave fp32)
             const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 114) : 0;
             const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-            if (lane == 0)
-                tl.qf[r] = fine ? a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23)) : NAN;
+            const float qf = a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23));
+            if (lane == 0) tl.qf[r] = !fine ? NAN : Sh::P16 ? fmaxf(qf, 0x1p-126f) : qf;   // (P16: -inf times it stays -inf)
 #pragma unroll
             for (int e = 0; e < EL; e += 2) {
                 if (BITS == 4) {
@@ -412,7 +425,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int d = lane * EL + e + z, x4 = d % 4, s = d / 64 * 4 + d % 16 / 8 * 2 + x4 / 2, t = d % 64 / 16;
-                        const float v = fine ? x[kk][e + z] * down : 0.f;
+                        const float v = fine ? x[kk][e + z] * (x4 % 2 ? down : down * 16.f) : 0.f;
                         __half* dst = reinterpret_cast<__half*>(qfrag + (((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + x4 % 2) + d % 8 / 4;
                         const __half hi = __float2half_rn(v);
                         *dst = hi;
@@ -447,6 +460,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) qreg[s][t][term] = qf_at(s, t, term);
         float qf[NT][2], m[NT][2], l[NT][2], o[KS][NT][4];
+        float bound[NT][2], sum[NT][4];   // P16: (m + OFF16 + SLACK16) / qf, and l as the tensor cores sum it
         int hi[NT][2];   // tokens first_seen(hi - 1) .. hi - 1 are seen
         int hi_min = 0x7fffffff, hi_max = -0x7fffffff;
 #pragma unroll
@@ -456,7 +470,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 const int r = t * 8 + 2 * tig + e;
                 qf[t][e] = tl.qf[r];
                 m[t][e] = NO_MAX;
-                l[t][e] = 0.f;
+                l[t][e] = sum[t][e] = sum[t][2 + e] = 0.f;
+                bound[t][e] = -3e38f;
                 hi[t][e] = pos_lo + token_of(min(r, rows - 1)) + 1;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) o[s][t][e] = o[s][t][2 + e] = 0.f;
@@ -483,12 +498,16 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 ksk[u] = BITS == 4 ? 1.f : __shfl_sync(~0u, ks, k % BATCH * SUB + u);
                 vsk[u] = BITS == 4 ? 1.f : __shfl_sync(~0u, vs, k % BATCH * SUB + u);
             }
-            const uint32_t st = used % Sh::STAGES;
-            alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], (used / Sh::STAGES) & 1, abort_flag, a.status));
+            const uint32_t st = BITS == 4 ? drain : used % Sh::STAGES;
+            alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], BITS == 4 ? turn : (used / Sh::STAGES) & 1, abort_flag, a.status));
             if (!alive) break;
+            if (BITS == 4) {
+                drain = drain + 1 == Sh::STAGES ? 0 : drain + 1;
+                turn ^= drain == 0;
+            }
             const uint8_t* stage = ring + st * Sh::STAGE;
 
-            constexpr int CH = 2 / SUB;                  // independent sums per piece (even and odd k steps)
+            constexpr int CH = SUB == 1 ? 2 : 1;         // independent sums per piece (even and odd k steps)
             float sc[SUB][CH][NT][4] = {};
             auto scores4 = [&](int u, int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
@@ -499,6 +518,15 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
                     }
             };
+            // a lane's two atoms of a block and their scales (zeros where the head has no such group)
+            auto atoms_at = [&](const uint8_t* codes, const uint8_t* scales, int at, bool there, uint4& w, uint32_t& s16) {
+                w = make_uint4(0u, 0u, 0u, 0u);
+                s16 = 0u;
+                if (FULL || there) {
+                    w = *reinterpret_cast<const uint4*>(codes + at * 8);
+                    s16 = *reinterpret_cast<const uint16_t*>(scales + at);
+                }
+            };
             if (BITS == 4) {
                 // 64 elements at a time: the lane's atoms of tokens g and g + 8, group tig of the four
 #pragma unroll
@@ -507,13 +535,10 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     for (int u = 0; u < SUB; ++u) {
                         const uint8_t* kb = stage + u * Sh::PART;
                         const int n = min(4, D / 16 - 4 * q), at = q * 64 + (g * n + tig) * 2;
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        uint32_t s16 = 0u;
-                        if (DP == D || tig < n) {
-                            w = *reinterpret_cast<const uint4*>(kb + at * 8);
-                            s16 = *reinterpret_cast<const uint16_t*>(kb + 16 * D + at);
-                        }
-                        const Scale2 sa = scale_f16(prmt(s16, 0u, 0x4040)), sb = scale_f16(prmt(s16, 0u, 0x4141));
+                        uint4 w;
+                        uint32_t s16;
+                        atoms_at(kb, kb + 16 * D, at, tig < n, w, s16);
+                        const Scale3 sa = scale_f16(prmt(s16, 0u, 0x4040)), sb = scale_f16(prmt(s16, 0u, 0x4141));
                         scores4(u, 4 * q, codes_f16<0>(w.x, sa), codes_f16<0>(w.z, sb), codes_f16<1>(w.x, sa), codes_f16<1>(w.z, sb));
                         scores4(u, 4 * q + 1, codes_f16<2>(w.x, sa), codes_f16<2>(w.z, sb), codes_f16<3>(w.x, sa), codes_f16<3>(w.z, sb));
                         scores4(u, 4 * q + 2, codes_f16<0>(w.y, sa), codes_f16<0>(w.w, sb), codes_f16<1>(w.y, sa), codes_f16<1>(w.w, sb));
@@ -555,6 +580,93 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
             bool above = false;
             float top[NT][2];
+            if constexpr (Sh::P16) {
+                // the largest score itself, against the bound over the row's factor; then one fused operation
+                // per exponent
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        top[t][e] = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            float& x0 = sc[u][0][t][e];
+                            float& x1 = sc[u][0][t][2 + e];
+                            if (CH == 2) x0 += sc[u][CH - 1][t][e], x1 += sc[u][CH - 1][t][2 + e];
+                            if (edge) {
+                                const int at = t0 + u * PIECE + g, from = first_seen(hi[t][e] - 1, a.window);
+                                if (at >= hi[t][e] || at < from) x0 = -INFINITY;
+                                if (at + 8 >= hi[t][e] || at + 8 < from) x1 = -INFINITY;
+                            }
+                            top[t][e] = fmaxf(top[t][e], fmaxf(x0, x1));
+                        }
+                        above |= top[t][e] > bound[t][e];
+                    }
+                if (__any_sync(~0u, above)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = top[t][e];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+                            x = fmaxf(fmaf(x, qf[t][e], -OFF16), m[t][e]);
+                            const float f = ex2(m[t][e] - x);
+                            m[t][e] = x;
+                            bound[t][e] = (x + (OFF16 + SLACK16)) / qf[t][e];
+                            sum[t][e] *= f;
+#pragma unroll
+                            for (int s = 0; s < KS; ++s) {
+                                o[s][t][e] *= f;
+                                o[s][t][2 + e] *= f;
+                            }
+                        }
+                }
+                constexpr uint32_t ONES = 0x3C003C00u;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t p[NT][2];   // weights as the B operand: tokens x rows
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const __half2 y = __floats2half2_rn(ex2(fmaf(sc[u][0][t][2 * z], qf[t][0], -m[t][0])),
+                                                                ex2(fmaf(sc[u][0][t][2 * z + 1], qf[t][1], -m[t][1])));
+                            p[t][z] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+                        }
+                        mma(sum[t], ONES, ONES, ONES, ONES, p[t][0], p[t][1]);   // (of all tokens, in every row of the result)
+                    }
+#pragma unroll
+                    for (int q = 0; q < CB; ++q) {
+                        // atoms of tokens 2 tig and + 1, + 8 and + 9, of the lane's group (DP 64: half a group), as words
+                        // of four elements, token 2 tig in the low half
+                        const uint8_t* vb = stage + u * Sh::PART + 8 * D;
+                        constexpr int W = Sh::ROWB / 32;
+                        const int n = min(8, D / 16 - 8 * q), gr = DP == 64 ? g >> 1 : g;
+                        uint32_t v[2][W];
+                        Scale3 vs[2];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            uint4 w;
+                            uint32_t s16;
+                            atoms_at(vb, vb + 9 * D, q * 128 + (z * n + gr) * 8 + tig * 2, gr < n, w, s16);
+                            vs[z] = scale_f16(prmt(s16 & 0x7F7Fu, 0u, 0x4140));
+                            const uint32_t lo = DP == 64 && (g & 1) ? w.y : w.x, hi = DP == 64 && (g & 1) ? w.w : w.z;
+                            v[z][0] = prmt(lo, hi, 0x5410), v[z][1] = prmt(lo, hi, 0x7632);
+                            if (W == 4) v[z][W - 2] = prmt(w.y, w.w, 0x5410), v[z][W - 1] = prmt(w.y, w.w, 0x7632);
+                        }
+#pragma unroll
+                        for (int w = 0; w < W; ++w)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                mma(o[q * (KS / CB) + w * 2][t], codes_f16<0>(v[0][w], vs[0]), codes_f16<1>(v[0][w], vs[0]),
+                                    codes_f16<0>(v[1][w], vs[1]), codes_f16<1>(v[1][w], vs[1]), p[t][0], p[t][1]);
+                                mma(o[q * (KS / CB) + w * 2 + 1][t], codes_f16<2>(v[0][w], vs[0]), codes_f16<3>(v[0][w], vs[0]),
+                                    codes_f16<2>(v[1][w], vs[1]), codes_f16<3>(v[1][w], vs[1]), p[t][0], p[t][1]);
+                            }
+                    }
+                }
+            } else {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -631,12 +743,9 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             const int at = q * 128 + (z * n + gr) * 8 + tig * 2;
-                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                            uint32_t s16 = 0u;
-                            if (DP == D || gr < n) {
-                                w = *reinterpret_cast<const uint4*>(vb + at * 8);
-                                s16 = *reinterpret_cast<const uint16_t*>(vb + 9 * D + at);
-                            }
+                            uint4 w;
+                            uint32_t s16;
+                            atoms_at(vb, vb + 9 * D, at, gr < n, w, s16);
                             vsc[z] = scale_bf16(prmt(s16, 0u, 0x4140));
                             // words of four elements, token 2 tig in the low half
                             const uint32_t lo = DP == 64 && (g & 1) ? w.y : w.x, hi = DP == 64 && (g & 1) ? w.w : w.z;
@@ -697,6 +806,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     }
                 }
             }
+            }
             ++used;
             __syncwarp();
             if (next < count) {
@@ -717,8 +827,10 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                if (Sh::P16) l[t][e] = sum[t][e];
+                else
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(~0u, l[t][e], d);
+                    for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(~0u, l[t][e], d);
                 if (g == 0) {
                     tl.m[warp][t * 8 + 2 * tig + e] = m[t][e];
                     tl.l[warp][t * 8 + 2 * tig + e] = l[t][e];
@@ -733,7 +845,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 float top = tl.m[0][r];
 #pragma unroll
                 for (int w = 1; w < WARPS; ++w) top = fmaxf(top, tl.m[w][r]);
-                const float f = ex2(m[t][e] - top);
+                const float f = ex2(m[t][e] - top), fe = Sh::P16 ? f * 16.f : f;   // (even elements are held over 16)
                 float* dst = join + (warp * RT + r) * DP;
 #pragma unroll
                 for (int q = 0; q < CB; ++q) {
@@ -743,8 +855,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int s = 0; s < SB; s += 2) {
                         const int d = q * 128 + g * (2 * SB) + 2 * s;
-                        float4 v = make_float4(o[q * SB + s][t][e] * f, o[q * SB + s][t][2 + e] * f,
-                                               o[q * SB + s + 1][t][e] * f, o[q * SB + s + 1][t][2 + e] * f);
+                        float4 v = make_float4(o[q * SB + s][t][e] * fe, o[q * SB + s][t][2 + e] * f,
+                                               o[q * SB + s + 1][t][e] * fe, o[q * SB + s + 1][t][2 + e] * f);
                         *reinterpret_cast<float4*>(dst + (d ^ (tig << 2))) = v;
                     }
                 }
@@ -817,22 +929,25 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
 }
 
-template <int BITS, bool F32, int DP, int NT>
+template <int BITS, bool F32, int DP, int NT, bool FULL>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     using Sh = Shape<BITS, F32, DP, NT>;
     static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace slots");
     // ranges are cut for OCC CTAs on each SM (of 228 KB, 1 KB of it the system's per CTA)
     static_assert(Sh::OCC * (Sh::SMEM + (int)sizeof(Tail) + 1024) <= 228 * 1024, "resident CTAs");
-    attend_split_kernel<BITS, F32, DP, NT>
+    attend_split_kernel<BITS, F32, DP, NT, FULL>
         <<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters, ws.zeros);
     return cudaGetLastError();
 }
 
 template <int BITS, bool F32, int DP, int NT>
 cudaError_t init() {
-    return cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Shape<BITS, F32, DP, NT>::SMEM);
+    constexpr int bytes = Shape<BITS, F32, DP, NT>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (BITS == 4 && e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT, BITS == 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e;
 }
 template <int BITS, bool F32>
 cudaError_t init_shapes() {
@@ -856,7 +971,9 @@ cudaError_t attend_split_init(int bits) {
 template <int BITS, bool F32, int DP>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    return rows <= 8 ? launch<BITS, F32, DP, 1>(a, ws, st) : launch<BITS, F32, DP, 2>(a, ws, st);
+    if (BITS == 4 && a.pages.dim == DP)
+        return rows <= 8 ? launch<BITS, F32, DP, 1, BITS == 4>(a, ws, st) : launch<BITS, F32, DP, 2, BITS == 4>(a, ws, st);
+    return rows <= 8 ? launch<BITS, F32, DP, 1, false>(a, ws, st) : launch<BITS, F32, DP, 2, false>(a, ws, st);
 }
 
 template <int BITS, bool F32>
