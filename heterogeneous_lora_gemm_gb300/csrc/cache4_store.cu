@@ -28,6 +28,10 @@ struct Row16 {
             w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         }
     }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
     __device__ __forceinline__ float at(int e) const {
         if (sizeof(T) == 4) return __uint_as_float(w[e]);
         return __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
@@ -39,26 +43,40 @@ struct Atom {
     uint32_t scale;   // e4m3
 };
 
-// rint(x * inv) + 8 in the low byte: adding 1.5 * 2^23 + 8 leaves the integer (ties to even) in the
-// sum's low mantissa bits.
-template <bool CLAMP>
-__device__ __forceinline__ uint32_t code_of(float x, float inv) {
-    float t = __fmul_rn(x, inv);
-    if (CLAMP) t = t != t ? 0.f : fminf(fmaxf(t, -7.f), 7.f);
-    return __float_as_uint(__fadd_rn(t, 12582920.f));
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
+// The largest |x|; NaN if one is NaN.
+__device__ __forceinline__ float largest(const Row16<float>& x) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max_nan(m, fabsf(x.at(e)));
+    return m;
+}
+__device__ __forceinline__ float largest(const Row16<__nv_bfloat16>& x) {
+    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x.w[i])));
+    return max_nan(__low2float(m), __high2float(m));
+}
+
+// rint(x * inv) + 8 for 16 x, a nibble each.  Adding 1.5 * 2^23 + 8 leaves the integer (ties to even) in
+// the sum's low mantissa bits; the sums' bits in a number to the base 16 are the nibbles once the
+// constant is taken off.
 template <bool CLAMP, typename T>
 __device__ __forceinline__ uint2 codes16(const Row16<T>& x, float inv) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint32_t c[8];
+        w[i] = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = code_of<CLAMP>(x.at(8 * i + e), inv);
-        auto bytes = [&](int e) {   // codes e, e + 2, e + 4, e + 6
-            return __byte_perm(__byte_perm(c[e], c[e + 2], 0x0040), __byte_perm(c[e + 4], c[e + 6], 0x0040), 0x5410);
-        };
-        w[i] = bytes(0) | bytes(1) << 4;
+        for (int e = 0; e < 8; ++e) {
+            float t = __fmul_rn(x.at(8 * i + e), inv);
+            if (CLAMP) t = t != t ? 0.f : fminf(fmaxf(t, -7.f), 7.f);
+            w[i] += __float_as_uint(__fadd_rn(t, 12582920.f)) * (1u << (4 * e));
+        }
     }
     return make_uint2(w[0], w[1]);
 }
@@ -66,14 +84,15 @@ __device__ __forceinline__ uint2 codes16(const Row16<T>& x, float inv) {
 // `grow` is 1 / (7 unit).
 template <typename T>
 __device__ __forceinline__ Atom quantise(const Row16<T>& x, float unit, float grow) {
-    float top = 0.f;
-    bool finite = true;
+    float top = largest(x);
+    const bool finite = top <= 3.402823466e38f;
+    if (!finite) {   // infinities and NaN do not enter the maximum
+        top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {   // infinities and NaN do not enter the maximum
-        const float a = fabsf(x.at(e));
-        const bool ok = a <= 3.402823466e38f;
-        finite &= ok;
-        top = fmaxf(top, ok ? a : 0.f);
+        for (int e = 0; e < 16; ++e) {
+            const float a = fabsf(x.at(e));
+            top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);
+        }
     }
     uint16_t s;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(__fmul_rn(top, grow)));
@@ -106,11 +125,10 @@ __device__ __forceinline__ PairOf pair_of(bool is_v, int it, int lane, int group
 }
 __device__ __forceinline__ int pairs_of(bool is_v, int groups) { return is_v ? (groups + 7) / 8 * 2 : (groups + 3) / 4; }
 
+// A warp per block and head; a lane's rows do not wait for the page that they go to.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) append_blocks_kernel(CachePages c, CacheStep s, RowsIn K, RowsIn V, uint32_t* status) {
-    const int part = blockIdx.y * (THREADS / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, h = part >> 1;
-    const bool is_v = part & 1;
+    const int h = blockIdx.y * (THREADS / 32) + threadIdx.x / 32, lane = threadIdx.x & 31, b = blockIdx.z;
     if (h >= c.heads) return;
     const SeqRec q = load_seq(s, c.page, b, status);
     const int start = max(q.start, 0), end = q.start + q.rows;
@@ -120,31 +138,29 @@ __global__ void __launch_bounds__(THREADS) append_blocks_kernel(CachePages c, Ca
     if (hi <= lo) return;
     const int page = j * 16 / c.page;
     const int id = load_page(s, c, b, page, status);
-    if (id < 0) return;
-    const RowsIn& R = is_v ? V : K;
-    const T* src = (const T*)R.ptr + (q.row0 + (int64_t)j * 16 - q.start) * R.row + h * R.head;
-    uint8_t* block = block_of(c, id, h, j - page * (c.page >> 4));
-    const int groups = c.dim >> 4;
-    uint8_t* codes = block + (is_v ? 8 * c.dim : 0);
-    uint8_t* scales = block + (is_v ? 17 * c.dim : 16 * c.dim);
-    const float unit = is_v ? c.v_unit : c.k_unit, grow = __fdiv_rn(1.f, __fmul_rn(7.f, unit));
-    const int n = pairs_of(is_v, groups);
-#pragma unroll 2
-    for (int it = 0; it < n; ++it) {
-        const PairOf p = pair_of(is_v, it, lane, groups);
+    const int64_t row = q.row0 + (int64_t)j * 16 - q.start;   // of the block's first token
+    const T* k_src = (const T*)K.ptr + row * K.row + h * K.head;
+    const T* v_src = (const T*)V.ptr + row * V.row + h * V.head;
+    const int groups = c.dim >> 4, keys = pairs_of(false, groups), n = keys + pairs_of(true, groups);
+    const float k_grow = __fdiv_rn(1.f, __fmul_rn(7.f, c.k_unit)), v_grow = __fdiv_rn(1.f, __fmul_rn(7.f, c.v_unit));
+    for (int i = 0; i < n; ++i) {
+        const bool is_v = i >= keys;
+        const PairOf p = pair_of(is_v, is_v ? i - keys : i, lane, groups);
         if (p.group >= groups) continue;
-        const int t1 = p.t + p.next;
-        const bool in0 = p.t >= lo && p.t < hi, in1 = t1 >= lo && t1 < hi;
+        const T* src = (is_v ? v_src : k_src) + p.group * 16;
+        const int64_t stride = is_v ? V.row : K.row;
+        const bool in0 = p.t >= lo && p.t < hi, in1 = p.t + p.next >= lo && p.t + p.next < hi;
+        Row16<T> x0, x1;
+        if (in0) x0.load(src + p.t * stride);
+        if (in1) x1.load(src + (p.t + p.next) * stride);
+        if (id < 0) return;
+        const float unit = is_v ? c.v_unit : c.k_unit, grow = is_v ? v_grow : k_grow;
+        uint8_t* block = block_of(c, id, h, j - page * (c.page >> 4));
+        uint8_t* codes = block + (is_v ? 8 * c.dim : 0);
+        uint8_t* scales = block + (is_v ? 17 * c.dim : 16 * c.dim);
         Atom a0, a1;
-        Row16<T> x;
-        if (in0) {
-            x.load(src + p.t * R.row + p.group * 16);
-            a0 = quantise(x, unit, grow);
-        }
-        if (in1) {
-            x.load(src + t1 * R.row + p.group * 16);
-            a1 = quantise(x, unit, grow);
-        }
+        if (in0) a0 = quantise(x0, unit, grow);
+        if (in1) a1 = quantise(x1, unit, grow);
         if (in0 && in1) {
             *reinterpret_cast<uint4*>(codes + p.atom * 8) = make_uint4(a0.codes.x, a0.codes.y, a1.codes.x, a1.codes.y);
             *reinterpret_cast<uint16_t*>(scales + p.atom) = (uint16_t)(a0.scale | a1.scale << 8);
@@ -180,41 +196,40 @@ __global__ void __launch_bounds__(THREADS) append_rows_kernel(CachePages c, Cach
     block[(is_v ? 17 * c.dim : 16 * c.dim) + at] = (uint8_t)a.scale;
 }
 
-// (code * scale) * unit, the first product exact
+// (code * scale) * unit, the first product exact: 16 elements as they lie in memory
 template <typename T>
-__device__ __forceinline__ void restore(T* p, uint2 codes, uint32_t scale, float unit) {
+__device__ __forceinline__ Row16<T> restored(uint2 codes, uint32_t scale, float unit) {
     const Scale2 s = scale_bf16(scale * 0x00010001u);
-    float v[16];
+    Row16<T> r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t w = i ? codes.y : codes.x;
         const uint32_t y[4] = {codes_bf16<0>(w, s), codes_bf16<1>(w, s), codes_bf16<2>(w, s), codes_bf16<3>(w, s)};
+        float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            v[8 * i + e] = __fmul_rn(__uint_as_float(y[e] << 16), unit);
-            v[8 * i + 4 + e] = __fmul_rn(__uint_as_float(y[e] & 0xFFFF0000u), unit);
+            v[e] = __fmul_rn(__uint_as_float(y[e] << 16), unit);
+            v[4 + e] = __fmul_rn(__uint_as_float(y[e] & 0xFFFF0000u), unit);
+        }
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.w[8 * i + e] = __float_as_uint(v[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                r.w[4 * i + e] = *reinterpret_cast<const uint32_t*>(&z);
+            }
         }
     }
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-        uint32_t y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            y[i] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-    }
+    return r;
 }
 
+// A warp per block and head.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) read_blocks_kernel(CachePages c, CacheStep s, RowsOut K, RowsOut V, uint32_t* status) {
-    const int part = blockIdx.y * (THREADS / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, h = part >> 1;
-    const bool is_v = part & 1;
+    constexpr int AHEAD = 2;   // pairs that are loaded together
+    const int h = blockIdx.y * (THREADS / 32) + threadIdx.x / 32, lane = threadIdx.x & 31, b = blockIdx.z;
     if (h >= c.heads) return;
     const SeqRec q = load_seq(s, c.page, b, status);
     const int j = (q.start >> 4) + (int)blockIdx.x;   // (rounded down) negative: rows that name no token
@@ -222,27 +237,37 @@ __global__ void __launch_bounds__(THREADS) read_blocks_kernel(CachePages c, Cach
     const int lo = (int)max(q.start - first, 0ll), hi = (int)min(q.start + q.rows - first, 16ll);
     if (hi <= lo) return;
     const int page = j >= 0 ? j * 16 / c.page : 0, id = j >= 0 ? load_page(s, c, b, page, status) : -1;
-    const RowsOut& R = is_v ? V : K;
-    T* dst = (T*)R.ptr + (q.row0 + first - q.start) * R.row + h * R.head;
+    const int64_t row = q.row0 + first - q.start;   // of the block's first token
+    T* k_dst = (T*)K.ptr + row * K.row + h * K.head;
+    T* v_dst = (T*)V.ptr + row * V.row + h * V.head;
     const uint8_t* block = block_of(c, max(id, 0), h, id < 0 ? 0 : j - page * (c.page >> 4));
-    const int groups = c.dim >> 4;
-    const uint8_t* codes = block + (is_v ? 8 * c.dim : 0);
-    const uint8_t* scales = block + (is_v ? 17 * c.dim : 16 * c.dim);
-    const float unit = is_v ? c.v_unit : c.k_unit;
-    const int n = pairs_of(is_v, groups);
-#pragma unroll 2
-    for (int it = 0; it < n; ++it) {
-        const PairOf p = pair_of(is_v, it, lane, groups);
-        if (p.group >= groups) continue;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t sc = 0u;
-        if (id >= 0) {
-            w = __ldcs(reinterpret_cast<const uint4*>(codes + p.atom * 8));
-            sc = *reinterpret_cast<const uint16_t*>(scales + p.atom);
+    const int groups = c.dim >> 4, keys = pairs_of(false, groups), n = keys + pairs_of(true, groups);
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+        uint4 w[AHEAD];
+        uint32_t sc[AHEAD];
+#pragma unroll
+        for (int z = 0; z < AHEAD; ++z) {
+            const bool is_v = i0 + z >= keys;
+            const PairOf p = pair_of(is_v, is_v ? i0 + z - keys : i0 + z, lane, groups);
+            w[z] = make_uint4(0u, 0u, 0u, 0u);
+            sc[z] = 0u;
+            if (id >= 0 && i0 + z < n && p.group < groups) {
+                w[z] = __ldcs(reinterpret_cast<const uint4*>(block + (is_v ? 8 * c.dim : 0) + p.atom * 8));
+                sc[z] = *reinterpret_cast<const uint16_t*>(block + (is_v ? 17 * c.dim : 16 * c.dim) + p.atom);
+            }
         }
-        const int t1 = p.t + p.next;
-        if (p.t >= lo && p.t < hi) restore(dst + p.t * R.row + p.group * 16, make_uint2(w.x, w.y), sc & 0xFFu, unit);
-        if (t1 >= lo && t1 < hi) restore(dst + t1 * R.row + p.group * 16, make_uint2(w.z, w.w), sc >> 8, unit);
+#pragma unroll
+        for (int z = 0; z < AHEAD; ++z) {
+            const bool is_v = i0 + z >= keys;
+            const PairOf p = pair_of(is_v, is_v ? i0 + z - keys : i0 + z, lane, groups);
+            if (i0 + z >= n || p.group >= groups) continue;
+            T* dst = (is_v ? v_dst : k_dst) + p.group * 16;
+            const int64_t stride = is_v ? V.row : K.row;
+            const float unit = is_v ? c.v_unit : c.k_unit;
+            const int t1 = p.t + p.next;
+            if (p.t >= lo && p.t < hi) restored<T>(make_uint2(w[z].x, w[z].y), sc[z] & 0xFFu, unit).store(dst + p.t * stride);
+            if (t1 >= lo && t1 < hi) restored<T>(make_uint2(w[z].z, w[z].w), sc[z] >> 8, unit).store(dst + t1 * stride);
+        }
     }
 }
 
@@ -266,23 +291,36 @@ __global__ void __launch_bounds__(THREADS) read_rows_kernel(CachePages c, CacheS
         sc = block[(is_v ? 17 * c.dim : 16 * c.dim) + at];
     }
     const RowsOut& R = is_v ? V : K;
-    restore((T*)R.ptr + (int64_t)(q.row0 + row) * R.row + h * R.head + group * 16, w, sc, is_v ? c.v_unit : c.k_unit);
+    restored<T>(w, sc, is_v ? c.v_unit : c.k_unit).store((T*)R.ptr + (int64_t)(q.row0 + row) * R.row + h * R.head + group * 16);
 }
 
 // 16-token blocks that max_new consecutive positions can touch.
 int most_blocks(int max_new) { return (int)(((long long)max_new + 14) / 16) + 1; }
 
-template <typename Rows, typename Blocks, typename Single>
-cudaError_t launch(Blocks blocks, Single single, const CachePages& c, const CacheStep& s, const Rows& k, const Rows& v,
-                   uint32_t* status, cudaStream_t st) {
-    if (s.max_new <= FEW) {
-        const int groups = c.dim / 16;
-        const dim3 grid((2 * c.heads * groups + THREADS - 1) / THREADS, s.max_new, s.n_seqs);
-        single<<<grid, THREADS, 0, st>>>(c, s, k, v, divide_by(groups), status);
-    } else {
-        const dim3 grid(most_blocks(s.max_new), (2 * c.heads + THREADS / 32 - 1) / (THREADS / 32), s.n_seqs);
-        blocks<<<grid, THREADS, 0, st>>>(c, s, k, v, status);
-    }
+// Steps of few rows: a thread per atom, [heads, keys or values, groups] x rows x sequences.
+template <typename Rows, typename Kernel>
+cudaError_t launch_rows(Kernel kernel, const CachePages& c, const CacheStep& s, const Rows& k, const Rows& v, uint32_t* status,
+                        cudaStream_t st) {
+    const int groups = c.dim / 16;
+    const dim3 grid((2 * c.heads * groups + THREADS - 1) / THREADS, s.max_new, s.n_seqs);
+    kernel<<<grid, THREADS, 0, st>>>(c, s, k, v, divide_by(groups), status);
+    return cudaGetLastError();
+}
+constexpr int WARPS = THREADS / 32;
+
+template <typename T>
+cudaError_t append(const CachePages& c, const CacheStep& s, const RowsIn& k, const RowsIn& v, uint32_t* status, cudaStream_t st) {
+    if (s.max_new <= FEW) return launch_rows(append_rows_kernel<T>, c, s, k, v, status, st);
+    const dim3 grid(most_blocks(s.max_new), (c.heads + WARPS - 1) / WARPS, s.n_seqs);
+    append_blocks_kernel<T><<<grid, THREADS, 0, st>>>(c, s, k, v, status);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t read(const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v, uint32_t* status, cudaStream_t st) {
+    if (s.max_new <= FEW) return launch_rows(read_rows_kernel<T>, c, s, k, v, status, st);
+    const dim3 grid(most_blocks(s.max_new), (c.heads + WARPS - 1) / WARPS, s.n_seqs);
+    read_blocks_kernel<T><<<grid, THREADS, 0, st>>>(c, s, k, v, status);
     return cudaGetLastError();
 }
 
@@ -290,14 +328,12 @@ cudaError_t launch(Blocks blocks, Single single, const CachePages& c, const Cach
 
 cudaError_t launch_append4(bool bf16, const CachePages& c, const CacheStep& s, const RowsIn& k, const RowsIn& v,
                            uint32_t* status, cudaStream_t st) {
-    return bf16 ? launch(append_blocks_kernel<__nv_bfloat16>, append_rows_kernel<__nv_bfloat16>, c, s, k, v, status, st)
-                : launch(append_blocks_kernel<float>, append_rows_kernel<float>, c, s, k, v, status, st);
+    return bf16 ? append<__nv_bfloat16>(c, s, k, v, status, st) : append<float>(c, s, k, v, status, st);
 }
 
 cudaError_t launch_read4(bool bf16, const CachePages& c, const CacheStep& s, const RowsOut& k, const RowsOut& v,
                          uint32_t* status, cudaStream_t st) {
-    return bf16 ? launch(read_blocks_kernel<__nv_bfloat16>, read_rows_kernel<__nv_bfloat16>, c, s, k, v, status, st)
-                : launch(read_blocks_kernel<float>, read_rows_kernel<float>, c, s, k, v, status, st);
+    return bf16 ? read<__nv_bfloat16>(c, s, k, v, status, st) : read<float>(c, s, k, v, status, st);
 }
 
 }  // namespace mlora

@@ -35,6 +35,11 @@ struct mlora_rotary {
 namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
+constexpr int MOST = 16;   // groups of heads that a warp takes at most
+// CTAs per SM (register limits): bf16 rows spill 5 words at 6 and are faster all the same (30k rows of 32/8
+// heads 109 us, 113 us at 5), fp32 rows would spill 20
+template <typename T>
+constexpr int CTAS = sizeof(T) == 2 ? 6 : 5;
 
 struct RotaryArgs {
     RowsIn q, k;
@@ -45,44 +50,80 @@ struct RotaryArgs {
     const float* k_weight;
     float eps;
     CacheStep step;
-    int q_chunks, per;   // chunks of the queries' heads (the keys' follow), groups of heads in a chunk
+    int q_groups, k_groups, per;   // groups of heads that a warp takes at a time, and how many of them a warp takes
     uint32_t* status;
 };
 
-// 8 adjacent elements
-__device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// pairs of fp32
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+__device__ __forceinline__ float2 unpair(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t a) {
+    const float2 v = unpair(a);
+    return pair(v.y, v.x);
 }
 
+// 16 elements as they lie in memory, 16 bytes at each of the places `at`; eight pairs of adjacent ones.
+template <typename T>
+struct Raw {
+    static constexpr int VEC = 16 / sizeof(T), N = 16 / VEC, W = 4 * N;   // elements in 16 bytes, such runs, words
+    uint32_t w[W];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const T* p, const int (&at)[N]) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + at[k]);
+            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void store(T* p, const int (&at)[N]) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            *reinterpret_cast<uint4*>(p + at[k]) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    __device__ __forceinline__ void get(uint64_t (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = sizeof(T) == 4 ? pair(__uint_as_float(w[2 * i % W]), __uint_as_float(w[(2 * i + 1) % W]))
+                                  : pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ void put(int i, uint64_t x) {
+        const float2 v = unpair(x);
+        if (sizeof(T) == 4) {
+            w[2 * i % W] = __float_as_uint(v.x);
+            w[(2 * i + 1) % W] = __float_as_uint(v.y);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+};
 // Sine and cosine of an angle in turns, 2^-64 each.
 __device__ __forceinline__ float2 cos_sin(uint64_t turns) {
     const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);
-    const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));   // within an eighth of a turn
+    const int rest = (int)((int64_t)(turns - ((uint64_t)quarter << 62)) >> 30);   // within an eighth of a turn, 2^-34 each
     float s, c;
-    sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
+    sincospif(__int2float_rn(rest) * 0x1p-33f, &s, &c);
     if (quarter & 1) {
         const float t = c;
         c = -s;
@@ -105,7 +146,7 @@ __device__ __forceinline__ int sequence_of(const CacheStep& s, int row, int lane
 
 // LANES: of a head (its 16-element slots, rounded up to a power of two)
 template <typename T, int LANES, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(THREADS, CTAS<T>) rotary_kernel(const RotaryArgs a) {
     constexpr int HEADS = 32 / LANES;   // at a time
     __shared__ float2 turn[WARPS][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,86 +156,123 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const RotaryArgs a) {
         for (int b = threadIdx.x; b < a.step.n_seqs; b += THREADS) load_seq(a.step, PAGE, b, a.status);
     const int row = blockIdx.x * WARPS + warp;
     if (row >= a.step.T) return;
+    const int sub = lane / LANES, slot = lane % LANES;
+    const bool mine = slot * 16 < a.dim, turns = slot * 16 < a.turned;
+    // the slot's runs of 16 bytes, such that those of a head's slots lie side by side: of the elements that
+    // turn, or of the others; the second half of the runs are the first half's partners
+    using Row = Raw<T>;
+    const int base = turns ? 0 : a.turned, length = turns ? a.turned : a.dim - a.turned;
+    int at[Row::N];
+#pragma unroll
+    for (int k = 0; k < Row::N; ++k) at[k] = base + (slot - base / 16) * Row::VEC + k * (length / Row::N);
+
+    // groups of heads [g0, g1): the queries' first, then the keys'.  The next group's elements are on
+    // their way while one is turned.
+    const int g0 = blockIdx.y * a.per, g1 = min(g0 + a.per, a.q_groups + a.k_groups);
+    Row next;
+    const T* src = nullptr;   // the lane's head of the group that is fetched next
+    int64_t src_step = 0;
+    auto seek = [&](int g) {
+        const bool is_k = g >= a.q_groups;
+        const int64_t head = is_k ? a.k.head : a.q.head;
+        src = (const T*)(is_k ? a.k.ptr : a.q.ptr) + row * (is_k ? a.k.row : a.q.row) + ((is_k ? g - a.q_groups : g) * HEADS + sub) * head;
+        src_step = HEADS * head;
+    };
+    auto there = [&](int g) { return mine && (g < a.q_groups ? g * HEADS + sub < a.q_heads : (g - a.q_groups) * HEADS + sub < a.kv_heads); };
+    auto fetch = [&](int g) {
+        if (g == a.q_groups) seek(g);
+        if (g < g1 && there(g)) next.load(src, at);
+        else next.clear();
+        src += src_step;
+    };
+    seek(g0);
+    fetch(g0);   // (before the row's position is known: that is a chain of loads)
+
     const int b = a.step.offsets ? sequence_of(a.step, row, lane) : row;
     const SeqRec s = load_seq(a.step, PAGE, b, a.status);
     const int i = row - s.row0;
     if (i < 0 || i >= s.rows) return;   // of no sequence
     const int pos = s.start + i;
-    const bool is_k = (int)blockIdx.y >= a.q_chunks;
-    const RowsIn& from = is_k ? a.k : a.q;
-    const RowsOut& to = is_k ? a.ko : a.qo;
-    const float* weight = is_k ? a.k_weight : a.q_weight;
-    const int heads = is_k ? a.kv_heads : a.q_heads;
-    const int head0 = (blockIdx.y - (is_k ? a.q_chunks : 0)) * a.per * HEADS + lane / LANES;
-    const int slot = lane % LANES;
-    const bool mine = slot * 16 < a.dim, turns = slot * 16 < a.turned;
-    // the slot's two runs of 8 elements: halves of eight pairs, or eight pairs side by side
-    const int at0 = turns && !INTERLEAVED ? slot * 8 : slot * 16;
-    const int at1 = turns && !INTERLEAVED ? a.turned / 2 + slot * 8 : slot * 16 + 8;
-
-    float c[8], sn[8];
     for (int p = lane; p < a.turned / 2; p += 32) turn[warp][p] = cos_sin((uint64_t)(int64_t)pos * a.turns[p]);
     __syncwarp();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float2 v = turns ? turn[warp][slot * 8 + e] : make_float2(1.f, 0.f);
-        c[e] = v.x;
-        sn[e] = v.y;
-    }
-    float w[16];
-    if (weight) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[e] = mine ? weight[at0 + e] : 0.f;
-            w[8 + e] = mine ? weight[at1 + e] : 0.f;
-        }
-    }
     const float inv_dim = 1.f / (float)a.dim;
-    for (int g = 0; g < a.per; ++g) {
-        const int h = head0 + g * HEADS;
-        if (h - lane / LANES >= heads) break;   // (the whole warp)
-        const bool in = mine && h < heads;
-        const T* src = (const T*)from.ptr + row * from.row + h * from.head;
-        T* dst = (T*)to.ptr + row * to.row + h * to.head;
-        float x[16];
+    for (int g = g0; g < g1;) {
+        // the queries' groups, or the keys'
+        const bool is_k = g >= a.q_groups;
+        const int last = is_k ? g1 : min(g1, a.q_groups);
+        const float* weight = is_k ? a.k_weight : a.q_weight;
+        const int64_t dst_head = is_k ? a.ko.head : a.qo.head;
+        T* dst = (T*)(is_k ? a.ko.ptr : a.qo.ptr) + row * (is_k ? a.ko.row : a.qo.row) + ((is_k ? g - a.q_groups : g) * HEADS + sub) * dst_head;
+        // A pair x of adjacent elements, and its partner o (the other half's pair, or x itself swapped):
+        // x' = x k0 + o k1 holds the weights and the turn (x' = x k0 for elements that do not turn)
+        uint64_t k0[8], k1[8];
+        {
+            float w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
-        if (in && pos >= 0) {
-            load8(src + at0, x);
-            load8(src + at1, x + 8);
-        }
-        if (weight && pos >= 0) {
-            auto squares = [&](float f) {
-                float t = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) t = fmaf(x[e] * f, x[e] * f, t);
-#pragma unroll
-                for (int d = 1; d < LANES; d <<= 1) t += __shfl_xor_sync(~0u, t, d);
-                return t;
-            };
-            float sum = squares(1.f), f = 1.f;
-            // squares that leave fp32, or are lost beside no eps: the head by a power of two
-            const bool far = !(sum <= 0x1p120f) || (sum < 0x1p-90f && a.eps < 0x1p-70f);
-            if (__any_sync(~0u, far)) {
-                const float up = !(sum <= 0x1p120f) ? 0x1p-70f : 0x1p60f;
-                const float again = squares(far ? up : 1.f);
-                if (far) sum = again, f = up;
+            for (int e = 0; e < 16; e += 4) {
+                const float4 v = weight && mine ? *reinterpret_cast<const float4*>(weight + at[e / Row::VEC] + e % Row::VEC)
+                                                : make_float4(1.f, 1.f, 1.f, 1.f);
+                w[e] = v.x, w[e + 1] = v.y, w[e + 2] = v.z, w[e + 3] = v.w;
             }
-            const float mean = sum * inv_dim + a.eps * f * f;
-            const float inv = mean == 0.f ? 0.f : __frcp_rn(__fsqrt_rn(mean)) * f;
+            float2 v[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * w[e];
-        }
-        float y[16];
+            for (int e = 0; e < 8; ++e) {   // of the lane's pairs
+                const int i = INTERLEAVED ? 2 * e : e, p = at[i / Row::VEC] + i % Row::VEC;
+                v[e] = turns ? turn[warp][INTERLEAVED ? p / 2 : p] : make_float2(1.f, 0.f);
+            }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int p = INTERLEAVED ? 2 * e : e, q = INTERLEAVED ? 2 * e + 1 : e + 8;
-            y[p] = x[p] * c[e] - x[q] * sn[e];
-            y[q] = x[p] * sn[e] + x[q] * c[e];
+            for (int i = 0; i < 8; ++i) {
+                if (INTERLEAVED) {
+                    k0[i] = pair(v[i].x * w[2 * i], v[i].x * w[2 * i + 1]);
+                    k1[i] = pair(-v[i].y * w[2 * i + 1], v[i].y * w[2 * i]);
+                } else {
+                    const int c = i % 4 * 2, o = (2 * i) ^ 8;   // (the partner's first element)
+                    const float sign = i < 4 ? -1.f : 1.f;
+                    k0[i] = pair(v[c].x * w[2 * i], v[c + 1].x * w[2 * i + 1]);
+                    k1[i] = pair(sign * v[c].y * w[o], sign * v[c + 1].y * w[o + 1]);
+                }
+            }
         }
-        if (in) {
-            store8(dst + at0, turns ? y : x);
-            store8(dst + at1, turns ? y + 8 : x + 8);
+#pragma unroll 1
+        for (; g < last; ++g) {
+            uint64_t x[8];
+            if (pos < 0) next.clear();
+            next.get(x);
+            fetch(g + 1);
+            float inv = 1.f;
+            if (weight && pos >= 0) {
+                auto squares = [&]() {
+                    uint64_t t = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) t = fma2(x[i], x[i], t);
+                    const float2 v = unpair(t);
+                    float r = v.x + v.y;
+#pragma unroll
+                    for (int d = 1; d < LANES; d <<= 1) r += __shfl_xor_sync(~0u, r, d);
+                    return r;
+                };
+                float sum = squares(), eps = a.eps;
+                // squares that leave fp32, or are lost beside no eps: the head by a power of two
+                const bool far = !(sum <= 0x1p120f) || (sum < 0x1p-90f && eps < 0x1p-70f);
+                if (__any_sync(~0u, far)) {
+                    const float f = !far ? 1.f : !(sum <= 0x1p120f) ? 0x1p-70f : 0x1p60f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], pair(f, f));
+                    sum = squares();
+                    eps = eps * f * f;
+                }
+                const float mean = fmaf(sum, inv_dim, eps), r = rsqrtf(mean);
+                inv = mean == 0.f || mean > 3.4e38f ? 0.f : fmaf(r * 0.5f, fmaf(-mean * r, r, 1.f), r);   // (a Newton step)
+            }
+            Row out;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint64_t y = mul2(x[i], k0[i]);
+                if (turns) y = fma2(INTERLEAVED ? swapped(x[i]) : x[i ^ 4], k1[i], y);
+                out.put(i, weight ? mul2(y, pair(inv, inv)) : y);
+            }
+            if (there(g)) out.store(dst, at);
+            dst += HEADS * dst_head;
         }
     }
 }
@@ -202,12 +280,14 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const RotaryArgs a) {
 template <typename T, int LANES>
 cudaError_t launch(RotaryArgs a, bool interleaved, int sms, cudaStream_t st) {
     constexpr int HEADS = 32 / LANES;
-    const int q_groups = (a.q_heads + HEADS - 1) / HEADS, k_groups = (a.kv_heads + HEADS - 1) / HEADS;
-    // groups of heads per warp: as many as leave some 32 warps to an SM, 8 at most
-    const long long groups = (long long)a.step.T * (q_groups + k_groups) / (32ll * sms);
-    a.per = groups < 1 ? 1 : groups > 8 ? 8 : (int)groups;
-    a.q_chunks = (q_groups + a.per - 1) / a.per;
-    const dim3 grid((unsigned)(((long long)a.step.T + WARPS - 1) / WARPS), a.q_chunks + (k_groups + a.per - 1) / a.per);
+    a.q_groups = (a.q_heads + HEADS - 1) / HEADS;
+    a.k_groups = (a.kv_heads + HEADS - 1) / HEADS;
+    // groups of heads per warp: as many as leave some 32 warps to an SM, MOST at most
+    const int all = a.q_groups + a.k_groups;
+    const long long groups = (long long)a.step.T * all / (32ll * sms);
+    a.per = groups < 1 ? 1 : groups > MOST ? MOST : (int)groups;
+    a.per = (all + (all + a.per - 1) / a.per - 1) / ((all + a.per - 1) / a.per);   // (as equal as they can be)
+    const dim3 grid((unsigned)(((long long)a.step.T + WARPS - 1) / WARPS), (all + a.per - 1) / a.per);
     if (interleaved) rotary_kernel<T, LANES, true><<<grid, THREADS, 0, st>>>(a);
     else rotary_kernel<T, LANES, false><<<grid, THREADS, 0, st>>>(a);
     return cudaGetLastError();
@@ -343,8 +423,8 @@ mlora_status mlora_rotary_apply(mlora_rotary_t r, const void* Q, int64_t q_row, 
     if (q_heads < 1 || q_heads > 32767 || kv_heads < 1 || kv_heads > 32767)
         return fail(MLORA_ERR_INVALID_ARG, "q_heads %d and kv_heads %d must lie in [1, 32767]", q_heads, kv_heads);
     if (!(eps >= 0.f && eps < 3.0e38f)) return fail(MLORA_ERR_INVALID_ARG, "eps %g", eps);
-    if (((uintptr_t)q_weight | (uintptr_t)k_weight) & 3u)
-        return fail(MLORA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+    if (((uintptr_t)q_weight | (uintptr_t)k_weight) & 15u)
+        return fail(MLORA_ERR_INVALID_ARG, "weights must be 16-byte aligned");
     if (!(T > 0 && n_seqs > 0 && max_new > 0)) return MLORA_OK;
     if (!lengths) return fail(MLORA_ERR_INVALID_ARG, "lengths is NULL");
     mlora_status st = check_rows("Q", Q, q_row, q_head, dtype);
@@ -357,7 +437,7 @@ mlora_status mlora_rotary_apply(mlora_rotary_t r, const void* Q, int64_t q_row, 
     const CacheStep step{offsets, lengths, nullptr, n_seqs, 1 << 15, T, max_new < T ? max_new : T};
     const RotaryArgs a{RowsIn{Q, q_row, q_head}, RowsIn{K, k_row, k_head}, RowsOut{Qo, qo_row, qo_head},
                        RowsOut{Ko, ko_row, ko_head}, q_heads, kv_heads, r->dim, r->turned, r->turns, q_weight, k_weight,
-                       eps, step, 0, 0, r->ws};
+                       eps, step, 0, 0, 0, r->ws};
     const cudaError_t e = dtype == MLORA_BF16
                               ? launch_by_dim<__nv_bfloat16>(a, r->interleaved, r->sms, (cudaStream_t)stream)
                               : launch_by_dim<float>(a, r->interleaved, r->sms, (cudaStream_t)stream);

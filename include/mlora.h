@@ -583,7 +583,7 @@ mlora_status mlora_rotary_destroy(mlora_rotary_t rotary);
  * calls: rows at negative positions name no token and come out as zeros, rows outside every
  * range are left alone, lengths are clamped to 0 .. 2^30; what is out of range sets the status bit that
  * mlora_rotary_status reports.
- *   q_weight, k_weight  device fp32 [head_dim], or NULL: no norm
+ *   q_weight, k_weight  device fp32 [head_dim], 16-byte aligned, or NULL: no norm
  *   eps                 >= 0 (not read without weights)
  * Allocates nothing.  Calls on one handle may overlap, on any streams.
  * Errors: INVALID_ARG, CUDA.

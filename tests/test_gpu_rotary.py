@@ -211,7 +211,7 @@ def test_refusals():
             bad()
     odd = torch.zeros((2, 130), device="cuda")
     for bad in (lambda: r.apply(x, x, i32([3])), lambda: r.apply(x, x, n, max_new=-1), lambda: r.apply(x, x, n, eps=-1.0),
-                lambda: r.apply(x, x, n, eps=float("nan")), lambda: r.apply(odd[:, 2:].unflatten(1, (2, 64)), x, n),
+                lambda: r.apply(x, x, n, eps=float("nan")), lambda: r.apply(x, x, n, q_weight=torch.ones(68, device="cuda")[1:65]), lambda: r.apply(odd[:, 2:].unflatten(1, (2, 64)), x, n),
                 lambda: Rotary(64, freq=[float("inf")] * 32)):
         with pytest.raises(mlora.MloraError) as e:
             bad()
