@@ -55,7 +55,7 @@ constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights sta
 constexpr float OFF16 = 12.f, SLACK16 = 3.f;
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
-template <int BITS, bool F32, int DP, int NT>
+template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query
     static constexpr bool P16 = BITS == 4 && !F32;     // weights and values in fp16
@@ -67,7 +67,10 @@ struct Shape {
     static constexpr int BOX = PIECE * ROWB;
     // a warp takes a chunk of two pieces at a time: waits, votes and issues are per chunk
     // (one where the accumulators leave no registers for two)
-    static constexpr int SUB = DP == 256 ? 1 : 2;
+    // (three in long ranges over 4 bits, whose chunks' own instructions count for more: 32 x 32k tokens 220 us,
+    // 230 us with two; one sequence of 777 tokens 9.6 and 8.7 us)
+    static constexpr int SUB = DP == 256 ? 1 : LONG ? 3 : 2;
+    static_assert(!LONG || (P16 && DP <= 128 && NT == 1), "long ranges");
     static constexpr int CHUNK_T = PIECE * SUB;
     static constexpr int PART = BITS == 4 ? 18 * DP : 2 * CB * BOX;   // keys and values of a piece
     static constexpr int STAGE = SUB * PART;
@@ -210,12 +213,12 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 }
 
 // `zeros`: a 4-bit block of zeros, in the place of one that cannot be read.  FULL: heads of DP elements,
-// so that a 4-bit block's offsets are constants.
-template <int BITS, bool F32, int DP, int NT, bool FULL>
-__global__ void __launch_bounds__(THREADS, (Shape<BITS, F32, DP, NT>::OCC))
+// so that a 4-bit block's offsets are constants.  LONG: chunks of three pieces.
+template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG>
+__global__ void __launch_bounds__(THREADS, (Shape<BITS, F32, DP, NT, FULL, LONG>::OCC))
 attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
                     float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
-    using Sh = Shape<BITS, F32, DP, NT>;
+    using Sh = Shape<BITS, F32, DP, NT, FULL, LONG>;
     using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int KS = Sh::KS, RT = Sh::RT, SUB = Sh::SUB, CHUNK_T = Sh::CHUNK_T, TERMS = Sh::TERMS, PTERMS = Sh::PTERMS, CB = Sh::CB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -929,24 +932,30 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
 }
 
-template <int BITS, bool F32, int DP, int NT, bool FULL>
+template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG = false>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    using Sh = Shape<BITS, F32, DP, NT>;
+    using Sh = Shape<BITS, F32, DP, NT, FULL, LONG>;
     static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace slots");
     // ranges are cut for OCC CTAs on each SM (of 228 KB, 1 KB of it the system's per CTA)
     static_assert(Sh::OCC * (Sh::SMEM + (int)sizeof(Tail) + 1024) <= 228 * 1024, "resident CTAs");
-    attend_split_kernel<BITS, F32, DP, NT, FULL>
+    attend_split_kernel<BITS, F32, DP, NT, FULL, LONG>
         <<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters, ws.zeros);
     return cudaGetLastError();
 }
 
+template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG = false>
+cudaError_t allow() {
+    return cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT, FULL, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Shape<BITS, F32, DP, NT, FULL, LONG>::SMEM);
+}
 template <int BITS, bool F32, int DP, int NT>
 cudaError_t init() {
-    constexpr int bytes = Shape<BITS, F32, DP, NT>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (BITS == 4 && e == cudaSuccess)
-        e = cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT, BITS == 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr bool LONG = BITS == 4 && !F32 && DP <= 128 && NT == 1;
+    cudaError_t e = allow<BITS, F32, DP, NT, false>();
+    if (BITS == 4 && e == cudaSuccess) e = allow<BITS, F32, DP, NT, BITS == 4>();
+    if (LONG && e == cudaSuccess) e = allow<BITS, F32, DP, NT, false, LONG>();
+    if (LONG && e == cudaSuccess) e = allow<BITS, F32, DP, NT, LONG, LONG>();
     return e;
 }
 template <int BITS, bool F32>
@@ -968,19 +977,28 @@ cudaError_t attend_split_init(int bits) {
 
 // Rows per tile: 8, or 16 where a sequence and head has more (past 16 only fp32 rows of more than
 // 128 elements come here, in tiles of 16; the rest are attend_prompt.cu's).
-template <int BITS, bool F32, int DP>
+template <int BITS, bool F32, int DP, bool FULL>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    if (BITS == 4 && a.pages.dim == DP)
-        return rows <= 8 ? launch<BITS, F32, DP, 1, BITS == 4>(a, ws, st) : launch<BITS, F32, DP, 2, BITS == 4>(a, ws, st);
-    return rows <= 8 ? launch<BITS, F32, DP, 1, false>(a, ws, st) : launch<BITS, F32, DP, 2, false>(a, ws, st);
+    if constexpr (BITS == 4 && !F32 && DP <= 128) {
+        // as many tokens as the page tables hold (lengths are not known here): from some 1000 for each CTA
+        // on, ranges are long
+        const long long most = (long long)a.step.n_seqs * a.step.width * a.pages.page * a.pages.heads;
+        if (rows <= 8 && most >= 1024ll * ws.sms * ATTEND_OCC) return launch<BITS, F32, DP, 1, FULL, true>(a, ws, st);
+    }
+    return rows <= 8 ? launch<BITS, F32, DP, 1, FULL>(a, ws, st) : launch<BITS, F32, DP, 2, FULL>(a, ws, st);
+}
+template <int BITS, bool F32, int DP>
+static cudaError_t by_width(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    if (BITS == 4 && a.pages.dim == DP) return by_rows<BITS, F32, DP, BITS == 4>(a, ws, st);
+    return by_rows<BITS, F32, DP, false>(a, ws, st);
 }
 
 template <int BITS, bool F32>
 static cudaError_t by_shape(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const int D = a.pages.dim;
-    return D <= 64 ? by_rows<BITS, F32, 64>(a, ws, st)
-                   : D <= 128 ? by_rows<BITS, F32, 128>(a, ws, st) : by_rows<BITS, F32, 256>(a, ws, st);
+    return D <= 64 ? by_width<BITS, F32, 64>(a, ws, st)
+                   : D <= 128 ? by_width<BITS, F32, 128>(a, ws, st) : by_width<BITS, F32, 256>(a, ws, st);
 }
 
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {

@@ -673,45 +673,53 @@ class Rotary:
         except Exception:
             pass
 
-    def _rows(self, x, out, code):
-        shape, strides, to = x.shape, x.stride(), out.stride()
-        if len(shape) != 3 or shape[2] != self.head_dim or out.shape != shape:
-            raise ValueError(f"rows are [T, heads, {self.head_dim}], got {tuple(shape)} into {tuple(out.shape)}")
-        if code is None or self._dtypes.get(x.dtype) != code or out.dtype != x.dtype:
-            raise ValueError("rows are bf16 or fp32, all operands alike")
-        if strides[2] != 1 or to[2] != 1:
-            raise ValueError("a head's elements must be adjacent")
-        if x.get_device() != self._index or out.get_device() != self._index:
-            raise ValueError(f"operands live on the rotary's device {self.device}")
-        return x.data_ptr(), strides[0], strides[1], out.data_ptr(), to[0], to[1], shape[1]
-
     def apply(self, Q, K, lengths, offsets=None, max_new: int = 1, q_weight=None, k_weight=None, eps: float = 1e-6,
               q_out=None, k_out=None, stream=None) -> None:
         """Norms (where there is a weight, fp32 [head_dim]) and turns the step's rows Q [T, q_heads, head_dim] and
         K [T, kv_heads, head_dim], in place or into q_out and k_out.  The step's arrays are the cache's."""
-        code, index = self._dtypes.get(Q.dtype), self._index
-        q = self._rows(Q, Q if q_out is None else q_out, code)
-        k = self._rows(K, K if k_out is None else k_out, code)
-        T, n_seqs = Q.shape[0], lengths.numel()
-        if K.shape[0] != T:
-            raise ValueError(f"Q has {T} rows, K {K.shape[0]}")
-        for t, n in ((lengths, n_seqs), (offsets, n_seqs + 1)):
-            if t is not None and (t.shape != (n,) or t.dtype != self._i32 or not t.is_contiguous() or
-                                  t.get_device() != index):
-                raise ValueError(f"lengths and offsets are contiguous int32 [n_seqs] and [n_seqs + 1] on {self.device}")
-        for t in (q_weight, k_weight):
-            if t is not None and (t.shape != (self.head_dim,) or t.dtype != self._f32 or not t.is_contiguous() or
-                                  t.get_device() != index):
-                raise ValueError(f"weights are contiguous fp32 [{self.head_dim}] on {self.device}")
+        q_out = Q if q_out is None else q_out
+        k_out = K if k_out is None else k_out
+        dtype, index, i32 = Q.dtype, self._index, self._i32
+        code, q, k = self._dtypes.get(dtype), Q.shape, K.shape
+        if code is None or K.dtype != dtype or q_out.dtype != dtype or k_out.dtype != dtype:
+            raise ValueError("rows are bf16 or fp32, all operands alike")
+        if (len(q) != 3 or len(k) != 3 or q[2] != self.head_dim or k[2] != self.head_dim or k[0] != q[0] or
+                q_out.shape != q or k_out.shape != k):
+            raise ValueError(f"rows are [T, heads, {self.head_dim}], got {tuple(q)} and {tuple(k)} into "
+                             f"{tuple(q_out.shape)} and {tuple(k_out.shape)}")
+        (ar, ah, ae), (br, bh, be), (cr, ch, ce), (dr, dh, de) = Q.stride(), q_out.stride(), K.stride(), k_out.stride()
+        if not ae == be == ce == de == 1:
+            raise ValueError("a head's elements must be adjacent")
+        T, n_seqs = q[0], lengths.numel()
+        if lengths.dim() != 1 or lengths.dtype != i32 or not lengths.is_contiguous():
+            raise ValueError("lengths is a contiguous int32 [n_seqs]")
+        there = (Q.get_device() == index and K.get_device() == index and lengths.get_device() == index and
+                 (q_out is Q or q_out.get_device() == index) and (k_out is K or k_out.get_device() == index))
+        at = wq = wk = None
+        if offsets is not None:
+            if offsets.shape != (n_seqs + 1,) or offsets.dtype != i32 or not offsets.is_contiguous():
+                raise ValueError("offsets is a contiguous int32 [n_seqs + 1]")
+            there = there and offsets.get_device() == index
+            at = offsets.data_ptr()
+        if q_weight is not None:
+            wq = self._weight(q_weight)
+        if k_weight is not None:
+            wk = self._weight(k_weight)
+        if not there:
+            raise ValueError(f"operands live on the rotary's device {self.device}")
         if not (-_INT_MAX <= max_new <= _INT_MAX and T <= _INT_MAX and n_seqs <= _INT_MAX):
             _ints(T=T, n_seqs=n_seqs, max_new=max_new)
-        handle = self._raw_stream(index) if stream is None else stream.cuda_stream
         status = self._lib.mlora_rotary_apply(
-            self.handle, *q, *k, code, T, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps, None if offsets is None else offsets.data_ptr(),
-            lengths.data_ptr(), n_seqs, max_new, handle)
+            self.handle, Q.data_ptr(), ar, ah, q_out.data_ptr(), br, bh, q[1], K.data_ptr(), cr, ch, k_out.data_ptr(), dr, dh,
+            k[1], code, T, wq, wk, eps, at, lengths.data_ptr(), n_seqs, max_new,
+            self._raw_stream(index) if stream is None else stream.cuda_stream)
         if status:
             check(status, "mlora_rotary_apply")
+
+    def _weight(self, w) -> int:
+        if w.shape != (self.head_dim,) or w.dtype != self._f32 or not w.is_contiguous() or w.get_device() != self._index:
+            raise ValueError(f"weights are contiguous fp32 [{self.head_dim}] on {self.device}")
+        return w.data_ptr()
 
     def status(self, stream=None) -> int:
         return mlora_rotary_status(self.handle, _stream_handle(stream))
