@@ -58,8 +58,7 @@ constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: 
 template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query
-    static constexpr bool P16 = BITS == 4 && !F32;     // weights and values in fp16
-    static constexpr int PTERMS = F32 ? 3 : P16 ? 1 : 2;   // of a weight
+    static constexpr int PTERMS = BITS == 4 ? (F32 ? 2 : 1) : F32 ? 3 : 2;   // of a weight (4 bits: in fp16, else bf16)
     static constexpr int KS = DP / 16;                 // k steps of q . k = 16-row tiles of O^T
     static constexpr int RT = 8 * NT;                  // query rows per tile
     static constexpr int CB = DP == 256 ? 2 : 1;       // column boxes
@@ -70,7 +69,7 @@ struct Shape {
     // (three in long ranges over 4 bits, whose chunks' own instructions count for more: 32 x 32k tokens 220 us,
     // 230 us with two; one sequence of 777 tokens 9.6 and 8.7 us)
     static constexpr int SUB = DP == 256 ? 1 : LONG ? 3 : 2;
-    static_assert(!LONG || (P16 && DP <= 128 && NT == 1), "long ranges");
+    static_assert(!LONG || (BITS == 4 && !F32 && DP <= 128 && NT == 1), "long ranges");
     static constexpr int CHUNK_T = PIECE * SUB;
     static constexpr int PART = BITS == 4 ? 18 * DP : 2 * CB * BOX;   // keys and values of a piece
     static constexpr int STAGE = SUB * PART;
@@ -419,7 +418,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 114) : 0;
             const float down = __uint_as_float((uint32_t)(127 - k) << 23);
             const float qf = a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23));
-            if (lane == 0) tl.qf[r] = !fine ? NAN : Sh::P16 ? fmaxf(qf, 0x1p-126f) : qf;   // (P16: -inf times it stays -inf)
+            if (lane == 0) tl.qf[r] = !fine ? NAN : BITS == 4 ? fmaxf(qf, 0x1p-126f) : qf;   // (4 bits: -inf times it stays -inf)
 #pragma unroll
             for (int e = 0; e < EL; e += 2) {
                 if (BITS == 4) {
@@ -463,7 +462,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) qreg[s][t][term] = qf_at(s, t, term);
         float qf[NT][2], m[NT][2], l[NT][2], o[KS][NT][4];
-        float bound[NT][2], sum[NT][4];   // P16: (m + OFF16 + SLACK16) / qf, and l as the tensor cores sum it
+        float bound[NT][2], sum[NT][4];   // 4 bits: (m + OFF16 + SLACK16) / qf, and l of bf16 rows as the tensor cores sum it
         int hi[NT][2];   // tokens first_seen(hi - 1) .. hi - 1 are seen
         int hi_min = 0x7fffffff, hi_max = -0x7fffffff;
 #pragma unroll
@@ -496,10 +495,11 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 vs1 = id1 >= 0 ? c.v_scale[(size_t)id1 * H + h] : 0.f;
             }
             float ksk[SUB], vsk[SUB];
+            if (BITS == 8)
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                ksk[u] = BITS == 4 ? 1.f : __shfl_sync(~0u, ks, k % BATCH * SUB + u);
-                vsk[u] = BITS == 4 ? 1.f : __shfl_sync(~0u, vs, k % BATCH * SUB + u);
+                ksk[u] = __shfl_sync(~0u, ks, k % BATCH * SUB + u);
+                vsk[u] = __shfl_sync(~0u, vs, k % BATCH * SUB + u);
             }
             const uint32_t st = BITS == 4 ? drain : used % Sh::STAGES;
             alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], BITS == 4 ? turn : (used / Sh::STAGES) & 1, abort_flag, a.status));
@@ -511,26 +511,27 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const uint8_t* stage = ring + st * Sh::STAGE;
 
             constexpr int CH = SUB == 1 ? 2 : 1;         // independent sums per piece (even and odd k steps)
+            // scores of tokens g and g + 8 of each piece, rows 2 tig and 2 tig + 1 of each tile
             float sc[SUB][CH][NT][4] = {};
-            auto scores4 = [&](int u, int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            if constexpr (BITS == 4) {
+                auto scores4 = [&](int u, int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int term = 0; term < TERMS; ++term) {
-                        const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
-                        mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
+                        for (int term = 0; term < TERMS; ++term) {
+                            const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
+                            mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
+                        }
+                };
+                // a lane's two atoms of a block and their scales (zeros where the head has no such group)
+                auto atoms_at = [&](const uint8_t* codes, const uint8_t* scales, int at, bool there, uint4& w, uint32_t& s16) {
+                    w = make_uint4(0u, 0u, 0u, 0u);
+                    s16 = 0u;
+                    if (FULL || there) {
+                        w = *reinterpret_cast<const uint4*>(codes + at * 8);
+                        s16 = *reinterpret_cast<const uint16_t*>(scales + at);
                     }
-            };
-            // a lane's two atoms of a block and their scales (zeros where the head has no such group)
-            auto atoms_at = [&](const uint8_t* codes, const uint8_t* scales, int at, bool there, uint4& w, uint32_t& s16) {
-                w = make_uint4(0u, 0u, 0u, 0u);
-                s16 = 0u;
-                if (FULL || there) {
-                    w = *reinterpret_cast<const uint4*>(codes + at * 8);
-                    s16 = *reinterpret_cast<const uint16_t*>(scales + at);
-                }
-            };
-            if (BITS == 4) {
+                };
                 // 64 elements at a time: the lane's atoms of tokens g and g + 8, group tig of the four
 #pragma unroll
                 for (int q = 0; q < DP / 64; ++q)
@@ -547,43 +548,10 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         scores4(u, 4 * q + 2, codes_f16<0>(w.y, sa), codes_f16<0>(w.w, sb), codes_f16<1>(w.y, sa), codes_f16<1>(w.w, sb));
                         scores4(u, 4 * q + 3, codes_f16<2>(w.y, sa), codes_f16<2>(w.w, sb), codes_f16<3>(w.y, sa), codes_f16<3>(w.w, sb));
                     }
-            }
-            constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
-            if (BITS == 8)
-#pragma unroll
-            for (int q = 0; q < CB; ++q)
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        const uint8_t* kb = stage + u * Sh::PART + q * Sh::BOX;
-                        const int ch = J * tig + j;
-                        const uint4 ra = *reinterpret_cast<const uint4*>(kb + swz<Sh::ROWB>(g, ch));
-                        const uint4 rb = *reinterpret_cast<const uint4*>(kb + swz<Sh::ROWB>(g + 8, ch));
-                        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int s = (q * J + j) * 4 + w;
-                            const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
-                            const uint32_t a0 = minus1152(prmt(xa, 0x64646464u, 0x4140)),
-                                           a1 = minus1152(prmt(xb, 0x64646464u, 0x4140)),
-                                           a2 = minus1152(prmt(xa, 0x64646464u, 0x4342)),
-                                           a3 = minus1152(prmt(xb, 0x64646464u, 0x4342));
-#pragma unroll
-                            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                                for (int term = 0; term < TERMS; ++term) {
-                                    const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
-                                    mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
-                                }
-                        }
-                    }
-            // scores -> x log2 e; tokens g and g + 8 of each piece, rows 2 tig and 2 tig + 1 of each tile
-            const int t0 = token_at(k);
-            const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
-            bool above = false;
-            float top[NT][2];
-            if constexpr (Sh::P16) {
+                const int t0 = token_at(k);
+                const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
+                bool above = false;
+                float top[NT][2];
                 // the largest score itself, against the bound over the row's factor; then one fused operation
                 // per exponent
 #pragma unroll
@@ -618,6 +586,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                             m[t][e] = x;
                             bound[t][e] = (x + (OFF16 + SLACK16)) / qf[t][e];
                             sum[t][e] *= f;
+                            l[t][e] *= f;
 #pragma unroll
                             for (int s = 0; s < KS; ++s) {
                                 o[s][t][e] *= f;
@@ -628,16 +597,25 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 constexpr uint32_t ONES = 0x3C003C00u;
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
-                    uint32_t p[NT][2];   // weights as the B operand: tokens x rows
+                    uint32_t p[NT][PTERMS][2];   // weights as the B operand: tokens x rows
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const __half2 y = __floats2half2_rn(ex2(fmaf(sc[u][0][t][2 * z], qf[t][0], -m[t][0])),
-                                                                ex2(fmaf(sc[u][0][t][2 * z + 1], qf[t][1], -m[t][1])));
-                            p[t][z] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+                            const float w0 = ex2(fmaf(sc[u][0][t][2 * z], qf[t][0], -m[t][0]));
+                            const float w1 = ex2(fmaf(sc[u][0][t][2 * z + 1], qf[t][1], -m[t][1]));
+                            const __half2 y = __floats2half2_rn(w0, w1);
+                            p[t][0][z] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+                            if (F32) {
+                                const float2 f = __half22float2(y);
+                                const __half2 low = __floats2half2_rn(w0 - f.x, w1 - f.y);
+                                p[t][PTERMS - 1][z] = transpose8(*reinterpret_cast<const uint32_t*>(&low));
+                                l[t][0] += w0;
+                                l[t][1] += w1;
+                            }
                         }
-                        mma(sum[t], ONES, ONES, ONES, ONES, p[t][0], p[t][1]);   // (of all tokens, in every row of the result)
+                        // bf16 rows: the sum of all tokens' weights, in every row of the result
+                        if (!F32) mma(sum[t], ONES, ONES, ONES, ONES, p[t][0][0], p[t][0][1]);
                     }
 #pragma unroll
                     for (int q = 0; q < CB; ++q) {
@@ -659,17 +637,65 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                             if (W == 4) v[z][W - 2] = prmt(w.y, w.w, 0x5410), v[z][W - 1] = prmt(w.y, w.w, 0x7632);
                         }
 #pragma unroll
-                        for (int w = 0; w < W; ++w)
+                        for (int w = 0; w < W; ++w) {
+                            auto values = [&](int z, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                mma(o[q * (KS / CB) + w * 2][t], codes_f16<0>(v[0][w], vs[0]), codes_f16<1>(v[0][w], vs[0]),
-                                    codes_f16<0>(v[1][w], vs[1]), codes_f16<1>(v[1][w], vs[1]), p[t][0], p[t][1]);
-                                mma(o[q * (KS / CB) + w * 2 + 1][t], codes_f16<2>(v[0][w], vs[0]), codes_f16<3>(v[0][w], vs[0]),
-                                    codes_f16<2>(v[1][w], vs[1]), codes_f16<3>(v[1][w], vs[1]), p[t][0], p[t][1]);
-                            }
+                                for (int t = 0; t < NT; ++t) {
+                                    float(&to)[4] = o[q * (KS / CB) + w * 2 + z][t];
+                                    if (!F32) {
+                                        mma(to, a0, a1, a2, a3, p[t][0][0], p[t][0][1]);
+                                        continue;
+                                    }
+                                    // (fp32 rows: the tensor cores sum 16 tokens, as below)
+                                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma(part, a0, a1, a2, a3, p[t][PTERMS - 1][0], p[t][PTERMS - 1][1]);
+                                    mma(part, a0, a1, a2, a3, p[t][0][0], p[t][0][1]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) to[e] += part[e];
+                                }
+                            };
+                            values(0, codes_f16<0>(v[0][w], vs[0]), codes_f16<1>(v[0][w], vs[0]), codes_f16<0>(v[1][w], vs[1]),
+                                   codes_f16<1>(v[1][w], vs[1]));
+                            values(1, codes_f16<2>(v[0][w], vs[0]), codes_f16<3>(v[0][w], vs[0]), codes_f16<2>(v[1][w], vs[1]),
+                                   codes_f16<3>(v[1][w], vs[1]));
+                        }
                     }
                 }
             } else {
+            constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
+#pragma unroll
+            for (int q = 0; q < CB; ++q)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        const uint8_t* kb = stage + u * Sh::PART + q * Sh::BOX;
+                        const int ch = J * tig + j;
+                        const uint4 ra = *reinterpret_cast<const uint4*>(kb + swz<Sh::ROWB>(g, ch));
+                        const uint4 rb = *reinterpret_cast<const uint4*>(kb + swz<Sh::ROWB>(g + 8, ch));
+                        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int s = (q * J + j) * 4 + w;
+                            const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
+                            const uint32_t a0 = minus1152(prmt(xa, 0x64646464u, 0x4140)),
+                                           a1 = minus1152(prmt(xb, 0x64646464u, 0x4140)),
+                                           a2 = minus1152(prmt(xa, 0x64646464u, 0x4342)),
+                                           a3 = minus1152(prmt(xb, 0x64646464u, 0x4342));
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int term = 0; term < TERMS; ++term) {
+                                    const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
+                                    mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
+                                }
+                        }
+                    }
+            // scores -> x log2 e
+            const int t0 = token_at(k);
+            const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
+            bool above = false;
+            float top[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -677,7 +703,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     top[t][e] = -INFINITY;
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
-                        const float f = BITS == 4 ? qf[t][e] : qf[t][e] * ksk[u];
+                        const float f = qf[t][e] * ksk[u];
                         float& x0 = sc[u][0][t][e];
                         float& x1 = sc[u][0][t][2 + e];
                         x0 = (CH == 2 ? x0 + sc[u][CH - 1][t][e] : x0) * f;
@@ -722,8 +748,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     l[t][1] += w[1] + w[3];
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        float x0 = w[2 * z], x1 = w[2 * z + 1];
-                        if (BITS == 8) x0 *= vsk[u], x1 *= vsk[u];
+                        float x0 = w[2 * z] * vsk[u], x1 = w[2 * z + 1] * vsk[u];
 #pragma unroll
                         for (int term = 0; term < PTERMS; ++term) {
                             const uint32_t y = bf2_of(x0, x1);
@@ -737,26 +762,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 constexpr int W = Sh::ROWB / 32;   // words of a box row per thread
 #pragma unroll
                 for (int q = 0; q < CB; ++q) {
-                    const uint8_t* vb = stage + u * Sh::PART + (BITS == 4 ? 8 * D : (CB + q) * Sh::BOX);
+                    const uint8_t* vb = stage + u * Sh::PART + (CB + q) * Sh::BOX;
                     uint32_t v[4][W];
-                    Scale2 vsc[2];
-                    if (BITS == 4) {
-                        // atoms of tokens 2 tig and + 1, + 8 and + 9, of the lane's group (DP 64: half a group)
-                        const int n = min(8, D / 16 - 8 * q), gr = DP == 64 ? g >> 1 : g;
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int at = q * 128 + (z * n + gr) * 8 + tig * 2;
-                            uint4 w;
-                            uint32_t s16;
-                            atoms_at(vb, vb + 9 * D, at, gr < n, w, s16);
-                            vsc[z] = scale_bf16(prmt(s16, 0u, 0x4140));
-                            // words of four elements, token 2 tig in the low half
-                            const uint32_t lo = DP == 64 && (g & 1) ? w.y : w.x, hi = DP == 64 && (g & 1) ? w.w : w.z;
-                            v[z][0] = prmt(lo, hi, 0x5410), v[z][1] = prmt(lo, hi, 0x7632);
-                            if (W == 4) v[z][W - 2] = prmt(w.y, w.w, 0x5410), v[z][W - 1] = prmt(w.y, w.w, 0x7632);
-                        }
-                    }
-                    if (BITS == 8)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         const int r = 2 * tig + (z & 1) + (z >> 1) * 8;
@@ -773,13 +780,6 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         uint32_t y[2][4];   // [token pair][element of the word]
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            if (BITS == 4) {
-                                y[z][0] = codes_bf16<0>(v[z][w], vsc[z]);
-                                y[z][1] = codes_bf16<1>(v[z][w], vsc[z]);
-                                y[z][2] = codes_bf16<2>(v[z][w], vsc[z]);
-                                y[z][3] = codes_bf16<3>(v[z][w], vsc[z]);
-                                continue;
-                            }
                             const uint32_t e0 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x5140),
                                            e1 = prmt(v[2 * z][w], v[2 * z + 1][w], 0x7362);
                             y[z][0] = bf16_codes(prmt(e0, 0x43434343u, 0x4140));
@@ -830,7 +830,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if (Sh::P16) l[t][e] = sum[t][e];
+                if (BITS == 4 && !F32) l[t][e] = sum[t][e];
                 else
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(~0u, l[t][e], d);
@@ -848,7 +848,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 float top = tl.m[0][r];
 #pragma unroll
                 for (int w = 1; w < WARPS; ++w) top = fmaxf(top, tl.m[w][r]);
-                const float f = ex2(m[t][e] - top), fe = Sh::P16 ? f * 16.f : f;   // (even elements are held over 16)
+                const float f = ex2(m[t][e] - top), fe = BITS == 4 ? f * 16.f : f;   // (even elements are held over 16)
                 float* dst = join + (warp * RT + r) * DP;
 #pragma unroll
                 for (int q = 0; q < CB; ++q) {
