@@ -13,7 +13,7 @@ namespace mlora {
 
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int THREADS = 64;
 constexpr int FEW = 8;   // rows of a sequence up to which a thread takes an atom
 
 // 16 elements of a row as they lie in memory
@@ -196,6 +196,12 @@ __global__ void __launch_bounds__(THREADS) append_rows_kernel(CachePages c, Cach
     block[(is_v ? 17 * c.dim : 16 * c.dim) + at] = (uint8_t)a.scale;
 }
 
+// the halves of a bf16 pair, each times f
+__device__ __forceinline__ void unpack_times(uint32_t w, float f, float& a, float& b) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(a), "=f"(b)
+        : "r"(w << 16), "r"(w & 0xFFFF0000u), "f"(f));
+}
 // (code * scale) * unit, the first product exact: 16 elements as they lie in memory
 template <typename T>
 __device__ __forceinline__ Row16<T> restored(uint2 codes, uint32_t scale, float unit) {
@@ -207,10 +213,7 @@ __device__ __forceinline__ Row16<T> restored(uint2 codes, uint32_t scale, float 
         const uint32_t y[4] = {codes_bf16<0>(w, s), codes_bf16<1>(w, s), codes_bf16<2>(w, s), codes_bf16<3>(w, s)};
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = __fmul_rn(__uint_as_float(y[e] << 16), unit);
-            v[4 + e] = __fmul_rn(__uint_as_float(y[e] & 0xFFFF0000u), unit);
-        }
+        for (int e = 0; e < 4; ++e) unpack_times(y[e], unit, v[e], v[4 + e]);
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) r.w[8 * i + e] = __float_as_uint(v[e]);
