@@ -1,13 +1,13 @@
 """A served attention layer: prompts of several tenants, then decode steps, through the
-multi-adapter projections and the 8-bit key/value cache.
+multi-adapter projections, the rotation and the key/value cache in 8 or in 4 bits.
 
     python examples/cached_layer.py
 
-Each step: the fused q|k|v projection with every row's adapter, the new keys and values
-appended to the pages, attention of the new rows over the cache, the output projection
-with every row's adapter.  Weights, adapters and inputs are random; positions are not
-encoded.  Prints the largest difference from the same layer in plain fp64 operations over
-keys and values that were never quantised.
+Each step: the fused q|k|v projection with every row's adapter, norms and rotation of the
+queries and keys by their positions, the new keys and values appended to the pages,
+attention of the new rows over the cache, the output projection with every row's adapter.
+Weights, adapters and inputs are random.  Prints the largest difference from the same layer
+in plain fp64 operations over keys and values that were never quantised.
 """
 from __future__ import annotations
 
@@ -21,9 +21,9 @@ class Layer:
     """Projections, adapters and cache of one layer."""
 
     def __init__(self, hidden=1024, q_heads=8, kv_heads=2, head_dim=128, tenants=3, rank=16, page_size=32,
-                 max_seqs=4, max_len=512, max_tokens=1024, seed=0):
+                 max_seqs=4, max_len=512, max_tokens=1024, seed=0, bits=8):
         import torch
-        from heterogeneous_lora_gemm_gb300 import Cache, Pool
+        from heterogeneous_lora_gemm_gb300 import Cache, Cache4, Pool, Rotary
         self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
@@ -47,9 +47,15 @@ class Layer:
         width = -(-max_len // page_size)
         shape = (max_seqs * width, kv_heads, page_size, head_dim)
         self.pages = torch.randperm(shape[0], device="cuda", generator=g).int().view(max_seqs, width)
-        self.cache = Cache(torch.zeros(shape, dtype=torch.int8, device="cuda"), torch.zeros(shape[:2], device="cuda"),
-                           torch.zeros(shape, dtype=torch.int8, device="cuda"), torch.zeros(shape[:2], device="cuda"),
-                           q_heads)
+        if bits == 4:
+            blocks = (max_seqs * width, kv_heads, page_size // 16, 18 * head_dim)
+            self.cache = Cache4(torch.empty(blocks, dtype=torch.uint8, device="cuda"), q_heads)
+        else:
+            codes, scale = dict(dtype=torch.int8, device="cuda"), dict(device="cuda")
+            self.cache = Cache(torch.zeros(shape, **codes), torch.zeros(shape[:2], **scale), torch.zeros(shape, **codes),
+                               torch.zeros(shape[:2], **scale), q_heads)
+        self.rotary = Rotary(head_dim)
+        self.q_norm, self.k_norm = (1 + 0.1 * torch.randn(head_dim, device="cuda", generator=g) for _ in range(2))
 
     def step(self, X, row_adapter, lengths, offsets=None, max_new=1):
         """One step of rows X [T, hidden]; lengths as they are after it."""
@@ -59,6 +65,7 @@ class Layer:
         self.qkv.forward(X, self.Wqkv, row_adapter, Y)
         q, k, v = Y.unflatten(1, (-1, D)).split([self.q_heads, self.kv_heads, self.kv_heads], dim=1)
         pages = self.pages[:lengths.shape[0]]
+        self.rotary.apply(q, k, lengths, offsets=offsets, max_new=max_new, q_weight=self.q_norm, k_weight=self.k_norm)
         self.cache.append(k, v, lengths, pages, offsets=offsets, max_new=max_new)
         A = torch.empty((T, self.q_heads * D), dtype=X.dtype, device=X.device)
         self.cache.attend(q, A.unflatten(1, (-1, D)), lengths, pages, offsets=offsets, max_new=max_new)
@@ -80,6 +87,16 @@ class Layer:
 
         q, k, v = project(X.double(), self.Wqkv, 0).unflatten(1, (-1, D)).split(
             [self.q_heads, self.kv_heads, self.kv_heads], dim=1)
+        held = keep[0].shape[0] if keep else 0
+        angle = torch.arange(held, held + X.shape[0], device=X.device).double()[:, None, None] * torch.tensor(
+            [10000.0 ** (-2 * i / D) for i in range(D // 2)], dtype=torch.float64, device=X.device)
+
+        def turn(y, weight):
+            y = y * weight.double() / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+            a, b = y.chunk(2, dim=-1)
+            return torch.cat([a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()], dim=-1)
+
+        q, k = turn(q, self.q_norm), turn(k, self.k_norm)
         keep[:] = [torch.cat([keep[0], k]), torch.cat([keep[1], v])] if keep else [k, v]
         k, v = (t.repeat_interleave(G, dim=1) for t in keep)
         n, L = X.shape[0], k.shape[0]
@@ -89,11 +106,11 @@ class Layer:
         return project(torch.einsum("hit,thd->ihd", w, v).flatten(1), self.Wo, 1)
 
 
-def main(prompts=(200, 33, 1, 97), adapters=(0, -1, 2, 1), decode_steps=8) -> float:
+def main(prompts=(200, 33, 1, 97), adapters=(0, -1, 2, 1), decode_steps=8, bits=8) -> float:
     """Prompts, then decode steps; returns the largest difference over the outputs' size."""
     import torch
     from heterogeneous_lora_gemm_gb300 import mlora
-    layer = Layer()
+    layer = Layer(bits=bits)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     i32 = dict(dtype=torch.int32, device="cuda")
@@ -109,9 +126,10 @@ def main(prompts=(200, 33, 1, 97), adapters=(0, -1, 2, 1), decode_steps=8) -> fl
             at = slice(sum(rows[:b]), sum(rows[:b + 1]))
             want = layer.plain(X[at], a, keep[b])
             worst = max(worst, float((Z[at] - want).norm() / want.norm()))
-    assert layer.cache.status() == layer.qkv.status() == layer.out.status() == mlora.MLORA_OK
+    assert layer.cache.status() == layer.rotary.status() == layer.qkv.status() == layer.out.status() == mlora.MLORA_OK
     return worst
 
 
 if __name__ == "__main__":
-    print(f"largest relative difference from fp64 without quantisation: {main():.4f}")
+    for bits in (8, 4):
+        print(f"{bits} bits: largest relative difference from fp64 without quantisation: {main(bits=bits):.4f}")
