@@ -11,7 +11,7 @@ constexpr int PROMPT_SLOT = 256 * (128 + 2);// floats of one partial result of t
 struct AttendWs {
     CUtensorMap k16, v16;   // 8-bit codes as rows of head_dim bytes, boxes of 16 tokens
     const uint8_t* zeros;   // a 4-bit block of zeros
-    float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT], or [sms][PROMPT_SLOT]
+    float* partial;         // [sms * ATTEND_OCC * 2][ATTEND_SLOT], or [sms][PROMPT_SLOT], or (4 bits) one per warp and two per CTA
     int* counters;          // [sms * ATTEND_OCC] arrivals, zero between calls
     int sms;
     uint8_t* operands;      // converted tiles of prompts (attend_prompt.cu), operand_bytes of them
@@ -19,8 +19,13 @@ struct AttendWs {
     int* operand_at;        // [n_seqs <= 65535] where a sequence's tiles are
 };
 
-cudaError_t attend_split_init(int bits);
+cudaError_t attend_split_init();
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
+
+// The same over the 4-bit cache (attend4_split.cu): a range of the work line per warp.
+cudaError_t attend4_split_init();
+size_t attend4_split_bytes(int dim);   // of partial results, per SM
+cudaError_t launch_attend4_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st);
 
 // Sequences with many rows (attend_prompt.cu): bf16, and fp32 with heads of up to 128 elements.
 cudaError_t attend_prompt_init(int bits);

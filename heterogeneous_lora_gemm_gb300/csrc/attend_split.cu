@@ -1,5 +1,5 @@
-// Causal attention over the 8-bit and the 4-bit cache for sequences with few rows in the step
-// (decode: one token), any row and head count (include/mlora.h).
+// Causal attention over the 8-bit cache for sequences with few rows in the step (decode:
+// one token), any row and head count (include/mlora.h).
 //
 // Mathematics.  With codes kc, vc and page scales ks, vs, row r (query token i, query head
 // g of the key/value head's group) has  x_t = scale ks_t (q_r . kc_t),  and
@@ -27,16 +27,11 @@
 // ranges, one per resident CTA; every CTA finds its range from the lengths.  An item is as
 // long as its tokens plus what its start costs (LEAD).  An item cut between CTAs is joined,
 // in range order, by the CTA that finishes it last, so results do not depend on timing.
-//
-// The 4-bit cache (BITS 4, block4.cuh): a code times its scale is exact in fp16 and in bf16, so that the
-// operands are the values themselves, over a unit that goes into the scores' factor (on the host)
-// and into the output.  A piece's keys, values and scales are one copy; an atom (8 bytes) is what a
-// lane turns into its rows' part of four k steps, so that it needs two scales per four steps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "attend.h"
-#include "block4.cuh"
+#include "attend_mma.cuh"
 #include "tc_ptx.cuh"
 
 namespace mlora {
@@ -50,15 +45,12 @@ constexpr int PIECE = 16;                 // tokens of a copied box and of a pro
 constexpr int LEAD = 1;                   // units (of WARPS chunks) that starting an item costs
 constexpr int MIN_UNITS = LEAD + 1;       // a CTA's range is at least so long
 constexpr float SLACK = 8.f;              // m moves when x > m + 8: weights stay below 2^8
-// fp16 weights: m is the largest x less OFF16 when it is set, and moves when x > m + OFF16 + SLACK16, so that
-// they stay below 2^15 and their 11 bits reach down to 2^-26 of the largest
-constexpr float OFF16 = 12.f, SLACK16 = 3.f;
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
-template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG>
+template <bool F32, int DP, int NT>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query
-    static constexpr int PTERMS = BITS == 4 ? (F32 ? 2 : 1) : F32 ? 3 : 2;   // of a weight (4 bits: in fp16, else bf16)
+    static constexpr int PTERMS = F32 ? 3 : 2;         // of a weight
     static constexpr int KS = DP / 16;                 // k steps of q . k = 16-row tiles of O^T
     static constexpr int RT = 8 * NT;                  // query rows per tile
     static constexpr int CB = DP == 256 ? 2 : 1;       // column boxes
@@ -66,24 +58,20 @@ struct Shape {
     static constexpr int BOX = PIECE * ROWB;
     // a warp takes a chunk of two pieces at a time: waits, votes and issues are per chunk
     // (one where the accumulators leave no registers for two)
-    // (three in long ranges over 4 bits, whose chunks' own instructions count for more: 32 x 32k tokens 220 us,
-    // 230 us with two; one sequence of 777 tokens 9.6 and 8.7 us)
-    static constexpr int SUB = DP == 256 ? 1 : LONG ? 3 : 2;
-    static_assert(!LONG || (BITS == 4 && !F32 && DP <= 128 && NT == 1), "long ranges");
+    static constexpr int SUB = DP == 256 ? 1 : 2;
     static constexpr int CHUNK_T = PIECE * SUB;
-    static constexpr int PART = BITS == 4 ? 18 * DP : 2 * CB * BOX;   // keys and values of a piece
+    static constexpr int PART = 2 * CB * BOX;          // keys and values of a piece
     static constexpr int STAGE = SUB * PART;
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
     // (64 KB of ring also where the queries' fragments leave no more, 16 fp32 rows of up to 256 elements: 2 x
     // 300 rows after 1000, 16/8 heads, 124 us, 188 us with the 96 KB that one CTA per SM has room for)
-    static constexpr int FIT = (OCC == 3 || (F32 && DP == 256 && NT == 2) ? 64 : 96) * 1024 / WARPS / STAGE;
-    static constexpr int STAGES = FIT < 8 ? FIT : 8;
-    static constexpr int JOIN = WARPS * RT * DP * 4;       // the join buffer lies in the ring
-    static constexpr int RING = WARPS * STAGES * STAGE > JOIN ? WARPS * STAGES * STAGE : JOIN;
+    static constexpr int STAGES = (OCC == 3 || (F32 && DP == 256 && NT == 2) ? 64 : 96) * 1024 / WARPS / STAGE;
+    static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int QWORDS = KS * NT * TERMS * 64;    // query fragments, 32-bit words
     static constexpr int SMEM = 1024 + RING + QWORDS * 4;
     static constexpr int SLOT = RT * (DP + 2);             // floats of a partial result: O, then m, l per row
+    static_assert(WARPS * RT * DP * 4 <= RING, "the join buffer lies in the ring");
 };
 
 // shared-memory offset of 16-byte chunk `c` of box row `r`
@@ -111,28 +99,6 @@ __device__ __forceinline__ void mma_bf(float (&c)[4], uint32_t a0, uint32_t a1, 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t bf2_of(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // A sequence's share of the work line: tiles x heads items, each LEAD + units long (1 where the
 // rows see nothing: zeros are written).
 struct Line {
@@ -193,31 +159,11 @@ __device__ __forceinline__ void load_elements(const __nv_bfloat16* p, bool there
     }
 }
 
-template <typename E>
-__device__ __forceinline__ void store4(E* p, float4 v);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, float4 v) {
-    *reinterpret_cast<float4*>(p) = v;
-}
-template <>
-__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-}
-
-__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-// `zeros`: a 4-bit block of zeros, in the place of one that cannot be read.  FULL: heads of DP elements,
-// so that a 4-bit block's offsets are constants.  LONG: chunks of three pieces.
-template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG>
-__global__ void __launch_bounds__(THREADS, (Shape<BITS, F32, DP, NT, FULL, LONG>::OCC))
+template <bool F32, int DP, int NT>
+__global__ void __launch_bounds__(THREADS, (Shape<F32, DP, NT>::OCC))
 attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttendArgs a,
-                    float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
-    using Sh = Shape<BITS, F32, DP, NT, FULL, LONG>;
+                    float* __restrict__ partial, int* __restrict__ counters) {
+    using Sh = Shape<F32, DP, NT>;
     using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int KS = Sh::KS, RT = Sh::RT, SUB = Sh::SUB, CHUNK_T = Sh::CHUNK_T, TERMS = Sh::TERMS, PTERMS = Sh::PTERMS, CB = Sh::CB;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -227,15 +173,15 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     __shared__ Tail tl;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
     const CachePages& c = a.pages;
-    const int H = c.heads, G = a.q_heads / H, D = FULL ? DP : c.dim;
+    const int H = c.heads, G = a.q_heads / H, D = c.dim;
 
     // ---- this CTA's range of the line
     if (lane == 0) {
-        for (int s = 0; s < Sh::STAGES; ++s) mbar_init(&tl.full[warp][s], BITS == 4 ? Sh::SUB : 1);
+        for (int s = 0; s < Sh::STAGES; ++s) mbar_init(&tl.full[warp][s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) tl.abort_flag = 0;
-    if (BITS == 8 && tid == 0) {
+    if (tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmK) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmV) : "memory");
     }
@@ -294,7 +240,6 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     n = tl.first;
 
     uint32_t issued = 0, used = 0;     // chunks copied and consumed by this warp, over all items
-    uint32_t fill = 0, drain = 0, turn = 0;   // 4 bits: their stages, and the phase of the one consumed
     uint8_t* ring = smem + warp * Sh::STAGES * Sh::STAGE;
     volatile int* abort_flag = &tl.abort_flag;
     bool alive = true;
@@ -352,8 +297,6 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             return k < count && t <= pos_hi ? load_page(a.step, c, b, quotient(a.page, t), a.status) : -1;
         };
         auto row_of = [&](int id, int t) {   // first code row of the piece; past the tensor for a bad page
-            if (BITS == 4)                   // the piece's block; -1 for a bad page
-                return id < 0 ? -1 : (id * H + h) * (c.page >> 4) + ((t - quotient(a.page, t) * c.page) >> 4);
             return id < 0 ? c.n_pages * H * c.page : (id * H + h) * c.page + t - quotient(a.page, t) * c.page;
         };
         const int my_k = lane / SUB, my_off = lane % SUB * PIECE;
@@ -366,26 +309,12 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const int id = t + PIECE > seen_from ? id_at(my_k, t) : -1;
             id1 = id_at(BATCH + my_k, t1);
             row = row_of(id, t), row1 = row_of(id1, t1);
-            if (BITS == 8) {
-                ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;
-                vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
-            }
+            ks = id >= 0 ? c.k_scale[(size_t)id * H + h] : 0.f;
+            vs = id >= 0 ? c.v_scale[(size_t)id * H + h] : 0.f;
         }
         // copies chunk k of the item, a box per lane; `row` holds batch `batch`
         const int box = lane % (2 * CB * SUB), box_sub = box / (2 * CB), box_v = box / CB & 1, box_q = box % CB;
         auto issue = [&](int k, int batch) {
-            if (BITS == 4) {   // (a block by the lane that looked its page up)
-                if (lane / SUB == k % BATCH) {
-                    const int r = k / BATCH == batch ? row : row1;
-                    uint64_t* bar = &tl.full[warp][fill];
-                    mbar_expect_tx(bar, block4_bytes(D));
-                    bulk_g2s(ring + fill * Sh::STAGE + lane % SUB * Sh::PART,
-                             r < 0 ? zeros : c.blocks + (size_t)(uint32_t)r * (uint32_t)block4_bytes(D), block4_bytes(D), bar);
-                }
-                fill = fill + 1 == Sh::STAGES ? 0 : fill + 1;
-                ++issued;
-                return;
-            }
             const int r = __shfl_sync(~0u, k / BATCH == batch ? row : row1, k % BATCH * SUB + box_sub);
             const uint32_t st = issued % Sh::STAGES;
             uint64_t* bar = &tl.full[warp][st];
@@ -417,24 +346,10 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             // stays below 2^14 (within fp16, where a factor of 2^128 would leave fp32)
             const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 114) : 0;
             const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-            const float qf = a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23));
-            if (lane == 0) tl.qf[r] = !fine ? NAN : BITS == 4 ? fmaxf(qf, 0x1p-126f) : qf;   // (4 bits: -inf times it stays -inf)
+            if (lane == 0)
+                tl.qf[r] = fine ? a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23)) : NAN;
 #pragma unroll
             for (int e = 0; e < EL; e += 2) {
-                if (BITS == 4) {
-                    // k step s takes, of each 64 elements, the pairs (x, x + 4) of the lane's group: codes that
-                    // lie in one nibble of a word's halves
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int d = lane * EL + e + z, x4 = d % 4, s = d / 64 * 4 + d % 16 / 8 * 2 + x4 / 2, t = d % 64 / 16;
-                        const float v = fine ? x[kk][e + z] * (x4 % 2 ? down : down * 16.f) : 0.f;
-                        __half* dst = reinterpret_cast<__half*>(qfrag + (((s * NT + r / 8) * TERMS) * 32 + r % 8 * 4 + t) * 2 + x4 % 2) + d % 8 / 4;
-                        const __half hi = __float2half_rn(v);
-                        *dst = hi;
-                        if (TERMS == 2) dst[128] = __float2half_rn(v - __half2float(hi));
-                    }
-                    continue;
-                }
                 const int d = lane * EL + e, ch = d % 128 / 16, w = d % 16 / 4;
                 const int s = DP == 64 ? w : d / 128 * 8 + ch % 2 * 4 + w, t = DP == 64 ? ch : ch / 2;
                 const float v0 = fine ? x[kk][e] * down : 0.f, v1 = fine ? x[kk][e + 1] * down : 0.f;
@@ -462,7 +377,6 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int term = 0; term < TERMS; ++term) qreg[s][t][term] = qf_at(s, t, term);
         float qf[NT][2], m[NT][2], l[NT][2], o[KS][NT][4];
-        float bound[NT][2], sum[NT][4];   // 4 bits: (m + OFF16 + SLACK16) / qf, and l of bf16 rows as the tensor cores sum it
         int hi[NT][2];   // tokens first_seen(hi - 1) .. hi - 1 are seen
         int hi_min = 0x7fffffff, hi_max = -0x7fffffff;
 #pragma unroll
@@ -472,8 +386,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 const int r = t * 8 + 2 * tig + e;
                 qf[t][e] = tl.qf[r];
                 m[t][e] = NO_MAX;
-                l[t][e] = sum[t][e] = sum[t][2 + e] = 0.f;
-                bound[t][e] = -3e38f;
+                l[t][e] = 0.f;
                 hi[t][e] = pos_lo + token_of(min(r, rows - 1)) + 1;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) o[s][t][e] = o[s][t][2 + e] = 0.f;
@@ -490,178 +403,23 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 id1 = id_at(k + BATCH + my_k, t);
                 row1 = row_of(id1, t);
             }
-            if (BITS == 8 && k % BATCH == BATCH / 4) {   // the next batch's scales, well before they are used
+            if (k % BATCH == BATCH / 4) {   // the next batch's scales, well before they are used
                 ks1 = id1 >= 0 ? c.k_scale[(size_t)id1 * H + h] : 0.f;
                 vs1 = id1 >= 0 ? c.v_scale[(size_t)id1 * H + h] : 0.f;
             }
             float ksk[SUB], vsk[SUB];
-            if (BITS == 8)
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 ksk[u] = __shfl_sync(~0u, ks, k % BATCH * SUB + u);
                 vsk[u] = __shfl_sync(~0u, vs, k % BATCH * SUB + u);
             }
-            const uint32_t st = BITS == 4 ? drain : used % Sh::STAGES;
-            alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], BITS == 4 ? turn : (used / Sh::STAGES) & 1, abort_flag, a.status));
+            const uint32_t st = used % Sh::STAGES;
+            alive = __all_sync(~0u, mbar_wait(&tl.full[warp][st], (used / Sh::STAGES) & 1, abort_flag, a.status));
             if (!alive) break;
-            if (BITS == 4) {
-                drain = drain + 1 == Sh::STAGES ? 0 : drain + 1;
-                turn ^= drain == 0;
-            }
             const uint8_t* stage = ring + st * Sh::STAGE;
 
-            constexpr int CH = SUB == 1 ? 2 : 1;         // independent sums per piece (even and odd k steps)
-            // scores of tokens g and g + 8 of each piece, rows 2 tig and 2 tig + 1 of each tile
+            constexpr int CH = 2 / SUB;                  // independent sums per piece (even and odd k steps)
             float sc[SUB][CH][NT][4] = {};
-            if constexpr (BITS == 4) {
-                auto scores4 = [&](int u, int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int term = 0; term < TERMS; ++term) {
-                            const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
-                            mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
-                        }
-                };
-                // a lane's two atoms of a block and their scales (zeros where the head has no such group)
-                auto atoms_at = [&](const uint8_t* codes, const uint8_t* scales, int at, bool there, uint4& w, uint32_t& s16) {
-                    w = make_uint4(0u, 0u, 0u, 0u);
-                    s16 = 0u;
-                    if (FULL || there) {
-                        w = *reinterpret_cast<const uint4*>(codes + at * 8);
-                        s16 = *reinterpret_cast<const uint16_t*>(scales + at);
-                    }
-                };
-                // 64 elements at a time: the lane's atoms of tokens g and g + 8, group tig of the four
-#pragma unroll
-                for (int q = 0; q < DP / 64; ++q)
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        const uint8_t* kb = stage + u * Sh::PART;
-                        const int n = min(4, D / 16 - 4 * q), at = q * 64 + (g * n + tig) * 2;
-                        uint4 w;
-                        uint32_t s16;
-                        atoms_at(kb, kb + 16 * D, at, tig < n, w, s16);
-                        const Scale3 sa = scale_f16(prmt(s16, 0u, 0x4040)), sb = scale_f16(prmt(s16, 0u, 0x4141));
-                        scores4(u, 4 * q, codes_f16<0>(w.x, sa), codes_f16<0>(w.z, sb), codes_f16<1>(w.x, sa), codes_f16<1>(w.z, sb));
-                        scores4(u, 4 * q + 1, codes_f16<2>(w.x, sa), codes_f16<2>(w.z, sb), codes_f16<3>(w.x, sa), codes_f16<3>(w.z, sb));
-                        scores4(u, 4 * q + 2, codes_f16<0>(w.y, sa), codes_f16<0>(w.w, sb), codes_f16<1>(w.y, sa), codes_f16<1>(w.w, sb));
-                        scores4(u, 4 * q + 3, codes_f16<2>(w.y, sa), codes_f16<2>(w.w, sb), codes_f16<3>(w.y, sa), codes_f16<3>(w.w, sb));
-                    }
-                const int t0 = token_at(k);
-                const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
-                bool above = false;
-                float top[NT][2];
-                // the largest score itself, against the bound over the row's factor; then one fused operation
-                // per exponent
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        top[t][e] = -INFINITY;
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u) {
-                            float& x0 = sc[u][0][t][e];
-                            float& x1 = sc[u][0][t][2 + e];
-                            if (CH == 2) x0 += sc[u][CH - 1][t][e], x1 += sc[u][CH - 1][t][2 + e];
-                            if (edge) {
-                                const int at = t0 + u * PIECE + g, from = first_seen(hi[t][e] - 1, a.window);
-                                if (at >= hi[t][e] || at < from) x0 = -INFINITY;
-                                if (at + 8 >= hi[t][e] || at + 8 < from) x1 = -INFINITY;
-                            }
-                            top[t][e] = fmaxf(top[t][e], fmaxf(x0, x1));
-                        }
-                        above |= top[t][e] > bound[t][e];
-                    }
-                if (__any_sync(~0u, above)) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float x = top[t][e];
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-                            x = fmaxf(fmaf(x, qf[t][e], -OFF16), m[t][e]);
-                            const float f = ex2(m[t][e] - x);
-                            m[t][e] = x;
-                            bound[t][e] = (x + (OFF16 + SLACK16)) / qf[t][e];
-                            sum[t][e] *= f;
-                            l[t][e] *= f;
-#pragma unroll
-                            for (int s = 0; s < KS; ++s) {
-                                o[s][t][e] *= f;
-                                o[s][t][2 + e] *= f;
-                            }
-                        }
-                }
-                constexpr uint32_t ONES = 0x3C003C00u;
-#pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    uint32_t p[NT][PTERMS][2];   // weights as the B operand: tokens x rows
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const float w0 = ex2(fmaf(sc[u][0][t][2 * z], qf[t][0], -m[t][0]));
-                            const float w1 = ex2(fmaf(sc[u][0][t][2 * z + 1], qf[t][1], -m[t][1]));
-                            const __half2 y = __floats2half2_rn(w0, w1);
-                            p[t][0][z] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
-                            if (F32) {
-                                const float2 f = __half22float2(y);
-                                const __half2 low = __floats2half2_rn(w0 - f.x, w1 - f.y);
-                                p[t][PTERMS - 1][z] = transpose8(*reinterpret_cast<const uint32_t*>(&low));
-                                l[t][0] += w0;
-                                l[t][1] += w1;
-                            }
-                        }
-                        // bf16 rows: the sum of all tokens' weights, in every row of the result
-                        if (!F32) mma(sum[t], ONES, ONES, ONES, ONES, p[t][0][0], p[t][0][1]);
-                    }
-#pragma unroll
-                    for (int q = 0; q < CB; ++q) {
-                        // atoms of tokens 2 tig and + 1, + 8 and + 9, of the lane's group (DP 64: half a group), as words
-                        // of four elements, token 2 tig in the low half
-                        const uint8_t* vb = stage + u * Sh::PART + 8 * D;
-                        constexpr int W = Sh::ROWB / 32;
-                        const int n = min(8, D / 16 - 8 * q), gr = DP == 64 ? g >> 1 : g;
-                        uint32_t v[2][W];
-                        Scale3 vs[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            uint4 w;
-                            uint32_t s16;
-                            atoms_at(vb, vb + 9 * D, q * 128 + (z * n + gr) * 8 + tig * 2, gr < n, w, s16);
-                            vs[z] = scale_f16(prmt(s16 & 0x7F7Fu, 0u, 0x4140));
-                            const uint32_t lo = DP == 64 && (g & 1) ? w.y : w.x, hi = DP == 64 && (g & 1) ? w.w : w.z;
-                            v[z][0] = prmt(lo, hi, 0x5410), v[z][1] = prmt(lo, hi, 0x7632);
-                            if (W == 4) v[z][W - 2] = prmt(w.y, w.w, 0x5410), v[z][W - 1] = prmt(w.y, w.w, 0x7632);
-                        }
-#pragma unroll
-                        for (int w = 0; w < W; ++w) {
-                            auto values = [&](int z, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    float(&to)[4] = o[q * (KS / CB) + w * 2 + z][t];
-                                    if (!F32) {
-                                        mma(to, a0, a1, a2, a3, p[t][0][0], p[t][0][1]);
-                                        continue;
-                                    }
-                                    // (fp32 rows: the tensor cores sum 16 tokens, as below)
-                                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma(part, a0, a1, a2, a3, p[t][PTERMS - 1][0], p[t][PTERMS - 1][1]);
-                                    mma(part, a0, a1, a2, a3, p[t][0][0], p[t][0][1]);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) to[e] += part[e];
-                                }
-                            };
-                            values(0, codes_f16<0>(v[0][w], vs[0]), codes_f16<1>(v[0][w], vs[0]), codes_f16<0>(v[1][w], vs[1]),
-                                   codes_f16<1>(v[1][w], vs[1]));
-                            values(1, codes_f16<2>(v[0][w], vs[0]), codes_f16<3>(v[0][w], vs[0]), codes_f16<2>(v[1][w], vs[1]),
-                                   codes_f16<3>(v[1][w], vs[1]));
-                        }
-                    }
-                }
-            } else {
             constexpr int J = Sh::ROWB == 128 ? 2 : 1;   // 16-byte chunks of a box row per thread
 #pragma unroll
             for (int q = 0; q < CB; ++q)
@@ -687,11 +445,11 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                                 for (int term = 0; term < TERMS; ++term) {
                                     const uint2 f = QREG ? qreg[s][t][term] : qf_at(s, t, term);
-                                    mma(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
+                                    mma_f16(sc[u][s % CH][t], a0, a1, a2, a3, f.x, f.y);
                                 }
                         }
                     }
-            // scores -> x log2 e
+            // scores -> x log2 e; tokens g and g + 8 of each piece, rows 2 tig and 2 tig + 1 of each tile
             const int t0 = token_at(k);
             const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
             bool above = false;
@@ -809,7 +567,6 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                     }
                 }
             }
-            }
             ++used;
             __syncwarp();
             if (next < count) {
@@ -830,10 +587,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if (BITS == 4 && !F32) l[t][e] = sum[t][e];
-                else
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(~0u, l[t][e], d);
+                for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(~0u, l[t][e], d);
                 if (g == 0) {
                     tl.m[warp][t * 8 + 2 * tig + e] = m[t][e];
                     tl.l[warp][t * 8 + 2 * tig + e] = l[t][e];
@@ -848,7 +603,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 float top = tl.m[0][r];
 #pragma unroll
                 for (int w = 1; w < WARPS; ++w) top = fmaxf(top, tl.m[w][r]);
-                const float f = ex2(m[t][e] - top), fe = BITS == 4 ? f * 16.f : f;   // (even elements are held over 16)
+                const float f = ex2(m[t][e] - top);
                 float* dst = join + (warp * RT + r) * DP;
 #pragma unroll
                 for (int q = 0; q < CB; ++q) {
@@ -858,8 +613,8 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
                     for (int s = 0; s < SB; s += 2) {
                         const int d = q * 128 + g * (2 * SB) + 2 * s;
-                        float4 v = make_float4(o[q * SB + s][t][e] * fe, o[q * SB + s][t][2 + e] * f,
-                                               o[q * SB + s + 1][t][e] * fe, o[q * SB + s + 1][t][2 + e] * f);
+                        float4 v = make_float4(o[q * SB + s][t][e] * f, o[q * SB + s][t][2 + e] * f,
+                                               o[q * SB + s + 1][t][e] * f, o[q * SB + s + 1][t][2 + e] * f);
                         *reinterpret_cast<float4*>(dst + (d ^ (tig << 2))) = v;
                     }
                 }
@@ -882,7 +637,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
             if (whole) {
                 if (r < rows && d < D) {
-                    const float inv = sum == 0.f ? 0.f : (BITS == 4 ? c.v_unit : 1.f) / sum;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     store4<E>(out_of(r) + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             } else {
@@ -920,7 +675,7 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                         sum = fmaf(__ldcg(p + RT * DP + RT + r), f, sum);
                         v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
                     }
-                    const float inv = sum == 0.f ? 0.f : (BITS == 4 ? c.v_unit : 1.f) / sum;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     store4<E>(out_of(r) + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             }
@@ -932,78 +687,51 @@ attend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
 }
 
-template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG = false>
+template <bool F32, int DP, int NT>
 cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    using Sh = Shape<BITS, F32, DP, NT, FULL, LONG>;
+    using Sh = Shape<F32, DP, NT>;
     static_assert(Sh::SLOT <= ATTEND_SLOT, "workspace slot");
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace slots");
     // ranges are cut for OCC CTAs on each SM (of 228 KB, 1 KB of it the system's per CTA)
     static_assert(Sh::OCC * (Sh::SMEM + (int)sizeof(Tail) + 1024) <= 228 * 1024, "resident CTAs");
-    attend_split_kernel<BITS, F32, DP, NT, FULL, LONG>
-        <<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters, ws.zeros);
+    attend_split_kernel<F32, DP, NT><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(ws.k16, ws.v16, a, ws.partial, ws.counters);
     return cudaGetLastError();
 }
 
-template <int BITS, bool F32, int DP, int NT, bool FULL, bool LONG = false>
-cudaError_t allow() {
-    return cudaFuncSetAttribute(attend_split_kernel<BITS, F32, DP, NT, FULL, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Shape<BITS, F32, DP, NT, FULL, LONG>::SMEM);
-}
-template <int BITS, bool F32, int DP, int NT>
+template <bool F32, int DP, int NT>
 cudaError_t init() {
-    constexpr bool LONG = BITS == 4 && !F32 && DP <= 128 && NT == 1;
-    cudaError_t e = allow<BITS, F32, DP, NT, false>();
-    if (BITS == 4 && e == cudaSuccess) e = allow<BITS, F32, DP, NT, BITS == 4>();
-    if (LONG && e == cudaSuccess) e = allow<BITS, F32, DP, NT, false, LONG>();
-    if (LONG && e == cudaSuccess) e = allow<BITS, F32, DP, NT, LONG, LONG>();
-    return e;
-}
-template <int BITS, bool F32>
-cudaError_t init_shapes() {
-    cudaError_t e = cudaSuccess;
-    auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
-    one(init<BITS, F32, 64, 1>()), one(init<BITS, F32, 64, 2>()), one(init<BITS, F32, 128, 1>()), one(init<BITS, F32, 128, 2>());
-    one(init<BITS, F32, 256, 1>()), one(init<BITS, F32, 256, 2>());
-    return e;
+    return cudaFuncSetAttribute(attend_split_kernel<F32, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Shape<F32, DP, NT>::SMEM);
 }
 
 }  // namespace
 
-cudaError_t attend_split_init(int bits) {
-    cudaError_t e = bits == 4 ? init_shapes<4, false>() : init_shapes<8, false>();
-    if (e == cudaSuccess) e = bits == 4 ? init_shapes<4, true>() : init_shapes<8, true>();
+cudaError_t attend_split_init() {
+    cudaError_t e = cudaSuccess;
+    auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
+    one(init<false, 64, 1>()), one(init<false, 64, 2>()), one(init<false, 128, 1>()), one(init<false, 128, 2>());
+    one(init<false, 256, 1>()), one(init<false, 256, 2>());
+    one(init<true, 64, 1>()), one(init<true, 64, 2>()), one(init<true, 128, 1>()), one(init<true, 128, 2>());
+    one(init<true, 256, 1>()), one(init<true, 256, 2>());
     return e;
 }
 
 // Rows per tile: 8, or 16 where a sequence and head has more (past 16 only fp32 rows of more than
 // 128 elements come here, in tiles of 16; the rest are attend_prompt.cu's).
-template <int BITS, bool F32, int DP, bool FULL>
+template <bool F32, int DP>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const long long rows = (long long)a.step.max_new * (a.q_heads / a.pages.heads);
-    if constexpr (BITS == 4 && !F32 && DP <= 128) {
-        // as many tokens as the page tables hold (lengths are not known here): from some 1000 for each CTA
-        // on, ranges are long
-        const long long most = (long long)a.step.n_seqs * a.step.width * a.pages.page * a.pages.heads;
-        if (rows <= 8 && most >= 1024ll * ws.sms * ATTEND_OCC) return launch<BITS, F32, DP, 1, FULL, true>(a, ws, st);
-    }
-    return rows <= 8 ? launch<BITS, F32, DP, 1, FULL>(a, ws, st) : launch<BITS, F32, DP, 2, FULL>(a, ws, st);
-}
-template <int BITS, bool F32, int DP>
-static cudaError_t by_width(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    if (BITS == 4 && a.pages.dim == DP) return by_rows<BITS, F32, DP, BITS == 4>(a, ws, st);
-    return by_rows<BITS, F32, DP, false>(a, ws, st);
+    return rows <= 8 ? launch<F32, DP, 1>(a, ws, st) : launch<F32, DP, 2>(a, ws, st);
 }
 
-template <int BITS, bool F32>
+template <bool F32>
 static cudaError_t by_shape(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const int D = a.pages.dim;
-    return D <= 64 ? by_width<BITS, F32, 64>(a, ws, st)
-                   : D <= 128 ? by_width<BITS, F32, 128>(a, ws, st) : by_width<BITS, F32, 256>(a, ws, st);
+    return D <= 64 ? by_rows<F32, 64>(a, ws, st) : D <= 128 ? by_rows<F32, 128>(a, ws, st) : by_rows<F32, 256>(a, ws, st);
 }
 
 cudaError_t launch_attend_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    if (a.pages.blocks) return bf16 ? by_shape<4, false>(a, ws, st) : by_shape<4, true>(a, ws, st);
-    return bf16 ? by_shape<8, false>(a, ws, st) : by_shape<8, true>(a, ws, st);
+    return bf16 ? by_shape<false>(a, ws, st) : by_shape<true>(a, ws, st);
 }
 
 }  // namespace mlora

@@ -132,14 +132,15 @@ mlora_status make_cache(const CachePages& pages, int q_heads, uint64_t prompt_by
     // the status word, (4 bits) a block of zeros, the join counters: all cleared
     const size_t ctas = (size_t)sms * ATTEND_OCC, front = 256 + (bits == 4 ? block4_bytes(256) : 0);
     const size_t head = front + (ctas * sizeof(int) + 255) / 256 * 256;
-    const size_t split = 2 * ctas * ATTEND_SLOT * sizeof(float), prompt = (size_t)sms * PROMPT_SLOT * sizeof(float);
+    const size_t split = bits == 4 ? sms * attend4_split_bytes(pages.dim) : 2 * ctas * ATTEND_SLOT * sizeof(float);
+    const size_t prompt = (size_t)sms * PROMPT_SLOT * sizeof(float);
     const size_t slots = split > prompt ? split : prompt, table = 65536 * sizeof(int);
     // converted prompt tiles: no more than all pages' tokens (and a tile's rest per page)
     const size_t most = attend_prompt_bytes(c->pages, (long long)pages.n_pages * pages.page + 128);
     const size_t operands = (size_t)prompt_bytes < most ? (size_t)prompt_bytes : most;
     if (e == cudaSuccess) e = cudaMalloc((void**)&c->ws, head + slots + table + operands);
     if (e == cudaSuccess) e = cudaMemset(c->ws, 0, head);
-    if (e == cudaSuccess) e = attend_split_init(bits);
+    if (e == cudaSuccess) e = bits == 4 ? attend4_split_init() : attend_split_init();
     if (e == cudaSuccess) e = attend_prompt_init(bits);
     if (e == cudaSuccess && bits == 8 &&
         !(encode_codes(&c->attend.k16, pages.k_codes, pages) && encode_codes(&c->attend.v16, pages.v_codes, pages)))
@@ -268,8 +269,8 @@ mlora_status mlora_cache_attend(mlora_cache_t c, const void* Q, int64_t q_row, i
     AttendArgs a{c->pages, s, RowsIn{Q, q_row, q_head}, RowsOut{O, o_row, o_head}, c->q_heads, c->page_div,
                  c->group_div, scale, window, (uint32_t*)c->ws};
     const bool bf16 = dtype == MLORA_BF16;
-    CU_TRY(attend_prompt_takes(bf16, a) ? launch_attend_prompt(bf16, a, c->attend, (cudaStream_t)stream)
-                                        : launch_attend_split(bf16, a, c->attend, (cudaStream_t)stream));
+    const auto launch = attend_prompt_takes(bf16, a) ? launch_attend_prompt : c->pages.blocks ? launch_attend4_split : launch_attend_split;
+    CU_TRY(launch(bf16, a, c->attend, (cudaStream_t)stream));
     return MLORA_OK;
 }
 

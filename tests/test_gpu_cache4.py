@@ -1,7 +1,10 @@
 """The 4-bit key/value cache and its attention through the public entry points, against plain
 implementations: blocks byte for byte (the definition's fp32 operations in numpy), attention in
 64 bits.  The tolerances are test_gpu_cache.py's, whose derivation holds here: a code times its
-scale is exact in the products' operands, so that weights, sums and the output are what rounds."""
+scale is exact in the products' operands, so that weights, sums and the output are what rounds.
+One term more: up to 16 rows a sequence and key head, weights are fp16 numbers of which a row's
+largest is 2^12 or more, so that each is also off by up to 2^-25: 2^-37 of the weights' sum.  It
+shows where a token holds a zero, as one in 15 codes is, and nearly all of the weight."""
 import numpy as np
 import pytest
 
@@ -12,7 +15,7 @@ if not torch.cuda.is_available():   # pragma: no cover - CPU machine
     pytest.skip("needs a GPU", allow_module_level=True)
 
 from heterogeneous_lora_gemm_gb300 import Cache4, mlora  # noqa: E402
-from test_gpu_cache import (APPENDS, ATTENDS, F, TDT, as_np, check_attend, offsets_of, plain_attend,  # noqa: E402
+from test_gpu_cache import (APPENDS, ATTENDS, F, TDT, as_np, offsets_of, plain_attend,  # noqa: E402
                             strided, tolerance)
 
 # e4m3 without its sign: bytes 0 .. 126
@@ -54,14 +57,14 @@ def pack(blocks, keys, codes, scales):
 class Setup4:
     """Blocks with random codes and scales in their tokens, random bytes everywhere else, shuffled page tables."""
 
-    def __init__(self, lengths, H, D, ps, Hq=None, seed=0, spare=3, k_unit=0.05, v_unit=0.02, scales=None, room=256 << 20, width=1):
+    def __init__(self, lengths, H, D, ps, Hq=None, seed=0, spare=3, k_unit=0.05, v_unit=0.02, scales=None, room=256 << 20):
         rng = np.random.default_rng(seed)
         self.lengths, self.H, self.D, self.ps, self.Hq = list(lengths), H, D, ps, Hq or H
         self.units, self.room = (k_unit, v_unit), room
         used = [-(-max(n, 0) // ps) for n in lengths]
         self.n_pages = sum(used) + spare
         order = rng.permutation(self.n_pages)
-        self.width = max([width] + used)      # (entries past the sequences' blocks are never read)
+        self.width = max([1] + used)
         self.table = np.full((len(lengths), self.width), -7, np.int32)   # unused entries are never read
         at = 0
         for b, u in enumerate(used):
@@ -223,6 +226,28 @@ def test_read_restores_values(rows, lengths, H, D, ps, dtype):
 
 
 # ---- attend ---------------------------------------------------------------- #
+def check_attend(u, rows, dtype, window=0, q_size=1.0, scale=None, q=None):
+    T = sum(rows)
+    if q is None:
+        q = (np.random.default_rng(11).standard_normal((T, u.Hq, u.D)) * q_size).astype(F)
+    Q = strided(q, dtype, 3)
+    wide = torch.full((T, u.Hq + 1, u.D), 5.0, dtype=TDT[dtype], device="cuda")
+    off = None if rows and set(rows) == {1} else offsets_of(rows)
+    u.cache.attend(Q, wide[:, :u.Hq], u.len, u.pages, offsets=off, max_new=max(rows), scale=scale, window=window)
+    got = as_np(wide[:, :u.Hq]).astype(np.float64)
+    o, A, S = plain_attend(u, as_np(Q), rows, u.D ** -0.5 if scale is None else scale, window)
+    low = np.zeros((T, 1, 1))
+    at = np.concatenate([[0], np.cumsum(rows)])
+    for b, n in enumerate(u.lengths):
+        if n > 0:
+            low[at[b]:at[b + 1]] = 2.0 ** -37 * n * np.abs(u.values(False, None, b)).max()
+    bad = ~(np.abs(got - o) <= tolerance(o, A, S, dtype) + low)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off, worst {np.abs(got - o)[bad].max()}, first {np.argwhere(bad)[0]}"
+    assert torch.all(wide[:, u.Hq] == 5.0)
+    assert u.cache.status() == mlora.MLORA_OK
+    return wide[:, :u.Hq]
+
+
 @pytest.mark.parametrize("G", [1, 12, 20])
 @pytest.mark.parametrize("D", [16, 64, 128, 256])
 def test_every_scale_and_code_is_exact(D, G):
@@ -252,14 +277,6 @@ def test_attend_matches_64_bits(rows, lengths, H, G, D, ps, window, dtype):
     check_attend(Setup4(lengths, H, D, ps, Hq=H * G, seed=9), rows, dtype, window)
 
 
-@pytest.mark.parametrize("rows,lengths,H,G,D,ps,window", [case for case in ATTENDS if max(case[0]) * case[3] <= 8] + [
-    ([1, 1], [70, 300], 2, 4, 48, 32, 0), ([1], [9000], 1, 8, 64, 16, 0), ([2, 1], [9000, 170], 1, 4, 128, 48, 700)])
-def test_attend_under_page_tables_for_long_sequences(rows, lengths, H, G, D, ps, window):
-    """Tables of over a thousand tokens per CTA, whatever of them the sequences use."""
-    width = 500000 // (len(lengths) * H * ps) + 1
-    check_attend(Setup4(lengths, H, D, ps, Hq=H * G, seed=9, width=width), rows, "bf16", window)
-
-
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,lengths,D", [([1, 1], [777, 130], 128), ([140], [333], 128), ([3], [90], 256), ([40], [90], 64)])
 @pytest.mark.parametrize("q_size,k_unit,v_unit", [(30.0, 0.05, 1.0), (1e-4, 0.05, 2.0 ** 60), (1e6, 1e-7, 2.0 ** -60),
@@ -268,6 +285,16 @@ def test_attend_over_units_and_sizes_of_queries(rows, lengths, D, q_size, k_unit
     """Peaked and flat softmax; queries outside fp16's range; the units' limits."""
     u = Setup4(lengths, 2, D, 64, Hq=4, seed=10, k_unit=k_unit, v_unit=v_unit)
     check_attend(u, rows, dtype, q_size=q_size)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,lengths,D", [([1, 1], [300, 64], 128), ([131, 30], [200, 30], 128), ([3], [90], 64), ([9], [90], 256)])
+def test_the_largest_queries(rows, lengths, D, dtype):
+    """Rows up to 2^128 beside rows of 2^100, and a scale that brings the scores of the first to some tens."""
+    u = Setup4(lengths, 1, D, 64, Hq=2, seed=58, k_unit=2.0 ** -60, scales=lambda shape: np.random.default_rng(1).integers(1, 12, shape))
+    q = np.random.default_rng(59).uniform(-2.0 ** 100, 2.0 ** 100, (sum(rows), 2, D))
+    q[::2] *= 2.0 ** 27.5
+    check_attend(u, rows, dtype, q=q.astype(F), scale=2.0 ** -59)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -372,17 +399,13 @@ WINDOWS = [(rows, lengths, 1, G, 64, 16, w)
            for w in (1, 2, 16, 17, 63, 64, 65)]
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32", "bf16, long tables"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,lengths,H,G,D,ps,window", ATTENDS + PARTS + AHEAD + WINDOWS)
 def test_every_token_counts_once(rows, lengths, H, G, D, ps, window, dtype):
     """All scores are equal, and token t's value is 7 scales in element t mod D and 0 elsewhere: an output
     is a count of tokens over another (test_gpu_cache_tokens.py has the tolerance's derivation; the
     weights are 2^0 here)."""
-    if "long" in dtype and max(rows) * G > 8:
-        pytest.skip("one form")
-    u = Setup4(lengths, H, D, ps, Hq=H * G, seed=60, v_unit=1.0,
-               width=500000 // (len(lengths) * H * ps) + 1 if "long" in dtype else 1)
-    dtype = dtype.split(",")[0]
+    u = Setup4(lengths, H, D, ps, Hq=H * G, seed=60, v_unit=1.0)
     kc, ks, vc, vs = u.held(lambda s: np.zeros(s, np.int8), lambda s: np.full(s, 56))       # scales of 1
     for t, n in zip(u.table, lengths):
         at = np.arange(max(n, 0))
