@@ -21,7 +21,7 @@
 // rows are fp32) and writes an item that is its own from registers.
 // Work split: all (sequence, row tile, head) items' chunks in one line, cut into equal ranges, one
 // per resident warp; every CTA finds its warps' ranges from the lengths.  An item is as long as its
-// chunks plus what its start costs (LEAD).  An item cut between warps is joined at their CTA's end,
+// chunks plus what its start costs.  An item cut between warps is joined at their CTA's end,
 // one cut between CTAs then by the CTA that gets there last; either in range order, so that results do
 // not depend on timing.
 #include <cuda_fp16.h>
@@ -39,14 +39,12 @@ namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int PIECE = 16;                 // tokens of a block and of a product
-constexpr int LEAD = 2;                   // chunks that starting an item costs
-constexpr int MIN_UNITS = LEAD + 1;       // a warp's range is at least so long
 // m is the largest x less OFF when it is set, and moves when x > m + OFF + SLACK: weights stay below
 // 2^15, within fp16, and their 11 bits reach down to 2^-26 of the largest
 constexpr float OFF = 12.f, SLACK = 3.f;
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
-template <bool F32, int DP, int NT>
+template <bool F32, int DP, int NT, bool LONG>
 struct Shape {
     static constexpr int TERMS = F32 ? 2 : 1;          // of a query and of a weight
     static constexpr int KS = DP / 16;                 // k steps of q . k = 16-row tiles of O^T
@@ -55,8 +53,10 @@ struct Shape {
     static constexpr int W = DP == 64 ? 2 : 4;         // words of four elements per lane and unit
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
-    // pieces that a warp takes at a time: waits, votes and issues are per chunk
-    static constexpr int SUB = DP == 256 ? 1 : OCC == 3 ? 4 : 2;
+    // pieces that a warp takes at a time: waits, votes and issues are per chunk.  (32 sequences of 32k tokens
+    // 210 us with four, 226 us with two; one sequence of 777 tokens 13.4 and 10.4 us)
+    static constexpr int SUB = DP == 256 ? 1 : LONG ? 4 : 2;
+    static_assert(!LONG || OCC == 3, "long ranges");
     static constexpr int CHUNK_T = PIECE * SUB;
     static constexpr int PART = 18 * DP;               // bytes of a piece
     static constexpr int STAGE = SUB * PART;
@@ -71,18 +71,24 @@ struct Shape {
     static constexpr int SLOT = RT * (DP + 2);         // floats of a partial result: O, then m, l per row
 };
 
-// A sequence's share of the work line: tiles x heads items, each LEAD + units long (1 where the
+// How the line is cut: what starting an item costs, in chunks, and the least length of a range.
+struct Cut {
+    int lead, least;
+};
+// A sequence's share of the work line: tiles x heads items, each lead + units long (1 where the
 // rows see nothing: zeros are written).
 struct Line {
     SeqRec s;
     int c0;           // first chunk that its rows see
     int tiles, units; // row tiles, chunks per item
-    __device__ int length() const { return units ? LEAD + units : 1; }
+    int lead;
+    __device__ int length() const { return units ? lead + units : 1; }
     __device__ long long total(int heads) const { return (long long)tiles * heads * length(); }
 };
 template <int RT, int CHUNK_T>
-__device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
+__device__ __forceinline__ Line line_of(const AttendArgs& a, const Cut& cut, int G, int b) {
     Line n;
+    n.lead = cut.lead;
     n.s = load_seq(a.step, a.pages.page, b, a.status);
     const int last = n.s.start + n.s.rows - 1;   // position of the last processed row
     n.c0 = first_seen(n.s.start, a.window) / CHUNK_T;
@@ -136,10 +142,10 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 
 // `zeros`: a block of zeros, in the place of one that cannot be read.  FULL: heads of DP elements, so
 // that a block's offsets are constants.
-template <bool F32, int DP, int NT, bool FULL>
-__global__ void __launch_bounds__(THREADS, (Shape<F32, DP, NT>::OCC))
-attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
-    using Sh = Shape<F32, DP, NT>;
+template <bool F32, int DP, int NT, bool LONG, bool FULL>
+__global__ void __launch_bounds__(THREADS, (Shape<F32, DP, NT, LONG>::OCC))
+attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
+    using Sh = Shape<F32, DP, NT, LONG>;
     using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int KS = Sh::KS, RT = Sh::RT, SUB = Sh::SUB, CHUNK_T = Sh::CHUNK_T, TERMS = Sh::TERMS, CB = Sh::CB, W = Sh::W;
     extern __shared__ __align__(128) uint8_t smem4[];
@@ -159,7 +165,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
     const int per = (a.step.n_seqs + THREADS - 1) / THREADS;
     const int b_lo = min(tid * per, a.step.n_seqs), b_hi = min(b_lo + per, a.step.n_seqs);
     long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += line_of<RT, CHUNK_T>(a, G, b).total(H);
+    for (int b = b_lo; b < b_hi; ++b) mine += line_of<RT, CHUNK_T>(a, cut, G, b).total(H);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -176,7 +182,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
     }
     before += incl - mine;
     const int all = gridDim.x * WARPS;
-    const int workers = total >= (long long)MIN_UNITS * all ? all : (int)((total + MIN_UNITS - 1) / MIN_UNITS);
+    const int workers = total >= (long long)cut.least * all ? all : (int)((total + cut.least - 1) / cut.least);
     const int cta = blockIdx.x, worker = cta * WARPS + warp;
     if (cta * WARPS >= workers) return;
     // ranges: the first `over` of them one longer than the others
@@ -184,8 +190,8 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
     const int over = (int)(total - each * workers);
     auto range_at = [&](int i) { return each * i + min(i, over); };
     auto worker_of = [&](long long u) {   // the one whose range holds position u
-        const long long cut = (each + 1) * over, v = u < cut ? u : u - cut, w = u < cut ? each + 1 : each;
-        return (u < cut ? 0 : over) + (int)(total >> 31 ? v / w : (uint32_t)v / (uint32_t)w);
+        const long long mark = (each + 1) * over, v = u < mark ? u : u - mark, w = u < mark ? each + 1 : each;
+        return (u < mark ? 0 : over) + (int)(total >> 31 ? v / w : (uint32_t)v / (uint32_t)w);
     };
 #pragma unroll 1
     for (int w = 0; w < WARPS; ++w) {   // where each of the CTA's ranges begins
@@ -195,7 +201,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
         long long p = before;
         int b = b_lo;
         for (; per > 1 && b < b_hi - 1; ++b) {
-            const long long length = line_of<RT, CHUNK_T>(a, G, b).total(H);
+            const long long length = line_of<RT, CHUNK_T>(a, cut, G, b).total(H);
             if (from < p + length) break;
             p += length;
         }
@@ -208,7 +214,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
     const long long end = works ? range_at(worker + 1) : 0;
     int b = works ? tl.first_b[warp] : 0;
     long long b_at = works ? tl.first_at[warp] : 0;   // where sequence b begins on the line
-    Line n = line_of<RT, CHUNK_T>(a, G, b);
+    Line n = line_of<RT, CHUNK_T>(a, cut, G, b);
     int parts = 0;
 
     uint8_t* ring = smem + warp * Sh::OWN;
@@ -221,7 +227,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
     while (at < end) {
         while (at >= b_at + n.total(H)) {
             b_at += n.total(H);
-            n = line_of<RT, CHUNK_T>(a, G, ++b);
+            n = line_of<RT, CHUNK_T>(a, cut, G, ++b);
         }
         const long long into = at - b_at;
         const int item = (int)(into >> 31 ? into / n.length() : (uint32_t)into / (uint32_t)n.length());
@@ -243,7 +249,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
             at = item_at + 1;
             continue;
         }
-        const int u0 = (int)max(at - item_at - LEAD, 0ll), u1 = (int)(min((long long)n.length(), end - item_at) - LEAD);
+        const int u0 = (int)max(at - item_at - cut.lead, 0ll), u1 = (int)(min((long long)n.length(), end - item_at) - cut.lead);
         at = item_at + n.length();
         if (u1 <= u0) break;   // only the lead is in this range: the item is the next warp's
         // positions that the tile's rows may see: row r at start + i0 + token_of(r)
@@ -666,7 +672,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
         while (tl.order[i + k] >= 0 && part(i + k).item_at == p.item_at) ++k;
         auto warp_slot = [&](int z) { return part(i + z).slot; };
         // the item's CTAs first .. last
-        const int first = worker_of(p.item_at + LEAD) / WARPS, last = worker_of(p.item_at + p.length - 1) / WARPS;
+        const int first = worker_of(p.item_at + cut.lead) / WARPS, last = worker_of(p.item_at + p.length - 1) / WARPS;
         if (first == last) join(p, k, warp_slot, nullptr);
         else {
             auto cta_slot = [&](int z) { return partial + (size_t)(all + 2 * (first + z) + (z == 0 ? 1 : 0)) * Sh::SLOT; };
@@ -686,26 +692,30 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
     }
 }
 
-template <bool F32, int DP, int NT, bool FULL>
-cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
-    using Sh = Shape<F32, DP, NT>;
+template <bool F32, int DP, int NT, bool LONG, bool FULL>
+cudaError_t launch(const AttendArgs& a, const Cut& cut, const AttendWs& ws, cudaStream_t st) {
+    using Sh = Shape<F32, DP, NT, LONG>;
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace counters");
     static_assert(sizeof(Tail) <= 1024 && Sh::OCC * (Sh::SMEM + 1024 + 1024) <= 228 * 1024, "resident CTAs");
-    attend4_split_kernel<F32, DP, NT, FULL><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(a, ws.partial, ws.counters, ws.zeros);
+    attend4_split_kernel<F32, DP, NT, LONG, FULL><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(a, cut, ws.partial, ws.counters, ws.zeros);
     return cudaGetLastError();
 }
 
-template <bool F32, int DP, int NT>
+template <bool F32, int DP, int NT, bool LONG = false>
 cudaError_t allow() {
-    cudaError_t e = cudaFuncSetAttribute(attend4_split_kernel<F32, DP, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<F32, DP, NT>::SMEM);
+    constexpr int bytes = Shape<F32, DP, NT, LONG>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(attend4_split_kernel<F32, DP, NT, LONG, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attend4_split_kernel<F32, DP, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<F32, DP, NT>::SMEM);
+        e = cudaFuncSetAttribute(attend4_split_kernel<F32, DP, NT, LONG, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     return e;
 }
-template <bool F32, int DP>
-size_t slot_bytes() {
-    const size_t one = (size_t)Shape<F32, DP, 1>::OCC * Shape<F32, DP, 1>::SLOT, two = (size_t)Shape<F32, DP, 2>::OCC * Shape<F32, DP, 2>::SLOT;
-    return (WARPS + 2) * sizeof(float) * (one > two ? one : two);   // one per warp, two per CTA
+template <int DP, int NT>
+constexpr size_t slot_bytes() {   // one per warp, two per CTA (fp32 rows need no more)
+    return (size_t)(WARPS + 2) * sizeof(float) * Shape<false, DP, NT, false>::OCC * Shape<false, DP, NT, false>::SLOT;
+}
+template <int DP>
+constexpr size_t most_bytes() {
+    return slot_bytes<DP, 1>() > slot_bytes<DP, 2>() ? slot_bytes<DP, 1>() : slot_bytes<DP, 2>();
 }
 
 }  // namespace
@@ -714,29 +724,39 @@ cudaError_t attend4_split_init() {
     cudaError_t e = cudaSuccess;
     auto one = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
     one(allow<false, 64, 1>()), one(allow<false, 64, 2>()), one(allow<false, 128, 1>()), one(allow<false, 128, 2>());
+    one(allow<false, 64, 1, true>()), one(allow<false, 128, 1, true>());
     one(allow<false, 256, 1>()), one(allow<false, 256, 2>());
     one(allow<true, 64, 1>()), one(allow<true, 64, 2>()), one(allow<true, 128, 1>()), one(allow<true, 128, 2>());
     one(allow<true, 256, 1>()), one(allow<true, 256, 2>());
     return e;
 }
 
-size_t attend4_split_bytes(int dim) {   // (fp32 rows need no more)
-    return dim <= 64 ? slot_bytes<false, 64>() : dim <= 128 ? slot_bytes<false, 128>() : slot_bytes<false, 256>();
-}
+size_t attend4_split_bytes(int dim) { return dim <= 64 ? most_bytes<64>() : dim <= 128 ? most_bytes<128>() : most_bytes<256>(); }
 
 // Rows per tile: 8, or 16 where a sequence and head has more (past 16 only fp32 rows of more than
 // 128 elements come here, in tiles of 16; the rest are attend_prompt.cu's).
-template <bool F32, int DP>
+template <bool F32, int DP, bool FULL>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const bool few = (long long)a.step.max_new * (a.q_heads / a.pages.heads) <= 8;
-    if (a.pages.dim == DP) return few ? launch<F32, DP, 1, true>(a, ws, st) : launch<F32, DP, 2, true>(a, ws, st);
-    return few ? launch<F32, DP, 1, false>(a, ws, st) : launch<F32, DP, 2, false>(a, ws, st);
+    // By the tokens that the page tables hold (lengths are not known here), from 128 for each of 12 warps
+    // per SM on, the fewest and longest ranges; below, ranges down to one chunk: 8 x 2000 tokens of 8 key heads
+    // 17 us and 15.6 us so, one sequence of 32000 22.3 us and 23.7 us.
+    const long long most = (long long)a.step.n_seqs * a.step.width * a.pages.page * a.pages.heads;
+    const bool lots = most >= 128ll * 12 * ws.sms;
+    const Cut cut = lots ? Cut{2, 3} : Cut{1, 1};
+    if constexpr (!F32 && DP <= 128)
+        if (few && lots) return launch<F32, DP, 1, true, FULL>(a, cut, ws, st);
+    return few ? launch<F32, DP, 1, false, FULL>(a, cut, ws, st) : launch<F32, DP, 2, false, FULL>(a, cut, ws, st);
+}
+template <bool F32, int DP>
+static cudaError_t by_width(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
+    return a.pages.dim == DP ? by_rows<F32, DP, true>(a, ws, st) : by_rows<F32, DP, false>(a, ws, st);
 }
 
 template <bool F32>
 static cudaError_t by_shape(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const int D = a.pages.dim;
-    return D <= 64 ? by_rows<F32, 64>(a, ws, st) : D <= 128 ? by_rows<F32, 128>(a, ws, st) : by_rows<F32, 256>(a, ws, st);
+    return D <= 64 ? by_width<F32, 64>(a, ws, st) : D <= 128 ? by_width<F32, 128>(a, ws, st) : by_width<F32, 256>(a, ws, st);
 }
 
 cudaError_t launch_attend4_split(bool bf16, const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {

@@ -57,14 +57,14 @@ def pack(blocks, keys, codes, scales):
 class Setup4:
     """Blocks with random codes and scales in their tokens, random bytes everywhere else, shuffled page tables."""
 
-    def __init__(self, lengths, H, D, ps, Hq=None, seed=0, spare=3, k_unit=0.05, v_unit=0.02, scales=None, room=256 << 20):
+    def __init__(self, lengths, H, D, ps, Hq=None, seed=0, spare=3, k_unit=0.05, v_unit=0.02, scales=None, room=256 << 20, width=1):
         rng = np.random.default_rng(seed)
         self.lengths, self.H, self.D, self.ps, self.Hq = list(lengths), H, D, ps, Hq or H
         self.units, self.room = (k_unit, v_unit), room
         used = [-(-max(n, 0) // ps) for n in lengths]
         self.n_pages = sum(used) + spare
         order = rng.permutation(self.n_pages)
-        self.width = max([1] + used)
+        self.width = max([width] + used)      # (entries past the sequences' blocks are never read)
         self.table = np.full((len(lengths), self.width), -7, np.int32)   # unused entries are never read
         at = 0
         for b, u in enumerate(used):
@@ -277,6 +277,20 @@ def test_attend_matches_64_bits(rows, lengths, H, G, D, ps, window, dtype):
     check_attend(Setup4(lengths, H, D, ps, Hq=H * G, seed=9), rows, dtype, window)
 
 
+def long_table(lengths, H, ps):
+    """Columns of a page table of so many tokens that ranges are cut as for long sequences."""
+    return 300000 // (len(lengths) * H * ps) + 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,window", [case for case in ATTENDS if max(case[0]) * case[3] <= 16] + [
+    ([1, 1], [70, 300], 2, 4, 48, 32, 0), ([1], [9000], 1, 8, 64, 16, 0), ([2, 1], [9000, 170], 1, 4, 128, 48, 700),
+    ([1] * 600, [40] * 600, 4, 1, 64, 16, 0)])
+def test_attend_under_page_tables_for_long_sequences(rows, lengths, H, G, D, ps, window, dtype):
+    """Whatever of the tables the sequences use."""
+    check_attend(Setup4(lengths, H, D, ps, Hq=H * G, seed=9, width=long_table(lengths, H, ps)), rows, dtype, window)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,lengths,D", [([1, 1], [777, 130], 128), ([140], [333], 128), ([3], [90], 256), ([40], [90], 64)])
 @pytest.mark.parametrize("q_size,k_unit,v_unit", [(30.0, 0.05, 1.0), (1e-4, 0.05, 2.0 ** 60), (1e6, 1e-7, 2.0 ** -60),
@@ -400,12 +414,13 @@ WINDOWS = [(rows, lengths, 1, G, 64, 16, w)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,lengths,H,G,D,ps,window", ATTENDS + PARTS + AHEAD + WINDOWS)
-def test_every_token_counts_once(rows, lengths, H, G, D, ps, window, dtype):
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,window,table", [case + (z,) for case in ATTENDS + PARTS + AHEAD + WINDOWS for z in (
+    ("short", "long") if max(case[0]) * case[3] <= 16 else ("short",))])
+def test_every_token_counts_once(rows, lengths, H, G, D, ps, window, table, dtype):
     """All scores are equal, and token t's value is 7 scales in element t mod D and 0 elsewhere: an output
     is a count of tokens over another (test_gpu_cache_tokens.py has the tolerance's derivation; the
     weights are 2^0 here)."""
-    u = Setup4(lengths, H, D, ps, Hq=H * G, seed=60, v_unit=1.0)
+    u = Setup4(lengths, H, D, ps, Hq=H * G, seed=60, v_unit=1.0, width=long_table(lengths, H, ps) if table == "long" else 1)
     kc, ks, vc, vs = u.held(lambda s: np.zeros(s, np.int8), lambda s: np.full(s, 56))       # scales of 1
     for t, n in zip(u.table, lengths):
         at = np.arange(max(n, 0))
