@@ -144,8 +144,8 @@ __device__ __forceinline__ int sequence_of(const CacheStep& s, int row, int lane
     return min(lo, s.n_seqs - 1);
 }
 
-// LANES: of a head (its 16-element slots, rounded up to a power of two)
-template <typename T, int LANES, bool INTERLEAVED>
+// LANES: of a head (its 16-element slots, rounded up to a power of two).  ALL: every element turns.
+template <typename T, int LANES, bool INTERLEAVED, bool ALL>
 __global__ void __launch_bounds__(THREADS, CTAS<T>) rotary_kernel(const RotaryArgs a) {
     constexpr int HEADS = 32 / LANES;   // at a time
     __shared__ float2 turn[WARPS][128];
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<T>) rotary_kernel(const RotaryAr
     const int row = blockIdx.x * WARPS + warp;
     if (row >= a.step.T) return;
     const int sub = lane / LANES, slot = lane % LANES;
-    const bool mine = slot * 16 < a.dim, turns = slot * 16 < a.turned;
+    const bool mine = slot * 16 < a.dim, turns = ALL || slot * 16 < a.turned;
     // the slot's runs of 16 bytes, such that those of a head's slots lie side by side: of the elements that
     // turn, or of the others; the second half of the runs are the first half's partners
     using Row = Raw<T>;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<T>) rotary_kernel(const RotaryAr
 #pragma unroll
             for (int e = 0; e < 8; ++e) {   // of the lane's pairs
                 const int i = INTERLEAVED ? 2 * e : e, p = at[i / Row::VEC] + i % Row::VEC;
-                v[e] = turns ? turn[warp][INTERLEAVED ? p / 2 : p] : make_float2(1.f, 0.f);
+                v[e] = turns && (!ALL || mine) ? turn[warp][INTERLEAVED ? p / 2 : p] : make_float2(1.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<T>) rotary_kernel(const RotaryAr
             for (int i = 0; i < 8; ++i) {
                 uint64_t y = mul2(x[i], k0[i]);
                 if (turns) y = fma2(INTERLEAVED ? swapped(x[i]) : x[i ^ 4], k1[i], y);
-                out.put(i, weight ? mul2(y, pair(inv, inv)) : y);
+                out.put(i, mul2(y, pair(inv, inv)));   // (exact where there is no norm)
             }
             if (there(g)) out.store(dst, at);
             dst += HEADS * dst_head;
@@ -288,8 +288,10 @@ cudaError_t launch(RotaryArgs a, bool interleaved, int sms, cudaStream_t st) {
     a.per = groups < 1 ? 1 : groups > MOST ? MOST : (int)groups;
     a.per = (all + (all + a.per - 1) / a.per - 1) / ((all + a.per - 1) / a.per);   // (as equal as they can be)
     const dim3 grid((unsigned)(((long long)a.step.T + WARPS - 1) / WARPS), (all + a.per - 1) / a.per);
-    if (interleaved) rotary_kernel<T, LANES, true><<<grid, THREADS, 0, st>>>(a);
-    else rotary_kernel<T, LANES, false><<<grid, THREADS, 0, st>>>(a);
+    const bool whole = a.turned == a.dim;
+    const auto kernel = interleaved ? (whole ? rotary_kernel<T, LANES, true, true> : rotary_kernel<T, LANES, true, false>)
+                                    : (whole ? rotary_kernel<T, LANES, false, true> : rotary_kernel<T, LANES, false, false>);
+    kernel<<<grid, THREADS, 0, st>>>(a);
     return cudaGetLastError();
 }
 
