@@ -51,7 +51,8 @@
 //
 // The 4-bit cache (BITS 4, block4.cuh): a code times its scale is exact in bf16, so that the operand
 // tiles hold the values themselves, over a unit that goes into the scores' factor (on the host) and
-// into the output; tokens have no scales left.
+// into the output; tokens have no scales left (8192 tokens 358 us, 382 us over 8 bits; 4 prompts of
+// 6000 rows after 1024 134 and 140 us).
 //
 // Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
 // operand tiles or 8-15 read codes and convert them into keys and values in bf16 (tokens as rows; the

@@ -7,9 +7,15 @@
 // integers, is the angle modulo a turn with no loss at any position; its nearest quarter turn is
 // taken off before it becomes a float.
 //
-// A warp takes a row and some heads of its queries or of its keys.  A lane takes 16 elements of a head,
-// eight pairs, whose sines and cosines the warp computes once for all its heads; 16 lanes at most
-// share a head and its sum of squares.
+// A warp takes a row and some heads of its queries and keys.  A lane takes 16 elements of a head, in
+// runs of 16 bytes that lie side by side with its neighbours'; sines and cosines are computed once for
+// all the warp's heads and go, with the weights, into factors that the lane keeps: x' = x k0 + o k1, o
+// being x's partner.  16 lanes at most share a head and its sum of squares.  Arithmetic is in pairs.
+//
+// Bound: HBM, each element read and written once: 29.6k rows of 32/8 heads of 128 in bf16 take 105 us,
+// 5.8 TB/s (a plain copy of as many bytes 89 us), in fp32 178 us, 6.8 TB/s; 4000 rows of 15 heads of
+// 80 in fp32 11.5 us and 8 rows 2.9 us, a launch and the chain of offsets, length and sines.  What
+// measured slower: two groups of heads on their way (117 us), rows without the factors (120 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

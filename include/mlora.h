@@ -478,7 +478,8 @@ typedef struct mlora_cache* mlora_cache_t;
  *              per key head (of 128 where head_dim > 128 or the rows are fp32).  Shorter ones,
  *              and all others, are converted again for every tile (0: always)
  * The handle allocates its workspace (a status word, the partial results of split
- * sequences, about 20 MB, and prompt_bytes) here; append, read and attend allocate nothing.
+ * sequences, about 20 MB, 30 MB in 4 bits where head_dim > 128, and prompt_bytes) here; append,
+ * read and attend allocate nothing.
  * One handle serves all layers of a model where their pages lie in one array (a page table
  * per layer names them): the workspace is then there once, as one layer's step uses it at a time.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes; n_pages * kv_heads * page_size >= 2^31),
@@ -536,7 +537,8 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * scales under 2^-96 lose low bits, under 2^-120 they may count as 0; 4-bit sums hold values over
  * their unit, which the output takes at the end); O is rounded once.  Weights are held in 24 bits for fp32 rows and in 16 for bf16 rows, in 8 where
  * max_new * q_heads / kv_heads > 16; in that form sums of one sign come out 0.25% low over
- * 2^20 tokens, and lower over more.  O must not overlap Q: fp32 rows of it may hold sums
+ * 2^20 tokens, and lower over more.  In 4 bits, up to 16 such rows (or heads of more than 128 elements of
+ * fp32 rows), weights have 22 and 11 bits, fewer from 2^-26 of the row's largest down, and none under 2^-37 of it.  O must not overlap Q: fp32 rows of it may hold sums
  * during the call.
  * Errors: INVALID_ARG, UNSUPPORTED (with max_new taken as T where it is larger: max_new *
  * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34; in 4 bits, scale * k_unit outside [2^-120, 3e38)), CUDA.
