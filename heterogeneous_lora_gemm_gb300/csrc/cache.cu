@@ -2,11 +2,9 @@
 // workspace, and launches.  Host side only; the caller owns the pages.
 #include <cuda_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <new>
 
-#include "../../include/mlora.h"
+#include "abi.h"
 #include "attend.h"
 #include "block4.cuh"
 #include "tc.h"
@@ -24,45 +22,11 @@ struct mlora_cache {
 
 namespace {
 
-mlora_status fail(mlora_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
-
-mlora_status cuda_fail(cudaError_t e, const char* what) {
-    cudaGetLastError();   // reported here: not the next launch's error
-    return fail(MLORA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
 #define CU_TRY(expr)                                              \
     do {                                                          \
         cudaError_t e_ = (expr);                                  \
         if (e_ != cudaSuccess) return cuda_fail(e_, #expr);       \
     } while (0)
-
-// Makes the cache's device current for the scope of one call and restores the caller's.
-struct DeviceGuard {
-    int prev = -1;
-    bool moved = false;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceGuard(int dev) {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            moved = err == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (moved) cudaSetDevice(prev);
-    }
-};
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // The arguments that append, read and attend share.  `run` is false where the call has
 // nothing to do (no rows or no sequences).
@@ -82,15 +46,6 @@ mlora_status check_step(mlora_cache_t c, mlora_dtype dtype, int T, const int32_t
     if (!*run) return MLORA_OK;
     if (!lengths || (!pages && width > 0)) return fail(MLORA_ERR_INVALID_ARG, "lengths/pages is NULL");
     *step = CacheStep{offsets, lengths, pages, n_seqs, width, T, max_new < T ? max_new : T};
-    return MLORA_OK;
-}
-
-mlora_status check_rows(const char* name, const void* p, int64_t row, int64_t head, mlora_dtype dtype) {
-    const int64_t unit = dtype == MLORA_BF16 ? 8 : 4;   // elements per 16 bytes
-    if (!p) return fail(MLORA_ERR_INVALID_ARG, "%s is NULL", name);
-    if (!aligned16(p) || row % unit || head % unit || row < 0 || head < 0)
-        return fail(MLORA_ERR_INVALID_ARG, "%s: 16-byte alignment (strides %lld, %lld elements)", name, (long long)row,
-                    (long long)head);
     return MLORA_OK;
 }
 

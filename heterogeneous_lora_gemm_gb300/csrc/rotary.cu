@@ -20,12 +20,10 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <new>
 #include <type_traits>
 
-#include "../../include/mlora.h"
+#include "abi.h"
 #include "cache.h"
 
 using namespace mlora;
@@ -309,47 +307,6 @@ cudaError_t launch_by_dim(const RotaryArgs& a, bool interleaved, int sms, cudaSt
          : slots <= 4 ? launch<T, 4>(a, interleaved, sms, st)
          : slots <= 8 ? launch<T, 8>(a, interleaved, sms, st)
                       : launch<T, 16>(a, interleaved, sms, st);
-}
-
-mlora_status fail(mlora_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_last_error(buf);
-    return s;
-}
-
-mlora_status cuda_fail(cudaError_t e, const char* what) {
-    cudaGetLastError();   // reported here: not the next launch's error
-    return fail(MLORA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-// Makes a device current for the scope of one call and restores the caller's.
-struct DeviceGuard {
-    int prev = -1;
-    bool moved = false;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceGuard(int dev) {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            moved = err == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (moved) cudaSetDevice(prev);
-    }
-};
-
-mlora_status check_rows(const char* name, const void* p, int64_t row, int64_t head, mlora_dtype dtype) {
-    const int64_t unit = dtype == MLORA_BF16 ? 8 : 4;   // elements per 16 bytes
-    if (!p) return fail(MLORA_ERR_INVALID_ARG, "%s is NULL", name);
-    if (((uintptr_t)p & 15u) || row % unit || head % unit || row < 0 || head < 0)
-        return fail(MLORA_ERR_INVALID_ARG, "%s: 16-byte alignment (strides %lld, %lld elements)", name, (long long)row,
-                    (long long)head);
-    return MLORA_OK;
 }
 
 // A frequency in radians per position as turns per position, modulo 1, in 2^-64: 1 / 2 pi in two
