@@ -38,6 +38,8 @@
 // alone (215 us, one short sequence 17 us).
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attend.h"
 #include "attend_mma.cuh"
 #include "block4.cuh"
@@ -629,9 +631,9 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
     }
     __syncthreads();
     auto part = [&](int i) -> const Part& { return tl.parts[tl.order[i] >> 1][tl.order[i] & 1]; };
-    // joins slots slot_at(0 .. k - 1), some loads at a time: rows of item p, or (`to`) a slot again
-    auto join = [&](const Part& p, int k, auto slot_at, float* to) {
-        constexpr int BATCH = 4;
+    // joins slots slot_at(0 .. k - 1), a batch of loads at a time: rows of item p, or (`to`) a slot again
+    auto join = [&](auto batch, const Part& p, int k, auto slot_at, float* to) {
+        constexpr int BATCH = decltype(batch)::value;
         for (int i = tid; i < RT * DP / 4; i += THREADS) {
             const int r = i / (DP / 4), d = i % (DP / 4) * 4;
             if (!to && (r >= p.rows || d >= D)) continue;
@@ -642,13 +644,17 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
                 float4 y[BATCH];
 #pragma unroll
                 for (int z = 0; z < BATCH; ++z) {
-                    const volatile float* from = slot_at(min(z0 + z, k - 1));   // (other threads' results)
-                    mz[z] = z0 + z < k ? from[RT * DP + r] : NO_MAX;
-                    lz[z] = z0 + z < k ? from[RT * DP + RT + r] : 0.f;
-                    asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(y[z].x), "=f"(y[z].y), "=f"(y[z].z), "=f"(y[z].w)
-                                 : "l"(const_cast<const float*>(from) + r * DP + d)
-                                 : "memory");
+                    mz[z] = NO_MAX, lz[z] = 0.f;
+                    y[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (z0 + z < k) {   // (other threads' results, of this CTA or another)
+                        const float* from = slot_at(z0 + z);
+                        asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(mz[z]) : "l"(from + RT * DP + r) : "memory");
+                        asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(lz[z]) : "l"(from + RT * DP + RT + r) : "memory");
+                        asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(y[z].x), "=f"(y[z].y), "=f"(y[z].z), "=f"(y[z].w)
+                                     : "l"(from + r * DP + d)
+                                     : "memory");
+                    }
                 }
                 float now = top;
 #pragma unroll
@@ -658,7 +664,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
                 total *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
 #pragma unroll
                 for (int z = 0; z < BATCH; ++z) {
-                    const float w = z0 + z < k ? ex2(mz[z] - now) : 0.f;
+                    const float w = ex2(mz[z] - now);   // (times 0 where there is none)
                     total = fmaf(lz[z], w, total);
                     v.x = fmaf(y[z].x, w, v.x), v.y = fmaf(y[z].y, w, v.y), v.z = fmaf(y[z].z, w, v.z), v.w = fmaf(y[z].w, w, v.w);
                 }
@@ -685,10 +691,11 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
         auto warp_slot = [&](int z) { return part(i + z).slot; };
         // the item's CTAs first .. last
         const int first = worker_of(p.item_at + cut.lead) / WARPS, last = worker_of(p.item_at + p.length - 1) / WARPS;
-        if (first == last) join(p, k, warp_slot, nullptr);
+        using Warps = std::integral_constant<int, WARPS>;
+        if (first == last) join(Warps(), p, k, warp_slot, nullptr);
         else {
             auto cta_slot = [&](int z) { return partial + (size_t)(all + 2 * (first + z) + (z == 0 ? 1 : 0)) * Sh::SLOT; };
-            join(p, k, warp_slot, cta_slot(cta - first));
+            join(Warps(), p, k, warp_slot, cta_slot(cta - first));
             __syncthreads();
             if (tid == 0) {   // (release and acquire for the whole CTA, around its barriers)
                 int seen;
@@ -697,7 +704,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
                 if (tl.last_of) counters[first] = 0;
             }
             __syncthreads();
-            if (tl.last_of) join(p, last - first + 1, cta_slot, nullptr);
+            if (tl.last_of) join(std::integral_constant<int, 8>(), p, last - first + 1, cta_slot, nullptr);
             __syncthreads();
         }
         i += k;
