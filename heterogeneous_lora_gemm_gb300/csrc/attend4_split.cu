@@ -483,10 +483,12 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
                     for (int z = 0; z < 2; ++z) {
                         const float w0 = ex2(fmaf(sc[u][0][t][2 * z], qf[t][0], -m[t][0]));
                         const float w1 = ex2(fmaf(sc[u][0][t][2 * z + 1], qf[t][1], -m[t][1]));
-                        const __half2 y = __floats2half2_rn(w0, w1);
-                        p[t][0][z] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+                        // (scores near 2^23, whose bound rounds by 1, may bring a weight to 2^16: 65504)
+                        uint32_t y;
+                        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(w1), "f"(w0));
+                        p[t][0][z] = transpose8(y);
                         if (F32) {
-                            const float2 f = __half22float2(y);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
                             const __half2 low = __floats2half2_rn(w0 - f.x, w1 - f.y);
                             p[t][TERMS - 1][z] = transpose8(*reinterpret_cast<const uint32_t*>(&low));
                             l[t][0] += w0;

@@ -294,7 +294,8 @@ def test_attend_under_page_tables_for_long_sequences(rows, lengths, H, G, D, ps,
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,lengths,D", [([1, 1], [777, 130], 128), ([140], [333], 128), ([3], [90], 256), ([40], [90], 64)])
 @pytest.mark.parametrize("q_size,k_unit,v_unit", [(30.0, 0.05, 1.0), (1e-4, 0.05, 2.0 ** 60), (1e6, 1e-7, 2.0 ** -60),
-                                                  (1.0, 2.0 ** -60, 1.0), (1e-18, 2.0 ** 60, 1.0), (1e-24, 2.0 ** 60, 1.0)])
+                                                  (1.0, 2.0 ** -60, 1.0), (1e-18, 2.0 ** 60, 1.0), (1e-24, 2.0 ** 60, 1.0),
+                                                  (3e6, 0.05, 1.0), (3e7, 0.05, 1.0)])
 def test_attend_over_units_and_sizes_of_queries(rows, lengths, D, q_size, k_unit, v_unit, dtype):
     """Peaked and flat softmax; queries outside fp16's range; the units' limits."""
     u = Setup4(lengths, 2, D, 64, Hq=4, seed=10, k_unit=k_unit, v_unit=v_unit)
