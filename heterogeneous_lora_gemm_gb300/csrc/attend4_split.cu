@@ -20,8 +20,8 @@
 // holds its rows' queries as fragments (a lane's share of a row is 32 adjacent bytes of it, 64 where
 // rows are fp32) and writes an item that is its own from registers.
 // Work split: all (sequence, row tile, head) items' chunks in one line, cut into equal ranges, one
-// per resident warp; every CTA finds its warps' ranges from the lengths.  An item is as long as its
-// chunks plus what its start costs.  An item cut between warps is joined at their CTA's end,
+// per resident warp; every CTA finds its warps' ranges from the lengths (Shape, below: what an item's
+// length is).  An item cut between warps is joined at their CTA's end,
 // one cut between CTAs then by the CTA that gets there last; either in range order, so that results do
 // not depend on timing.
 //
@@ -29,7 +29,7 @@
 // 32/8 heads of 128, bf16, take 210 us, 5.7 TB/s, where the copies alone take 180 us and everything
 // but the copies 195 us; of 300 instructions per block and warp 145 convert, the vector units' integer
 // pipe is busy 46% of the time, half-precision 30%, mma.sync 24%.  32 of 129 to 4096 with as many key heads as
-// query heads take 57 us, 4.1 TB/s, one short sequence 10.3 us: a CTA's start, a range's loads, two joins.
+// query heads take 57 us, 4.1 TB/s, one of 777 tokens 9.0 us: a CTA's start, a range's loads, a join.
 //
 // What measured slower (32 sequences of 32k): bf16 weights in two terms and bf16 values (347 us);
 // a chunk's scores taken with the last one's values (233 against 230 at the time); four CTAs per SM
@@ -56,6 +56,9 @@ constexpr int PIECE = 16;                 // tokens of a block and of a product
 // m is the largest x less OFF when it is set, and moves when x > m + OFF + SLACK: weights stay below
 // 2^15, within fp16, and their 11 bits reach down to 2^-26 of the largest
 constexpr float OFF = 12.f, SLACK = 3.f;
+// Items of up to this length are taken by a CTA each where CTAs are left over (8 key heads of 200 tokens, 8
+// long, 8.0 us, cut between CTAs 8.8; of 400 tokens, 16 long, 9.7 and 9.1 us)
+constexpr int ALONE = 2 * WARPS;
 constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
 
 template <bool F32, int DP, int NT, bool LONG>
@@ -68,7 +71,7 @@ struct Shape {
     // CTAs per SM: three where the accumulators of 8 rows leave the registers, else two
     static constexpr int OCC = !F32 && DP <= 128 && NT == 1 ? 3 : 2;
     // pieces that a warp takes at a time: waits, votes and issues are per chunk.  (32 sequences of 32k tokens
-    // 210 us with four, 226 us with two; one sequence of 777 tokens 13.4 and 10.4 us)
+    // 210 us with four, 226 us with two; one sequence of 777 tokens 13.4 and 9.0 us)
     static constexpr int SUB = DP == 256 ? 1 : LONG ? 4 : 2;
     static_assert(!LONG || OCC == 3, "long ranges");
     static constexpr int CHUNK_T = PIECE * SUB;
@@ -83,31 +86,32 @@ struct Shape {
     static_assert(STAGES >= 2 && OWN >= RT * (DP + 2) * 4, "ring; a partial result in its place");
     static constexpr int SMEM = 128 + WARPS * OWN;
     static constexpr int SLOT = RT * (DP + 2);         // floats of a partial result: O, then m, l per row
+    // How the line is cut.  Long ranges: starting an item costs as much as LEAD chunks, and a range has at least
+    // LEAST.  Short ones: an item of more than one chunk is brought to a multiple of WARPS, so that the CTAs'
+    // ranges begin where items do as far as can be; every end of one inside an item is a join more.  (8 key heads
+    // of 777 tokens 9.0 us, 10.3 us with starts of a chunk; of 100 tokens 7.5 and 10.5 us)
+    static constexpr int LEAD = LONG ? 2 : 0, LEAST = LONG ? 2 : 1;
 };
 
-// How the line is cut: what starting an item costs, in chunks, and the least length of a range.
-struct Cut {
-    int lead, least;
-};
 // A sequence's share of the work line: tiles x heads items, each lead + units long (1 where the
 // rows see nothing: zeros are written).
 struct Line {
     SeqRec s;
     int c0;           // first chunk that its rows see
     int tiles, units; // row tiles, chunks per item
-    int lead;
-    __device__ int length() const { return units ? lead + units : 1; }
-    __device__ long long total(int heads) const { return (long long)tiles * heads * length(); }
+    int length;       // 1 where the rows see nothing: zeros are written
+    __device__ long long total(int heads) const { return (long long)tiles * heads * length; }
 };
-template <int RT, int CHUNK_T>
-__device__ __forceinline__ Line line_of(const AttendArgs& a, const Cut& cut, int G, int b) {
+template <typename Sh>
+__device__ __forceinline__ Line line_of(const AttendArgs& a, int G, int b) {
+    constexpr int RT = Sh::RT, CHUNK_T = Sh::CHUNK_T;
     Line n;
-    n.lead = cut.lead;
     n.s = load_seq(a.step, a.pages.page, b, a.status);
     const int last = n.s.start + n.s.rows - 1;   // position of the last processed row
     n.c0 = first_seen(n.s.start, a.window) / CHUNK_T;
     n.tiles = (n.s.rows * G + RT - 1) / RT;
     n.units = last >= 0 ? last / CHUNK_T + 1 - n.c0 : 0;
+    n.length = n.units == 0 ? 1 : Sh::LEAD ? Sh::LEAD + n.units : n.units == 1 ? 1 : (n.units + WARPS - 1) / WARPS * WARPS;
     return n;
 }
 
@@ -122,6 +126,7 @@ struct Part {
 struct Tail {
     uint64_t full[WARPS][8];
     long long scan[WARPS], first_at[WARPS];
+    int longest[WARPS];
     Part parts[WARPS][2];
     int first_b[WARPS], count[WARPS], order[2 * WARPS + 1];
     int abort_flag, last_of;
@@ -158,7 +163,7 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 // that a block's offsets are constants.
 template <bool F32, int DP, int NT, bool LONG, bool FULL>
 __global__ void __launch_bounds__(THREADS, (Shape<F32, DP, NT, LONG>::OCC))
-attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
+attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __restrict__ counters, const uint8_t* __restrict__ zeros) {
     using Sh = Shape<F32, DP, NT, LONG>;
     using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int KS = Sh::KS, RT = Sh::RT, SUB = Sh::SUB, CHUNK_T = Sh::CHUNK_T, TERMS = Sh::TERMS, CB = Sh::CB, W = Sh::W;
@@ -179,24 +184,35 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
     const int per = (a.step.n_seqs + THREADS - 1) / THREADS;
     const int b_lo = min(tid * per, a.step.n_seqs), b_hi = min(b_lo + per, a.step.n_seqs);
     long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += line_of<RT, CHUNK_T>(a, cut, G, b).total(H);
+    int longest = 0;   // item
+    for (int b = b_lo; b < b_hi; ++b) {
+        const Line n = line_of<Sh>(a, G, b);
+        mine += n.total(H);
+        longest = max(longest, n.length);
+    }
+    if (!LONG) longest = __reduce_max_sync(~0u, longest);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long v = __shfl_up_sync(~0u, incl, d);
         if (lane >= d) incl += v;
     }
-    if (lane == 31) tl.scan[warp] = incl;
+    if (lane == 31) {
+        tl.scan[warp] = incl;
+        if (!LONG) tl.longest[warp] = longest;
+    }
     __syncthreads();
     long long total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += tl.scan[w];
         total += tl.scan[w];
+        if (!LONG) longest = max(longest, tl.longest[w]);
     }
     before += incl - mine;
     const int all = gridDim.x * WARPS;
-    const int workers = total >= (long long)cut.least * all ? all : (int)((total + cut.least - 1) / cut.least);
+    const int least = !LONG && longest > WARPS && longest <= ALONE ? longest / WARPS : Sh::LEAST;
+    const int workers = total >= (long long)least * all ? all : (int)((total + least - 1) / least);
     const int cta = blockIdx.x, worker = cta * WARPS + warp;
     if (cta * WARPS >= workers) return;
     // ranges: the first `over` of them one longer than the others
@@ -215,7 +231,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
         long long p = before;
         int b = b_lo;
         for (; per > 1 && b < b_hi - 1; ++b) {
-            const long long length = line_of<RT, CHUNK_T>(a, cut, G, b).total(H);
+            const long long length = line_of<Sh>(a, G, b).total(H);
             if (from < p + length) break;
             p += length;
         }
@@ -228,7 +244,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
     const long long end = works ? range_at(worker + 1) : 0;
     int b = works ? tl.first_b[warp] : 0;
     long long b_at = works ? tl.first_at[warp] : 0;   // where sequence b begins on the line
-    Line n = line_of<RT, CHUNK_T>(a, cut, G, b);
+    Line n = line_of<Sh>(a, G, b);
     int parts = 0;
 
     uint8_t* ring = smem + warp * Sh::OWN;
@@ -241,11 +257,11 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
     while (at < end) {
         while (at >= b_at + n.total(H)) {
             b_at += n.total(H);
-            n = line_of<RT, CHUNK_T>(a, cut, G, ++b);
+            n = line_of<Sh>(a, G, ++b);
         }
         const long long into = at - b_at;
-        const int item = (int)(into >> 31 ? into / n.length() : (uint32_t)into / (uint32_t)n.length());
-        const long long item_at = b_at + (long long)item * n.length();
+        const int item = (int)(into >> 31 ? into / n.length : (uint32_t)into / (uint32_t)n.length);
+        const long long item_at = b_at + (long long)item * n.length;
         const int tile = item / H, h = item - tile * H;
         const int r0 = tile * RT, rows = min(RT, n.s.rows * G - r0);
         const int i0 = quotient(a.group, r0);   // the tile's first query token, and its head in the group
@@ -263,8 +279,8 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
             at = item_at + 1;
             continue;
         }
-        const int u0 = (int)max(at - item_at - cut.lead, 0ll), u1 = (int)(min((long long)n.length(), end - item_at) - cut.lead);
-        at = item_at + n.length();
+        const int u0 = (int)max(at - item_at - Sh::LEAD, 0ll), u1 = (int)(min((long long)n.length, end - item_at) - Sh::LEAD);
+        at = item_at + n.length;
         if (u1 <= u0) break;   // only the lead is in this range: the item is the next warp's
         // positions that the tile's rows may see: row r at start + i0 + token_of(r)
         const int pos_lo = n.s.start + i0, pos_hi = pos_lo + token_of(rows - 1);
@@ -586,7 +602,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
                 }
             }
         };
-        if (u0 == 0 && u1 == n.units) {
+        if (u0 == 0 && u1 == n.length - Sh::LEAD) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -610,7 +626,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
                     slot[RT * DP + RT + r] = l[t][e];
                 }
             }
-        if (lane == 0) tl.parts[warp][parts] = Part{item_at, slot, n.length(), n.s.row0 + i0, g0, h, rows};
+        if (lane == 0) tl.parts[warp][parts] = Part{item_at, slot, n.length, n.s.row0 + i0, g0, h, rows};
         ++parts;
     }
     // copies in flight land before the warp goes
@@ -692,7 +708,7 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
         while (tl.order[i + k] >= 0 && part(i + k).item_at == p.item_at) ++k;
         auto warp_slot = [&](int z) { return part(i + z).slot; };
         // the item's CTAs first .. last
-        const int first = worker_of(p.item_at + cut.lead) / WARPS, last = worker_of(p.item_at + p.length - 1) / WARPS;
+        const int first = worker_of(p.item_at + Sh::LEAD) / WARPS, last = worker_of(p.item_at + p.length - 1) / WARPS;
         using Warps = std::integral_constant<int, WARPS>;
         if (first == last) join(Warps(), p, k, warp_slot, nullptr);
         else {
@@ -714,11 +730,15 @@ attend4_split_kernel(const AttendArgs a, const Cut cut, float* __restrict__ part
 }
 
 template <bool F32, int DP, int NT, bool LONG, bool FULL>
-cudaError_t launch(const AttendArgs& a, const Cut& cut, const AttendWs& ws, cudaStream_t st) {
+cudaError_t launch(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     using Sh = Shape<F32, DP, NT, LONG>;
     static_assert(Sh::OCC <= ATTEND_OCC, "workspace counters");
     static_assert(sizeof(Tail) <= 1024 && Sh::OCC * (Sh::SMEM + 1024 + 1024) <= 228 * 1024, "resident CTAs");
-    attend4_split_kernel<F32, DP, NT, LONG, FULL><<<ws.sms * Sh::OCC, THREADS, Sh::SMEM, st>>>(a, cut, ws.partial, ws.counters, ws.zeros);
+    // as many CTAs as are resident, or as the longest line that the page tables allow has ranges for
+    const double tiles = (double)a.step.max_new * (a.q_heads / a.pages.heads) / Sh::RT + 1;
+    const double chunks = (double)a.step.width * a.pages.page / Sh::CHUNK_T + WARPS + Sh::LEAD;
+    const double ctas = a.step.n_seqs * tiles * a.pages.heads * chunks / (WARPS * Sh::LEAST) + 1, most = ws.sms * Sh::OCC;
+    attend4_split_kernel<F32, DP, NT, LONG, FULL><<<(int)(ctas < most ? ctas : most), THREADS, Sh::SMEM, st>>>(a, ws.partial, ws.counters, ws.zeros);
     return cudaGetLastError();
 }
 
@@ -759,15 +779,14 @@ size_t attend4_split_bytes(int dim) { return dim <= 64 ? most_bytes<64>() : dim 
 template <bool F32, int DP, bool FULL>
 static cudaError_t by_rows(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
     const bool few = (long long)a.step.max_new * (a.q_heads / a.pages.heads) <= 8;
-    // By the tokens that the page tables hold (lengths are not known here), from 128 for each of 12 warps
-    // per SM on, the fewest and longest ranges; below, ranges down to one chunk: 8 x 2000 tokens of 8 key heads
-    // 17 us and 15.6 us so, one sequence of 32000 22.3 us and 23.7 us.
-    const long long most = (long long)a.step.n_seqs * a.step.width * a.pages.page * a.pages.heads;
-    const bool lots = most >= 128ll * 12 * ws.sms;
-    const Cut cut = lots ? Cut{2, 3} : Cut{1, 1};
-    if constexpr (!F32 && DP <= 128)
-        if (few && lots) return launch<F32, DP, 1, true, FULL>(a, cut, ws, st);
-    return few ? launch<F32, DP, 1, false, FULL>(a, cut, ws, st) : launch<F32, DP, 2, false, FULL>(a, cut, ws, st);
+    if constexpr (!F32 && DP <= 128) {
+        // By the tokens that the page tables hold (lengths are not known here), from 128 for each of 12 warps
+        // per SM on, long ranges: 32 sequences of 32k tokens take 210 us so and 226 us with short ones, one of
+        // 777 tokens 13.4 us and 9.0 us.
+        const long long most = (long long)a.step.n_seqs * a.step.width * a.pages.page * a.pages.heads;
+        if (few && most >= 128ll * 12 * ws.sms) return launch<F32, DP, 1, true, FULL>(a, ws, st);
+    }
+    return few ? launch<F32, DP, 1, false, FULL>(a, ws, st) : launch<F32, DP, 2, false, FULL>(a, ws, st);
 }
 template <bool F32, int DP>
 static cudaError_t by_width(const AttendArgs& a, const AttendWs& ws, cudaStream_t st) {
