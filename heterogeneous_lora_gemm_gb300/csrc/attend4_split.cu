@@ -80,7 +80,7 @@ struct Shape {
     // query fragments: in registers where they are few, else a lane's own words of shared memory
     static constexpr int QUERY = KS * NT * TERMS * 256;    // bytes per warp
     static constexpr bool QREG = QUERY <= 16 * 256;
-    static constexpr int ROOM = (228 * 1024 / OCC - 3072) / WARPS - (QREG ? 0 : QUERY);
+    static constexpr int ROOM = (228 * 1024 / OCC - 3 * 1024) / WARPS - (QREG ? 0 : QUERY);
     static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
     static constexpr int OWN = STAGES * STAGE + (QREG ? 0 : QUERY);   // of a warp: ring, fragments
     static_assert(STAGES >= 2 && OWN >= RT * (DP + 2) * 4, "ring; a partial result in its place");

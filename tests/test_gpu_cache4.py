@@ -291,6 +291,18 @@ def test_attend_under_page_tables_for_long_sequences(rows, lengths, H, G, D, ps,
     check_attend(Setup4(lengths, H, D, ps, Hq=H * G, seed=9, width=long_table(lengths, H, ps)), rows, dtype, window)
 
 
+SHORT = [1, 31, 32, 33, 64, 65, 128, 129, 160, 256, 257, 288, 289, 512, 513, 0, 1000]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,G,window", [([n], 4, 0) for n in SHORT if n] + [(SHORT, 1, 0), (SHORT, 4, 100),
+                                              (SHORT * 8, 16, 0), (SHORT * 40, 2, 0), ([256] * 300, 4, 33)])
+def test_items_of_few_chunks(lengths, G, window, dtype):
+    """Below, at and past the lengths that one warp, one CTA and several take; fewer and more of them than
+    there are CTAs; sequences of no token between."""
+    check_attend(Setup4(lengths, 2, 64, 32, Hq=2 * G, seed=70), [1] * len(lengths), dtype, window)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,lengths,D", [([1, 1], [777, 130], 128), ([140], [333], 128), ([3], [90], 256), ([40], [90], 64)])
 @pytest.mark.parametrize("q_size,k_unit,v_unit", [(30.0, 0.05, 1.0), (1e-4, 0.05, 2.0 ** 60), (1e6, 1e-7, 2.0 ** -60),
