@@ -397,6 +397,11 @@ mlora_status mlora_rotary_apply(mlora_rotary_t r, const void* Q, int64_t q_row, 
     if (st == MLORA_OK) st = check_rows("K", K, k_row, k_head, dtype);
     if (st == MLORA_OK) st = check_rows("K_out", Ko, ko_row, ko_head, dtype);
     if (st != MLORA_OK) return st;
+    if (Qo == Ko) return fail(MLORA_ERR_INVALID_ARG, "Q_out and K_out are the same memory");
+    // (heads of an output that lie in one another would be written by several warps)
+    if ((T > 1 && (qo_row < r->dim || ko_row < r->dim)) || (q_heads > 1 && qo_head < r->dim) || (kv_heads > 1 && ko_head < r->dim))
+        return fail(MLORA_ERR_INVALID_ARG, "an output's heads of %d elements overlap (strides %lld, %lld and %lld, %lld)", r->dim,
+                    (long long)qo_row, (long long)qo_head, (long long)ko_row, (long long)ko_head);
     DeviceGuard g(r->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, "cudaSetDevice");
     const CacheStep step{offsets, lengths, nullptr, n_seqs, 1 << 15, T, max_new < T ? max_new : T};

@@ -220,3 +220,28 @@ def test_refusals():
     r.apply(none, none, n[:0])
     r.apply(none, none, n[:1], offsets=i32([0, 0]), max_new=3)
     assert r.status() == mlora.MLORA_OK
+
+
+def test_outputs_that_overlap_are_refused():
+    x, k, n = torch.ones((2, 2, 64), device="cuda"), torch.ones((2, 1, 64), device="cuda"), i32([3, 4])
+    r = Rotary(64)
+    for q_out, k_out in ((x[:1].expand(2, 2, 64), k), (x[:, :1].expand(2, 2, 64), k), (x, k[:1].expand(2, 1, 64)),
+                         (x.view(-1).as_strided((2, 2, 64), (128, 32, 1)), k), (x, x[:, :1])):
+        with pytest.raises(mlora.MloraError) as e:
+            r.apply(x.clone(), k.clone(), n, q_out=q_out, k_out=k_out)
+        assert e.value.status == mlora.MLORA_ERR_INVALID_ARG
+    assert torch.all(x == 1) and torch.all(k == 1) and r.status() == mlora.MLORA_OK
+    one = torch.ones((1, 64), device="cuda")   # a single row or head has no stride
+    r.apply(x[:1, :1].expand(1, 1, 64), one.as_strided((1, 1, 64), (0, 0, 1)), i32([1]))
+    assert torch.all(one == 1)   # position 0
+
+
+def test_broadcast_inputs():
+    """One row for all positions, one head for all heads."""
+    x, k = torch.randn((1, 1, 64), device="cuda"), torch.randn((5, 1, 64), device="cuda")
+    out = torch.empty((5, 3, 64), device="cuda")
+    r = Rotary(64)
+    r.apply(x.expand(5, 3, 64), k, i32([9]), offsets=i32([0, 5]), max_new=5, q_out=out)
+    want, size = plain(x.expand(5, 3, 64), np.arange(4, 9), [10000.0 ** (-2.0 * i / 64) for i in range(32)], False, None, 0.0)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -19 * size)
+    assert r.status() == mlora.MLORA_OK
