@@ -2,10 +2,13 @@
 // token), any row and head count (include/mlora.h).
 //
 // Mathematics.  With values kc, vc (code times scale) and units ku, vu, row r (query token i, query
-// head g of the key/value head's group) has  x_t = scale ku (q_r . kc_t),  and
-//     o_r = vu sum_t 2^(x'_t - m) vc_t / sum_t 2^(x'_t - m),   x' = x log2 e,
-// with a running m: only a lower bound of the maximum is needed, so m moves (and the accumulators
-// are rescaled) only when some x' exceeds m + OFF + SLACK.  ku is in `scale`, vu is taken at the end.
+// head g of the key/value head's group) has raw scores  y_t = q_r . kc_t,  and
+//     o_r = vu sum_t w_t vc_t / sum_t w_t,   w_t = 2^(f (y_t - ref) + OFF),   f = scale ku log2 e,
+// with a running ref: only a lower bound of the largest y is needed, so ref moves (and the accumulators
+// are rescaled) only when some f (y - ref) exceeds SLACK.  The difference is taken before the factor: near
+// the row's largest it is exact, however large f y is, so that the largest weight is always
+// 2^OFF to 2^(OFF + SLACK).  (As f y - (f ref - OFF) it would be off by the rounding of the latter: past a score
+// of 2^24 weights left fp16 at both ends.)  ku is in `scale`, vu is taken at the end.
 //
 // Products run on mma.sync m16n8k16 in fp16 with fp32 sums, transposed: tokens (S^T = K Q^T) and
 // head elements (O^T = V^T P^T) are the 16-row side, query rows the 8-column side, so that a group
@@ -43,6 +46,7 @@
 #include "attend.h"
 #include "attend_mma.cuh"
 #include "block4.cuh"
+#include "f32x2.cuh"
 #include "tc_ptx.cuh"
 
 namespace mlora {
@@ -53,13 +57,16 @@ namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int PIECE = 16;                 // tokens of a block and of a product
-// m is the largest x less OFF when it is set, and moves when x > m + OFF + SLACK: weights stay below
-// 2^15, within fp16, and their 11 bits reach down to 2^-26 of the largest
+// ref is the largest y when it is set, of weight 2^OFF, and moves when one's weight would exceed 2^(OFF + SLACK):
+// weights stay below 2^15, within fp16, and their 11 bits reach down to 2^-26 of the largest
 constexpr float OFF = 12.f, SLACK = 3.f;
 // Items of up to this length are taken by a CTA each where CTAs are left over (8 key heads of 200 tokens, 8
 // long, 8.0 us, cut between CTAs 8.8; of 400 tokens, 16 long, 9.7 and 9.1 us)
 constexpr int ALONE = 2 * WARPS;
-constexpr float NO_MAX = -1e38f;          // m before anything is seen (finite: -inf - m stays -inf)
+// ref before anything is seen: far below any score, finite (-inf less it stays -inf), and so that the bound set
+// from it (SLACK / f is 2.6e38 at the most) lies below any score as well
+constexpr float NO_MAX = -3e38f;
+constexpr int EXTRA = 3;                  // of a partial result beside O, per row: ref, the weights' sum, f
 
 template <bool F32, int DP, int NT, bool LONG>
 struct Shape {
@@ -83,9 +90,9 @@ struct Shape {
     static constexpr int ROOM = (228 * 1024 / OCC - 3 * 1024) / WARPS - (QREG ? 0 : QUERY);
     static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
     static constexpr int OWN = STAGES * STAGE + (QREG ? 0 : QUERY);   // of a warp: ring, fragments
-    static_assert(STAGES >= 2 && OWN >= RT * (DP + 2) * 4, "ring; a partial result in its place");
+    static_assert(STAGES >= 2 && OWN >= RT * (DP + EXTRA) * 4, "ring; a partial result in its place");
     static constexpr int SMEM = 128 + WARPS * OWN;
-    static constexpr int SLOT = RT * (DP + 2);         // floats of a partial result: O, then m, l per row
+    static constexpr int SLOT = RT * (DP + EXTRA);     // floats of a partial result: O, then ref, l, f per row
     // How the line is cut.  Long ranges: starting an item costs as much as LEAD chunks, and a range has at least
     // LEAST.  Short ones: an item of more than one chunk is brought to a multiple of WARPS, so that the CTAs'
     // ranges begin where items do as far as can be; every end of one inside an item is a join more.  (8 key heads
@@ -131,6 +138,12 @@ struct Tail {
     int first_b[WARPS], count[WARPS], order[2 * WARPS + 1];
     int abort_flag, last_of;
 };
+
+__device__ __forceinline__ float reciprocal(float x) {   // to 2^-22; 0 past 2^126
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // 16 adjacent elements as floats, zeros unless `there`
 __device__ __forceinline__ void load16(const float* p, bool there, float* x) {
@@ -349,7 +362,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                 const int k = fine ? min(max((int)(__float_as_uint(top) >> 23) - 126, -100), 118) : 0;
                 const float down = fine ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
                 const float f = a.scale * (1.4426950408889634f * __uint_as_float((uint32_t)(127 + k) << 23));
-                factor[t] = fine ? fmaxf(f, 0x1p-126f) : NAN;   // (-inf times it stays -inf)
+                factor[t] = fine ? fminf(fmaxf(f, 0x1p-126f), 0x1.fffffep127f) : NAN;   // (-inf times it stays -inf, 0 times it 0)
 #pragma unroll
                 for (int u = 0; u < DP / 64; ++u)
 #pragma unroll
@@ -378,15 +391,15 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                     }
             }
         }
-        float qf[NT][2], m[NT][2], l[NT][2], bound[NT][2], sum[NT][4], o[KS][NT][4];
+        float qf[NT][2], ref[NT][2], l[NT][2], bound[NT][2], sum[NT][4], o[KS][NT][4];
         int hi[NT][2];   // tokens first_seen(hi - 1) .. hi - 1 are seen
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qf[t][e] = __shfl_sync(~0u, factor[t], (2 * tig + e) * 4);
-                m[t][e] = NO_MAX;
-                bound[t][e] = -3e38f;   // (m + OFF + SLACK) / qf
+                ref[t][e] = NO_MAX;
+                bound[t][e] = NO_MAX;   // ref + SLACK / qf, or a little less
                 l[t][e] = sum[t][e] = sum[t][2 + e] = 0.f;
                 hi[t][e] = pos_lo + token_of(min(t * 8 + 2 * tig + e, rows - 1)) + 1;
 #pragma unroll
@@ -443,8 +456,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                     step(4 * q + 2, codes_f16<0>(w.y, sa), codes_f16<0>(w.w, sb), codes_f16<1>(w.y, sa), codes_f16<1>(w.w, sb));
                     step(4 * q + 3, codes_f16<2>(w.y, sa), codes_f16<2>(w.w, sb), codes_f16<3>(w.y, sa), codes_f16<3>(w.w, sb));
                 }
-            // the largest score itself, against the bound over the row's factor; then one fused operation per
-            // exponent
+            // the largest score itself, against the bound
             const int t0 = (ca + k) * CHUNK_T;
             const bool edge = t0 + CHUNK_T > hi_min || t0 < lo_max;
             bool above = false;
@@ -476,10 +488,10 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                         float x = top[t][e];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-                        x = fmaxf(fmaf(x, qf[t][e], -OFF), m[t][e]);
-                        const float f = ex2(m[t][e] - x);
-                        m[t][e] = x;
-                        bound[t][e] = (x + (OFF + SLACK)) / qf[t][e];
+                        x = fmaxf(x, ref[t][e]);
+                        const float f = ex2((ref[t][e] - x) * qf[t][e]);
+                        ref[t][e] = x;
+                        bound[t][e] = __fadd_rd(x, SLACK * 0.9999f * reciprocal(qf[t][e]));
                         sum[t][e] *= f;
                         l[t][e] *= f;
 #pragma unroll
@@ -497,14 +509,13 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        const float w0 = ex2(fmaf(sc[u][0][t][2 * z], qf[t][0], -m[t][0]));
-                        const float w1 = ex2(fmaf(sc[u][0][t][2 * z + 1], qf[t][1], -m[t][1]));
-                        // (scores near 2^23, whose bound rounds by 1, may bring a weight to 2^16: 65504)
-                        uint32_t y;
-                        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(w1), "f"(w0));
-                        p[t][0][z] = transpose8(y);
+                        const float2 x = unpair(fma2(add2(pair(sc[u][0][t][2 * z], sc[u][0][t][2 * z + 1]), pair(-ref[t][0], -ref[t][1])),
+                                                     pair(qf[t][0], qf[t][1]), pair(OFF, OFF)));
+                        const float w0 = ex2(x.x), w1 = ex2(x.y);
+                        const __half2 y = __floats2half2_rn(w0, w1);
+                        p[t][0][z] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
                         if (F32) {
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                            const float2 f = __half22float2(y);
                             const __half2 low = __floats2half2_rn(w0 - f.x, w1 - f.y);
                             p[t][TERMS - 1][z] = transpose8(*reinterpret_cast<const uint32_t*>(&low));
                             l[t][0] += w0;
@@ -622,8 +633,9 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                     for (int i = 0; i < EPL / 4; ++i)
                         *reinterpret_cast<float4*>(slot + r * DP + q * 128 + g * EPL + 4 * i) = four(t, e, q, i, 1.f);
                 if (g == 0) {
-                    slot[RT * DP + r] = m[t][e];
+                    slot[RT * DP + r] = ref[t][e];
                     slot[RT * DP + RT + r] = l[t][e];
+                    slot[RT * DP + 2 * RT + r] = qf[t][e];
                 }
             }
         if (lane == 0) tl.parts[warp][parts] = Part{item_at, slot, n.length, n.s.row0 + i0, g0, h, rows};
@@ -655,8 +667,9 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
         for (int i = tid; i < RT * DP / 4; i += THREADS) {
             const int r = i / (DP / 4), d = i % (DP / 4) * 4;
             if (!to && (r >= p.rows || d >= D)) continue;
-            float top = NO_MAX, total = 0.f;
+            float top = NO_MAX, total = 0.f, factor;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(factor) : "l"(slot_at(0) + RT * DP + 2 * RT + r) : "memory");
             for (int z0 = 0; z0 < k; z0 += BATCH) {
                 float mz[BATCH], lz[BATCH];
                 float4 y[BATCH];
@@ -677,12 +690,12 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                 float now = top;
 #pragma unroll
                 for (int z = 0; z < BATCH; ++z) now = fmaxf(now, mz[z]);
-                const float f = ex2(top - now);
+                const float f = ex2((top - now) * factor);
                 top = now;
                 total *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
 #pragma unroll
                 for (int z = 0; z < BATCH; ++z) {
-                    const float w = ex2(mz[z] - now);   // (times 0 where there is none)
+                    const float w = ex2((mz[z] - now) * factor);   // (times 0 where there is none)
                     total = fmaf(lz[z], w, total);
                     v.x = fmaf(y[z].x, w, v.x), v.y = fmaf(y[z].y, w, v.y), v.z = fmaf(y[z].z, w, v.z), v.w = fmaf(y[z].w, w, v.w);
                 }
@@ -692,6 +705,7 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
                 if (d == 0) {
                     to[RT * DP + r] = top;
                     to[RT * DP + RT + r] = total;
+                    to[RT * DP + 2 * RT + r] = factor;
                 }
             } else {
                 const float inv = total == 0.f ? 0.f : c.v_unit / total;
