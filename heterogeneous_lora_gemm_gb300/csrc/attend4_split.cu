@@ -397,11 +397,13 @@ attend4_split_kernel(const AttendArgs a, float* __restrict__ partial, int* __res
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                qf[t][e] = __shfl_sync(~0u, factor[t], (2 * tig + e) * 4);
                 ref[t][e] = NO_MAX;
                 bound[t][e] = NO_MAX;   // ref + SLACK / qf, or a little less
                 l[t][e] = sum[t][e] = sum[t][2 + e] = 0.f;
                 hi[t][e] = pos_lo + token_of(min(t * 8 + 2 * tig + e, rows - 1)) + 1;
+                // (a row that sees nothing may hold anything: its factor would make masked scores NaN)
+                const float f = __shfl_sync(~0u, factor[t], (2 * tig + e) * 4);
+                qf[t][e] = hi[t][e] > 0 ? f : 1.f;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) o[s][t][e] = o[s][t][2 + e] = 0.f;
             }

@@ -532,7 +532,8 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  *   O[i, h] = sum_j p_j v_j,  p = softmax_j(scale * Q[i, h] . k_j)
  * over the tokens j of the row's sequence with j <= pos(i), and j > pos(i) - window
  * where window > 0; query head h reads key/value head h / (q_heads / kv_heads).  A row
- * that sees no token gives zeros, a query that holds a NaN or an infinity NaN.  Sums
+ * that sees no token gives zeros, whatever its query holds; of the others a query that holds a
+ * NaN or an infinity gives NaN.  Sums
  * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, 8-bit value
  * scales under 2^-96 lose low bits, under 2^-120 they may count as 0; 4-bit sums hold values over
  * their unit, which the output takes at the end); O is rounded once.  Weights are held in 24 bits for fp32 rows and in 16 for bf16 rows, in 8 where

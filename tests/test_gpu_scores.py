@@ -100,3 +100,24 @@ def test_neighbouring_scores_of_any_size(rows, lengths, H, G, D, ps, width, orde
                 bad = ~(np.abs(mine - want) <= off + low)
                 assert not bad.any(), (f"2^{log2_common} by 2^{log2_step}, row {i} of {b}: {bad.sum()} of {bad.size} off, "
                                        f"first {np.argwhere(bad)[0]}: {mine[bad][:3]}")
+
+
+@pytest.mark.parametrize("rows,lengths,G,D", [([3], [1], 2, 128), ([4, 1], [2, 300], 4, 64), ([9], [3], 1, 256), ([40], [7], 2, 128),
+                                              ([200, 150], [60, 400], 1, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_rows_that_see_no_token_are_zeros_whatever_their_queries(rows, lengths, G, D, dtype, bits):
+    """Rows at negative positions beside rows that see something; the others are as without them."""
+    u = (Setup4 if bits == 4 else Setup)(lengths, 1, D, 64, Hq=G, seed=95)
+    q = torch.randn((sum(rows), G, D), device="cuda").to(TDT[dtype])
+    out = []
+    pos = np.concatenate([np.arange(n - r, n) for r, n in zip(rows, lengths)])
+    blind = torch.from_numpy(pos < 0).cuda()
+    for bad in (1.0, float("nan"), float("inf"), -float("inf")):
+        Q = q.clone()
+        Q[blind, :, 5] = bad
+        O = torch.full_like(Q, 9.0)
+        u.cache.attend(Q, O, u.len, u.pages, offsets=offsets_of(rows), max_new=max(rows))
+        out.append(O)
+        assert torch.all(O[blind] == 0) and torch.equal(O, out[0])
+    assert u.cache.status() == mlora.MLORA_OK
