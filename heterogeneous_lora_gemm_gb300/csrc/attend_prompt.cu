@@ -8,6 +8,9 @@
 // vs < 2^-120, whose codes append stores as 0, is converted to zeros under a scale of 1.  m is a
 // row's largest x when it was last set; a step whose weights sum to more than 2^14 sets it
 // again (no maximum is taken otherwise; bf16 and fp32 hold weights above 1 as well as below).
+// x - m takes the exact product and the rounded m, so that the largest weight is 2^d, d up to half of m's
+// last bit.  From 2^31 on that leaves fp32: a row whose m would reach 2^30 has all its x's divided by a
+// power of two.  (Unequal scores then lie 2^5 apart at the least: 2^-32 of the weight, where it was 2^-64 or less.)
 // Rows are (query token, query head of the group) pairs of one key/value head, 256 per CTA as
 // two tiles of 128 (one, where heads have more than 128 elements or rows are fp32): a converted
 // key/value tile serves both.
@@ -85,6 +88,7 @@ constexpr int REGS_SOFT = 128, REGS_REST = 72;
 static_assert(32 * (SOFT * REGS_SOFT + (CONV + 4) * REGS_REST) <= PROMPT_THREADS * 96, "register split");
 constexpr int FOLD = 16;                   // steps of fp32 rows between roundings of O into fp32 outside
 constexpr float MOST = 16384.f;            // sum of a step's weights over which m moves
+constexpr int FAR = 30;                    // a row's x's are divided so that |m| stays below 2^FAR
 constexpr float NO_MAX = -1e38f;           // m of a row that has seen nothing
 constexpr int MOST_DOWN = 114;             // queries are divided by 2^MOST_DOWN at most (scale 2^128 would leave fp32)
 constexpr float SMALL_SCALE = 0x1p-64f;    // value scales below it are brought up by 1 / SMALL_SCALE
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             }
         }
         __syncwarp();
-        const float qf = tl.qf[t][rl];
+        float qf = tl.qf[t][rl];
         const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t sbase = lane_base + t * TILE, obase = lane_base + Sh::O_AT + t * TILE;
         const int hi = s.start + r / G + 1, lo = first_seen(hi - 1, a.window);   // tokens [lo, hi) are seen
@@ -824,6 +828,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
         const int hi_min = s.start + rt / G + 1, hi_max = s.start + min(R - 1, rt + TILE - 1) / G + 1;
         const int lo_max = first_seen(hi_max - 1, a.window);
         float m = NO_MAX;
+        // what the row's x's are divided by, a power of two (tl.qf holds their factor before that)
+        auto divisor = [&]() { return __uint_as_float(__float_as_uint(tl.qf[t][rl]) - __float_as_uint(qf) + 0x3F800000u); };
         uint64_t l2 = pair(0.f, 0.f);
         bool ok = true;
         // 32 elements of the row, from 32 q on, times f, into the queries' place (the products that read
@@ -939,9 +945,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
                     if (move) {
                         // (fp32 rows: the lower terms of weights that are dropped land before the next ones')
                         if constexpr (F32) tmem_wait_st();
-                        const float mx = row_max<BITS == 4>(sat, sc, qf, lo - t0, hi - t0);
-                        const float now = above ? fmaxf(mx, m) : m, f = ex2(m - now);
-                        m = now;
+                        const float q = tl.qf[t][rl], up = divisor(), was = m * up;
+                        const float mx = row_max<BITS == 4>(sat, sc, q, lo - t0, hi - t0);
+                        const float now = above ? fmaxf(mx, was) : was, f = ex2(was - now);
+                        const uint32_t far = max((__float_as_uint(now) >> 23 & 0xFFu), 126u + FAR) - (126u + FAR);
+                        const float down = now == NO_MAX ? 1.f : __uint_as_float((127u - far) << 23);
+                        m = now * down;
+                        qf = q * down;
+                        if constexpr (F32) under *= up * down;
                         l2 = mul2(l2, pair(f, f));
                         if (i > 0) {
                             // O, once the last step's product is complete (the one before it is: these
@@ -1000,7 +1011,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1) attend_prompt_kernel(const 
             }
             if (parts == 1) put_rows();
             else if (live) {
-                ml[0] = m;
+                ml[0] = m * divisor();
                 ml[Sh::ROWS] = l;
             }
         }

@@ -540,7 +540,8 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * max_new * q_heads / kv_heads > 16; in that form sums of one sign come out 0.25% low over
  * 2^20 tokens, and lower over more.  In 4 bits, up to 16 such rows (or heads of more than 128 elements of
  * fp32 rows), weights have 22 and 11 bits, fewer from 2^-26 of the row's largest down, and none under 2^-37 of it.  O must not overlap Q: fp32 rows of it may hold sums
- * during the call.
+ * during the call.  Scores may have any size up to 2^126 (of unequal ones past 2^29 in fp32 the larger
+ * has all of the weight); larger ones may give NaN.
  * Errors: INVALID_ARG, UNSUPPORTED (with max_new taken as T where it is larger: max_new *
  * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34; in 4 bits, scale * k_unit outside [2^-120, 3e38)), CUDA.
  */

@@ -13,9 +13,11 @@ from heterogeneous_lora_gemm_gb300 import mlora  # noqa: E402
 from test_gpu_cache import F, Setup, TDT, offsets_of  # noqa: E402
 from test_gpu_cache4 import Setup4  # noqa: E402
 
-# rows, lengths, key heads, query heads of each, head size, page, columns of the page table: the forms of the kernels for few rows
+# rows, lengths, key heads, query heads of each, head size, page, columns of the page table: every form of the kernels
 FEW = [([1], [300], 2, 4, 128, 64, 1), ([1], [300], 2, 4, 128, 64, 3000), ([1], [9000], 1, 8, 64, 16, 1), ([1, 1], [70, 300], 2, 4, 48, 32, 1),
        ([4], [600], 1, 4, 128, 48, 1), ([3, 2], [300, 290], 1, 3, 96, 16, 1), ([1], [700], 1, 2, 256, 32, 1), ([9], [400], 1, 1, 256, 64, 1)]
+MANY = [([40], [300], 1, 2, 128, 64, 1), ([20], [3000], 1, 1, 128, 64, 1), ([150, 30], [500, 300], 1, 2, 64, 16, 1), ([40], [300], 1, 1, 256, 64, 1),
+        ([250, 60], [1250, 500], 1, 16, 128, 64, 1), ([900], [1300], 1, 8, 80, 32, 1)]
 
 
 def attended(u, q, rows, scale, dtype):
@@ -27,7 +29,7 @@ def attended(u, q, rows, scale, dtype):
     return O.double().cpu().numpy()
 
 
-@pytest.mark.parametrize("rows,lengths,H,G,D,ps,width", FEW)
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,width", FEW + MANY)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("negative,at", [(False, "first"), (True, "last")])
@@ -63,7 +65,7 @@ def test_one_token_with_all_of_the_weight(rows, lengths, H, G, D, ps, width, dty
             assert not bad.any(), f"2^{log2_score}: {bad.sum()} of {bad.size} off, first {np.argwhere(bad)[0]}: {mine[bad][:3]}"
 
 
-@pytest.mark.parametrize("rows,lengths,H,G,D,ps,width", FEW)
+@pytest.mark.parametrize("rows,lengths,H,G,D,ps,width", FEW + MANY)
 @pytest.mark.parametrize("order", ["rising", "mixed"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_neighbouring_scores_of_any_size(rows, lengths, H, G, D, ps, width, order, dtype):
