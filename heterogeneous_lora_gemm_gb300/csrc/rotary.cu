@@ -318,6 +318,22 @@ uint64_t turns_of(double f) {
     return (uint64_t)((t - std::floor(t)) * 0x1p64) + (uint64_t)(int64_t)std::llrint(rest * 0x1p64);   // (the difference is exact)
 }
 
+// Whether two of rows x heads runs of `dim` elements, at i row + j head (strides >= 0), have an element
+// in common: whether |i row - j head| < dim for some i < rows and j < heads that are not both 0.
+bool heads_overlap(int rows, int64_t row, int heads, int64_t head, int dim) {
+    if ((rows > 1 && row < dim) || (heads > 1 && head < dim)) return true;
+    if (rows == 1 || heads == 1) return false;
+    // rows that end before the next begins, heads that do
+    if ((__int128)(heads - 1) * head + dim <= row || (__int128)(rows - 1) * row + dim <= head) return false;
+    for (int j = 1; j < heads; ++j) {   // the rows to both sides of head j of row 0
+        const __int128 at = (__int128)j * head, i = at / row, past = at - i * row;
+        if (i >= rows) return false;
+        if (i > 0 && past < dim) return true;
+        if (i + 1 < rows && row - past < dim) return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -399,7 +415,7 @@ mlora_status mlora_rotary_apply(mlora_rotary_t r, const void* Q, int64_t q_row, 
     if (st != MLORA_OK) return st;
     if (Qo == Ko) return fail(MLORA_ERR_INVALID_ARG, "Q_out and K_out are the same memory");
     // (heads of an output that lie in one another would be written by several warps)
-    if ((T > 1 && (qo_row < r->dim || ko_row < r->dim)) || (q_heads > 1 && qo_head < r->dim) || (kv_heads > 1 && ko_head < r->dim))
+    if (heads_overlap(T, qo_row, q_heads, qo_head, r->dim) || heads_overlap(T, ko_row, kv_heads, ko_head, r->dim))
         return fail(MLORA_ERR_INVALID_ARG, "an output's heads of %d elements overlap (strides %lld, %lld and %lld, %lld)", r->dim,
                     (long long)qo_row, (long long)qo_head, (long long)ko_row, (long long)ko_head);
     DeviceGuard g(r->device);

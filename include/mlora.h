@@ -583,7 +583,7 @@ mlora_status mlora_rotary_destroy(mlora_rotary_t rotary);
 /*
  * Turns the step's query rows Q into Q_out and its key rows K into K_out, each [T][heads][head_dim]
  * with strides and alignment as mlora_cache_append's rows; an output may be its input itself (same
- * strides), and overlaps no other operand or itself (strides under head_dim are refused).  offsets, lengths and max_new describe the step as for the cache's
+ * strides), and overlaps no other operand or itself (an output two heads of which share elements is refused).  offsets, lengths and max_new describe the step as for the cache's
  * calls: rows at negative positions name no token and come out as zeros, rows outside every
  * range are left alone, lengths are clamped to 0 .. 2^30; what is out of range sets the status bit that
  * mlora_rotary_status reports.

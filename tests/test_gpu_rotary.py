@@ -236,6 +236,38 @@ def test_outputs_that_overlap_are_refused():
     assert torch.all(one == 1)   # position 0
 
 
+@pytest.mark.parametrize("T,heads,row,head", [(2, 2, 1, 1), (2, 32, 1, 1), (3, 6, 5, 2), (11, 4, 3, 10), (2, 5, 8, 2), (40, 33, 2, 64),
+                                              (2, 2, 1.25, 1), (2, 2, 1, 1.25), (9, 9, 1.25, 9)])
+def test_outputs_whose_rows_lie_among_their_heads_are_refused(T, heads, row, head):
+    """Strides of a head and more, in heads: two heads of unequal rows share elements."""
+    x, k = torch.ones((T, heads, 64), device="cuda"), torch.ones((T, 1, 64), device="cuda")
+    r, n = Rotary(64), i32([T])
+    row, head = int(row * 64), int(head * 64)
+    out = torch.full(((T - 1) * row + (heads - 1) * head + 64,), 7.0, device="cuda")
+    mine = out.as_strided((T, heads, 64), (row, head, 1))
+    for kw, q, kk in ((dict(q_out=mine), x, k), (dict(k_out=mine), k, x)):
+        with pytest.raises(mlora.MloraError) as e:
+            r.apply(q.clone(), kk.clone(), n, offsets=i32([0, T]), max_new=T, **kw)
+        assert e.value.status == mlora.MLORA_ERR_INVALID_ARG
+    assert torch.all(out == 7.0) and r.status() == mlora.MLORA_OK
+
+
+@pytest.mark.parametrize("T,heads,row,head", [(2, 4, 5, 2), (3, 3, 1, 3), (5, 4, 4, 1), (2, 2, 3, 2), (3, 2, 2, 7), (2, 3, 1.25, 2.5)])
+def test_outputs_whose_rows_lie_among_their_heads_without_overlap(T, heads, row, head):
+    row, head = int(row * 64), int(head * 64)
+    x, k = torch.randn((T, heads, 64), device="cuda"), torch.randn((T, 1, 64), device="cuda")
+    r, n = Rotary(64), i32([T + 5])
+    out = torch.full(((T - 1) * row + (heads - 1) * head + 64,), 7.0, device="cuda")
+    mine = out.as_strided((T, heads, 64), (row, head, 1))
+    want, other = torch.empty_like(x), torch.empty_like(k)
+    step = dict(offsets=i32([0, T]), max_new=T, k_out=other)
+    r.apply(x, k, n, q_out=want, **step)
+    r.apply(x, k, n, q_out=mine, **step)
+    assert torch.equal(mine, want)
+    mine.fill_(7.0)
+    assert torch.all(out == 7.0)      # (what lies between was left alone)
+
+
 def test_broadcast_inputs():
     """One row for all positions, one head for all heads."""
     x, k = torch.randn((1, 1, 64), device="cuda"), torch.randn((5, 1, 64), device="cuda")
