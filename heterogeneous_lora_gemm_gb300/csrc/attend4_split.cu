@@ -166,12 +166,6 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, bool there, float
     }
 }
 
-__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // `zeros`: a block of zeros, in the place of one that cannot be read.  FULL: heads of DP elements, so
 // that a block's offsets are constants.
 template <bool F32, int DP, int NT, bool LONG, bool FULL>
