@@ -32,9 +32,11 @@
 // 32/8 heads of 128, bf16, take 210 us, 5.7 TB/s, where the copies alone take 180 us and everything
 // but the copies 195 us; of 300 instructions per block and warp 145 convert, the vector units' integer
 // pipe is busy 46% of the time, half-precision 30%, mma.sync 24%.  32 of 129 to 4096 with as many key heads as
-// query heads take 57 us, 4.1 TB/s, one of 777 tokens 9.0 us: a CTA's start, a range's loads, a join.
+// query heads take 57 us, 4.1 TB/s, one of 777 tokens 9.0 us (13.4 under a page table for 32k: by_rows below): a CTA's
+// start, a range's loads, a join.
 //
-// What measured slower (32 sequences of 32k): bf16 weights in two terms and bf16 values (347 us);
+// What measured slower (32 sequences of 32k): weights in two terms, 22 bits, for bf16 rows as well (248 us, the 57 us
+// above 66; the error stays 0.0017), as bf16 with bf16 values 347 us;
 // a chunk's scores taken with the last one's values (233 against 230 at the time); four CTAs per SM
 // (233), two (270); a CTA per range, its warps in turns over the chunks, joined per item (221 us, and
 // 50 against 39 us for 81 sequences of 194 tokens, 64/32 heads, fp32); parts joined through global memory

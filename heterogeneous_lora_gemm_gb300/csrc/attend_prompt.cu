@@ -54,8 +54,11 @@
 //
 // The 4-bit cache (BITS 4, block4.cuh): a code times its scale is exact in bf16, so that the operand
 // tiles hold the values themselves, over a unit that goes into the scores' factor (on the host) and
-// into the output; tokens have no scales left (8192 tokens 358 us, 382 us over 8 bits; 4 prompts of
-// 6000 rows after 1024 134 and 140 us).
+// into the output; tokens have no scales left (8192 tokens 360 us, 382 us over 8 bits; 4 prompts of
+// 6000 rows after 1024 134 and 140 us).  Values and weights of bf16 rows could be fp16 (weights in 11 bits: error
+// 0.0017, in bf16 0.0021), but fp16 holds no weight under 2^-24: with m 12 below the largest, so that the weights
+// reach as far as attend4_split.cu's, it moves often (442 and 152 us; scores of three times the size 615 us,
+// 407 in bf16); with m 6 below, 495 us at that size, and tokens under 2^-31 of the largest are lost.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of tile 0 and 1 (a thread per row), 8 copies
 // operand tiles or 8-15 read codes and convert them into keys and values in bf16 (tokens as rows; the
@@ -1240,7 +1243,11 @@ size_t attend_prompt_bytes(const CachePages& c, long long tokens) {
 // against 22, 79, 145, at 4 tokens 25, 61, 127 against 22, 46, 81; fp32 rows at 6 tokens 38, 133, 267
 // against 49, 140, 255, at 12 tokens 134 against 243 (16 sequences), at 4 tokens 35, 100, 220 against
 // 24, 59, 104.  The rule knows neither the number of sequences nor the type: it costs one sequence of
-// bf16 rows 3 us and 64 of fp32 rows 12 us at 6 tokens.
+// bf16 rows 3 us and 64 of fp32 rows 12 us at 6 tokens.  Over 4 bits it is the same rule, this kernel against
+// attend4_split.cu, for 1 (after 5000), 16 (after 4000) and 64 (after 1000) sequences: bf16 rows at 5 tokens
+// 27, 55, 73 us against 21, 54, 63, at 12 tokens 27, 56, 75 against 25, 74, 84; fp32 rows at 5 tokens 39, 115, 136
+// against 25, 77, 86, at 12 tokens 39, 117, 142 against 30, 106, 119, at 16 tokens 39, 119, 144 against 25, 135, 153:
+// from 17 to 32 rows fp32 rows pay up to 60%, bf16 rows of heads of 256 50% (160 against 106 us).
 bool attend_prompt_takes(bool bf16, const AttendArgs& a) {
     return (bf16 || a.pages.dim <= 128) && (long long)a.step.max_new * (a.q_heads / a.pages.heads) > 16;
 }

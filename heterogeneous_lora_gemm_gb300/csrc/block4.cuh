@@ -4,7 +4,7 @@
 // An atom, 8 bytes, holds 16 adjacent elements of a token: element e in nibble e, as code + 8.  A
 // block of D elements is D atoms of keys, D atoms of values, then a byte of scale (e4m3) per atom
 // in the same order; all of it 18 D bytes, one copy.  The orders are those in which the lanes of
-// mma.sync fragments take them (attend_split.cu): a lane's two atoms of 16 bytes lie together, a
+// mma.sync fragments take them (attend4_split.cu): a lane's two atoms of 16 bytes lie together, a
 // warp's 512 bytes in its lanes' order, so that neither copies nor reads of shared memory meet a
 // bank conflict.
 #pragma once

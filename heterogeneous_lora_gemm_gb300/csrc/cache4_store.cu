@@ -8,7 +8,7 @@
 //
 // Bound: HBM, 2 + 9/16 bytes per bf16 element: 28k prompt tokens of 8 heads of 128 are appended in 30 us,
 // 5.2 TB/s, and 29.6k read back in 30 us, 5.1 TB/s (floors 23 us each); the rows of 256 sequences, 32
-// heads, take 3.2 us and the pages that they lie in 34 us to read (floor 26).  Both wait for the chain of
+// heads, take 3.2 us and the pages that they lie in 34 us to read (floor 26); 29k fp32 rows are appended in 46 us and read in 67 (together 0.70 of the floor).  Both wait for the chain of
 // length, page and rows more than for memory; the read's 32-byte pieces of rows keep L1 busy at three
 // quarters of its rate.  What measured slower: a lane per 16 bytes of a row, side by side (prompts read in
 // 36 us); lanes that trade halves so that a store fills 32 bytes (30 us, and 39 for the decode pages);

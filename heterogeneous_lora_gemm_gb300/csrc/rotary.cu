@@ -5,7 +5,7 @@
 //     a' = a cos - b sin,  b' = a sin + b cos.
 // Angles are held in turns: f / 2 pi as a 64-bit fraction, so that p times it, in wrapping
 // integers, is the angle modulo a turn with no loss at any position; its nearest quarter turn is
-// taken off before it becomes a float.
+// taken off before it becomes a float (of 24 bits: off by up to 2^-28 of a turn).
 //
 // A warp takes a row and some heads of its queries and keys.  A lane takes 16 elements of a head, in
 // runs of 16 bytes that lie side by side with its neighbours'; sines and cosines are computed once for
@@ -13,7 +13,7 @@
 // being x's partner.  16 lanes at most share a head and its sum of squares.  Arithmetic is in pairs.
 //
 // Bound: HBM, each element read and written once: 29.6k rows of 32/8 heads of 128 in bf16 take 105 us,
-// 5.8 TB/s (a plain copy of as many bytes 89 us), in fp32 178 us, 6.8 TB/s; 4000 rows of 15 heads of
+// 5.8 TB/s (a plain copy of as many bytes 89 us), half of each head 108 us, of neighbours 109, in fp32 178 us, 6.8 TB/s; 4000 rows of 15 heads of
 // 80 in fp32 11.5 us and 8 rows 2.9 us, a launch and the chain of offsets, length and sines.  What
 // measured slower: two groups of heads on their way (117 us), rows without the factors (120 us).
 #include <cuda_bf16.h>
@@ -41,8 +41,8 @@ namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int MOST = 16;   // groups of heads that a warp takes at most
-// CTAs per SM (register limits): bf16 rows spill 5 words at 6 and are faster all the same (30k rows of 32/8
-// heads 109 us, 113 us at 5), fp32 rows would spill 20
+// CTAs per SM (register limits): bf16 rows spill at 6 (a word; neighbours 4, of part of a head 8) and are faster all
+// the same (30k rows of 32/8 heads 109 us, 113 us at 5, before whole heads had a form), fp32 rows would spill 20
 template <typename T>
 constexpr int CTAS = sizeof(T) == 2 ? 6 : 5;
 

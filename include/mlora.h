@@ -533,15 +533,18 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * over the tokens j of the row's sequence with j <= pos(i), and j > pos(i) - window
  * where window > 0; query head h reads key/value head h / (q_heads / kv_heads).  A row
  * that sees no token gives zeros, whatever its query holds; of the others a query that holds a
- * NaN or an infinity gives NaN.  Sums
- * and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, 8-bit value
+ * NaN or an infinity gives NaN.  O must not overlap Q: fp32 rows of it may hold sums during the call.
+ * Sums and softmax statistics are fp32 (values of 2^80 and more may overflow the sums, 8-bit value
  * scales under 2^-96 lose low bits, under 2^-120 they may count as 0; 4-bit sums hold values over
- * their unit, which the output takes at the end); O is rounded once.  Weights are held in 24 bits for fp32 rows and in 16 for bf16 rows, in 8 where
- * max_new * q_heads / kv_heads > 16; in that form sums of one sign come out 0.25% low over
- * 2^20 tokens, and lower over more.  In 4 bits, up to 16 such rows (or heads of more than 128 elements of
- * fp32 rows), weights have 22 and 11 bits, fewer from 2^-26 of the row's largest down, and none under 2^-37 of it.  O must not overlap Q: fp32 rows of it may hold sums
- * during the call.  Scores may have any size up to 2^126 (of unequal ones past 2^29 in fp32 the larger
- * has all of the weight); larger ones may give NaN.
+ * their unit, which the output takes at the end); O is rounded once.  Weights are held in 24 bits
+ * for fp32 rows and in 16 for bf16 rows, in 8 where max_new * q_heads / kv_heads > 16; in that form
+ * sums of one sign come out 0.25% low over 2^20 tokens, and lower over more.  In 4 bits, up to 16 such
+ * rows (or heads of more than 128 elements of fp32 rows), weights have 22 and 11 bits, fewer from 2^-26
+ * of the row's largest down, and none under 2^-37 of it.  Scores may have any size up to 2^126 (of
+ * unequal ones past 2^29 the larger has all of the weight); larger ones may give NaN.
+ * What the arguments cost: max_new chooses one form for all of a step, so that single rows and a prompt
+ * go faster as two calls; over 4 bits `width` chooses the form of few rows, so that a table is best no
+ * wider than its longest sequence (one of 777 tokens: 9 us, 13 us under a table for 32k).
  * Errors: INVALID_ARG, UNSUPPORTED (with max_new taken as T where it is larger: max_new *
  * q_heads / kv_heads > 2^30, or max_new * q_heads > 2^34; in 4 bits, scale * k_unit outside [2^-120, 3e38)), CUDA.
  */
@@ -565,8 +568,9 @@ mlora_status mlora_debug_cache_expire_wait(mlora_cache_t cache, long long cycles
  *   y = weight * x / sqrt(mean(x^2) + eps)        (y = x where the weight is NULL)
  *   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos),  angle p * freq[i],  for each pair
  *   i < rotary_dim / 2: (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if interleaved
- * elements from rotary_dim on do not turn.  fp32 inside, rounded once; angles are exact modulo a
- * turn to 2^-32 of one.  A head of zeros under eps = 0 gives zeros.
+ * elements from rotary_dim on do not turn.  fp32 inside, rounded once; an
+ * angle is reduced to an eighth of a turn to 2^-32 of a turn and then rounded to fp32, by up to 2^-28
+ * of a turn.  A head of zeros under eps = 0 gives zeros.
  */
 typedef struct mlora_rotary* mlora_rotary_t;
 
@@ -588,7 +592,7 @@ mlora_status mlora_rotary_destroy(mlora_rotary_t rotary);
  * range are left alone, lengths are clamped to 0 .. 2^30; what is out of range sets the status bit that
  * mlora_rotary_status reports.
  *   q_weight, k_weight  device fp32 [head_dim], 16-byte aligned, or NULL: no norm
- *   eps                 >= 0 (not read without weights)
+ *   eps                 >= 0, without weights as well (where it changes nothing)
  * Allocates nothing.  Calls on one handle may overlap, on any streams.
  * Errors: INVALID_ARG, CUDA.
  */

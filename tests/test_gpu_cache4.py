@@ -700,3 +700,19 @@ def test_attention_over_2_30_tokens(rows, dtype, off, D):
     want = torch.from_numpy(u.values(False, None, 0)[:ps, 0].mean(0)).cuda()
     assert ((O[:, 0].double() - want).abs() <= off * want).all()
     assert u.cache.status() == mlora.MLORA_OK
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_an_expired_wait_is_reported_until_read(rows):
+    """As over 8 bits: a wait that gives up sets the status; later calls leave it set and are right."""
+    u = Setup4([300, 20], 1, 64, 16, Hq=2, seed=56)
+    q = strided(np.random.default_rng(57).standard_normal((2 * rows, 2, 64)).astype(F), "bf16")
+    out = [torch.empty_like(q) for _ in range(2)]
+    step = dict(offsets=offsets_of([rows, rows]), max_new=rows)
+    u.cache.attend(q, out[0], u.len, u.pages, **step)
+    assert u.cache.status() == mlora.MLORA_OK
+    mlora.mlora_debug_cache_expire_wait(u.cache.handle, 2_000_000, torch.cuda.current_stream().cuda_stream)
+    u.cache.attend(q, out[1], u.len, u.pages, **step)
+    assert u.cache.status() == mlora.MLORA_ERR_DEVICE_TIMEOUT
+    assert u.cache.status() == mlora.MLORA_OK
+    assert torch.equal(out[0], out[1])
