@@ -540,8 +540,9 @@ mlora_status mlora_cache_read(mlora_cache_t cache, void* K, int64_t k_row_stride
  * for fp32 rows and in 16 for bf16 rows, in 8 where max_new * q_heads / kv_heads > 16; in that form
  * sums of one sign come out 0.25% low over 2^20 tokens, and lower over more.  In 4 bits, up to 16 such
  * rows (or heads of more than 128 elements of fp32 rows), weights have 22 and 11 bits, fewer from 2^-26
- * of the row's largest down, and none under 2^-37 of it.  Scores may have any size up to 2^126 (of
- * unequal ones past 2^29 the larger has all of the weight); larger ones may give NaN.
+ * of the row's largest down, and none under 2^-37 of it.  Scores may have any size up to 2^126 (over 8
+ * bits under a scale of 2^-28 or more; of unequal ones past 2^29 the larger has all of the weight); larger
+ * ones may give NaN.
  * What the arguments cost: max_new chooses one form for all of a step, so that single rows and a prompt
  * go faster as two calls; over 4 bits `width` chooses the form of few rows, so that a table is best no
  * wider than its longest sequence (one of 777 tokens: 9 us, 13 us under a table for 32k).
